@@ -11,8 +11,11 @@
  *   - a host-side block manager (O(1) free list, per-block refcounts, fork,
  *     append with copy-on-write, free, swap out and in),
  * and beyond it: fp8 (E4M3) and int8 caches (quantising write, decode over the
- * codes), swapping of blocks to and from page-locked host memory, and causal
- * prefill attention over the paged cache on the 5th-generation tensor cores.
+ * codes), swapping of blocks to and from page-locked host memory, causal
+ * prefill attention over the paged cache on the 5th-generation tensor cores, and
+ * the operators of a decode loop around the attention: rotary positions joined to
+ * the cache write, attention weights accumulated per cached token and eviction by
+ * them, and beam search's selection with the reordering of the beams' tables.
  *
  * Conventions (all entry points):
  *   - Every function returns an int status: PKV_OK (0) or a negative PKV_ERR_*.
@@ -71,7 +74,8 @@ enum pkv_device_status {
   PKV_DEV_BAD_CONTEXT_LEN = 1, /* a context length was < 0 or > max_blocks_per_seq * block_size; clamped */
   PKV_DEV_BAD_BLOCK_ID = 2,    /* a block-table entry was outside [0, num_blocks); read as zeros */
   PKV_DEV_WAIT_TIMEOUT = 4,    /* a copy into shared memory did not complete within ~1 s; unit skipped */
-  PKV_DEV_WORKSPACE_MISMATCH = 8 /* the workspace was last used with another (num_warps, group, head_dim) */
+  PKV_DEV_WORKSPACE_MISMATCH = 8,/* the workspace was last used with another (num_warps, group, head_dim) */
+  PKV_DEV_BAD_POSITION = 16      /* a token's position was outside the rotary table; clamped */
 };
 
 /* Message of the last failure in this thread ("" if none).  Never NULL. */
@@ -474,6 +478,263 @@ int pkv_decode_step_int8(const void* q, const void* k_new, const void* v_new, vo
                          size_t workspace_bytes, int32_t num_warps, int32_t dtype, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* Rotary positions                                                           */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * Rotary positions turn pairs (x1, x2) of a head's first rotary_dim elements by the
+ * angle a = position * f_i (i < rotary_dim / 2):
+ *   y1 = x1 cos a - x2 sin a,   y2 = x2 cos a + x1 sin a.
+ * Half layout (interleaved = 0): pair i is elements i and i + rotary_dim / 2;
+ * interleaved layout: elements 2i and 2i + 1.  Elements from rotary_dim on pass
+ * through.  (The pages do not treat positions; the formulas stand here in full.)
+ */
+
+/* How the frequencies are scaled for contexts longer than a model was trained on. */
+enum pkv_rotary_scaling {
+  PKV_ROTARY_PLAIN = 0,  /* f_i = base^(-2i / rotary_dim) */
+  PKV_ROTARY_LINEAR = 1, /* f_i / factor */
+  PKV_ROTARY_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) in place of base */
+  PKV_ROTARY_BANDS = 3   /* by turns within original_length, see below */
+};
+
+/*
+ * pkv_rotary_frequencies — the angles per position, computed on the host in 64 bits.
+ * PKV_ROTARY_BANDS: with n_i = original_length * f_i / (2 pi) the turns of pair i
+ * within the original length and t = clamp((n_i - low_turns) / (high_turns -
+ * low_turns), 0, 1), the frequency is f_i * ((1 - t) / factor + t): pairs of few
+ * turns are stretched by factor, pairs of many are kept.
+ * inv_freq   host double [rotary_dim / 2].
+ * rotary_dim even, 2 .. 256; base > 1; factor >= 1 (unused by PLAIN);
+ * original_length > 0 and 0 <= low_turns < high_turns (BANDS only).
+ * Errors: PKV_ERR_INVALID_ARG.
+ */
+int pkv_rotary_frequencies(int32_t rotary_dim, float base, int32_t scaling, float factor,
+                           int32_t original_length, float low_turns, float high_turns,
+                           double* inv_freq);
+
+/*
+ * pkv_rotary_table — fills a table of cos and sin for positions 0 .. max_positions-1:
+ *   table[p, i] = magnitude * cos(p f_i),  table[p, rotary_dim / 2 + i] = magnitude * sin(p f_i),
+ * i < rotary_dim / 2, angles and functions in 64 bits, rounded once to fp32.
+ * inv_freq   host double [rotary_dim / 2] (read before the call returns).
+ * magnitude  factor on every value (1 unless the scaling asks for another).
+ * table      device float [max_positions, rotary_dim], 16-byte aligned.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA.
+ */
+int pkv_rotary_table(const double* inv_freq, int32_t rotary_dim, float magnitude,
+                     int32_t max_positions, float* table, void* stream);
+
+/*
+ * pkv_rotary_write — turn q and k to their positions, write k and v into the cache:
+ * pkv_kv_write with the rotation joined to it, one launch.  For token i with
+ * p = positions[i] and slot s = slot_mapping[i] >= 0:
+ *   q_out[i, h, :]  = turned(q[i, h, :], p)
+ *   k_cache[s / block_size, g, s % block_size, :] = turned(k[i, g, :], p)
+ *   v_cache[s / block_size, g, s % block_size, :] = v[i, g, :]   (bit copy)
+ * Products and sums are fp32, each rounded once, the result rounded to dtype.
+ * q, k, v, q_out  device, token i at i * stride elements, its heads contiguous
+ *               ([num_heads, head_dim]): slices of one fused projection are taken as
+ *               they are.  q_out may be q (same address and stride); otherwise it
+ *               overlaps none of the inputs.
+ * positions     device int32 [num_tokens], in [0, max_positions): others are clamped
+ *               and set PKV_DEV_BAD_POSITION in *status.
+ * table         as pkv_rotary_table fills it: device float [max_positions, rotary_dim].
+ * slot_mapping, caches, num_blocks, block_size: as pkv_kv_write (a token with a negative slot
+ *               is padding: nothing is cached, q_out is written all the same).
+ * status        device int32 word or NULL; bits are ORed in.
+ * Requirements: rotary_dim even, <= head_dim <= 256; head_dim * element size a
+ * multiple of 16 bytes; caches and table 16-byte aligned, q, k, v and q_out aligned
+ * to their element (interleaved: strides even, addresses aligned to two elements).
+ * Strides and addresses that are multiples of 16 bytes, and rotary_dim a multiple
+ * of 16 bytes' elements (half layout: of 32), take the fast path.
+ * num_tokens == 0 is a no-op.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_rotary_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                     const void* v, int64_t v_stride, const int32_t* positions,
+                     const float* table, int32_t max_positions, int32_t rotary_dim,
+                     int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                     void* k_cache, void* v_cache, int32_t num_blocks, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+                     int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream);
+
+/*
+ * pkv_rotary_write_fp8, pkv_rotary_write_int8 — the same into 8-bit caches (layouts,
+ * scales and quantisation as pkv_kv_write_fp8 / _int8; block_size 16, head_dim a
+ * multiple of 16): the turned k is quantised straight from fp32.  dtype is that of
+ * q, k, v and q_out (PKV_F32, PKV_F16 or PKV_BF16).
+ */
+int pkv_rotary_write_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const int32_t* positions,
+                         const float* table, int32_t max_positions, int32_t rotary_dim,
+                         int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                         void* k_cache, void* v_cache, const float* k_scale,
+                         const float* v_scale, int32_t num_blocks, int32_t num_q_heads,
+                         int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+                         int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream);
+int pkv_rotary_write_int8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* positions,
+                          const float* table, int32_t max_positions, int32_t rotary_dim,
+                          int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                          void* k_cache, void* v_cache, const float* k_scale,
+                          const float* v_scale, int32_t num_blocks, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+                          int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Attention weights and eviction by them                                     */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * pkv_decode_attention_weights — pkv_decode_attention that also adds, for every
+ * cached position, its attention weight summed over the query heads of its KV group:
+ *   weight_sums[s, g, p] += sum_{h of group g} w_{s,h,p},   p < t = context_lens[s],
+ * w the softmax weights of pkv_decode_attention's formula (each head's sum to 1).
+ * Positions from t on, and sequences of t = 0, keep what they hold.  out is
+ * bit-identical to pkv_decode_attention's for the same num_warps.
+ *
+ * weight_sums   device float [num_seqs, num_kv_heads, sums_cols], one row a sequence
+ *               of the batch and KV head, updated in place (zero it for a new
+ *               sequence).  A context longer than sums_cols is reported as
+ *               PKV_DEV_BAD_CONTEXT_LEN; its positions from sums_cols on are dropped.
+ * workspace     >= pkv_decode_weights_workspace_size(...) bytes: the decode workspace
+ *               (same zero-filling and layout rules), then the fp32 scores of every
+ *               position a table of max_blocks_per_seq blocks can hold.
+ * The sums are fp32, a position's heads added in order by one thread: the same bits
+ * on every run.  Two launches.  After PKV_DEV_WAIT_TIMEOUT or PKV_DEV_BAD_BLOCK_ID
+ * the affected sums are not to be trusted.  Everything else as pkv_decode_attention.
+ * Errors: as pkv_decode_attention.
+ */
+int pkv_decode_attention_weights(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t block_size, int32_t num_blocks, float scale, void* out,
+                                 float* weight_sums, int32_t sums_cols, void* workspace,
+                                 size_t workspace_bytes, int32_t num_warps, int32_t dtype,
+                                 void* stream);
+
+/* The same over fp8 and int8 caches (as pkv_decode_attention_fp8 / _int8). */
+int pkv_decode_attention_weights_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* context_lens, int32_t num_seqs,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t block_size, int32_t num_blocks, float scale,
+                                     void* out, float* weight_sums, int32_t sums_cols,
+                                     void* workspace, size_t workspace_bytes, int32_t num_warps,
+                                     int32_t dtype, void* stream);
+int pkv_decode_attention_weights_int8(const void* q, const void* k_cache, const void* v_cache,
+                                      const float* k_scale, const float* v_scale,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, int32_t num_blocks, float scale,
+                                      void* out, float* weight_sums, int32_t sums_cols,
+                                      void* workspace, size_t workspace_bytes, int32_t num_warps,
+                                      int32_t dtype, void* stream);
+
+/*
+ * pkv_decode_weights_workspace_size — bytes of device workspace for a batch of at most
+ * num_seqs sequences with tables of at most max_blocks_per_seq blocks.  dtype
+ * PKV_FP8_E4M3 or PKV_INT8 stands for attention over that cache, as for
+ * pkv_decode_workspace_size.
+ */
+int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_seq,
+                                      int32_t block_size, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                                      int32_t num_warps, size_t* bytes);
+
+/*
+ * pkv_evict_select — which cached tokens stay, for every sequence and KV head.
+ * With t = context_lens[s] and n = min(keep_lens[s], t): r = min(recent, n) last
+ * positions stay, then f = min(first, n - r) first ones, and of the positions
+ * f .. t - r - 1 between them the n - r - f with the largest weight_sums[s, h, :]
+ * (equal sums: the lower position; NaN counts as -infinity, -0 as 0).
+ *   kept[s, h, j]     = the j-th kept position, ascending in j < n
+ *   new_sums[s, h, j] = weight_sums[s, h, kept[s, h, j]]
+ *   new_lens[s]       = n
+ * Columns from n on are left as they were.
+ * weight_sums   device float [num_seqs, num_kv_heads, sums_cols].
+ * context_lens, keep_lens  device int32 [num_seqs]; keep_lens below 0 counts as 0.
+ * kept          device int32 [num_seqs, num_kv_heads, kept_cols].
+ * new_sums      device float [num_seqs, num_kv_heads, new_cols]; overlaps no input.
+ * new_lens      device int32 [num_seqs]; not context_lens.
+ * status        device int32 word or NULL: PKV_DEV_BAD_CONTEXT_LEN for a context
+ *               length outside [0, sums_cols] or an n above kept_cols or new_cols
+ *               (clamped).
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_evict_select(const float* weight_sums, int32_t sums_cols, const int32_t* context_lens,
+                     const int32_t* keep_lens, int32_t num_seqs, int32_t num_kv_heads,
+                     int32_t first, int32_t recent, int32_t* kept, int32_t kept_cols,
+                     float* new_sums, int32_t new_cols, int32_t* new_lens, int32_t* status,
+                     void* stream);
+
+/*
+ * pkv_evict_gather — move the kept tokens' K and V rows of one layer into new blocks:
+ * for j < new_lens[s], with p = kept[s, h, j],
+ *   row (new_tables[s, j / B], h, j % B) = row (block_tables[s, p / B], h, p % B)
+ * in both caches (B = block_size; V tiles of 8-bit caches byte by byte).  Slots of
+ * the new blocks from new_lens[s] on are left as they were.
+ * new_tables    device int32 [num_seqs, max_new_blocks] (pkv_seq_evict hands them
+ *               out): blocks that no sequence's block_tables row and no other
+ *               new_tables row names, so that rows can move in any order.
+ * block_tables, caches: as pkv_decode_attention; dtype that of the caches.
+ * kept, new_lens: as pkv_evict_select writes them (any kept positions do).
+ * status        device int32 word or NULL: PKV_DEV_BAD_BLOCK_ID for a position or a
+ *               block id out of range (that row is not moved).
+ * Requirements: head_dim * element size a multiple of 16 bytes, at most 4096; caches
+ * 16-byte aligned; 8-bit caches block_size 16; num_seqs <= 65535.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
+                     int32_t max_blocks_per_seq, const int32_t* kept, int32_t kept_cols,
+                     const int32_t* new_lens, const int32_t* new_tables, int32_t max_new_blocks,
+                     int32_t num_seqs, int32_t num_blocks, int32_t num_kv_heads,
+                     int32_t block_size, int32_t head_dim, int32_t* status, int32_t dtype,
+                     void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Beam search                                                                */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * pkv_beam_select — the best num_out continuations of every request's beams.
+ * Candidate (b, v) of request s scores
+ *   beam_scores[s, b] + logits[s, b, v] - log(sum_u exp(logits[s, b, u])),
+ * and the num_out best of all num_beams * vocab come out in order: by score, equal
+ * scores by beam, within a beam by logit and equal logits by token (lower first).
+ *   scores[s, j], beams[s, j], tokens[s, j]  the j-th best candidate.
+ * ("Copy-on-Write for Beam Search and Parallel Sampling" names beam search as the
+ * user of forked tables; pkv_seq_reorder applies `beams` to them.)
+ * A NaN logit counts as -infinity (a banned token).  A beam whose score is not
+ * finite, or whose largest logit is not, has candidates of score -infinity only, in
+ * token order: such a beam's logits are not read if its score says so (the first
+ * step: one beam 0, the others -infinity).
+ * logits        device, request s, beam b at s * seq_stride + b * beam_stride
+ *               elements, vocab contiguous elements of dtype (PKV_F32, F16, BF16), at
+ *               any alignment of the element.
+ * beam_scores   device float [num_seqs, num_beams]; scores must not be this array.
+ * scores        device float [num_seqs, num_out]; beams, tokens device int32 likewise.
+ * workspace     >= pkv_beam_workspace_size(...) bytes, 256-byte aligned; it needs no
+ *               initial value and keeps none.  Calls that may overlap need their own.
+ * The log-sum-exp and the scores are 64-bit, scores rounded to fp32 at the end; equal
+ * rows of logits have equal log-sum-exps, wherever they lie.
+ * Supported: num_beams <= 64, num_out <= min(128, num_beams * vocab), num_seqs *
+ * num_beams <= 65535, ceil(vocab / 8192) * num_out <= 8192.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_beam_select(const void* logits, int64_t seq_stride, int64_t beam_stride,
+                    const float* beam_scores, int32_t num_seqs, int32_t num_beams, int32_t vocab,
+                    int32_t num_out, float* scores, int32_t* beams, int32_t* tokens,
+                    void* workspace, size_t workspace_bytes, int32_t dtype, void* stream);
+
+int pkv_beam_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_out,
+                            int32_t dtype, size_t* bytes);
+
+/* ------------------------------------------------------------------------- */
 /* Copy-on-write block copy                                                   */
 /* ------------------------------------------------------------------------- */
 
@@ -627,6 +888,35 @@ int pkv_seq_swap_out(pkv_allocator_t* a, int32_t seq, int32_t* ids_out, int32_t 
                      int32_t* n);
 int pkv_seq_swap_in(pkv_allocator_t* a, int32_t seq, int32_t* ids_out, int32_t capacity,
                     int32_t* n);
+
+/*
+ * pkv_seq_evict — the table of a sequence whose cached tokens are cut down to
+ * new_len: min(length, new_len) tokens in ceil(that / block_size) freshly allocated
+ * blocks, written to ids_out in logical order (*n of them).  The old blocks are then
+ * decremented in reverse table order: other holders keep theirs, the rest return to
+ * the pool.  Move the rows with pkv_evict_gather (old table: pkv_seq_table or
+ * pkv_export_tables before this call) on the stream before anything else writes to
+ * the blocks given back.  PKV_ERR_OUT_OF_BLOCKS (state unchanged) if the pool cannot
+ * supply every new block while the old ones are held; PKV_ERR_INVALID_ARG for a bad or
+ * swapped-out id, a negative new_len, or ids_out too small.
+ */
+int pkv_seq_evict(pkv_allocator_t* a, int32_t seq, int32_t new_len, int32_t* ids_out,
+                  int32_t capacity, int32_t* n);
+
+/*
+ * pkv_seq_reorder — beam search's reordering of states: sequence seqs[i] becomes a
+ * continuation of what seqs[parents[i]] was before the call (its table and length),
+ * for every i < k at once ("Copy-on-Write for Beam Search and Parallel Sampling":
+ * beams share their common blocks, a beam that no candidate continues gives its own
+ * back).  Every parent table's blocks are incremented first, then the old tables are
+ * decremented in list order, each in reverse table order.  No block is taken and no
+ * data is copied: the next append of a beam that shares its last, partial block
+ * reports the copy-on-write pair.
+ * seqs      host int32 [k], resident sequence ids, no id twice.
+ * parents   host int32 [k], each in [0, k).
+ * Errors: PKV_ERR_INVALID_ARG (state unchanged).  k = 0 is a no-op.
+ */
+int pkv_seq_reorder(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int32_t* parents);
 
 /* Blocks an append of n_tokens would take from the free list (CoW copy included). */
 int pkv_seq_blocks_needed(pkv_allocator_t* a, int32_t seq, int32_t n_tokens, int32_t* needed);

@@ -34,6 +34,12 @@ written from the pages that describe PagedAttention:
   relate to quantization?").
 * ``int8``             — the int8 quantised KV cache (symmetric codes in
   [-127, 127], per-KV-head scales, the fp8 cache's layouts; same FAQ).
+* ``rotary``           — rotary positions: frequencies and the turning of q and k.
+* ``eviction``         — a decode step's attention weights per cached token, the
+  choice of the tokens that stay, and the move of their rows.
+* ``beam``             — beam search's selection over beams and vocabulary
+  ("PagedAttention: How vLLM Borrowed Virtual Memory...", section "Copy-on-Write
+  for Beam Search and Parallel Sampling", whose forked tables it reorders).
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against values the
 pages print, library routines on special cases, closed forms and invariants.

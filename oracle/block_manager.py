@@ -49,6 +49,10 @@ The rules, in the pages' order:
   newly allocated blocks, all or nothing, in logical order.  A swapped-out
   sequence cannot be appended to, forked or exported until it is swapped in.
 
+* ``evict`` and ``reorder`` serve eviction and beam search: the first gives a sequence
+  fresh blocks for the tokens that stay (its old blocks may be shared), the second makes
+  every listed sequence the continuation of another's state, sharing its blocks.
+
 Sequence ids are handed out 0, 1, 2, ... and never reused.
 """
 from __future__ import annotations
@@ -152,6 +156,38 @@ class BlockManager:
         self.tables[sid] = table
         self.swapped.discard(sid)
         return table
+
+    def evict(self, sid: int, new_len: int) -> List[int]:
+        """Cut ``sid`` down to ``min(length, new_len)`` tokens in fresh blocks (all taken
+        before the old ones are given back, in reverse order); the new table."""
+        self._check_resident(sid)
+        if new_len < 0:
+            raise InvalidOperation("negative length")
+        n = min(self.lengths[sid], new_len)
+        need = -(-n // self.block_size)
+        if need > self.num_free():
+            raise OutOfBlocks("pool cannot hold the kept tokens beside the old blocks")
+        table = [self.alloc() for _ in range(need)]
+        for b in reversed(self.tables[sid]):
+            self.decref(b)
+        self.tables[sid], self.lengths[sid] = table, n
+        return list(table)
+
+    def reorder(self, seqs: Sequence[int], parents: Sequence[int]) -> None:
+        """Beam search: ``seqs[i]`` becomes the continuation of what ``seqs[parents[i]]``
+        was; all new tables are counted before the old ones are given back."""
+        for sid in seqs:
+            self._check_resident(sid)
+        if len(set(seqs)) != len(seqs) or any(not 0 <= p < len(seqs) for p in parents):
+            raise InvalidOperation("a sequence listed twice or a parent out of range")
+        new = [(list(self.tables[seqs[p]]), self.lengths[seqs[p]]) for p in parents]
+        for table, _ in new:
+            for b in table:
+                self.incref(b)
+        for sid, (table, length) in zip(seqs, new):
+            for b in reversed(self.tables[sid]):
+                self.decref(b)
+            self.tables[sid], self.lengths[sid] = table, length
 
     def blocks_needed(self, sid: int, n: int) -> int:
         """Blocks an append of ``n`` tokens would take from the free list."""

@@ -16,6 +16,15 @@ Public API (all device work runs in libpkv.so's sm_103a kernels):
 * ``paged_swap_out`` / ``paged_swap_in`` — blocks to and from pinned host memory
   (preemption by swapping, with ``BlockAllocator.swap_out`` / ``swap_in``);
   ``paged_swap_out_layers`` / ``paged_swap_in_layers`` — every layer's caches, one launch
+* rotary positions: ``rotary_frequencies``, ``rotary_table``; ``paged_rotary_write`` (and
+  ``_fp8``, ``_int8``) — q and k turned to their positions, k and v written into the cache,
+  one launch
+* eviction: ``paged_decode_attention_weights`` (and ``_fp8``, ``_int8``) — decode attention
+  that adds each cached token's attention weight to a running sum; ``paged_evict_select`` —
+  the tokens that stay; ``paged_evict_gather`` — their rows moved into fresh blocks (with
+  ``BlockAllocator.evict``)
+* beam search: ``beam_select`` — the best continuations over beams and vocabulary (with
+  ``BlockAllocator.reorder``)
 * ``BlockAllocator`` — host block manager (free list, refcounts, fork, CoW, free);
   ``DecodeStepTables`` — one decode step's appends and table export, pre-bound
 * ``decode_status(workspace)`` — the device-side status bits of the decode kernels;
@@ -35,6 +44,11 @@ def __getattr__(name):
                 "paged_decode_step_fp8", "paged_kv_write_int8", "paged_decode_attention_int8",
                 "paged_decode_step_int8", "paged_swap_out", "paged_swap_in", "paged_swap_out_layers", "paged_swap_in_layers",
                 "paged_prefill_attention",
+                "rotary_frequencies", "rotary_table", "paged_rotary_write",
+                "paged_rotary_write_fp8", "paged_rotary_write_int8",
+                "paged_decode_attention_weights", "paged_decode_attention_weights_fp8",
+                "paged_decode_attention_weights_int8", "weights_workspace_bytes",
+                "paged_evict_select", "paged_evict_gather", "beam_select", "beam_workspace_bytes",
                 "decode_status", "workspace_bytes", "default_num_warps", "get_workspace",
                 "wait_timeout_selftest"):
         from . import ops

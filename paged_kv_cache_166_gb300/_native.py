@@ -25,6 +25,9 @@ PKV_DEV_BAD_CONTEXT_LEN = 1
 PKV_DEV_BAD_BLOCK_ID = 2
 PKV_DEV_WAIT_TIMEOUT = 4
 PKV_DEV_WORKSPACE_MISMATCH = 8
+PKV_DEV_BAD_POSITION = 16
+
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
 
 PKV_STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -78,6 +81,37 @@ SIGNATURES = {
     "pkv_decode_step_int8": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _i32, _p, _i32, _i32,
                                             _i32, _i32, _i32, _i32, _f, _p, _p, _sz, _i32, _i32,
                                             _p]),
+    "pkv_rotary_frequencies": (ctypes.c_int, [_i32, _f, _i32, _f, _i32, _f, _f, _p]),
+    "pkv_rotary_table": (ctypes.c_int, [_p, _i32, _f, _i32, _p, _p]),
+    "pkv_rotary_write": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _i32, _i32, _p,
+                                        _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _i64, _p,
+                                        _i32, _p]),
+    "pkv_rotary_write_fp8": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _i32, _i32,
+                                            _p, _i32, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32,
+                                            _p, _i64, _p, _i32, _p]),
+    "pkv_rotary_write_int8": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _i32,
+                                             _i32, _p, _i32, _p, _p, _p, _p, _i32, _i32, _i32,
+                                             _i32, _i32, _p, _i64, _p, _i32, _p]),
+    "pkv_decode_attention_weights": (ctypes.c_int, [_p, _p, _p, _p, _i32, _p, _i32, _i32, _i32,
+                                                    _i32, _i32, _i32, _f, _p, _p, _i32, _p, _sz,
+                                                    _i32, _i32, _p]),
+    "pkv_decode_attention_weights_fp8": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i32, _p, _i32,
+                                                        _i32, _i32, _i32, _i32, _i32, _f, _p, _p,
+                                                        _i32, _p, _sz, _i32, _i32, _p]),
+    "pkv_decode_attention_weights_int8": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i32, _p, _i32,
+                                                         _i32, _i32, _i32, _i32, _i32, _f, _p, _p,
+                                                         _i32, _p, _sz, _i32, _i32, _p]),
+    "pkv_decode_weights_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                         _i32, ctypes.POINTER(_sz)]),
+    "pkv_evict_select": (ctypes.c_int, [_p, _i32, _p, _p, _i32, _i32, _i32, _i32, _p, _i32, _p,
+                                        _i32, _p, _p, _p]),
+    "pkv_evict_gather": (ctypes.c_int, [_p, _p, _p, _i32, _p, _i32, _p, _p, _i32, _i32, _i32, _i32,
+                                        _i32, _i32, _p, _i32, _p]),
+    "pkv_beam_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _p, _p, _p,
+                                       _sz, _i32, _p]),
+    "pkv_beam_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "pkv_seq_evict": (ctypes.c_int, [_p, _i32, _i32, _pi32, _i32, _pi32]),
+    "pkv_seq_reorder": (ctypes.c_int, [_p, _pi32, _i32, _pi32]),
     "pkv_allocator_create": (ctypes.c_int, [_i32, _i32, _pi32, ctypes.POINTER(_p)]),
     "pkv_allocator_destroy": (ctypes.c_int, [_p]),
     "pkv_block_alloc": (ctypes.c_int, [_p, _pi32]),

@@ -130,6 +130,27 @@ class BlockAllocator:
         N.check(self._lib.pkv_seq_swap_in(self._h, seq, _ptr(buf), len(buf), ctypes.byref(n)))
         return buf[:n.value].tolist()
 
+    def evict(self, seq: int, new_len: int) -> List[int]:
+        """Cut a sequence down to min(length, new_len) cached tokens in fresh blocks; returns
+        the new table.  The old blocks go back to the pool (or to their other holders):
+        export the old table before, and queue paged_evict_gather before anything else
+        writes to them."""
+        B = self.block_size
+        buf = np.empty(max(-(-min(self.length(seq), max(new_len, 0)) // B), 1), dtype=np.int32)
+        n = ctypes.c_int32(0)
+        N.check(self._lib.pkv_seq_evict(self._h, seq, new_len, _ptr(buf), len(buf),
+                                        ctypes.byref(n)))
+        return buf[:n.value].tolist()
+
+    def reorder(self, seqs: Sequence[int], parents: Sequence[int]) -> None:
+        """Beam search: each seqs[i] becomes the continuation of what seqs[parents[i]] was
+        (table and length), all at once; distinct ids, parents in [0, len(seqs))."""
+        ids = np.ascontiguousarray(seqs, dtype=np.int32)
+        par = np.ascontiguousarray(parents, dtype=np.int32)
+        if ids.ndim != 1 or ids.shape != par.shape:
+            raise ValueError("seqs and parents must be lists of one length")
+        N.check(self._lib.pkv_seq_reorder(self._h, _ptr(ids), len(ids), _ptr(par)))
+
     def length(self, seq: int) -> int:
         return self._out(self._lib.pkv_seq_len, seq)
 

@@ -14,7 +14,9 @@
 //     your GPU memory", section "Preemption: what happens when memory runs out
 //     anyway"): swap-out hands back the sequence's blocks (their contents go to
 //     host memory) and keeps its length; swap-in gives it ceil(len / B) fresh
-//     blocks, all or nothing.
+//     blocks, all or nothing;
+//   * eviction gives a sequence fresh blocks for the tokens that stay and hands the
+//     old ones back; reordering makes each listed sequence the continuation of another.
 // Every public call validates first and mutates only once it cannot fail, so a
 // failing call leaves the state unchanged.
 #include <algorithm>
@@ -65,11 +67,19 @@ struct pkv_allocator {
     int32_t len = 0;
     bool live = false;
     bool swapped = false;  // blocks handed back by swap-out, not yet swapped in
-    uint32_t mark = 0;     // batched append: the call that last listed it
+    uint32_t mark = 0;     // batched append, reorder: the call that last listed it
   };
   std::vector<Seq> seqs;             // indexed by sequence id
-  uint32_t mark_epoch = 0;           // batched append: calls so far
+  uint32_t mark_epoch = 0;           // batched calls so far
 
+  // Number of a batched call, for the marks of the sequences it lists.
+  uint32_t next_epoch() {
+    if (++mark_epoch == 0) {
+      for (auto& s : seqs) s.mark = 0;
+      mark_epoch = 1;
+    }
+    return mark_epoch;
+  }
   bool valid_block(int32_t b) const { return b >= 0 && b < num_blocks; }
   bool allocated(int32_t b) const { return valid_block(b) && refcount[b] > 0; }
   bool live_seq(int32_t s) const {
@@ -253,6 +263,65 @@ int pkv_seq_swap_in(pkv_allocator_t* a, int32_t seq, int32_t* ids_out, int32_t c
   });
 }
 
+int pkv_seq_evict(pkv_allocator_t* a, int32_t seq, int32_t new_len, int32_t* ids_out,
+                  int32_t capacity, int32_t* n) {
+  PKV_REQUIRE(a && n, PKV_ERR_INVALID_ARG, "NULL argument");
+  PKV_REQUIRE(a->resident_seq(seq), PKV_ERR_INVALID_ARG, "unknown or swapped-out sequence %d",
+              seq);
+  PKV_REQUIRE(new_len >= 0, PKV_ERR_INVALID_ARG, "negative length");
+  auto& s = a->seqs[seq];
+  const int32_t len = std::min(s.len, new_len);
+  const int64_t B = a->block_size;
+  const int32_t m = static_cast<int32_t>((len + B - 1) / B);
+  PKV_REQUIRE(m == 0 || (ids_out && capacity >= m), PKV_ERR_INVALID_ARG,
+              "ids_out holds %d ids, the sequence needs %d blocks", capacity, m);
+  PKV_REQUIRE(static_cast<size_t>(m) <= a->free_stack.size(), PKV_ERR_OUT_OF_BLOCKS,
+              "eviction needs %d blocks, %zu free", m, a->free_stack.size());
+  return guarded([&] {
+    std::vector<int32_t> table(m);  // before any block is taken; no effect if it throws
+    for (int32_t j = 0; j < m; ++j) table[j] = ids_out[j] = a->pop();
+    for (auto it = s.table.rbegin(); it != s.table.rend(); ++it) a->decref(*it);
+    s.table.swap(table);
+    s.len = len;
+    *n = m;
+    return pkv::ok();
+  });
+}
+
+int pkv_seq_reorder(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int32_t* parents) {
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL handle");
+  PKV_REQUIRE(k >= 0, PKV_ERR_INVALID_ARG, "negative sequence count");
+  PKV_REQUIRE(k == 0 || (seqs && parents), PKV_ERR_INVALID_ARG, "NULL array");
+  return guarded([&] {
+    const uint32_t epoch = a->next_epoch();
+    for (int32_t i = 0; i < k; ++i) {
+      PKV_REQUIRE(a->resident_seq(seqs[i]), PKV_ERR_INVALID_ARG,
+                  "unknown or swapped-out sequence %d", seqs[i]);
+      PKV_REQUIRE(a->seqs[seqs[i]].mark != epoch, PKV_ERR_INVALID_ARG,
+                  "sequence %d listed twice", seqs[i]);
+      a->seqs[seqs[i]].mark = epoch;
+      PKV_REQUIRE(parents[i] >= 0 && parents[i] < k, PKV_ERR_INVALID_ARG,
+                  "parent %d outside [0, %d)", parents[i], k);
+    }
+    // copies of the parents' tables, made before anything changes
+    std::vector<std::vector<int32_t>> tables(k);
+    std::vector<int32_t> lens(k);
+    for (int32_t i = 0; i < k; ++i) {
+      tables[i] = a->seqs[seqs[parents[i]]].table;
+      lens[i] = a->seqs[seqs[parents[i]]].len;
+    }
+    for (int32_t i = 0; i < k; ++i)
+      for (int32_t b : tables[i]) a->refcount[b] += 1;
+    for (int32_t i = 0; i < k; ++i) {
+      auto& s = a->seqs[seqs[i]];
+      for (auto it = s.table.rbegin(); it != s.table.rend(); ++it) a->decref(*it);
+      s.table.swap(tables[i]);
+      s.len = lens[i];
+    }
+    return pkv::ok();
+  });
+}
+
 int pkv_seq_blocks_needed(pkv_allocator_t* a, int32_t seq, int32_t n, int32_t* needed) {
   PKV_REQUIRE(a && needed, PKV_ERR_INVALID_ARG, "NULL argument");
   PKV_REQUIRE(a->resident_seq(seq), PKV_ERR_INVALID_ARG, "unknown or swapped-out sequence %d",
@@ -318,11 +387,7 @@ int pkv_seq_append_one_each(pkv_allocator_t* a, const int32_t* seqs, int32_t k,
     std::vector<std::pair<int32_t, int32_t>> drops;  // (block, refcount dropped so far)
     int64_t need = 0;
     // a sequence listed twice is found by its mark (this call's number), in O(k)
-    if (++a->mark_epoch == 0) {
-      for (auto& s : a->seqs) s.mark = 0;
-      a->mark_epoch = 1;
-    }
-    const uint32_t epoch = a->mark_epoch;
+    const uint32_t epoch = a->next_epoch();
     for (int32_t i = 0; i < k; ++i) {
       const int32_t q = seqs[i];
       PKV_REQUIRE(a->resident_seq(q), PKV_ERR_INVALID_ARG, "unknown or swapped-out sequence %d",

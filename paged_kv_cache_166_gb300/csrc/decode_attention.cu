@@ -48,6 +48,10 @@
 // exactly to f16 pairs by integer operations and scaled per KV head around the same
 // tensor-core contractions.
 //
+// With kWeights (decode_weights.cu) the kernel also leaves, for every step, the scores of
+// its 16 tokens and, for every query head, the log-sum-exp of its context: what the
+// attention weights are computed from once all of a head's context has been seen.
+//
 // The kernel is launched with programmatic stream serialisation: its prologue
 // (schedule, block-table prefetch) overlaps the tail of the preceding cache write
 // (pkv_kv_write, or the decode step's write of each new token), and
@@ -131,6 +135,11 @@ struct DecodeArgs {
   int32_t q_stride;  // per-stage q slot
   int32_t unit_cost; // start-up cost of a unit, in quarter steps
   float scale_log2;  // scale * log2(e)
+  // kWeights only: scores [steps, 16, G] in log2 units (a step's position in the flat
+  // list is its index), their log-sum-exp [S, Hq] in log2 units, the schedule's pre [S + 1]
+  float* scores;
+  float* lse;
+  int32_t* steps;
 };
 
 // Cache element tags of the 8-bit caches, fp8 (E4M3) and int8 codes with
@@ -177,7 +186,7 @@ struct Shape {
 // Warp w owns the steps whose cost position lies in [w R, (w+1) R): equal cost,
 // not equal step count, so warps holding many short contexts get fewer steps.
 // ---------------------------------------------------------------------------------
-__device__ void build_schedule(const int32_t* __restrict__ context_lens, int S, int MAXB,
+static __device__ void build_schedule(const int32_t* __restrict__ context_lens, int S, int MAXB,
                                int block_size, int Hkv,
                                int unit_cost, int32_t* ctx_s, int32_t* pre, int32_t* prew,
                                int32_t* scratch, int32_t* status) {
@@ -337,6 +346,30 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk16) {
   }
 }
 
+// Scores of one step (rows gid and gid + 8 of the 16 tokens, heads 2 tig and 2 tig + 1)
+// to sc [16, G]: for G = 8 a warp's two stores fill 256 contiguous bytes each.
+__device__ __forceinline__ void store_scores(const float (&x)[4], float* sc, int G, int lane) {
+  const int gid = lane >> 2, h = 2 * (lane & 3);
+  if (G == 1) {
+    if (h == 0) {
+      sc[gid] = x[0];
+      sc[gid + 8] = x[2];
+    }
+  } else if (h < G) {
+    *reinterpret_cast<float2*>(sc + gid * G + h) = make_float2(x[0], x[1]);
+    *reinterpret_cast<float2*>(sc + (gid + 8) * G + h) = make_float2(x[2], x[3]);
+  }
+}
+
+// Log-sum-exps (log2 units) of heads 2 tig and 2 tig + 1, from the lanes of row 0.
+__device__ __forceinline__ void store_lse(float m0, float l0, float m1, float l1, float* lse,
+                                          int G, int lane) {
+  const int h = 2 * (lane & 3);
+  if ((lane >> 2) != 0) return;
+  if (h < G) lse[h] = m0 + log2f(l0);
+  if (h + 1 < G) lse[h + 1] = m1 + log2f(l1);
+}
+
 template <typename T, int D>
 struct MmaState {
   static constexpr int KS = D / 16;
@@ -445,9 +478,11 @@ struct MmaState {
     a[3] &= mhi;
   }
 
-  // Whole step reading the tile from shared memory as it goes.
+  // Whole step reading the tile from shared memory as it goes; kWeights: its scores
+  // are left at sc [16, G] too.
+  template <bool kWeights>
   __device__ __forceinline__ void step_smem(uint32_t ktile, uint32_t vtile, int valid,
-                                            float scale_log2, int lane) {
+                                            float scale_log2, int lane, float* sc, int G) {
     float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -464,6 +499,7 @@ struct MmaState {
       if (gid >= valid) x[0] = x[1] = -INFINITY;
       if (gid + 8 >= valid) x[2] = x[3] = -INFINITY;
     }
+    if constexpr (kWeights) store_scores(x, sc, G, lane);
     uint32_t pb0, pb1;
     softmax(x, pb0, pb1);
 #pragma unroll
@@ -481,6 +517,10 @@ struct MmaState {
       l0 += __shfl_xor_sync(0xffffffffu, l0, off);
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
+  }
+
+  __device__ __forceinline__ void write_lse(float* lse, int G, int lane) {
+    store_lse(m0, l0, m1, l1, lse, G, lane);
   }
 
   // Normalised rows of the G heads into out[s, g*G + h, :].
@@ -607,8 +647,9 @@ struct Q8State {
     }
   }
 
+  template <bool kWeights>
   __device__ __forceinline__ void step_smem(uint32_t ktile, uint32_t vtile, int valid,
-                                            float /*scale_log2*/, int lane) {
+                                            float /*scale_log2*/, int lane, float* sc, int G) {
     const int gid = lane >> 2, tig = lane & 3, mi = lane >> 3, r = lane & 7;
     float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
     // ldmatrix of K: matrices {tok 0-7, chunk 2p}, {tok 8-15, 2p}, {0-7, 2p+1}, {8-15, 2p+1}
@@ -635,6 +676,7 @@ struct Q8State {
       if (gid >= valid) x[0] = x[1] = -INFINITY;
       if (gid + 8 >= valid) x[2] = x[3] = -INFINITY;
     }
+    if constexpr (kWeights) store_scores(x, sc, G, lane);
     // online softmax, P^T as the f16 B operand
     float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
@@ -707,6 +749,10 @@ struct Q8State {
     }
   }
 
+  __device__ __forceinline__ void write_lse(float* lse, int G, int lane) {
+    store_lse(m0, l0, m1, l1, lse, G, lane);
+  }
+
   __device__ __forceinline__ void write_out(T* out_rows, int G, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
     const float i0 = vs / l0, i1 = vs / l1;
@@ -775,8 +821,9 @@ struct FmaState {
                                            (d & 3) * 4);
   }
 
+  template <bool kWeights>
   __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int valid,
-                                       float scale_log2, int G, int lane) {
+                                       float scale_log2, int G, int lane, float* scores) {
     float kv[kTok][E];
 #pragma unroll
     for (int t = 0; t < kTok; ++t)
@@ -796,6 +843,9 @@ struct FmaState {
         for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
         sc[t] = t < valid ? part * scale_log2 : -INFINITY;
         mx = fmaxf(mx, sc[t]);
+        if constexpr (kWeights) {
+          if (lane == t) scores[t * G + h] = sc[t];
+        }
       }
       const float mn = fmaxf(m[h], mx);
       const float al = exp2f(m[h] - mn);
@@ -819,6 +869,12 @@ struct FmaState {
   }
 
   __device__ __forceinline__ void reduce_sums() {}
+
+  __device__ __forceinline__ void write_lse(float* lse, int G, int lane) {
+#pragma unroll
+    for (int h = 0; h < kMaxGroup; ++h)
+      if (h < G && lane == h) lse[h] = m[h] + log2f(l[h]);
+  }
 
   __device__ __forceinline__ void write_out(float* out_rows, int G, int lane) {
 #pragma unroll
@@ -855,7 +911,7 @@ __device__ __forceinline__ int64_t piece_slot(int w, int first_warp) {
 // The warp's lanes split the G heads and, within a head, the head_dim; the lanes
 // of one head share the max over pieces, and piece loads are issued two at a
 // time so the merge costs a few L2 round trips, not one per value.
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool kWeights>
 __device__ void merge_pieces_g(const DecodeArgs& a, int s, int g, int w0, int w1, int lane) {
   constexpr int LPH = 32 / G;          // lanes per head
   constexpr int E = D / LPH;           // contiguous elements of the row per lane
@@ -891,19 +947,22 @@ __device__ void merge_pieces_g(const DecodeArgs& a, int s, int g, int w0, int w1
     }
   }
   const float inv = 1.f / lsum;
+  if constexpr (kWeights) {
+    if (sub == 0) a.lse[static_cast<int64_t>(s) * a.Hq + g * G + h] = M + log2f(lsum);
+  }
   T* const row = reinterpret_cast<T*>(a.out) + (static_cast<int64_t>(s) * a.Hq + g * G + h) * D +
                  sub * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) row[e] = ptx::from_float<T>(acc[e] * inv);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWeights>
 __device__ void merge_pieces(const DecodeArgs& a, int s, int g, int w0, int w1, int lane) {
   switch (a.G) {
-    case 1: merge_pieces_g<T, D, 1>(a, s, g, w0, w1, lane); break;
-    case 2: merge_pieces_g<T, D, 2>(a, s, g, w0, w1, lane); break;
-    case 4: merge_pieces_g<T, D, 4>(a, s, g, w0, w1, lane); break;
-    default: merge_pieces_g<T, D, 8>(a, s, g, w0, w1, lane); break;
+    case 1: merge_pieces_g<T, D, 1, kWeights>(a, s, g, w0, w1, lane); break;
+    case 2: merge_pieces_g<T, D, 2, kWeights>(a, s, g, w0, w1, lane); break;
+    case 4: merge_pieces_g<T, D, 4, kWeights>(a, s, g, w0, w1, lane); break;
+    default: merge_pieces_g<T, D, 8, kWeights>(a, s, g, w0, w1, lane); break;
   }
 }
 
@@ -916,7 +975,7 @@ struct CutUnit {
 // run), with every load of both issued before any is used: one L2 round trip
 // instead of two per cut.  Same operations in the same order as merge_pieces_g, so
 // the same bits.
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool kWeights>
 __device__ void merge_pairs_g(const DecodeArgs& a, const CutUnit* u, int n, int lane) {
   constexpr int LPH = 32 / G;
   constexpr int E = D / LPH;
@@ -968,6 +1027,9 @@ __device__ void merge_pairs_g(const DecodeArgs& a, const CutUnit* u, int n, int 
           for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, o[k][p][e], acc[e]);
         }
         const float inv = 1.f / lsum;
+        if constexpr (kWeights) {
+          if (sub == 0) a.lse[static_cast<int64_t>(c.s) * a.Hq + c.g * G + h] = M + log2f(lsum);
+        }
         T* const row = reinterpret_cast<T*>(a.out) +
                        (static_cast<int64_t>(c.s) * a.Hq + c.g * G + h) * D + sub * E;
 #pragma unroll
@@ -977,13 +1039,13 @@ __device__ void merge_pairs_g(const DecodeArgs& a, const CutUnit* u, int n, int 
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWeights>
 __device__ void merge_pairs(const DecodeArgs& a, const CutUnit* u, int n, int lane) {
   switch (a.G) {
-    case 1: merge_pairs_g<T, D, 1>(a, u, n, lane); break;
-    case 2: merge_pairs_g<T, D, 2>(a, u, n, lane); break;
-    case 4: merge_pairs_g<T, D, 4>(a, u, n, lane); break;
-    default: merge_pairs_g<T, D, 8>(a, u, n, lane); break;
+    case 1: merge_pairs_g<T, D, 1, kWeights>(a, u, n, lane); break;
+    case 2: merge_pairs_g<T, D, 2, kWeights>(a, u, n, lane); break;
+    case 4: merge_pairs_g<T, D, 4, kWeights>(a, u, n, lane); break;
+    default: merge_pairs_g<T, D, 8, kWeights>(a, u, n, lane); break;
   }
 }
 
@@ -992,7 +1054,7 @@ __device__ void merge_pairs(const DecodeArgs& a, const CutUnit* u, int n, int la
 // ---------------------------------------------------------------------------------
 // kBlk: 16 for caches of 16-token blocks; 0 for 8- or 32-token blocks (the size
 // then comes from the arguments).
-template <typename T, typename C, int D, int kBlk>
+template <typename T, typename C, int D, int kBlk, bool kWeights>
 __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     decode_attention_kernel(const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
@@ -1045,6 +1107,10 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     a.status[1] = a.total_warps;
     a.status[2] = a.G;
     a.status[3] = D;
+  }
+  if constexpr (kWeights) {
+    if (blockIdx.x == 0)
+      for (int s = threadIdx.x; s <= a.S; s += blockDim.x) a.steps[s] = pre[s];
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1275,11 +1341,14 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     }
     const int valid = (cc.j == cc.nb - 1) ? ctx_s[cc.s] - cc.j * kTok : kTok;
     const uint32_t kt = tiles + c_stage * Sh::kStageBytes;
+    float* sc = nullptr;
+    if constexpr (kWeights) sc = a.scores + static_cast<int64_t>(f0 + n) * (kTok * a.G);
     if constexpr (sizeof(T) == 2) {
-      st_.step_smem(kt, kt + Sh::kTileBytes, valid, a.scale_log2, lane);
+      st_.template step_smem<kWeights>(kt, kt + Sh::kTileBytes, valid, a.scale_log2, lane, sc,
+                                       a.G);
     } else {
       const uint8_t* ktp = base + (kt - base_s);
-      st_.step(ktp, ktp + Sh::kTileBytes, valid, a.scale_log2, a.G, lane);
+      st_.template step<kWeights>(ktp, ktp + Sh::kTileBytes, valid, a.scale_log2, a.G, lane, sc);
     }
     // the stage is refilled once its arithmetic is done
     __syncwarp();
@@ -1290,6 +1359,8 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
       st_.reduce_sums();
       if (unit_end && first_j == 0) {
         st_.write_out(out + (static_cast<int64_t>(cc.s) * a.Hq + cc.g * a.G) * D, a.G, lane);
+        if constexpr (kWeights)
+          st_.write_lse(a.lse + static_cast<int64_t>(cc.s) * a.Hq + cc.g * a.G, a.G, lane);
       } else {
         const int slot = 2 * gw + (first_j == 0 ? 1 : 0);
         st_.write_partial(a.part_o + static_cast<int64_t>(slot) * a.G * D,
@@ -1324,10 +1395,10 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     }
     if (nmine > 0) {
       __threadfence();
-      if (npairs > 0) merge_pairs<T, D>(a, pairs, npairs, lane);
+      if (npairs > 0) merge_pairs<T, D, kWeights>(a, pairs, npairs, lane);
       for (int i = 0; i < nmine; ++i) {
         const CutUnit& u = mine[i];
-        if (u.w1 != u.w0 + 1) merge_pieces<T, D>(a, u.s, u.g, u.w0, u.w1, lane);
+        if (u.w1 != u.w0 + 1) merge_pieces<T, D, kWeights>(a, u.s, u.g, u.w0, u.w1, lane);
         if (lane == 0) a.tickets[u.w0] = 0;  // ready for the next launch
       }
     }
@@ -1357,6 +1428,9 @@ struct HostArgs {
   int32_t codes = 0;  // 8-bit caches with per-KV-head scales: PKV_FP8_E4M3 or PKV_INT8
   const float* k_scale = nullptr;
   const float* v_scale = nullptr;
+  float* scores = nullptr;  // kWeights: as in DecodeArgs
+  float* lse = nullptr;
+  int32_t* steps = nullptr;
 };
 
 bool supported_head_dim(int32_t dtype, int32_t D) {
@@ -1383,7 +1457,7 @@ int device_smem_optin(int* bytes) {
   return PKV_OK;
 }
 
-template <typename T, typename C, int D, int kBlk>
+template <typename T, typename C, int D, int kBlk, bool kWeights>
 int ensure_smem_attr() {
   // Raise the dynamic shared-memory limit once per device for this instantiation.
   static std::once_flag flags[64];
@@ -1395,7 +1469,7 @@ int ensure_smem_attr() {
   int rc = device_smem_optin(&optin);
   if (rc != PKV_OK) return rc;
   std::call_once(flags[dev], [&] {
-    results[dev] = cudaFuncSetAttribute(decode_attention_kernel<T, C, D, kBlk>,
+    results[dev] = cudaFuncSetAttribute(decode_attention_kernel<T, C, D, kBlk, kWeights>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
   });
   if (results[dev] != cudaSuccess)
@@ -1522,13 +1596,16 @@ DecodeArgs device_args(const HostArgs& h, int W) {
   a.scale_log2 = h.scale * 1.4426950408889634f;
   a.k_scale = h.k_scale;
   a.v_scale = h.v_scale;
+  a.scores = h.scores;
+  a.lse = h.lse;
+  a.steps = h.steps;
   return a;
 }
 
-template <typename T, typename C, int D, int kBlk>
+template <typename T, typename C, int D, int kBlk, bool kWeights>
 int launch_decode(const HostArgs& h, int W) {
   using Sh = Shape<C, D>;
-  int rc = ensure_smem_attr<T, C, D, kBlk>();
+  int rc = ensure_smem_attr<T, C, D, kBlk, kWeights>();
   if (rc != PKV_OK) return rc;
   int optin = 0;
   rc = device_smem_optin(&optin);
@@ -1592,14 +1669,16 @@ int launch_decode(const HostArgs& h, int W) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  PKV_CUDA(cudaLaunchKernelEx(&cfg, decode_attention_kernel<T, C, D, kBlk>, kmap, vmap, a));
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, decode_attention_kernel<T, C, D, kBlk, kWeights>, kmap, vmap,
+                              a));
   return PKV_OK;
 }
 
+template <bool kWeights>
 int dispatch(const HostArgs& h, int W) {
   if (h.codes != 0) {
 #define PKV_CASE8(CT, DT, TT, DD) \
-  if (h.dtype == DT && h.D == DD) return launch_decode<TT, CT, DD, kTok>(h, W);
+  if (h.dtype == DT && h.D == DD) return launch_decode<TT, CT, DD, kTok, kWeights>(h, W);
     if (h.codes == PKV_FP8_E4M3) {
       PKV_CASE8(E4M3, PKV_BF16, __nv_bfloat16, 128)
       PKV_CASE8(E4M3, PKV_BF16, __nv_bfloat16, 256)
@@ -1616,7 +1695,7 @@ int dispatch(const HostArgs& h, int W) {
   }
   if (h.block_size != kTok) {
 #define PKV_CASEB(DT, TT, DD) \
-  if (h.dtype == DT && h.D == DD) return launch_decode<TT, TT, DD, 0>(h, W);
+  if (h.dtype == DT && h.D == DD) return launch_decode<TT, TT, DD, 0, kWeights>(h, W);
     PKV_CASEB(PKV_BF16, __nv_bfloat16, 64)
     PKV_CASEB(PKV_BF16, __nv_bfloat16, 128)
     PKV_CASEB(PKV_BF16, __nv_bfloat16, 256)
@@ -1627,7 +1706,7 @@ int dispatch(const HostArgs& h, int W) {
     return fail(PKV_ERR_UNSUPPORTED, "block_size %d needs an f16 or bf16 cache", h.block_size);
   }
 #define PKV_CASE(DT, TT, DD) \
-  if (h.dtype == DT && h.D == DD) return launch_decode<TT, TT, DD, kTok>(h, W);
+  if (h.dtype == DT && h.D == DD) return launch_decode<TT, TT, DD, kTok, kWeights>(h, W);
   PKV_CASE(PKV_BF16, __nv_bfloat16, 64)
   PKV_CASE(PKV_BF16, __nv_bfloat16, 128)
   PKV_CASE(PKV_BF16, __nv_bfloat16, 256)
@@ -1641,8 +1720,41 @@ int dispatch(const HostArgs& h, int W) {
   return fail(PKV_ERR_UNSUPPORTED, "head_dim %d unsupported for dtype %d", h.D, h.dtype);
 }
 
+HostArgs host_args(const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                   const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                   float scale, void* out, void* workspace, size_t workspace_bytes,
+                   int32_t num_warps, int32_t dtype, void* stream) {
+  HostArgs h;
+  h.q = q;
+  h.k_cache = k_cache;
+  h.v_cache = v_cache;
+  h.block_tables = block_tables;
+  h.MAXB = max_blocks_per_seq;
+  h.context_lens = context_lens;
+  h.S = num_seqs;
+  h.Hq = num_q_heads;
+  h.Hkv = num_kv_heads;
+  h.D = head_dim;
+  h.block_size = block_size;
+  h.NB = num_blocks;
+  h.scale = scale;
+  h.out = out;
+  h.workspace = workspace;
+  h.workspace_bytes = workspace_bytes;
+  h.num_warps = num_warps;
+  h.dtype = dtype;
+  h.stream = static_cast<cudaStream_t>(stream);
+  return h;
+}
+
 }  // namespace
 }  // namespace pkv
+
+// The translation unit of the attention weights takes the templates above and brings
+// its own entry points.
+#ifndef PKV_DECODE_TEMPLATES_ONLY
 
 using namespace pkv;
 
@@ -1676,41 +1788,12 @@ int pkv_decode_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t
 }
 
 namespace {
-HostArgs host_args(const void* q, const void* k_cache, const void* v_cache,
-                   const int32_t* block_tables, int32_t max_blocks_per_seq,
-                   const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
-                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
-                   float scale, void* out, void* workspace, size_t workspace_bytes,
-                   int32_t num_warps, int32_t dtype, void* stream) {
-  HostArgs h;
-  h.q = q;
-  h.k_cache = k_cache;
-  h.v_cache = v_cache;
-  h.block_tables = block_tables;
-  h.MAXB = max_blocks_per_seq;
-  h.context_lens = context_lens;
-  h.S = num_seqs;
-  h.Hq = num_q_heads;
-  h.Hkv = num_kv_heads;
-  h.D = head_dim;
-  h.block_size = block_size;
-  h.NB = num_blocks;
-  h.scale = scale;
-  h.out = out;
-  h.workspace = workspace;
-  h.workspace_bytes = workspace_bytes;
-  h.num_warps = num_warps;
-  h.dtype = dtype;
-  h.stream = static_cast<cudaStream_t>(stream);
-  return h;
-}
-
 int decode_entry(const HostArgs& h) {
   int W = 0;
   int rc = validate(h, &W);
   if (rc != PKV_OK) return rc;
   if (h.S == 0) return ok();
-  rc = dispatch(h, W);
+  rc = dispatch<false>(h, W);
   return rc == PKV_OK ? ok() : rc;
 }
 }  // namespace
@@ -1746,7 +1829,7 @@ int pkv_decode_step(const void* q, const void* k_new, const void* v_new, void* k
                             num_seqs, k_cache, v_cache, num_blocks, num_kv_heads, block_size,
                             head_dim, dtype, stream);
   if (rc != PKV_OK) return rc;
-  rc = dispatch(h, W);
+  rc = dispatch<false>(h, W);
   return rc == PKV_OK ? ok() : rc;
 }
 
@@ -1789,7 +1872,7 @@ int decode_step_q8_entry(int32_t codes, const void* q, const void* k_new, const 
                           num_seqs, k_cache, v_cache, k_scale, v_scale, num_blocks, num_kv_heads,
                           head_dim, dtype, codes, stream);
   if (rc != PKV_OK) return rc;
-  rc = dispatch(h, W);
+  rc = dispatch<false>(h, W);
   return rc == PKV_OK ? ok() : rc;
 }
 }  // namespace
@@ -1938,6 +2021,8 @@ extern "C" int pkv_decode_attention_static_scratch(
   // start at zero; the partial states are always written before they are read.
   PKV_CUDA(cudaMemsetAsync(scratch, 0, workspace_layout(num_q_heads / num_kv_heads, head_dim, W).ml,
                            static_cast<cudaStream_t>(stream)));
-  rc = dispatch(h, W_checked);
+  rc = dispatch<false>(h, W_checked);
   return rc == PKV_OK ? ok() : rc;
 }
+
+#endif  // PKV_DECODE_TEMPLATES_ONLY

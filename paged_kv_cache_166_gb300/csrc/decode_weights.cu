@@ -1,0 +1,242 @@
+// Decode attention that also accumulates attention weights, for eviction by use.
+//
+// Besides out[s, h, :], every cached token's weight, summed over the query heads of its
+// KV group, is added to a running sum:
+//   sums[s, g, p] += sum_{h of group g} softmax_p(scale * q[s, h] . K[slot(p), g]),  p < t.
+// A weight needs the log-sum-exp of its whole context, which the attention's single pass
+// over K and V knows only at its end.  So that pass (decode_attention.cu, kWeights) leaves
+// the fp32 scores behind, 4 bytes per token and query head beside the 4 * head_dim bytes
+// (16-bit caches) of the token's K and V per KV head, and the kernel here turns them into
+// weights: w = 2^(x - lse), x and lse in log2 units.  Reading K a second time instead
+// would cost half of the K and V bytes again; the scores cost 4 G bytes twice, an eighth
+// of them at G = 8 and head_dim 128.
+//
+// The kernel below is bound by memory: scores read once, sums read and written once.
+// Every sum belongs to one thread and its heads are added in order: no atomics, the same
+// bits on every run.
+#define PKV_DECODE_TEMPLATES_ONLY
+#include "decode_attention.cu"
+
+namespace pkv {
+namespace {
+
+constexpr int kSumThreads = 256;
+constexpr int kSumUnroll = 4;  // steps a half-warp has in flight
+
+struct SumArgs {
+  const float* scores;
+  const float* lse;
+  const int32_t* steps;
+  const int32_t* context_lens;
+  float* sums;
+  int32_t* status;
+  int32_t S, Hkv, limit, cols;  // limit: positions a block table holds
+};
+
+// A half-warp handles one step (16 tokens, one a lane) at a time; a warp walks its run of
+// the flat step list two steps at once.
+template <int G>
+__global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const SumArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, half = lane >> 4, tok = lane & 15;
+  const int warps = gridDim.x * (kSumThreads / 32);
+  const int gw = blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
+  const int total = a.steps[a.S];
+  const int per = ((total + warps - 1) / warps + 1) & ~1;
+  const int64_t first = static_cast<int64_t>(gw) * per + half;
+  if (first >= total) return;
+  const int f0 = static_cast<int>(first);
+  const int f1 = min(static_cast<int64_t>(total), static_cast<int64_t>(gw) * per + per);
+  Cursor c = cursor_at(a.steps, a.S, a.Hkv, f0);
+  for (int f = f0; f < f1; f += 2 * kSumUnroll) {
+    float x[kSumUnroll][G], l[kSumUnroll][G], old[kSumUnroll];
+    float* at[kSumUnroll];
+#pragma unroll
+    for (int i = 0; i < kSumUnroll; ++i) {
+      at[i] = nullptr;
+      if (f + 2 * i < f1) {
+        const float* row = a.scores + (static_cast<int64_t>(f + 2 * i) * kTok + tok) * G;
+        const float* lr = a.lse + (static_cast<int64_t>(c.s) * a.Hkv + c.g) * G;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          x[i][h] = row[h];
+          l[i][h] = lr[h];
+        }
+        const int p = c.j * kTok + tok;
+        int n = kTok * c.nb;  // positions below n are all in the context but in its last step
+        if (c.j == c.nb - 1) n = min(a.context_lens[c.s], a.limit);
+        if (n > a.cols && tok == 0 && a.status != nullptr && c.j == c.nb - 1)
+          atomicOr(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+        if (p < n && p < a.cols) {
+          at[i] = a.sums + (static_cast<int64_t>(c.s) * a.Hkv + c.g) * a.cols + p;
+          old[i] = *at[i];
+        }
+        advance(c, a.steps, a.S, a.Hkv);
+        if (c.s < a.S) advance(c, a.steps, a.S, a.Hkv);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSumUnroll; ++i) {
+      if (at[i] != nullptr) {
+        float w = 0.f;
+#pragma unroll
+        for (int h = 0; h < G; ++h) w += exp2f(x[i][h] - l[i][h]);
+        *at[i] = old[i] + w;
+      }
+    }
+  }
+}
+
+struct WeightsLayout {
+  size_t steps, lse, scores, total;
+};
+
+// The decode workspace, then what the weights need.  steps a sequence can have:
+// ceil(max_blocks * block_size / 16) per KV head.
+WeightsLayout weights_layout(int32_t S, int32_t MAXB, int32_t B, int32_t Hq, int32_t Hkv,
+                             int32_t D, int32_t W) {
+  WeightsLayout L;
+  L.steps = round256(workspace_bytes_for(Hq / Hkv, D, W));
+  L.lse = L.steps + round256((static_cast<size_t>(S) + 1) * sizeof(int32_t));
+  L.scores = L.lse + round256(static_cast<size_t>(S) * Hq * sizeof(float));
+  const size_t steps = (static_cast<size_t>(MAXB) * B + kTok - 1) / kTok;
+  L.total = L.scores + static_cast<size_t>(S) * Hq * steps * kTok * sizeof(float);
+  return L;
+}
+
+int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
+  int W = 0;
+  int rc = validate(h, &W);
+  if (rc != PKV_OK) return rc;
+  PKV_REQUIRE(sums_cols > 0, PKV_ERR_INVALID_ARG, "weight_sums must have columns");
+  const WeightsLayout L = weights_layout(h.S, h.MAXB, h.block_size, h.Hq, h.Hkv, h.D, W);
+  PKV_REQUIRE(h.workspace_bytes >= L.total, PKV_ERR_INVALID_ARG,
+              "workspace of %zu bytes < %zu needed", h.workspace_bytes, L.total);
+  if (h.S == 0) return ok();
+  PKV_REQUIRE(weight_sums && aligned(weight_sums, 4), PKV_ERR_INVALID_ARG,
+              "weight_sums is NULL or misaligned");
+  char* ws = static_cast<char*>(h.workspace);
+  h.steps = reinterpret_cast<int32_t*>(ws + L.steps);
+  h.lse = reinterpret_cast<float*>(ws + L.lse);
+  h.scores = reinterpret_cast<float*>(ws + L.scores);
+  rc = dispatch<true>(h, W);
+  if (rc != PKV_OK) return rc;
+  SumArgs a{};
+  a.scores = h.scores;
+  a.lse = h.lse;
+  a.steps = h.steps;
+  a.context_lens = h.context_lens;
+  a.sums = weight_sums;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.S = h.S;
+  a.Hkv = h.Hkv;
+  a.limit = h.MAXB * h.block_size;
+  a.cols = sums_cols;
+  int sms = 0, dev = 0;
+  rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  // no more warps than half the steps a batch this wide can have
+  const int64_t most = (static_cast<int64_t>(h.S) * h.Hkv *
+                            ((static_cast<int64_t>(h.MAXB) * h.block_size + kTok - 1) / kTok) +
+                        2 * kSumThreads / 32 - 1) / (2 * kSumThreads / 32);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most < 8 * sms ? most : 8 * sms));
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = h.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  switch (h.Hq / h.Hkv) {
+    case 1: PKV_CUDA(cudaLaunchKernelEx(&cfg, weight_sums_kernel<1>, a)); break;
+    case 2: PKV_CUDA(cudaLaunchKernelEx(&cfg, weight_sums_kernel<2>, a)); break;
+    case 4: PKV_CUDA(cudaLaunchKernelEx(&cfg, weight_sums_kernel<4>, a)); break;
+    default: PKV_CUDA(cudaLaunchKernelEx(&cfg, weight_sums_kernel<8>, a)); break;
+  }
+  return ok();
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_seq,
+                                      int32_t block_size, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                                      int32_t num_warps, size_t* bytes) {
+  PKV_REQUIRE(bytes != nullptr, PKV_ERR_INVALID_ARG, "bytes is NULL");
+  PKV_REQUIRE(element_bytes(dtype) != 0, PKV_ERR_DTYPE, "unknown dtype %d", dtype);
+  PKV_REQUIRE(num_seqs >= 0 && max_blocks_per_seq > 0 && block_size > 0, PKV_ERR_INVALID_ARG,
+              "sizes must be positive (num_seqs >= 0)");
+  PKV_REQUIRE(num_q_heads > 0 && num_kv_heads > 0 && num_q_heads % num_kv_heads == 0,
+              PKV_ERR_INVALID_ARG, "bad head counts %d / %d", num_q_heads, num_kv_heads);
+  PKV_REQUIRE(supported_head_dim(dtype, head_dim), PKV_ERR_UNSUPPORTED,
+              "head_dim %d unsupported for dtype %d", head_dim, dtype);
+  PKV_REQUIRE(num_warps >= 0, PKV_ERR_INVALID_ARG, "negative num_warps");
+  int W = num_warps;
+  if (W == 0) {
+    W = default_warps(dtype, head_dim);
+    if (W < 0) return W;
+  }
+  *bytes = weights_layout(num_seqs, max_blocks_per_seq, block_size, num_q_heads, num_kv_heads,
+                          head_dim, W).total;
+  return ok();
+}
+
+int pkv_decode_attention_weights(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t block_size, int32_t num_blocks, float scale, void* out,
+                                 float* weight_sums, int32_t sums_cols, void* workspace,
+                                 size_t workspace_bytes, int32_t num_warps, int32_t dtype,
+                                 void* stream) {
+  return weights_entry(host_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                 context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                 block_size, num_blocks, scale, out, workspace, workspace_bytes,
+                                 num_warps, dtype, stream),
+                       weight_sums, sums_cols);
+}
+
+int pkv_decode_attention_weights_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* context_lens, int32_t num_seqs,
+                                     int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                     float scale, void* out, float* weight_sums,
+                                     int32_t sums_cols, void* workspace, size_t workspace_bytes,
+                                     int32_t num_warps, int32_t dtype, void* stream) {
+  HostArgs h = host_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                         num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         scale, out, workspace, workspace_bytes, num_warps, dtype, stream);
+  h.codes = PKV_FP8_E4M3;
+  h.k_scale = k_scale;
+  h.v_scale = v_scale;
+  return weights_entry(h, weight_sums, sums_cols);
+}
+
+int pkv_decode_attention_weights_int8(const void* q, const void* k_cache, const void* v_cache,
+                                      const float* k_scale, const float* v_scale,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                      float scale, void* out, float* weight_sums,
+                                      int32_t sums_cols, void* workspace,
+                                      size_t workspace_bytes, int32_t num_warps, int32_t dtype,
+                                      void* stream) {
+  HostArgs h = host_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                         num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         scale, out, workspace, workspace_bytes, num_warps, dtype, stream);
+  h.codes = PKV_INT8;
+  h.k_scale = k_scale;
+  h.v_scale = v_scale;
+  return weights_entry(h, weight_sums, sums_cols);
+}
+
+}  // extern "C"

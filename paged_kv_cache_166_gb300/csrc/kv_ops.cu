@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "quant8.cuh"
 
 namespace pkv {
 namespace {
@@ -126,12 +127,6 @@ __global__ void decode_append_kernel(const uint4* __restrict__ k, const uint4* _
 }
 
 // ---- 8-bit (fp8 E4M3 or int8) quantising cache write --------------------------------
-// Byte of token t (0..15) inside a 16-byte head_dim row of an 8-bit V tile: the
-// tokens are stored in the order 0 1 8 9 2 3 10 11 4 5 12 13 6 7 14 15.
-__device__ __forceinline__ int fp8_v_pos(int t) {
-  return t < 8 ? 4 * (t >> 1) + (t & 1) : 4 * ((t - 8) >> 1) + 2 + (t & 1);
-}
-
 // The bytes of 16 consecutive input elements (16-byte aligned source), loaded as
 // they are: widened to fp32 by widen16 once they are needed.
 template <typename Tin>
@@ -201,9 +196,7 @@ __device__ __forceinline__ uint4 quantize16_int8(const float (&x)[16], float sca
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const float q = __fdiv_rn(x[j], scale);
-    int c = __float2int_rn(q);           // saturates at the int range for +-inf
-    c = q != q ? 0 : (c < -127 ? -127 : (c > 127 ? 127 : c));
+    const int c = int8_code(x[j], scale);
     w[j >> 2] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (j & 3));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

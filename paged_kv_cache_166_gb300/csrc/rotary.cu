@@ -1,0 +1,452 @@
+// Rotary positions of q and k, with k and v written into the paged cache.
+//
+// A head's first rotary_dim elements form pairs (x1, x2); pair i of a token at
+// position p is turned by the angle p * f_i:
+//   y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin,
+// so the dot product of a turned q and a turned k depends on the distance of their
+// positions.  Half layout: pair i is elements i and i + rotary_dim / 2; interleaved
+// layout: elements 2i and 2i + 1.  Elements from rotary_dim on pass through.  The
+// turned q goes to q_out, the turned k and the v into their slots (the cache write of
+// kv_ops.cu, quantised for 8-bit caches), so k is read once and written once.
+//
+// Arithmetic: fp32 with every product and sum rounded once (no contraction), then one
+// rounding to q's type, or one quantisation straight from fp32 for an 8-bit cache: the
+// results are those of the written formula whatever the compiler does.  cos and sin
+// come from a table of fp32 values computed in 64 bits: an angle p * f_i near 131,072
+// has only 2^-7 left of its fraction in fp32.
+//
+// Bound by memory: q, k, v read once, q_out and the cache rows written once.  A CTA
+// serves one token; a thread keeps its place in the head, so the cos and sin it needs
+// are loaded once and used for every head it turns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "quant8.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kMaxRotaryPairs = 128;  // rotary_dim <= 256
+
+struct RotaryArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const int32_t* positions;
+  const float* table;  // [P, rot]: cos of the rot / 2 angles, then their sin
+  const int32_t* slots;
+  void* kc;
+  void* vc;
+  const float* ks;  // 8-bit caches: per-KV-head scales
+  const float* vs;
+  int32_t* status;  // or NULL
+  int64_t q_stride, k_stride, v_stride, qo_stride;  // elements from token to token
+  int32_t Hq, Hkv, D, rot, B, NB, P;
+};
+
+// N consecutive elements, moved at once.
+template <typename T, int N>
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
+  T x[N];
+};
+
+template <typename T>
+__device__ __forceinline__ float widen(T x) {
+  if constexpr (std::is_same<T, float>::value) return x;
+  else return ptx::to_float(x);
+}
+
+// Codes of N consecutive elements (kCodes 1: E4M3, 2: int8).
+template <int kCodes, int N>
+__device__ __forceinline__ Pack<uint8_t, N> codes_of(const float (&x)[N], float scale) {
+  Pack<uint8_t, N> c;
+#pragma unroll
+  for (int i = 0; i < N; ++i) c.x[i] = kCodes == 1 ? e4m3_code(x[i], scale) : int8_code(x[i], scale);
+  return c;
+}
+
+// One CTA per token (blockIdx.x), its heads split over gridDim.y CTAs.  VEC: elements
+// a thread moves at once (16 bytes where rotary_dim, the strides and the addresses
+// allow it, else the smallest piece that holds whole pairs).
+template <typename T, int VEC, bool kInter, int kCodes>
+__global__ void __launch_bounds__(256) rotary_write_kernel(const RotaryArgs a) {
+  // a decode launch queued behind may start its prologue; it reads the caches and
+  // q_out only after this grid has completed
+  asm volatile("griddepcontrol.launch_dependents;");
+  using P = Pack<T, VEC>;
+  constexpr int kAng = kInter ? VEC / 2 : VEC;  // pairs a thread turns at once
+  const int64_t t = blockIdx.x;
+  const int half = a.rot >> 1;
+  const int nturn = kInter ? a.rot / VEC : half / VEC;      // turning units of a row
+  const int units = nturn + (a.D - a.rot) / VEC;            // and passing ones
+  const int rows = blockDim.x / units;                      // rows in flight in the CTA
+  const int u = threadIdx.x % units, r0 = threadIdx.x / units;
+
+  const int32_t slot = __ldg(a.slots + t);
+  const bool write = slot >= 0 && static_cast<int64_t>(slot) < static_cast<int64_t>(a.NB) * a.B;
+  int32_t pos = __ldg(a.positions + t);
+  if (pos < 0 || pos >= a.P) {
+    if (a.status != nullptr && threadIdx.x == 0 && blockIdx.y == 0)
+      atomicOr(a.status, PKV_DEV_BAD_POSITION);
+    pos = pos < 0 ? 0 : a.P - 1;
+  }
+  const int32_t block = write ? slot / a.B : 0, off = write ? slot - block * a.B : 0;
+
+  if (r0 < rows) {
+    const bool turns = u < nturn;
+    float c[kAng], s[kAng];
+    if (turns) {
+      const float* row = a.table + static_cast<int64_t>(pos) * a.rot + u * kAng;
+      const Pack<float, kAng> pc = *reinterpret_cast<const Pack<float, kAng>*>(row);
+      const Pack<float, kAng> ps = *reinterpret_cast<const Pack<float, kAng>*>(row + half);
+#pragma unroll
+      for (int i = 0; i < kAng; ++i) {
+        c[i] = pc.x[i];
+        s[i] = ps.x[i];
+      }
+    }
+    const int d = turns ? u * VEC : a.rot + (u - nturn) * VEC;  // first element of the unit
+    const T* const q = static_cast<const T*>(a.q) + t * a.q_stride + d;
+    const T* const k = static_cast<const T*>(a.k) + t * a.k_stride + d;
+    T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + d;
+    const int heads = a.Hq + a.Hkv;
+#pragma unroll 4
+    for (int h = r0 + rows * static_cast<int>(blockIdx.y); h < heads;
+         h += rows * static_cast<int>(gridDim.y)) {
+      const bool is_q = h < a.Hq;
+      const int g = h - a.Hq;
+      const T* const src = is_q ? q + static_cast<int64_t>(h) * a.D
+                                : k + static_cast<int64_t>(g) * a.D;
+      const bool pair = turns && !kInter;
+      P x1 = *reinterpret_cast<const P*>(src), x2 = x1;
+      if (pair) x2 = *reinterpret_cast<const P*>(src + half);
+      float y1[VEC], y2[VEC];
+      if (!turns) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) y1[i] = y2[i] = widen(x1.x[i]);
+      } else if constexpr (kInter) {
+#pragma unroll
+        for (int i = 0; i < kAng; ++i) {
+          const float p = widen(x1.x[2 * i]), r = widen(x1.x[2 * i + 1]);
+          y1[2 * i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
+          y1[2 * i + 1] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kAng; ++i) {
+          const float p = widen(x1.x[i]), r = widen(x2.x[i]);
+          y1[i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
+          y2[i] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
+        }
+      }
+      if (kCodes != 0 && !is_q) {
+        if (!write) continue;
+        const int64_t tile = static_cast<int64_t>(block) * a.Hkv + g;
+        uint8_t* const dst = static_cast<uint8_t*>(a.kc) + (tile * 16 + off) * a.D + d;
+        const float scale = __ldg(a.ks + g);
+        *reinterpret_cast<Pack<uint8_t, VEC>*>(dst) = codes_of<kCodes, VEC>(y1, scale);
+        if (pair)
+          *reinterpret_cast<Pack<uint8_t, VEC>*>(dst + half) = codes_of<kCodes, VEC>(y2, scale);
+        continue;
+      }
+      if (!is_q && !write) continue;
+      T* const dst = is_q ? qo + static_cast<int64_t>(h) * a.D
+                          : static_cast<T*>(a.kc) +
+                                ((static_cast<int64_t>(block) * a.Hkv + g) * a.B + off) * a.D + d;
+      P o1, o2;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        // a passing element keeps its bits (a NaN's too)
+        o1.x[i] = turns ? ptx::from_float<T>(y1[i]) : x1.x[i];
+        if (!kInter) o2.x[i] = ptx::from_float<T>(y2[i]);
+      }
+      *reinterpret_cast<P*>(dst) = o1;
+      if (pair) *reinterpret_cast<P*>(dst + half) = o2;
+    }
+  }
+
+  // V rows: copied, or quantised into their transposed tiles.
+  if (!write) return;
+  const int vunits = a.D / VEC;
+  const T* const v = static_cast<const T*>(a.v) + t * a.v_stride;
+#pragma unroll 2
+  for (int i = threadIdx.x + blockDim.x * blockIdx.y; i < a.Hkv * vunits;
+       i += blockDim.x * gridDim.y) {
+    const int g = i / vunits, d = (i - g * vunits) * VEC;
+    const P x = *reinterpret_cast<const P*>(v + static_cast<int64_t>(g) * a.D + d);
+    const int64_t tile = static_cast<int64_t>(block) * a.Hkv + g;
+    if constexpr (kCodes == 0) {
+      *reinterpret_cast<P*>(static_cast<T*>(a.vc) + (tile * a.B + off) * a.D + d) = x;
+    } else {
+      float y[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) y[j] = widen(x.x[j]);
+      const Pack<uint8_t, VEC> c = codes_of<kCodes, VEC>(y, __ldg(a.vs + g));
+      uint8_t* const col = static_cast<uint8_t*>(a.vc) + (tile * a.D + d) * 16 + fp8_v_pos(off);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) col[j * 16] = c.x[j];
+    }
+  }
+}
+
+struct Frequencies {
+  double f[kMaxRotaryPairs];
+};
+
+// table[p, i] = m cos(p f_i), table[p, rot / 2 + i] = m sin(p f_i), angles in 64 bits.
+__global__ void rotary_table_kernel(const __grid_constant__ Frequencies fr, double magnitude,
+                                    int32_t half, int64_t total, float* table) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += stride) {
+    const int64_t p = i / half;
+    const int j = static_cast<int>(i - p * half);
+    double s, c;
+    sincos(static_cast<double>(p) * fr.f[j], &s, &c);
+    table[p * 2 * half + j] = static_cast<float>(c * magnitude);
+    table[p * 2 * half + half + j] = static_cast<float>(s * magnitude);
+  }
+}
+
+template <typename T, int VEC, int kCodes>
+void launch_layout(const RotaryArgs& a, bool interleaved, dim3 grid, int threads,
+                   cudaStream_t st) {
+  if (interleaved) {
+    // a thread's piece holds whole pairs
+    constexpr int V = VEC < 2 ? 2 : VEC;
+    rotary_write_kernel<T, V, true, kCodes><<<grid, threads, 0, st>>>(a);
+  } else {
+    rotary_write_kernel<T, VEC, false, kCodes><<<grid, threads, 0, st>>>(a);
+  }
+}
+
+template <typename T, int kCodes>
+int launch_typed(const RotaryArgs& a, int32_t tokens, bool interleaved, cudaStream_t st) {
+  // 16-byte pieces where every row start, the pairs' halves and the strides allow them
+  constexpr int W = 16 / sizeof(T);
+  const int unit = interleaved ? W : 2 * W;
+  const bool wide = a.rot % unit == 0 && a.D % W == 0 && a.q_stride % W == 0 &&
+                    a.k_stride % W == 0 && a.v_stride % W == 0 && a.qo_stride % W == 0 &&
+                    aligned(a.q, 16) && aligned(a.k, 16) && aligned(a.v, 16) &&
+                    aligned(a.q_out, 16);
+  int sms = 0, dev = 0;
+  const int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  const int vec = wide ? W : (interleaved ? 2 : 1);
+  const int units = (interleaved ? a.rot / vec : a.rot / (2 * vec)) + (a.D - a.rot) / vec;
+  const int threads = units <= 128 ? 128 : 256;  // units < head_dim <= 256
+  const int rows = threads / units;
+  const int heads = a.Hq + a.Hkv;
+  // few tokens: their heads are spread over more CTAs until the SMs have a few each
+  int split = 1;
+  while (split * rows < heads && static_cast<int64_t>(tokens) * split < 4 * sms) split *= 2;
+  const dim3 grid(tokens, split);
+  if (wide) launch_layout<T, W, kCodes>(a, interleaved, grid, threads, st);
+  else launch_layout<T, 1, kCodes>(a, interleaved, grid, threads, st);
+  PKV_CUDA(cudaGetLastError());
+  return PKV_OK;
+}
+
+int rotary_entry(int32_t codes, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                 const void* v, int64_t v_stride, const int32_t* positions, const float* table,
+                 int32_t max_positions, int32_t rotary_dim, int32_t interleaved,
+                 const int32_t* slot_mapping, int32_t num_tokens, void* k_cache, void* v_cache,
+                 const float* k_scale, const float* v_scale, int32_t num_blocks,
+                 int32_t num_q_heads, int32_t num_kv_heads, int32_t block_size, int32_t head_dim,
+                 void* q_out, int64_t q_out_stride, int32_t* status, int32_t dtype,
+                 void* stream) {
+  PKV_REQUIRE(dtype == PKV_F32 || dtype == PKV_F16 || dtype == PKV_BF16, PKV_ERR_DTYPE,
+              "dtype %d is not f32, f16 or bf16", dtype);
+  PKV_REQUIRE(num_tokens >= 0 && num_blocks > 0 && num_q_heads > 0 && num_kv_heads > 0 &&
+                  block_size > 0 && head_dim > 0,
+              PKV_ERR_INVALID_ARG, "sizes must be positive (num_tokens >= 0)");
+  PKV_REQUIRE(rotary_dim > 0 && rotary_dim % 2 == 0 && rotary_dim <= head_dim,
+              PKV_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, head_dim %d]",
+              rotary_dim, head_dim);
+  PKV_REQUIRE(head_dim <= 2 * kMaxRotaryPairs, PKV_ERR_UNSUPPORTED, "head_dim %d above %d",
+              head_dim, 2 * kMaxRotaryPairs);
+  PKV_REQUIRE(max_positions > 0, PKV_ERR_INVALID_ARG, "max_positions must be positive");
+  const int elt = element_bytes(dtype);
+  if (codes != 0) {
+    PKV_REQUIRE(block_size == 16, PKV_ERR_UNSUPPORTED, "8-bit caches use block_size 16, not %d",
+                block_size);
+    PKV_REQUIRE(head_dim % 16 == 0, PKV_ERR_INVALID_ARG, "head_dim must be a multiple of 16");
+  }
+  PKV_REQUIRE((static_cast<int64_t>(head_dim) * elt) % 16 == 0, PKV_ERR_INVALID_ARG,
+              "head_dim * element size must be a multiple of 16 bytes");
+  PKV_REQUIRE(static_cast<int64_t>(num_blocks) * block_size < (int64_t(1) << 31),
+              PKV_ERR_INVALID_ARG, "num_blocks * block_size must be < 2^31");
+  PKV_REQUIRE(q_stride >= static_cast<int64_t>(num_q_heads) * head_dim &&
+                  k_stride >= static_cast<int64_t>(num_kv_heads) * head_dim &&
+                  v_stride >= static_cast<int64_t>(num_kv_heads) * head_dim &&
+                  q_out_stride >= static_cast<int64_t>(num_q_heads) * head_dim,
+              PKV_ERR_INVALID_ARG, "a token stride is smaller than the token's row");
+  if (num_tokens == 0) return ok();
+  PKV_REQUIRE(q && k && v && positions && table && slot_mapping && k_cache && v_cache && q_out &&
+                  (codes == 0 || (k_scale && v_scale)),
+              PKV_ERR_INVALID_ARG, "NULL pointer");
+  PKV_REQUIRE(aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(table, 16),
+              PKV_ERR_INVALID_ARG, "caches and table must be 16-byte aligned");
+  PKV_REQUIRE(aligned(q, elt) && aligned(k, elt) && aligned(v, elt) && aligned(q_out, elt) &&
+                  aligned(positions, 4) && aligned(slot_mapping, 4) && aligned(status, 4) &&
+                  aligned(k_scale, 4) && aligned(v_scale, 4),
+              PKV_ERR_INVALID_ARG, "a pointer is not aligned to its element");
+  // a pair of interleaved elements is moved at once
+  PKV_REQUIRE(!interleaved || (q_stride % 2 == 0 && k_stride % 2 == 0 && v_stride % 2 == 0 &&
+                               q_out_stride % 2 == 0 && aligned(q, 2 * elt) &&
+                               aligned(k, 2 * elt) && aligned(v, 2 * elt) &&
+                               aligned(q_out, 2 * elt)),
+              PKV_ERR_INVALID_ARG, "interleaved pairs must be aligned to their two elements");
+  RotaryArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.positions = positions;
+  a.table = table;
+  a.slots = slot_mapping;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.status = status;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.qo_stride = q_out_stride;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.D = head_dim;
+  a.rot = rotary_dim;
+  a.B = block_size;
+  a.NB = num_blocks;
+  a.P = max_positions;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = PKV_OK;
+#define PKV_ROTARY(C)                                                                          \
+  rc = dtype == PKV_F32   ? launch_typed<float, C>(a, num_tokens, interleaved != 0, st)         \
+       : dtype == PKV_F16 ? launch_typed<__half, C>(a, num_tokens, interleaved != 0, st)        \
+                          : launch_typed<__nv_bfloat16, C>(a, num_tokens, interleaved != 0, st)
+  if (codes == 0) PKV_ROTARY(0);
+  else if (codes == PKV_FP8_E4M3) PKV_ROTARY(1);
+  else PKV_ROTARY(2);
+#undef PKV_ROTARY
+  return rc == PKV_OK ? ok() : rc;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_rotary_frequencies(int32_t rotary_dim, float base, int32_t scaling, float factor,
+                           int32_t original_length, float low_turns, float high_turns,
+                           double* inv_freq) {
+  PKV_REQUIRE(rotary_dim > 0 && rotary_dim % 2 == 0 && rotary_dim <= 2 * kMaxRotaryPairs,
+              PKV_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, %d]", rotary_dim,
+              2 * kMaxRotaryPairs);
+  PKV_REQUIRE(inv_freq != nullptr, PKV_ERR_INVALID_ARG, "inv_freq is NULL");
+  PKV_REQUIRE(std::isfinite(base) && base > 1.f, PKV_ERR_INVALID_ARG, "base must be above 1");
+  PKV_REQUIRE(scaling >= PKV_ROTARY_PLAIN && scaling <= PKV_ROTARY_BANDS, PKV_ERR_INVALID_ARG,
+              "unknown scaling %d", scaling);
+  PKV_REQUIRE(scaling == PKV_ROTARY_PLAIN || (std::isfinite(factor) && factor >= 1.f),
+              PKV_ERR_INVALID_ARG, "factor must be finite and at least 1");
+  PKV_REQUIRE(scaling != PKV_ROTARY_BANDS ||
+                  (original_length > 0 && std::isfinite(low_turns) && std::isfinite(high_turns) &&
+                   low_turns >= 0.f && high_turns > low_turns),
+              PKV_ERR_INVALID_ARG,
+              "bands need original_length > 0 and 0 <= low_turns < high_turns");
+  const double pi = 3.14159265358979323846;
+  double b = base;
+  if (scaling == PKV_ROTARY_NTK && rotary_dim > 2)
+    b *= std::pow(static_cast<double>(factor), rotary_dim / (rotary_dim - 2.0));
+  for (int32_t i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(b, -2.0 * i / rotary_dim);
+    if (scaling == PKV_ROTARY_LINEAR) f /= factor;
+    if (scaling == PKV_ROTARY_BANDS) {
+      const double turns = original_length * f / (2.0 * pi);
+      double t = (turns - low_turns) / (static_cast<double>(high_turns) - low_turns);
+      t = t < 0.0 ? 0.0 : (t > 1.0 ? 1.0 : t);
+      f *= (1.0 - t) / factor + t;
+    }
+    inv_freq[i] = f;
+  }
+  return ok();
+}
+
+int pkv_rotary_table(const double* inv_freq, int32_t rotary_dim, float magnitude,
+                     int32_t max_positions, float* table, void* stream) {
+  PKV_REQUIRE(rotary_dim > 0 && rotary_dim % 2 == 0 && rotary_dim <= 2 * kMaxRotaryPairs,
+              PKV_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, %d]", rotary_dim,
+              2 * kMaxRotaryPairs);
+  PKV_REQUIRE(max_positions > 0, PKV_ERR_INVALID_ARG, "max_positions must be positive");
+  PKV_REQUIRE(inv_freq && table, PKV_ERR_INVALID_ARG, "NULL pointer");
+  PKV_REQUIRE(aligned(table, 16), PKV_ERR_INVALID_ARG, "table must be 16-byte aligned");
+  Frequencies fr{};
+  const int32_t half = rotary_dim / 2;
+  for (int32_t i = 0; i < half; ++i) fr.f[i] = inv_freq[i];
+  const int64_t total = static_cast<int64_t>(max_positions) * half;
+  int sms = 0, dev = 0;
+  const int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  const int64_t want = (total + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
+  rotary_table_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0,
+                        static_cast<cudaStream_t>(stream)>>>(
+      fr, static_cast<double>(magnitude), half, total, table);
+  PKV_CUDA(cudaGetLastError());
+  return ok();
+}
+
+int pkv_rotary_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                     const void* v, int64_t v_stride, const int32_t* positions,
+                     const float* table, int32_t max_positions, int32_t rotary_dim,
+                     int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                     void* k_cache, void* v_cache, int32_t num_blocks, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+                     int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream) {
+  return rotary_entry(0, q, q_stride, k, k_stride, v, v_stride, positions, table, max_positions,
+                      rotary_dim, interleaved, slot_mapping, num_tokens, k_cache, v_cache,
+                      nullptr, nullptr, num_blocks, num_q_heads, num_kv_heads, block_size,
+                      head_dim, q_out, q_out_stride, status, dtype, stream);
+}
+
+int pkv_rotary_write_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const int32_t* positions,
+                         const float* table, int32_t max_positions, int32_t rotary_dim,
+                         int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                         void* k_cache, void* v_cache, const float* k_scale,
+                         const float* v_scale, int32_t num_blocks, int32_t num_q_heads,
+                         int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+                         int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream) {
+  return rotary_entry(PKV_FP8_E4M3, q, q_stride, k, k_stride, v, v_stride, positions, table,
+                      max_positions, rotary_dim, interleaved, slot_mapping, num_tokens, k_cache,
+                      v_cache, k_scale, v_scale, num_blocks, num_q_heads, num_kv_heads,
+                      block_size, head_dim, q_out, q_out_stride, status, dtype, stream);
+}
+
+int pkv_rotary_write_int8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* positions,
+                          const float* table, int32_t max_positions, int32_t rotary_dim,
+                          int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens,
+                          void* k_cache, void* v_cache, const float* k_scale,
+                          const float* v_scale, int32_t num_blocks, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t block_size, int32_t head_dim,
+                          void* q_out, int64_t q_out_stride, int32_t* status, int32_t dtype,
+                          void* stream) {
+  return rotary_entry(PKV_INT8, q, q_stride, k, k_stride, v, v_stride, positions, table,
+                      max_positions, rotary_dim, interleaved, slot_mapping, num_tokens, k_cache,
+                      v_cache, k_scale, v_scale, num_blocks, num_q_heads, num_kv_heads,
+                      block_size, head_dim, q_out, q_out_stride, status, dtype, stream);
+}
+
+}  // extern "C"

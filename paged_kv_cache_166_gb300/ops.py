@@ -6,6 +6,7 @@ work happens in the library's kernels; nothing here computes attention.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -507,3 +508,348 @@ def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor,
     N.check(N.lib().pkv_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(),
                                     src_dst_pairs.data_ptr(), n, NB, block_elems, code,
                                     _stream(dev)))
+
+
+# ---------------------------------------------------------------------------------
+# Operators of a decode loop around the attention: rotary positions, eviction, beams
+# ---------------------------------------------------------------------------------
+def _current(dev: torch.device):
+    """A context in which ``dev`` is the current device (the library launches there)."""
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _check_status(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
+    if status is None:
+        return None
+    if status.device != dev or status.dtype != torch.int32 or status.numel() < 1:
+        raise ValueError("status must be a device int32 tensor")
+    return status.data_ptr()
+
+
+def _scratch(dev: torch.device, nbytes: int, zeroed: int, key: tuple) -> torch.Tensor:
+    """Workspace of ``nbytes`` whose first ``zeroed`` bytes start at zero: cached per device
+    and stream, or, while a graph is captured, the graph's own (two graphs, or a graph and
+    eager calls, never share one)."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        if zeroed:
+            ws[:zeroed].zero_()
+        return ws
+    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream) + key
+    ws = _WORKSPACES.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        if zeroed:
+            ws[:zeroed].zero_()
+        _WORKSPACES[key] = ws
+    return ws
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, original_length: int = 0, low_turns: float = 1.0,
+                       high_turns: float = 4.0) -> torch.Tensor:
+    """Angle per position of each pair of elements, float64 [rotary_dim / 2] on the host.
+    ``scaling``: "none", "linear", "ntk" or "bands" (the last by the turns of a pair within
+    ``original_length``, between ``low_turns`` and ``high_turns``)."""
+    if scaling not in N.ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(N.ROTARY_SCALINGS)}")
+    out = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
+    N.check(N.lib().pkv_rotary_frequencies(rotary_dim, base, N.ROTARY_SCALINGS[scaling], factor,
+                                           original_length, low_turns, high_turns,
+                                           out.data_ptr()))
+    return out
+
+
+def rotary_table(max_positions: int, inv_freq: torch.Tensor, magnitude: float = 1.0,
+                 device=None) -> torch.Tensor:
+    """cos and sin of positions 0 .. max_positions - 1 for ``rotary_frequencies``' angles:
+    float32 [max_positions, rotary_dim] on ``device``, a row's first half cos, the rest sin."""
+    if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 \
+            or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 [rotary_dim / 2] host tensor")
+    if max_positions <= 0:
+        raise ValueError("max_positions must be positive")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    rot = 2 * inv_freq.numel()
+    table = torch.empty((max_positions, rot), dtype=torch.float32, device=dev)
+    with _current(table.device):
+        N.check(N.lib().pkv_rotary_table(inv_freq.data_ptr(), rot, magnitude, max_positions,
+                                         table.data_ptr(), _stream(table.device)))
+    return table
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from token to token of [T, H, D] whose heads are contiguous."""
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}'s heads must be contiguous [H, D] for every token")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _rotary_write(kind, q, k, v, positions, table, slot_mapping, k_cache, v_cache, k_scale,
+                  v_scale, q_out, interleaved, status):
+    kc, vc = _q8_caches(k_cache, v_cache, kind) if kind else (k_cache, v_cache)
+    dev = _check_cuda(positions, table, slot_mapping, kc, vc, *((k_scale, v_scale) if kind else ()))
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
+        if t.device != dev:
+            raise ValueError(f"{name} must be on the caches' device")
+        if t.dim() != 3:
+            raise ValueError("expected q, q_out [T, Hq, D] and k, v [T, Hkv, D]")
+    _check_index(positions, "positions")
+    _check_index(slot_mapping, "slot_mapping")
+    T, Hq, D = q.shape
+    if kc.dim() != 4 or vc.dim() != 4:
+        raise ValueError("caches must be [NB, Hkv, B, D]")
+    NB, Hkv, B, D2 = kc.shape
+    if D2 != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or q_out.shape != q.shape \
+            or vc.shape != ((NB, Hkv, D, B) if kind else (NB, Hkv, B, D)):
+        raise ValueError("shape mismatch between q, k, v, q_out and caches")
+    if positions.shape != (T,) or slot_mapping.shape != (T,):
+        raise ValueError("positions and slot_mapping must be [T]")
+    if table.dim() != 2 or table.dtype != torch.float32:
+        raise ValueError("table must be float32 [max_positions, rotary_dim]")
+    if not (q.dtype == k.dtype == v.dtype == q_out.dtype) or (not kind and not (
+            kc.dtype == vc.dtype == q.dtype)):
+        raise TypeError("q, k, v, q_out" + ("" if kind else " and caches") + " must share a dtype")
+    if kind:
+        _check_scales(k_scale, v_scale, Hkv)
+    st = _check_status(status, dev)
+    L = N.lib()
+    fn = {"": L.pkv_rotary_write, "fp8": L.pkv_rotary_write_fp8,
+          "int8": L.pkv_rotary_write_int8}[kind]
+    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else ()
+    with _current(dev):
+        N.check(fn(q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
+                   v.data_ptr(), _token_stride(v, "v"), positions.data_ptr(), table.data_ptr(),
+                   table.shape[0], table.shape[1], 1 if interleaved else 0,
+                   slot_mapping.data_ptr(), T, kc.data_ptr(), vc.data_ptr(), *scales, NB, Hq, Hkv,
+                   B, D, q_out.data_ptr(), _token_stride(q_out, "q_out"), st, dtype_code(q),
+                   _stream(dev)))
+    return q_out
+
+
+def paged_rotary_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor, table: torch.Tensor, slot_mapping: torch.Tensor,
+                       k_cache: torch.Tensor, v_cache: torch.Tensor, q_out: torch.Tensor,
+                       interleaved: bool = False,
+                       status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Turn q [T, Hq, D] and k [T, Hkv, D] to positions [T] (``rotary_table``; its width is
+    the part of the head that turns), write the turned k and v at slot_mapping [T] of the
+    caches; writes and returns q_out.  q, k and v may be slices of one projection (any
+    stride from token to token), and q_out may be q."""
+    return _rotary_write("", q, k, v, positions, table, slot_mapping, k_cache, v_cache, None,
+                         None, q_out, interleaved, status)
+
+
+def paged_rotary_write_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                           positions: torch.Tensor, table: torch.Tensor,
+                           slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           q_out: torch.Tensor, interleaved: bool = False,
+                           status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_rotary_write into fp8 caches: the turned k and v quantised as
+    paged_kv_write_fp8 does."""
+    return _rotary_write("fp8", q, k, v, positions, table, slot_mapping, k_cache, v_cache,
+                         k_scale, v_scale, q_out, interleaved, status)
+
+
+def paged_rotary_write_int8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            positions: torch.Tensor, table: torch.Tensor,
+                            slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                            q_out: torch.Tensor, interleaved: bool = False,
+                            status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_rotary_write into int8 caches: the turned k and v quantised as
+    paged_kv_write_int8 does."""
+    return _rotary_write("int8", q, k, v, positions, table, slot_mapping, k_cache, v_cache,
+                         k_scale, v_scale, q_out, interleaved, status)
+
+
+def weights_workspace_bytes(num_seqs: int, max_blocks: int, block_size: int, num_q_heads: int,
+                            num_kv_heads: int, head_dim: int, dtype, num_warps: int = 0) -> int:
+    """Workspace bytes of ``paged_decode_attention_weights``; ``dtype`` as in
+    ``workspace_bytes``."""
+    code = _CODES[dtype] if isinstance(dtype, str) else _DTYPES[dtype]
+    n = ctypes.c_size_t(0)
+    N.check(N.lib().pkv_decode_weights_workspace_size(num_seqs, max_blocks, block_size,
+                                                      num_q_heads, num_kv_heads, head_dim, code,
+                                                      num_warps, ctypes.byref(n)))
+    return n.value
+
+
+def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                    scale, out, weight_sums, workspace, num_warps):
+    if kind:
+        kc, vc = _q8_caches(k_cache, v_cache, kind)
+        dev = _check_cuda(q, kc, vc, k_scale, v_scale, block_tables, context_lens, out, weight_sums)
+        S, Hq, D, NB, Hkv, B, MAXB = _q8_shapes(q, kc, vc, block_tables, context_lens, out)
+        _check_scales(k_scale, v_scale, Hkv)
+    else:
+        kc, vc = k_cache, v_cache
+        dev = _check_cuda(q, kc, vc, block_tables, context_lens, out, weight_sums)
+        S, Hq, D, NB, Hkv, B, MAXB = _decode_shapes(q, kc, vc, block_tables, context_lens, out)
+    if weight_sums.dtype != torch.float32 or weight_sums.dim() != 3 \
+            or weight_sums.shape[:2] != (S, Hkv):
+        raise ValueError(f"weight_sums must be float32 [{S}, {Hkv}, columns]")
+    code = dtype_code(q)
+    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else ()
+    L = N.lib()
+    fn = {"": L.pkv_decode_attention_weights, "fp8": L.pkv_decode_attention_weights_fp8,
+          "int8": L.pkv_decode_attention_weights_int8}[kind]
+    with _current(dev):
+        need = weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, kind or q.dtype, num_warps)
+        if workspace is None:
+            head = workspace_bytes(Hq, Hkv, D, kind or q.dtype, num_warps)
+            ws = _scratch(dev, need, head, (Hq // Hkv, D, num_warps, "weights" + kind))
+        else:
+            ws = workspace
+            if ws.device != dev or ws.numel() * ws.element_size() < need:
+                raise ValueError(f"workspace smaller than the {need} bytes needed")
+        N.check(fn(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), *scales, block_tables.data_ptr(),
+                   MAXB, context_lens.data_ptr(), S, Hq, Hkv, D, B, NB, float(scale),
+                   out.data_ptr(), weight_sums.data_ptr(), weight_sums.shape[2], ws.data_ptr(),
+                   ws.numel() * ws.element_size(), num_warps, code, _stream(dev)))
+    return out
+
+
+def paged_decode_attention_weights(q: torch.Tensor, k_cache: torch.Tensor,
+                                   v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                   context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                                   weight_sums: torch.Tensor,
+                                   workspace: Optional[torch.Tensor] = None,
+                                   num_warps: int = 0) -> torch.Tensor:
+    """paged_decode_attention that also adds each cached position's attention weight, summed
+    over the query heads of its KV group, to weight_sums [S, Hkv, columns] (float32, in
+    place); writes and returns out, the same bits as paged_decode_attention's."""
+    return _decode_weights("", q, k_cache, v_cache, None, None, block_tables, context_lens,
+                           scale, out, weight_sums, workspace, num_warps)
+
+
+def paged_decode_attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor,
+                                       v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                       v_scale: torch.Tensor, block_tables: torch.Tensor,
+                                       context_lens: torch.Tensor, scale: float,
+                                       out: torch.Tensor, weight_sums: torch.Tensor,
+                                       workspace: Optional[torch.Tensor] = None,
+                                       num_warps: int = 0) -> torch.Tensor:
+    """paged_decode_attention_weights over fp8 caches."""
+    return _decode_weights("fp8", q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                           context_lens, scale, out, weight_sums, workspace, num_warps)
+
+
+def paged_decode_attention_weights_int8(q: torch.Tensor, k_cache: torch.Tensor,
+                                        v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                        v_scale: torch.Tensor, block_tables: torch.Tensor,
+                                        context_lens: torch.Tensor, scale: float,
+                                        out: torch.Tensor, weight_sums: torch.Tensor,
+                                        workspace: Optional[torch.Tensor] = None,
+                                        num_warps: int = 0) -> torch.Tensor:
+    """paged_decode_attention_weights over int8 caches."""
+    return _decode_weights("int8", q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                           context_lens, scale, out, weight_sums, workspace, num_warps)
+
+
+def paged_evict_select(weight_sums: torch.Tensor, context_lens: torch.Tensor,
+                       keep_lens: torch.Tensor, kept: torch.Tensor, new_sums: torch.Tensor,
+                       new_lens: torch.Tensor, first: int = 0, recent: int = 0,
+                       status: Optional[torch.Tensor] = None) -> None:
+    """Which tokens stay: for every sequence and KV head the first ``first``, the last
+    ``recent`` and those with the largest weight_sums [S, Hkv, columns] between, n =
+    min(keep_lens, context_lens) in all.  Their ascending positions go to kept
+    [S, Hkv, kept columns] (int32), their sums to new_sums [S, Hkv, new columns], n to
+    new_lens [S]."""
+    dev = _check_cuda(weight_sums, context_lens, keep_lens, kept, new_sums, new_lens)
+    if weight_sums.dim() != 3 or kept.dim() != 3 or new_sums.dim() != 3 \
+            or weight_sums.shape[:2] != kept.shape[:2] or weight_sums.shape[:2] != new_sums.shape[:2]:
+        raise ValueError("expected weight_sums, kept and new_sums [S, Hkv, columns]")
+    if weight_sums.dtype != torch.float32 or new_sums.dtype != torch.float32:
+        raise TypeError("weight_sums and new_sums must be float32")
+    S, Hkv = weight_sums.shape[:2]
+    for t, name in ((context_lens, "context_lens"), (keep_lens, "keep_lens"),
+                    (new_lens, "new_lens")):
+        _check_index(t, name)
+        if t.shape != (S,):
+            raise ValueError(f"{name} must be [{S}]")
+    _check_index(kept, "kept")
+    st = _check_status(status, dev)
+    with _current(dev):
+        N.check(N.lib().pkv_evict_select(
+            weight_sums.data_ptr(), weight_sums.shape[2], context_lens.data_ptr(),
+            keep_lens.data_ptr(), S, Hkv, first, recent, kept.data_ptr(), kept.shape[2],
+            new_sums.data_ptr(), new_sums.shape[2], new_lens.data_ptr(), st, _stream(dev)))
+
+
+def paged_evict_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                       kept: torch.Tensor, new_lens: torch.Tensor, new_tables: torch.Tensor,
+                       status: Optional[torch.Tensor] = None) -> None:
+    """Move the kept tokens' rows (``paged_evict_select``) from block_tables' blocks to
+    positions 0 .. new_lens - 1 of new_tables [S, new blocks], in one layer's caches (16-
+    and 32-bit, fp8 or int8).  The new blocks belong to one sequence alone
+    (``BlockAllocator.evict``)."""
+    kc, vc = k_cache, v_cache
+    code = _copy_code(kc)
+    dev = _check_cuda(kc, vc, block_tables, kept, new_lens, new_tables)
+    if kc.dim() != 4 or vc.dim() != 4 or kc.dtype != vc.dtype:
+        raise ValueError("caches must be 4-dimensional and share a dtype")
+    NB, Hkv, B, D = kc.shape
+    if vc.shape != ((NB, Hkv, D, B) if code in _CODES.values() else kc.shape):
+        raise ValueError("v_cache must be [NB, Hkv, B, D] ([NB, Hkv, D, 16] if 8-bit)")
+    for t, name in ((block_tables, "block_tables"), (kept, "kept"), (new_lens, "new_lens"),
+                    (new_tables, "new_tables")):
+        _check_index(t, name)
+    S = new_lens.shape[0] if new_lens.dim() == 1 else -1
+    if block_tables.dim() != 2 or new_tables.dim() != 2 or kept.dim() != 3 \
+            or block_tables.shape[0] != S or new_tables.shape[0] != S or kept.shape[:2] != (S, Hkv):
+        raise ValueError("block_tables, new_tables [S, blocks], kept [S, Hkv, columns], new_lens [S]")
+    st = _check_status(status, dev)
+    with _current(dev):
+        N.check(N.lib().pkv_evict_gather(
+            kc.data_ptr(), vc.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            kept.data_ptr(), kept.shape[2], new_lens.data_ptr(), new_tables.data_ptr(),
+            new_tables.shape[1], S, NB, Hkv, B, D, st, code, _stream(dev)))
+
+
+def beam_workspace_bytes(num_seqs: int, num_beams: int, vocab: int, num_out: int, dtype) -> int:
+    """Workspace bytes of ``beam_select``."""
+    n = ctypes.c_size_t(0)
+    N.check(N.lib().pkv_beam_workspace_size(num_seqs, num_beams, vocab, num_out, _DTYPES[dtype],
+                                            ctypes.byref(n)))
+    return n.value
+
+
+def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.Tensor,
+                beams: torch.Tensor, tokens: torch.Tensor,
+                workspace: Optional[torch.Tensor] = None) -> None:
+    """The best continuations of every request's beams: of logits [S, K, V] (V contiguous,
+    any other strides) and beam_scores [S, K] (float32) the N best candidates by
+    beam_scores + log_softmax(logits), in order, into scores (float32), beams and tokens
+    (int32), all [S, N]."""
+    dev = _check_cuda(beam_scores, scores, beams, tokens)
+    if logits.device != dev:
+        raise ValueError("logits must be on the device of beam_scores")
+    if logits.dim() != 3 or beam_scores.shape != logits.shape[:2]:
+        raise ValueError("expected logits [S, K, V] and beam_scores [S, K]")
+    S, K, V = logits.shape
+    if scores.dim() != 2 or scores.shape[0] != S or beams.shape != scores.shape \
+            or tokens.shape != scores.shape:
+        raise ValueError("scores, beams and tokens must be [S, N]")
+    if V > 1 and logits.stride(2) != 1:
+        raise ValueError("logits' vocabulary must be contiguous")
+    if beam_scores.dtype != torch.float32 or scores.dtype != torch.float32:
+        raise TypeError("beam_scores and scores must be float32")
+    if scores.data_ptr() == beam_scores.data_ptr() and S > 0:
+        raise ValueError("scores must not be beam_scores")
+    _check_index(beams, "beams")
+    _check_index(tokens, "tokens")
+    code, n = dtype_code(logits), scores.shape[1]
+    with _current(dev):
+        need = beam_workspace_bytes(S, K, V, n, logits.dtype)
+        ws = _scratch(dev, need, 0, ("beam",)) if workspace is None else workspace
+        if ws.device != dev or ws.numel() * ws.element_size() < need:
+            raise ValueError(f"workspace smaller than the {need} bytes needed")
+        N.check(N.lib().pkv_beam_select(
+            logits.data_ptr(), logits.stride(0) if S > 1 else 0, logits.stride(1) if K > 1 else 0,
+            beam_scores.data_ptr(), S, K, V, n, scores.data_ptr(), beams.data_ptr(),
+            tokens.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), code, _stream(dev)))
