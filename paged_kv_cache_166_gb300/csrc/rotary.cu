@@ -49,7 +49,8 @@ struct RotaryArgs {
   const float* vs;
   int32_t* status;  // or NULL
   int64_t q_stride, k_stride, v_stride, qo_stride;  // elements from token to token
-  int32_t Hq, Hkv, D, rot, B, NB, P;
+  int32_t T, Hq, Hkv, D, rot, B, NB, P;
+  int32_t v_parts;  // 8-bit caches: CTAs of one window of V
 };
 
 // N consecutive elements, moved at once.
@@ -73,9 +74,154 @@ __device__ __forceinline__ Pack<uint8_t, N> codes_of(const float (&x)[N], float 
   return c;
 }
 
-// One CTA per token (blockIdx.x), its heads split over gridDim.y CTAs.  VEC: elements
-// a thread moves at once (16 bytes where rotary_dim, the strides and the addresses
-// allow it, else the smallest piece that holds whole pairs).
+// Turns U heads' pieces at once (loads first), heads h = h0, h0 + step, ... < H of src
+// [H, D]; put(h, first, y1, y2, x1): the turned pieces, x1 the unturned first one.
+template <typename T, int VEC, bool kInter, typename Put>
+__device__ __forceinline__ void turn_heads(const T* src, int H, int D, int h0, int step, int half,
+                                           bool turns,
+                                           const float (&c)[kInter ? VEC / 2 : VEC],
+                                           const float (&s)[kInter ? VEC / 2 : VEC], Put put) {
+  using P = Pack<T, VEC>;
+  constexpr int U = 4;
+  for (int h = h0; h < H; h += U * step) {
+    P x1[U], x2[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u * step < H) {
+        const T* const at = src + static_cast<int64_t>(h + u * step) * D;
+        x1[u] = *reinterpret_cast<const P*>(at);
+        if (!kInter && turns) x2[u] = *reinterpret_cast<const P*>(at + half);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u * step < H) {
+        float y1[VEC], y2[VEC];
+        if (!turns) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) y1[i] = y2[i] = widen(x1[u].x[i]);
+        } else if constexpr (kInter) {
+#pragma unroll
+          for (int i = 0; i < VEC / 2; ++i) {
+            const float p = widen(x1[u].x[2 * i]), r = widen(x1[u].x[2 * i + 1]);
+            y1[2 * i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
+            y1[2 * i + 1] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float p = widen(x1[u].x[i]), r = widen(x2[u].x[i]);
+            y1[i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
+            y2[i] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
+          }
+        }
+        put(h + u * step, y1, y2, x1[u]);
+      }
+    }
+  }
+}
+
+// V of 8-bit caches: a token is one byte of each 16-byte row of its transposed tile.  A
+// run of consecutive tokens in consecutive slots of one block is written as a whole, a
+// thread two rows: 32 contiguous bytes if the run fills the block (a prompt's usual case),
+// else byte pairs and bytes.  The CTAs of window w own the runs that begin in tokens
+// 16 w .. 16 w + 15, and take their work items (run, head, two rows) in turn.
+template <typename T, bool kPairs, int kCodes>
+__device__ __forceinline__ void write_v8(const RotaryArgs& a, int window, int part, int parts) {
+  __shared__ int slot_s[48];  // tokens 16 (w - 1) .. 16 (w + 2) - 1; -1: nothing to write
+  __shared__ int run_first[16], run_len[16], run_count;
+  const int tid = threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(window) * 16 - 16;
+  if (tid < 48) {
+    int slot = -1;
+    if (t0 + tid >= 0 && t0 + tid < a.T) slot = __ldg(a.slots + t0 + tid);
+    if (slot < 0 || slot >= a.NB * 16) slot = -1;
+    slot_s[tid] = slot;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    // token i goes on its predecessor's run
+    auto goes_on = [&](int i) {
+      return slot_s[i] > 0 && slot_s[i] % 16 != 0 && slot_s[i - 1] == slot_s[i] - 1;
+    };
+    const int i = 16 + tid;
+    const bool begins = tid < 16 && slot_s[i] >= 0 && !goes_on(i);
+    const uint32_t all = __ballot_sync(0xffffffffu, begins);
+    if (begins) {
+      int n = 1;
+      while (i + n < 48 && goes_on(i + n)) ++n;  // at most 16: a run ends with its block
+      const int at = __popc(all & ((1u << tid) - 1));
+      run_first[at] = i;
+      run_len[at] = n;
+    }
+    if (tid == 0) run_count = __popc(all);
+  }
+  __syncthreads();
+  const int pairs = a.D / 2, per_run = a.Hkv * pairs;
+  const int items = run_count * per_run;
+  for (int it = part * blockDim.x + tid; it < items; it += parts * blockDim.x) {
+    const int run = it / per_run, g = (it - run * per_run) / pairs;
+    const int d = 2 * (it - run * per_run - g * pairs);
+    const int first = run_first[run], n = run_len[run], slot = slot_s[first];
+    const int off = slot % 16;
+    const float scale = __ldg(a.vs + g);
+    const T* const src = static_cast<const T*>(a.v) + (t0 + first - off) * a.v_stride +
+                         static_cast<int64_t>(g) * a.D + d;  // row of the block's token 0
+    T lo[16], hi[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      lo[t] = hi[t] = ptx::from_float<T>(0.f);
+      if (t >= off && t < off + n) {
+        const T* const at = src + t * a.v_stride;
+        if constexpr (kPairs) {
+          const Pack<T, 2> x = *reinterpret_cast<const Pack<T, 2>*>(at);
+          lo[t] = x.x[0];
+          hi[t] = x.x[1];
+        } else {
+          lo[t] = at[0];
+          hi[t] = at[1];
+        }
+      }
+    }
+    uint8_t* const dst = static_cast<uint8_t*>(a.vc) +
+                         ((static_cast<int64_t>(slot / 16) * a.Hkv + g) * a.D + d) * 16;
+    Pack<uint8_t, 16> w0, w1;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const float x[2] = {widen(lo[t]), widen(hi[t])};
+      const Pack<uint8_t, 2> c = codes_of<kCodes, 2>(x, scale);
+      w0.x[fp8_v_pos(t)] = c.x[0];
+      w1.x[fp8_v_pos(t)] = c.x[1];
+    }
+    if (n == 16) {
+      reinterpret_cast<Pack<uint8_t, 16>*>(dst)[0] = w0;
+      reinterpret_cast<Pack<uint8_t, 16>*>(dst)[1] = w1;
+    } else {
+      // tokens 2i and 2i + 1 lie side by side
+#pragma unroll
+      for (int t = 0; t < 16; t += 2) {
+        const bool x = t >= off && t < off + n, y = t + 1 >= off && t + 1 < off + n;
+        const int at = fp8_v_pos(t);
+        if (x && y) {
+          *reinterpret_cast<Pack<uint8_t, 2>*>(dst + at) = Pack<uint8_t, 2>{{w0.x[at], w0.x[at + 1]}};
+          *reinterpret_cast<Pack<uint8_t, 2>*>(dst + 16 + at) =
+              Pack<uint8_t, 2>{{w1.x[at], w1.x[at + 1]}};
+        } else if (x) {
+          dst[at] = w0.x[at];
+          dst[16 + at] = w1.x[at];
+        } else if (y) {
+          dst[at + 1] = w0.x[at + 1];
+          dst[17 + at] = w1.x[at + 1];
+        }
+      }
+    }
+  }
+}
+
+// One CTA per token (blockIdx.x < T), its heads split over gridDim.y CTAs; 8-bit caches:
+// then those of V's windows, a.v_parts each.  VEC: elements a thread moves at once (16
+// bytes where rotary_dim, the strides and the addresses allow it, else the smallest piece
+// that holds whole pairs).
 template <typename T, int VEC, bool kInter, int kCodes>
 __global__ void __launch_bounds__(256) rotary_write_kernel(const RotaryArgs a) {
   // a decode launch queued behind may start its prologue; it reads the caches and
@@ -84,6 +230,16 @@ __global__ void __launch_bounds__(256) rotary_write_kernel(const RotaryArgs a) {
   using P = Pack<T, VEC>;
   constexpr int kAng = kInter ? VEC / 2 : VEC;  // pairs a thread turns at once
   const int64_t t = blockIdx.x;
+  if constexpr (kCodes != 0) {
+    if (t >= a.T) {
+      const int64_t i = (t - a.T) * gridDim.y + blockIdx.y;
+      const int64_t window = i / a.v_parts;
+      if (window * 16 < a.T)
+        write_v8<T, VEC != 1, kCodes>(a, static_cast<int>(window),
+                                      static_cast<int>(i - window * a.v_parts), a.v_parts);
+      return;
+    }
+  }
   const int half = a.rot >> 1;
   const int nturn = kInter ? a.rot / VEC : half / VEC;      // turning units of a row
   const int units = nturn + (a.D - a.rot) / VEC;            // and passing ones
@@ -114,85 +270,65 @@ __global__ void __launch_bounds__(256) rotary_write_kernel(const RotaryArgs a) {
       }
     }
     const int d = turns ? u * VEC : a.rot + (u - nturn) * VEC;  // first element of the unit
-    const T* const q = static_cast<const T*>(a.q) + t * a.q_stride + d;
-    const T* const k = static_cast<const T*>(a.k) + t * a.k_stride + d;
-    T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + d;
-    const int heads = a.Hq + a.Hkv;
-#pragma unroll 4
-    for (int h = r0 + rows * static_cast<int>(blockIdx.y); h < heads;
-         h += rows * static_cast<int>(gridDim.y)) {
-      const bool is_q = h < a.Hq;
-      const int g = h - a.Hq;
-      const T* const src = is_q ? q + static_cast<int64_t>(h) * a.D
-                                : k + static_cast<int64_t>(g) * a.D;
-      const bool pair = turns && !kInter;
-      P x1 = *reinterpret_cast<const P*>(src), x2 = x1;
-      if (pair) x2 = *reinterpret_cast<const P*>(src + half);
-      float y1[VEC], y2[VEC];
-      if (!turns) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y1[i] = y2[i] = widen(x1.x[i]);
-      } else if constexpr (kInter) {
-#pragma unroll
-        for (int i = 0; i < kAng; ++i) {
-          const float p = widen(x1.x[2 * i]), r = widen(x1.x[2 * i + 1]);
-          y1[2 * i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
-          y1[2 * i + 1] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kAng; ++i) {
-          const float p = widen(x1.x[i]), r = widen(x2.x[i]);
-          y1[i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
-          y2[i] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
-        }
-      }
-      if (kCodes != 0 && !is_q) {
-        if (!write) continue;
-        const int64_t tile = static_cast<int64_t>(block) * a.Hkv + g;
-        uint8_t* const dst = static_cast<uint8_t*>(a.kc) + (tile * 16 + off) * a.D + d;
-        const float scale = __ldg(a.ks + g);
-        *reinterpret_cast<Pack<uint8_t, VEC>*>(dst) = codes_of<kCodes, VEC>(y1, scale);
-        if (pair)
-          *reinterpret_cast<Pack<uint8_t, VEC>*>(dst + half) = codes_of<kCodes, VEC>(y2, scale);
-        continue;
-      }
-      if (!is_q && !write) continue;
-      T* const dst = is_q ? qo + static_cast<int64_t>(h) * a.D
-                          : static_cast<T*>(a.kc) +
-                                ((static_cast<int64_t>(block) * a.Hkv + g) * a.B + off) * a.D + d;
+    const bool pair = turns && !kInter;
+    const int h0 = r0 + rows * static_cast<int>(blockIdx.y);
+    const int step = rows * static_cast<int>(gridDim.y);
+    // a turned piece, rounded to the type; a passing one keeps its bits (a NaN's too)
+    auto store = [&](T* dst, const float (&y1)[VEC], const float (&y2)[VEC], const P& x) {
       P o1, o2;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        // a passing element keeps its bits (a NaN's too)
-        o1.x[i] = turns ? ptx::from_float<T>(y1[i]) : x1.x[i];
+        o1.x[i] = turns ? ptx::from_float<T>(y1[i]) : x.x[i];
         if (!kInter) o2.x[i] = ptx::from_float<T>(y2[i]);
       }
       *reinterpret_cast<P*>(dst) = o1;
       if (pair) *reinterpret_cast<P*>(dst + half) = o2;
+    };
+    T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + d;
+    turn_heads<T, VEC, kInter>(
+        static_cast<const T*>(a.q) + t * a.q_stride + d, a.Hq, a.D, h0, step, half, turns, c, s,
+        [&](int h, const float (&y1)[VEC], const float (&y2)[VEC], const P& x) {
+          store(qo + static_cast<int64_t>(h) * a.D, y1, y2, x);
+        });
+    if (write) {
+      turn_heads<T, VEC, kInter>(
+          static_cast<const T*>(a.k) + t * a.k_stride + d, a.Hkv, a.D, h0, step, half, turns, c, s,
+          [&](int g, const float (&y1)[VEC], const float (&y2)[VEC], const P& x) {
+            const int64_t row = (static_cast<int64_t>(block) * a.Hkv + g) * a.B + off;
+            if constexpr (kCodes != 0) {
+              using C = Pack<uint8_t, VEC>;
+              uint8_t* const dst = static_cast<uint8_t*>(a.kc) + row * a.D + d;
+              const float scale = __ldg(a.ks + g);
+              *reinterpret_cast<C*>(dst) = codes_of<kCodes, VEC>(y1, scale);
+              if (pair) *reinterpret_cast<C*>(dst + half) = codes_of<kCodes, VEC>(y2, scale);
+            } else {
+              store(static_cast<T*>(a.kc) + row * a.D + d, y1, y2, x);
+            }
+          });
     }
   }
 
-  // V rows: copied, or quantised into their transposed tiles.
-  if (!write) return;
-  const int vunits = a.D / VEC;
-  const T* const v = static_cast<const T*>(a.v) + t * a.v_stride;
-#pragma unroll 2
-  for (int i = threadIdx.x + blockDim.x * blockIdx.y; i < a.Hkv * vunits;
-       i += blockDim.x * gridDim.y) {
-    const int g = i / vunits, d = (i - g * vunits) * VEC;
-    const P x = *reinterpret_cast<const P*>(v + static_cast<int64_t>(g) * a.D + d);
-    const int64_t tile = static_cast<int64_t>(block) * a.Hkv + g;
-    if constexpr (kCodes == 0) {
-      *reinterpret_cast<P*>(static_cast<T*>(a.vc) + (tile * a.B + off) * a.D + d) = x;
-    } else {
-      float y[VEC];
+  // V rows, copied.
+  if constexpr (kCodes == 0) {
+    if (!write) return;
+    constexpr int U = 4;
+    const int vunits = a.D / VEC, total = a.Hkv * vunits;
+    const int step = blockDim.x * gridDim.y;
+    const P* const v = reinterpret_cast<const P*>(static_cast<const T*>(a.v) + t * a.v_stride);
+    for (int i0 = threadIdx.x + blockDim.x * blockIdx.y; i0 < total; i0 += U * step) {
+      P x[U];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = widen(x.x[j]);
-      const Pack<uint8_t, VEC> c = codes_of<kCodes, VEC>(y, __ldg(a.vs + g));
-      uint8_t* const col = static_cast<uint8_t*>(a.vc) + (tile * a.D + d) * 16 + fp8_v_pos(off);
+      for (int w = 0; w < U; ++w)
+        if (i0 + w * step < total) x[w] = v[i0 + w * step];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) col[j * 16] = c.x[j];
+      for (int w = 0; w < U; ++w) {
+        const int i = i0 + w * step;
+        if (i < total) {
+          const int g = i / vunits;
+          const int64_t row = (static_cast<int64_t>(block) * a.Hkv + g) * a.B + off;
+          *reinterpret_cast<P*>(static_cast<T*>(a.vc) + row * a.D + (i - g * vunits) * VEC) = x[w];
+        }
+      }
     }
   }
 }
@@ -229,7 +365,7 @@ void launch_layout(const RotaryArgs& a, bool interleaved, dim3 grid, int threads
 }
 
 template <typename T, int kCodes>
-int launch_typed(const RotaryArgs& a, int32_t tokens, bool interleaved, cudaStream_t st) {
+int launch_typed(RotaryArgs a, bool interleaved, cudaStream_t st) {
   // 16-byte pieces where every row start, the pairs' halves and the strides allow them
   constexpr int W = 16 / sizeof(T);
   const int unit = interleaved ? W : 2 * W;
@@ -247,8 +383,18 @@ int launch_typed(const RotaryArgs& a, int32_t tokens, bool interleaved, cudaStre
   const int heads = a.Hq + a.Hkv;
   // few tokens: their heads are spread over more CTAs until the SMs have a few each
   int split = 1;
-  while (split * rows < heads && static_cast<int64_t>(tokens) * split < 4 * sms) split *= 2;
-  const dim3 grid(tokens, split);
+  while (split * rows < heads && static_cast<int64_t>(a.T) * split < 4 * sms) split *= 2;
+  int64_t columns = a.T;
+  if (kCodes != 0) {
+    // V's windows: split likewise, to one item a thread when all its runs are single tokens
+    const int64_t windows = (a.T + 15) / 16;
+    const int64_t most = (static_cast<int64_t>(a.Hkv) * a.D * 8 + threads - 1) / threads;
+    int64_t parts = 1;
+    while (parts < most && windows * parts < 8 * sms) parts *= 2;
+    a.v_parts = static_cast<int32_t>(parts);
+    columns += (windows * parts + split - 1) / split;
+  }
+  const dim3 grid(static_cast<unsigned>(columns), split);
   if (wide) launch_layout<T, W, kCodes>(a, interleaved, grid, threads, st);
   else launch_layout<T, 1, kCodes>(a, interleaved, grid, threads, st);
   PKV_CUDA(cudaGetLastError());
@@ -322,6 +468,7 @@ int rotary_entry(int32_t codes, const void* q, int64_t q_stride, const void* k, 
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.qo_stride = q_out_stride;
+  a.T = num_tokens;
   a.Hq = num_q_heads;
   a.Hkv = num_kv_heads;
   a.D = head_dim;
@@ -332,9 +479,9 @@ int rotary_entry(int32_t codes, const void* q, int64_t q_stride, const void* k, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc = PKV_OK;
 #define PKV_ROTARY(C)                                                                          \
-  rc = dtype == PKV_F32   ? launch_typed<float, C>(a, num_tokens, interleaved != 0, st)         \
-       : dtype == PKV_F16 ? launch_typed<__half, C>(a, num_tokens, interleaved != 0, st)        \
-                          : launch_typed<__nv_bfloat16, C>(a, num_tokens, interleaved != 0, st)
+  rc = dtype == PKV_F32   ? launch_typed<float, C>(a, interleaved != 0, st)         \
+       : dtype == PKV_F16 ? launch_typed<__half, C>(a, interleaved != 0, st)        \
+                          : launch_typed<__nv_bfloat16, C>(a, interleaved != 0, st)
   if (codes == 0) PKV_ROTARY(0);
   else if (codes == PKV_FP8_E4M3) PKV_ROTARY(1);
   else PKV_ROTARY(2);
