@@ -21,7 +21,7 @@ namespace pkv {
 namespace {
 
 constexpr int kSumThreads = 256;
-constexpr int kSumUnroll = 4;  // steps a half-warp has in flight
+constexpr int kSumUnroll = 4;  // tokens a lane has in flight
 
 struct SumArgs {
   const float* scores;
@@ -33,57 +33,69 @@ struct SumArgs {
   int32_t S, Hkv, limit, cols;  // limit: positions a block table holds
 };
 
-// A half-warp handles one step (16 tokens, one a lane) at a time; a warp walks its run of
-// the flat step list two steps at once.
+// A warp walks its run of the flat step list unit by unit: a unit's tokens, scores and sums
+// are contiguous, its G log-sum-exps stay in registers.
 template <int G>
 __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const SumArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, half = lane >> 4, tok = lane & 15;
+  const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * (kSumThreads / 32);
   const int gw = blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
   const int total = a.steps[a.S];
-  const int per = ((total + warps - 1) / warps + 1) & ~1;
-  const int64_t first = static_cast<int64_t>(gw) * per + half;
-  if (first >= total) return;
-  const int f0 = static_cast<int>(first);
-  const int f1 = min(static_cast<int64_t>(total), static_cast<int64_t>(gw) * per + per);
-  Cursor c = cursor_at(a.steps, a.S, a.Hkv, f0);
-  for (int f = f0; f < f1; f += 2 * kSumUnroll) {
-    float x[kSumUnroll][G], l[kSumUnroll][G], old[kSumUnroll];
-    float* at[kSumUnroll];
+  const int per = max(2, (total + warps - 1) / warps);
+  if (static_cast<int64_t>(gw) * per >= total) return;
+  int f = gw * per;
+  const int f1 = total - f < per ? total : f + per;
+  Cursor c = cursor_at(a.steps, a.S, a.Hkv, f);
+  while (f < f1) {
+    const int j1 = min(c.nb, c.j + (f1 - f));  // steps c.j .. j1 - 1 of unit (c.s, c.g)
+    int end = j1 * kTok;                       // positions in the context
+    if (j1 == c.nb) {
+      end = min(a.context_lens[c.s], a.limit);
+      if (end > a.cols && lane == 0) atomicOr(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+    }
+    const int n = min(end, a.cols) - c.j * kTok;
+    const int64_t unit = static_cast<int64_t>(c.s) * a.Hkv + c.g;
+    const float* const x = a.scores + static_cast<int64_t>(f) * (kTok * G);
+    float* const sums = a.sums + unit * a.cols + c.j * kTok;
+    float lse[G];
 #pragma unroll
-    for (int i = 0; i < kSumUnroll; ++i) {
-      at[i] = nullptr;
-      if (f + 2 * i < f1) {
-        const float* row = a.scores + (static_cast<int64_t>(f + 2 * i) * kTok + tok) * G;
-        const float* lr = a.lse + (static_cast<int64_t>(c.s) * a.Hkv + c.g) * G;
+    for (int h = 0; h < G; ++h) lse[h] = a.lse[unit * G + h];
+    for (int t = lane; t < n; t += 32 * kSumUnroll) {
+      float v[kSumUnroll][G], old[kSumUnroll];
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          x[i][h] = row[h];
-          l[i][h] = lr[h];
+      for (int u = 0; u < kSumUnroll; ++u) {
+        if (t + 32 * u < n) {
+          const float* const row = x + static_cast<int64_t>(t + 32 * u) * G;
+          if constexpr (G % 4 == 0) {
+#pragma unroll
+            for (int h = 0; h < G; h += 4) {
+              const float4 y = __ldcs(reinterpret_cast<const float4*>(row + h));
+              v[u][h] = y.x;
+              v[u][h + 1] = y.y;
+              v[u][h + 2] = y.z;
+              v[u][h + 3] = y.w;
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < G; ++h) v[u][h] = __ldcs(row + h);
+          }
+          old[u] = sums[t + 32 * u];
         }
-        const int p = c.j * kTok + tok;
-        int n = kTok * c.nb;  // positions below n are all in the context but in its last step
-        if (c.j == c.nb - 1) n = min(a.context_lens[c.s], a.limit);
-        if (n > a.cols && tok == 0 && a.status != nullptr && c.j == c.nb - 1)
-          atomicOr(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-        if (p < n && p < a.cols) {
-          at[i] = a.sums + (static_cast<int64_t>(c.s) * a.Hkv + c.g) * a.cols + p;
-          old[i] = *at[i];
+      }
+#pragma unroll
+      for (int u = 0; u < kSumUnroll; ++u) {
+        if (t + 32 * u < n) {
+          float w = 0.f;
+#pragma unroll
+          for (int h = 0; h < G; ++h) w += exp2f(v[u][h] - lse[h]);
+          sums[t + 32 * u] = old[u] + w;
         }
-        advance(c, a.steps, a.S, a.Hkv);
-        if (c.s < a.S) advance(c, a.steps, a.S, a.Hkv);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kSumUnroll; ++i) {
-      if (at[i] != nullptr) {
-        float w = 0.f;
-#pragma unroll
-        for (int h = 0; h < G; ++h) w += exp2f(x[i][h] - l[i][h]);
-        *at[i] = old[i] + w;
-      }
-    }
+    f += j1 - c.j;
+    c.j = j1 - 1;
+    advance(c, a.steps, a.S, a.Hkv);
   }
 }
 
