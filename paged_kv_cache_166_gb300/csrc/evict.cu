@@ -9,11 +9,11 @@
 // the old ones: those may be shared with other sequences (fork, common prefixes), and
 // every row can then move at once.
 //
-// Select is exact: the m-th largest sum is found by its bits, most significant digits
-// first (a histogram a digit), and the tokens above it, plus the lowest positions equal to
-// it, are compacted with prefix counts.  A row of sums is read from memory once: a
-// cluster of CTAs holds it in shared memory, one slice each, and adds its histograms over
-// distributed shared memory.  Gather is a copy, bound by memory.
+// Select is exact: the m-th largest sum is found by its bits, and the tokens above it, plus
+// the lowest positions equal to it, are compacted with prefix counts.  A row of sums is read
+// from memory once.  A short row's keys stay in a warp's registers; a long row lies in the
+// shared memory of a cluster of CTAs, one slice each, whose histograms of the keys' digits
+// are added over distributed shared memory.  Gather is a copy, bound by memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -54,9 +54,146 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the block's threads; the block's total in *total.
+// A row's ends, and the candidates between them.
+struct Row {
+  int c, n, r, f, m, M;  // tokens, kept ones, last and first kept ones, picked of M between
+  const float* sums;
+  int32_t* kept;
+  float* out;
+};
+
+// Reads the row's lengths; `lead` (one thread of a sequence) writes the new length.
+__device__ __forceinline__ Row row_of(const SelectArgs& a, int64_t row, bool lead) {
+  Row w;
+  const int s = static_cast<int>(row / a.Hkv);
+  int c = a.context_lens[s], n = a.keep_lens[s];
+  bool bad = c < 0 || c > a.cols;
+  c = min(max(c, 0), a.cols);
+  n = min(max(n, 0), c);
+  const int most = min(a.kept_cols, a.new_cols);
+  bad |= n > most;
+  n = min(n, most);
+  if (lead && row % a.Hkv == 0) {
+    a.new_lens[s] = n;
+    if (bad && a.status != nullptr) atomicOr(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+  }
+  w.c = c;
+  w.n = n;
+  w.r = min(a.recent, n);
+  w.f = min(a.first, n - w.r);
+  w.m = n - w.r - w.f;
+  w.M = c - w.r - w.f;
+  w.sums = a.sums + row * a.cols;
+  w.kept = a.kept + row * a.kept_cols;
+  w.out = a.new_sums + row * a.new_cols;
+  return w;
+}
+
+// The ends, which stay whatever their sums, by threads t of T.
+__device__ __forceinline__ void keep_ends(const Row& w, int t, int T) {
+  for (int i = t; i < w.f + w.r; i += T) {
+    const int j = i < w.f ? i : w.n - w.r + (i - w.f), p = i < w.f ? i : w.c - w.r + (i - w.f);
+    w.kept[j] = p;
+    w.out[j] = w.sums[p];
+  }
+}
+
+// Where the kept ones of 32 consecutive candidates go: those above the threshold, and
+// equal ones while `ties` last; gt and eq count the ones before, and move on.
+__device__ __forceinline__ int place_of(bool g, bool e, int ties, int lane, int& gt, int& eq) {
+  const uint32_t mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
+  const uint32_t below = (1u << lane) - 1;
+  const int ng = gt + __popc(mg & below), ne = eq + __popc(me & below);
+  gt += __popc(mg);
+  eq += __popc(me);
+  return g || (e && ne < ties) ? ng + min(ne, ties) : -1;
+}
+
+// ---- short rows: a warp each, the keys in registers -------------------------------
+
+constexpr int kShortCols = 2048;
+constexpr int kShortWarps = 4;
+
+// kKeys keys a lane, M <= 32 kKeys.  The threshold's bits are found one at a time, from the
+// highest in which the keys differ, by counting the keys it would leave: a few tens of
+// register compares and one warp sum a bit, and no barrier; it is done early once the
+// count is the number wanted.
+template <int kKeys>
+__device__ __forceinline__ void select_short(const Row& w, int lane) {
+  uint32_t key[kKeys];
+  const float* const vals = w.sums + w.f;
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int p = 32 * i + lane;
+    key[i] = p < w.M ? key_of(vals[p]) : 0u;  // 0: no token
+  }
+  uint32_t t = 1;  // everything stays
+  int ties = 0;
+  if (w.m < w.M) {
+    uint32_t hi = 0, lo = ~0u;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      hi = max(hi, key[i]);
+      lo = min(lo, key[i] == 0 ? ~0u : key[i]);
+    }
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    int bit = 31 - __clz(hi ^ lo);  // -1 if all are equal
+    t = bit < 0 ? hi : (hi >> bit >> 1) << bit << 1;
+    int count = w.M;                // keys >= t
+    for (; bit >= 0 && count != w.m; --bit) {
+      const uint32_t u = t | (1u << bit);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) n += key[i] >= u;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n >= w.m) {
+        t = u;
+        count = n;
+      }
+    }
+    if (count != w.m) {  // t is the m-th largest key itself, and more keys equal it than fit
+      int above = 0;
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) above += key[i] > t;
+      ties = w.m - __reduce_add_sync(0xffffffffu, above);
+    } else {
+      t -= 1;  // keys above t - 1
+    }
+  } else {
+    t = 0;
+  }
+  int gt = 0, eq = 0;
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    if (32 * i < w.M) {
+      const int at = place_of(key[i] > t, ties > 0 && key[i] == t, ties, lane, gt, eq);
+      if (at >= 0) {
+        const int p = 32 * i + lane;
+        w.kept[w.f + at] = w.f + p;
+        w.out[w.f + at] = vals[p];
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kShortWarps * 32)
+    evict_select_short_kernel(const SelectArgs a, int64_t rows) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const Row w = row_of(a, row, lane == 0);
+  keep_ends(w, lane, 32);
+  if (w.m == 0) return;
+  if (w.M <= 512) select_short<16>(w, lane);
+  else select_short<kShortCols / 32>(w, lane);
+}
+
+// ---- long rows: a cluster each, the sums in shared memory -------------------------
+
+// Exclusive prefix sum of v over the block's threads.
 template <int kThreads>
-__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
+__device__ __forceinline__ int block_prefix(int v, int* warp_sums) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -67,103 +204,93 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   __syncthreads();  // warp_sums may still be read from the call before
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  int base = 0, all = 0;
+  int base = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    const int y = warp_sums[i];
-    if (i < w) base += y;
-    all += y;
-  }
-  *total = all;
+  for (int i = 0; i < kThreads / 32; ++i) base += i < w ? warp_sums[i] : 0;
   return base + x - v;
 }
 
-// One cluster per (sequence, KV head).
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs a) {
+constexpr int kLongThreads = 512;
+constexpr int kLongSlice = 16384;  // sums of a CTA: 64 KB, so that two CTAs share an SM
+
+__global__ void __launch_bounds__(kLongThreads) evict_select_long_kernel(const SelectArgs a) {
+  constexpr int kWarps = kLongThreads / 32;
   extern __shared__ float slice_s[];
-  __shared__ int hist[kPasses][kDigitBins];
-  __shared__ int warp_sums[kThreads / 32];
-  __shared__ int counts[2];        // this CTA's tokens above the threshold, and equal to it
-  __shared__ int warp_gt[kThreads / 32], warp_eq[kThreads / 32];
+  __shared__ __align__(16) int hist[kPasses][kDigitBins];
+  __shared__ int warp_sums[kWarps];
+  __shared__ int counts[2];  // this CTA's tokens above the threshold, and equal to it
+  __shared__ int warp_gt[kWarps], warp_eq[kWarps];
   __shared__ uint32_t found_bin;
   __shared__ int found_above;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
-  const int64_t row = blockIdx.x / C;
-  const int s = static_cast<int>(row / a.Hkv);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  int c = a.context_lens[s], n = a.keep_lens[s];
-  bool bad = c < 0 || c > a.cols;
-  c = min(max(c, 0), a.cols);
-  n = min(max(n, 0), c);
-  bad |= n > a.kept_cols || n > a.new_cols;
-  n = min(n, min(a.kept_cols, a.new_cols));
-  const bool lead = rank == 0 && tid == 0 && row % a.Hkv == 0;
-  if (lead) {
-    a.new_lens[s] = n;
-    if (bad && a.status != nullptr) atomicOr(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-  }
-  const int r = min(a.recent, n), f = min(a.first, n - r), m = n - r - f;
-  const int M = c - r - f;  // candidates: positions f .. f + M - 1, m of which stay
-  const float* const sums = a.sums + row * a.cols;
-  int32_t* const kept = a.kept + row * a.kept_cols;
-  float* const out = a.new_sums + row * a.new_cols;
+  const Row w = row_of(a, blockIdx.x / C, rank == 0 && tid == 0);
 
   // this CTA's slice of the candidates
-  const int per = (M + C - 1) / C;
-  const int lo = f + min(M, rank * per), len = max(0, min(per, f + M - lo));
-  const float* vals = sums + lo;
+  const int per = (w.M + C - 1) / C;
+  const int lo = w.f + min(w.M, rank * per), len = max(0, min(per, w.f + w.M - lo));
+  const float* vals = w.sums + lo;
   if (len <= a.slots) {
-    for (int i = tid; i < len; i += kThreads) slice_s[i] = sums[lo + i];
+    constexpr int U = 8;  // loads in flight
+    for (int i0 = tid; i0 < len; i0 += U * kLongThreads) {
+      float x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * kLongThreads < len) x[u] = vals[i0 + u * kLongThreads];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * kLongThreads < len) slice_s[i0 + u * kLongThreads] = x[u];
+    }
     vals = slice_s;
   }
-  for (int i = tid; i < kPasses * kDigitBins; i += kThreads) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < kPasses * kDigitBins; i += kLongThreads) (&hist[0][0])[i] = 0;
   if (tid < 2) counts[tid] = 0;
-  // the ends that stay whatever their sums
-  for (int i = rank * kThreads + tid; i < f + r; i += C * kThreads) {
-    const int j = i < f ? i : n - r + (i - f), p = i < f ? i : c - r + (i - f);
-    kept[j] = p;
-    out[j] = sums[p];
-  }
+  keep_ends(w, rank * kLongThreads + tid, C * kLongThreads);
   __syncthreads();
 
   // The threshold: the m-th largest key, digit by digit; `above` keys are larger.
   uint32_t prefix = 0;
   int above = 0;
-  if (m > 0 && m < M) {
+  if (w.m > 0 && w.m < w.M) {
     int shift = 32;
     for (int pass = 0; pass < kPasses; ++pass) {
       const int bits = pass < 2 ? 11 : 10;
       const uint32_t fixed = shift == 32 ? 0u : ~0u << shift;
       shift -= bits;
-      for (int i = tid; i < len; i += kThreads) {
+#pragma unroll 4
+      for (int i = tid; i < len; i += kLongThreads) {
         const uint32_t k = key_of(vals[i]);
         if ((k & fixed) == prefix) atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
       }
       cluster.sync();
-      // bins from the top: thread t holds those from (kThreads - 1 - t) * kPer on
-      constexpr int kPer = kDigitBins / kThreads;
-      const int b0 = (kThreads - 1 - tid) * kPer;
-      int n_bin[kPer], sum = 0;
+      // bins from the top: thread t holds those from (kLongThreads - 1 - t) * 4 on
+      static_assert(kDigitBins == 4 * kLongThreads, "four bins a thread");
+      const int b0 = (kLongThreads - 1 - tid) * 4;
+      int4 part[kMaxCluster];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        int v = 0;
-        for (int q = 0; q < C; ++q) v += cluster.map_shared_rank(&hist[pass][0], q)[b0 + i];
-        n_bin[i] = v;
-        sum += v;
+      for (int q = 0; q < kMaxCluster; ++q)
+        if (q < C)
+          part[q] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&hist[pass][b0], q));
+      int n[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q < C) {
+          n[0] += part[q].x;
+          n[1] += part[q].y;
+          n[2] += part[q].z;
+          n[3] += part[q].w;
+        }
       }
-      int total;
-      int before = above + block_prefix<kThreads>(sum, warp_sums, &total);
+      int before = above + block_prefix<kLongThreads>(n[0] + n[1] + n[2] + n[3], warp_sums);
 #pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) {
-        if (before < m && before + n_bin[i] >= m) {
+      for (int i = 3; i >= 0; --i) {
+        if (before < w.m && before + n[i] >= w.m) {
           found_bin = static_cast<uint32_t>(b0 + i);
           found_above = before;
         }
-        before += n_bin[i];
+        before += n[i];
       }
       __syncthreads();
       prefix |= found_bin << shift;
@@ -172,19 +299,20 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
     }
   }
   // m == M: everything is above a threshold of 0 (no key is 0); m == 0: nothing stays
-  const bool all = m == M;
-  const int ties = all ? 0 : m - above;
+  const bool all = w.m == w.M;
+  const uint32_t t = all ? 0u : prefix;
+  const int ties = all ? 0 : w.m - above;
 
   // Compaction, ascending: warps take consecutive parts of the slice.
-  constexpr int kWarps = kThreads / 32;
   const int part = ((len + kWarps - 1) / kWarps + 31) & ~31;
   const int p0 = min(len, warp * part), p1 = min(len, p0 + part);
   int gt = 0, eq = 0;
-  if (m > 0) {
+  if (w.m > 0) {
+#pragma unroll 4
     for (int i = p0 + lane; i < p1; i += 32) {
       const uint32_t k = key_of(vals[i]);
-      gt += all || k > prefix;
-      eq += !all && k == prefix;
+      gt += k > t;
+      eq += k == t;
     }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
@@ -196,32 +324,27 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
     atomicAdd(&counts[1], eq);
   }
   cluster.sync();
-  if (m > 0) {
+  if (w.m > 0) {
     int gt0 = 0, eq0 = 0;
     for (int q = 0; q < rank; ++q) {
       const int* cq = cluster.map_shared_rank(&counts[0], q);
       gt0 += cq[0];
       eq0 += cq[1];
     }
-    for (int w = 0; w < warp; ++w) {
-      gt0 += warp_gt[w];
-      eq0 += warp_eq[w];
+    for (int i = 0; i < warp; ++i) {
+      gt0 += warp_gt[i];
+      eq0 += warp_eq[i];
     }
+#pragma unroll 4
     for (int i0 = p0; i0 < p1; i0 += 32) {
       const int i = i0 + lane;
       const float x = i < p1 ? vals[i] : 0.f;
       const uint32_t k = key_of(x);
-      const bool g = i < p1 && (all || k > prefix), e = i < p1 && !all && k == prefix;
-      const uint32_t mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
-      const uint32_t below = (1u << lane) - 1;
-      const int ng = gt0 + __popc(mg & below), ne = eq0 + __popc(me & below);
-      if (g || (e && ne < ties)) {
-        const int j = f + ng + min(ne, ties);
-        kept[j] = lo + i;
-        out[j] = x;
+      const int at = place_of(i < p1 && k > t, i < p1 && k == t, ties, lane, gt0, eq0);
+      if (at >= 0) {
+        w.kept[w.f + at] = lo + i;
+        w.out[w.f + at] = x;
       }
-      gt0 += __popc(mg);
-      eq0 += __popc(me);
     }
   }
   cluster.sync();  // no CTA leaves while others read its counts
@@ -230,7 +353,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const SelectArgs
 // ---- gather ---------------------------------------------------------------------
 
 constexpr int kGatherThreads = 256;
-constexpr int kGatherTokens = 64;  // kept tokens of one CTA
 
 struct GatherArgs {
   uint4* kc;
@@ -241,6 +363,7 @@ struct GatherArgs {
   const int32_t* new_tables;
   int32_t* status;  // or NULL
   int32_t Hkv, B, NB, MAXB, NEWB, kept_cols, row_vecs, D;
+  int32_t tokens;  // kept tokens of one CTA, at most kGatherThreads
 };
 
 // Slot row (in rows of the cache) of position p of a table row, or -1.
@@ -253,46 +376,54 @@ __device__ __forceinline__ int64_t cache_row(const int32_t* table, int max_block
   return (static_cast<int64_t>(b) * Hkv + h) * B + (p - j * B);
 }
 
-// grid: (pieces of kGatherTokens kept tokens, KV heads, sequences).  kV: the V rows are
-// laid out like the K rows (16- and 32-bit caches).
+// grid: (pieces of a.tokens kept tokens, KV heads, sequences).  Every thread looks up one
+// token's two rows, then the rows are moved 16 bytes a thread, U of them in flight.
+// kV: the V rows are laid out like the K rows (16- and 32-bit caches).
 template <bool kV>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const GatherArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ int64_t src_row[kGatherThreads], dst_row[kGatherThreads];
   const int s = blockIdx.z, h = blockIdx.y;
   const int n = min(max(a.new_lens[s], 0), a.kept_cols);
-  const int j0 = blockIdx.x * kGatherTokens, j1 = min(n, j0 + kGatherTokens);
+  const int j0 = blockIdx.x * a.tokens;
   if (j0 >= n) return;
+  const int count = min(a.tokens, n - j0);
+  if (static_cast<int>(threadIdx.x) < count) {
+    const int j = j0 + threadIdx.x;
+    const int p = __ldg(a.kept + (static_cast<int64_t>(s) * a.Hkv + h) * a.kept_cols + j);
+    const int64_t src = cache_row(a.tables + static_cast<int64_t>(s) * a.MAXB, a.MAXB, p, a.B,
+                                  a.NB, a.Hkv, h);
+    const int64_t dst = cache_row(a.new_tables + static_cast<int64_t>(s) * a.NEWB, a.NEWB, j, a.B,
+                                  a.NB, a.Hkv, h);
+    const bool bad = src < 0 || dst < 0;
+    if (bad && a.status != nullptr) atomicOr(a.status, PKV_DEV_BAD_BLOCK_ID);
+    src_row[threadIdx.x] = src;
+    dst_row[threadIdx.x] = bad ? -1 : dst;
+  }
+  __syncthreads();
   const int rows = kGatherThreads / a.row_vecs;
   const int v = threadIdx.x % a.row_vecs, r = threadIdx.x / a.row_vecs;
   if (r >= rows) return;
-  const int32_t* const kept = a.kept + (static_cast<int64_t>(s) * a.Hkv + h) * a.kept_cols;
-  const int32_t* const table = a.tables + static_cast<int64_t>(s) * a.MAXB;
-  const int32_t* const fresh = a.new_tables + static_cast<int64_t>(s) * a.NEWB;
   constexpr int U = 4;
-  for (int j = j0 + r; j < j1; j += U * rows) {
+  for (int j = r; j < count; j += U * rows) {
     int64_t dst[U];
     uint4 kx[U], vx[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int ju = j + u * rows;
-      dst[u] = -1;
-      if (ju < j1) {
-        const int64_t src = cache_row(table, a.MAXB, __ldg(kept + ju), a.B, a.NB, a.Hkv, h);
-        dst[u] = cache_row(fresh, a.NEWB, ju, a.B, a.NB, a.Hkv, h);
-        if (src < 0 || dst[u] < 0) {
-          if (a.status != nullptr && v == 0) atomicOr(a.status, PKV_DEV_BAD_BLOCK_ID);
-          dst[u] = -1;
-        } else {
-          kx[u] = a.kc[src * a.row_vecs + v];
-          if constexpr (kV) vx[u] = a.vc[src * a.row_vecs + v];
-        }
+      dst[u] = ju < count ? dst_row[ju] : -1;
+      if (dst[u] >= 0) {
+        const int64_t at = src_row[ju] * a.row_vecs + v;
+        kx[u] = __ldcs(a.kc + at);
+        if constexpr (kV) vx[u] = __ldcs(a.vc + at);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (dst[u] >= 0) {
-        a.kc[dst[u] * a.row_vecs + v] = kx[u];
-        if constexpr (kV) a.vc[dst[u] * a.row_vecs + v] = vx[u];
+        const int64_t at = dst[u] * a.row_vecs + v;
+        a.kc[at] = kx[u];
+        if constexpr (kV) a.vc[at] = vx[u];
       }
     }
   }
@@ -348,17 +479,27 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_v8_kernel(const G
   }
 }
 
-template <int kThreads>
-int launch_select(const SelectArgs& a0, int64_t rows, int cluster, int slice, cudaStream_t st) {
-  SelectArgs a = a0;
-  a.slots = slice;
-  const size_t smem = static_cast<size_t>(slice) * sizeof(float);
-  PKV_CUDA(cudaFuncSetAttribute(evict_select_kernel<kThreads>,
+// Short rows take a warp each.  Long ones: a slice of at most 16,384 sums (64 KB, so that
+// two CTAs share an SM) a CTA, up to eight CTAs; larger slices up to 160 KB, and what does
+// not fit then is read from memory once a pass.
+int launch_select(SelectArgs a, int64_t rows, cudaStream_t st) {
+  if (a.cols <= kShortCols) {
+    const int64_t ctas = (rows + kShortWarps - 1) / kShortWarps;
+    evict_select_short_kernel<<<static_cast<unsigned>(ctas), kShortWarps * 32, 0, st>>>(a, rows);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+  }
+  int cluster = 1;
+  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kLongSlice < a.cols) cluster *= 2;
+  const int slice = (a.cols + cluster - 1) / cluster;
+  a.slots = slice <= 40960 ? slice : 0;
+  const size_t smem = static_cast<size_t>(a.slots) * sizeof(float);
+  PKV_CUDA(cudaFuncSetAttribute(evict_select_long_kernel,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(smem)));
+                                40960 * static_cast<int>(sizeof(float))));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kLongThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -368,7 +509,7 @@ int launch_select(const SelectArgs& a0, int64_t rows, int cluster, int slice, cu
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_select_kernel<kThreads>, a));
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_select_long_kernel, a));
   return PKV_OK;
 }
 
@@ -413,19 +554,7 @@ int pkv_evict_select(const float* weight_sums, int32_t sums_cols, const int32_t*
   a.first = first;
   a.recent = recent;
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
-  // Short rows: one small CTA each.  Long ones: a slice of at most 16,384 sums (64 KB, so
-  // that three CTAs share an SM) a CTA, up to eight CTAs; what does not fit then is read
-  // from memory once a pass instead.
-  int rc;
-  if (sums_cols <= 2048) {
-    rc = launch_select<128>(a, rows, 1, sums_cols, static_cast<cudaStream_t>(stream));
-  } else {
-    int cluster = 1;
-    while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * 16384 < sums_cols) cluster *= 2;
-    const int slice = (sums_cols + cluster - 1) / cluster;
-    rc = launch_select<512>(a, rows, cluster, slice <= 40960 ? slice : 0,
-                            static_cast<cudaStream_t>(stream));
-  }
+  const int rc = launch_select(a, rows, static_cast<cudaStream_t>(stream));
   return rc == PKV_OK ? ok() : rc;
 }
 
@@ -480,7 +609,14 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
   a.row_vecs = static_cast<int32_t>(row_bytes / 16);
   a.D = head_dim;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((kept_cols + kGatherTokens - 1) / kGatherTokens, num_kv_heads, num_seqs);
+  // 256 tokens a CTA, or fewer while the SMs would not have a few CTAs each
+  int sms = 0, dev = 0;
+  const int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  a.tokens = kGatherThreads;
+  const int64_t heads = static_cast<int64_t>(num_seqs) * num_kv_heads;
+  while (a.tokens > 32 && heads * ((kept_cols + a.tokens - 1) / a.tokens) < 4 * sms) a.tokens /= 2;
+  cfg.gridDim = dim3((kept_cols + a.tokens - 1) / a.tokens, num_kv_heads, num_seqs);
   cfg.blockDim = dim3(kGatherThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
