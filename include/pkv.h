@@ -718,14 +718,17 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
  *               any alignment of the element.
  * beam_scores   device float [num_seqs, num_beams]; scores must not be this array.
  * scores        device float [num_seqs, num_out]; beams, tokens device int32 likewise.
- * workspace     >= pkv_beam_workspace_size(...) bytes, 256-byte aligned; it needs no
- *               initial value and keeps none.  Calls that may overlap need their own.
+ * workspace     >= pkv_beam_workspace_size(...) bytes, 256-byte aligned; its first
+ *               PKV_BEAM_TICKET_BYTES zero before its first use, and left so by every
+ *               call, so one workspace serves calls of any sizes.  Calls that may
+ *               overlap need their own.
  * The log-sum-exp and the scores are 64-bit, scores rounded to fp32 at the end; equal
  * rows of logits have equal log-sum-exps, wherever they lie.
  * Supported: num_beams <= 64, num_out <= min(128, num_beams * vocab), num_seqs *
  * num_beams <= 65535, ceil(vocab / 8192) * num_out <= 8192.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  */
+#define PKV_BEAM_TICKET_BYTES (512u << 10)
 int pkv_beam_select(const void* logits, int64_t seq_stride, int64_t beam_stride,
                     const float* beam_scores, int32_t num_seqs, int32_t num_beams, int32_t vocab,
                     int32_t num_out, float* scores, int32_t* beams, int32_t* tokens,
@@ -890,18 +893,22 @@ int pkv_seq_swap_in(pkv_allocator_t* a, int32_t seq, int32_t* ids_out, int32_t c
                     int32_t* n);
 
 /*
- * pkv_seq_evict — the table of a sequence whose cached tokens are cut down to
- * new_len: min(length, new_len) tokens in ceil(that / block_size) freshly allocated
- * blocks, written to ids_out in logical order (*n of them).  The old blocks are then
- * decremented in reverse table order: other holders keep theirs, the rest return to
- * the pool.  Move the rows with pkv_evict_gather (old table: pkv_seq_table or
- * pkv_export_tables before this call) on the stream before anything else writes to
- * the blocks given back.  PKV_ERR_OUT_OF_BLOCKS (state unchanged) if the pool cannot
- * supply every new block while the old ones are held; PKV_ERR_INVALID_ARG for a bad or
- * swapped-out id, a negative new_len, or ids_out too small.
+ * pkv_seq_evict — the tables of sequences whose cached tokens are cut down: seqs[i] to
+ * min(length, new_lens[i]) tokens in ceil(that / block_size) freshly allocated blocks,
+ * row i of tables_out (host int32 [k, max_blocks], entries past a table's end 0).  Every
+ * new block is taken before any old one is given back, so that one pkv_evict_gather can
+ * move all the sequences' rows; then the old tables are decremented in list order, each
+ * in reverse table order: other holders keep their blocks, the rest return to the pool.
+ * Export the old tables before this call, and queue the gather on the stream before
+ * anything else writes to the blocks given back.
+ * seqs      host int32 [k], resident sequence ids, no id twice.
+ * new_lens  host int32 [k], not negative.
+ * All or nothing: PKV_ERR_OUT_OF_BLOCKS (state unchanged) if the pool cannot supply every
+ * new block while the old ones are held; PKV_ERR_INVALID_ARG for a bad, swapped-out or
+ * repeated id, a negative length or a table longer than max_blocks.  k = 0 is a no-op.
  */
-int pkv_seq_evict(pkv_allocator_t* a, int32_t seq, int32_t new_len, int32_t* ids_out,
-                  int32_t capacity, int32_t* n);
+int pkv_seq_evict(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int32_t* new_lens,
+                  int32_t max_blocks, int32_t* tables_out);
 
 /*
  * pkv_seq_reorder — beam search's reordering of states: sequence seqs[i] becomes a

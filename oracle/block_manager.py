@@ -157,21 +157,24 @@ class BlockManager:
         self.swapped.discard(sid)
         return table
 
-    def evict(self, sid: int, new_len: int) -> List[int]:
-        """Cut ``sid`` down to ``min(length, new_len)`` tokens in fresh blocks (all taken
-        before the old ones are given back, in reverse order); the new table."""
-        self._check_resident(sid)
-        if new_len < 0:
-            raise InvalidOperation("negative length")
-        n = min(self.lengths[sid], new_len)
-        need = -(-n // self.block_size)
-        if need > self.num_free():
+    def evict(self, seqs: Sequence[int], new_lens: Sequence[int]) -> List[List[int]]:
+        """Cut each ``seqs[i]`` down to ``min(length, new_lens[i])`` tokens in fresh blocks,
+        all taken before the old ones are given back (list order, each in reverse); the
+        new tables."""
+        for sid in seqs:
+            self._check_resident(sid)
+        if len(set(seqs)) != len(seqs) or any(n < 0 for n in new_lens):
+            raise InvalidOperation("a sequence listed twice or a negative length")
+        lens = [min(self.lengths[s], n) for s, n in zip(seqs, new_lens)]
+        need = [-(-n // self.block_size) for n in lens]
+        if sum(need) > self.num_free():
             raise OutOfBlocks("pool cannot hold the kept tokens beside the old blocks")
-        table = [self.alloc() for _ in range(need)]
-        for b in reversed(self.tables[sid]):
-            self.decref(b)
-        self.tables[sid], self.lengths[sid] = table, n
-        return list(table)
+        tables = [[self.alloc() for _ in range(n)] for n in need]
+        for sid, table, n in zip(seqs, tables, lens):
+            for b in reversed(self.tables[sid]):
+                self.decref(b)
+            self.tables[sid], self.lengths[sid] = list(table), n
+        return tables
 
     def reorder(self, seqs: Sequence[int], parents: Sequence[int]) -> None:
         """Beam search: ``seqs[i]`` becomes the continuation of what ``seqs[parents[i]]``

@@ -30,6 +30,7 @@ PKV_DEV_BAD_POSITION = 16
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
 
 PKV_STATIC_SCRATCH_BYTES = 16 << 20
+PKV_BEAM_TICKET_BYTES = 512 << 10
 
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -110,7 +111,7 @@ SIGNATURES = {
     "pkv_beam_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _p, _p, _p,
                                        _sz, _i32, _p]),
     "pkv_beam_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
-    "pkv_seq_evict": (ctypes.c_int, [_p, _i32, _i32, _pi32, _i32, _pi32]),
+    "pkv_seq_evict": (ctypes.c_int, [_p, _pi32, _i32, _pi32, _i32, _pi32]),
     "pkv_seq_reorder": (ctypes.c_int, [_p, _pi32, _i32, _pi32]),
     "pkv_allocator_create": (ctypes.c_int, [_i32, _i32, _pi32, ctypes.POINTER(_p)]),
     "pkv_allocator_destroy": (ctypes.c_int, [_p]),

@@ -130,17 +130,20 @@ class BlockAllocator:
         N.check(self._lib.pkv_seq_swap_in(self._h, seq, _ptr(buf), len(buf), ctypes.byref(n)))
         return buf[:n.value].tolist()
 
-    def evict(self, seq: int, new_len: int) -> List[int]:
-        """Cut a sequence down to min(length, new_len) cached tokens in fresh blocks; returns
-        the new table.  The old blocks go back to the pool (or to their other holders):
-        export the old table before, and queue paged_evict_gather before anything else
-        writes to them."""
-        B = self.block_size
-        buf = np.empty(max(-(-min(self.length(seq), max(new_len, 0)) // B), 1), dtype=np.int32)
-        n = ctypes.c_int32(0)
-        N.check(self._lib.pkv_seq_evict(self._h, seq, new_len, _ptr(buf), len(buf),
-                                        ctypes.byref(n)))
-        return buf[:n.value].tolist()
+    def evict(self, seqs: Sequence[int], new_lens: Sequence[int], max_blocks: int) -> np.ndarray:
+        """Cut each seqs[i] down to min(length, new_lens[i]) cached tokens in fresh blocks;
+        returns their new tables, int32 [len(seqs), max_blocks] (padding 0).  All new blocks
+        are taken before the old ones go back to the pool (or to their other holders):
+        export the old tables before, and queue paged_evict_gather before anything else
+        writes to the blocks given back.  All or nothing."""
+        ids = np.ascontiguousarray(seqs, dtype=np.int32)
+        lens = np.ascontiguousarray(new_lens, dtype=np.int32)
+        if ids.ndim != 1 or ids.shape != lens.shape:
+            raise ValueError("seqs and new_lens must be lists of one length")
+        out = np.zeros((len(ids), max_blocks), dtype=np.int32)
+        N.check(self._lib.pkv_seq_evict(self._h, _ptr(ids), len(ids), _ptr(lens), max_blocks,
+                                        _ptr(out)))
+        return out
 
     def reorder(self, seqs: Sequence[int], parents: Sequence[int]) -> None:
         """Beam search: each seqs[i] becomes the continuation of what seqs[parents[i]] was

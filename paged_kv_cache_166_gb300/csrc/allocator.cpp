@@ -15,8 +15,8 @@
 //     anyway"): swap-out hands back the sequence's blocks (their contents go to
 //     host memory) and keeps its length; swap-in gives it ceil(len / B) fresh
 //     blocks, all or nothing;
-//   * eviction gives a sequence fresh blocks for the tokens that stay and hands the
-//     old ones back; reordering makes each listed sequence the continuation of another.
+//   * eviction gives sequences fresh blocks for the tokens that stay, all of them before
+//     any old one is handed back (one launch moves all their rows); reordering makes each listed sequence the continuation of another.
 // Every public call validates first and mutates only once it cannot fail, so a
 // failing call leaves the state unchanged.
 #include <algorithm>
@@ -263,27 +263,45 @@ int pkv_seq_swap_in(pkv_allocator_t* a, int32_t seq, int32_t* ids_out, int32_t c
   });
 }
 
-int pkv_seq_evict(pkv_allocator_t* a, int32_t seq, int32_t new_len, int32_t* ids_out,
-                  int32_t capacity, int32_t* n) {
-  PKV_REQUIRE(a && n, PKV_ERR_INVALID_ARG, "NULL argument");
-  PKV_REQUIRE(a->resident_seq(seq), PKV_ERR_INVALID_ARG, "unknown or swapped-out sequence %d",
-              seq);
-  PKV_REQUIRE(new_len >= 0, PKV_ERR_INVALID_ARG, "negative length");
-  auto& s = a->seqs[seq];
-  const int32_t len = std::min(s.len, new_len);
-  const int64_t B = a->block_size;
-  const int32_t m = static_cast<int32_t>((len + B - 1) / B);
-  PKV_REQUIRE(m == 0 || (ids_out && capacity >= m), PKV_ERR_INVALID_ARG,
-              "ids_out holds %d ids, the sequence needs %d blocks", capacity, m);
-  PKV_REQUIRE(static_cast<size_t>(m) <= a->free_stack.size(), PKV_ERR_OUT_OF_BLOCKS,
-              "eviction needs %d blocks, %zu free", m, a->free_stack.size());
+int pkv_seq_evict(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int32_t* new_lens,
+                  int32_t max_blocks, int32_t* tables_out) {
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL handle");
+  PKV_REQUIRE(k >= 0 && max_blocks >= 0, PKV_ERR_INVALID_ARG, "negative size");
+  PKV_REQUIRE(k == 0 || (seqs && new_lens && (max_blocks == 0 || tables_out)),
+              PKV_ERR_INVALID_ARG, "NULL array");
   return guarded([&] {
-    std::vector<int32_t> table(m);  // before any block is taken; no effect if it throws
-    for (int32_t j = 0; j < m; ++j) table[j] = ids_out[j] = a->pop();
-    for (auto it = s.table.rbegin(); it != s.table.rend(); ++it) a->decref(*it);
-    s.table.swap(table);
-    s.len = len;
-    *n = m;
+    const int64_t B = a->block_size;
+    const uint32_t epoch = a->next_epoch();
+    std::vector<std::vector<int32_t>> tables(k);  // all room made before any block is taken
+    int64_t need = 0;
+    for (int32_t i = 0; i < k; ++i) {
+      PKV_REQUIRE(a->resident_seq(seqs[i]), PKV_ERR_INVALID_ARG,
+                  "unknown or swapped-out sequence %d", seqs[i]);
+      auto& s = a->seqs[seqs[i]];
+      PKV_REQUIRE(s.mark != epoch, PKV_ERR_INVALID_ARG, "sequence %d listed twice", seqs[i]);
+      s.mark = epoch;
+      PKV_REQUIRE(new_lens[i] >= 0, PKV_ERR_INVALID_ARG, "negative length");
+      const int64_t m = (std::min(s.len, new_lens[i]) + B - 1) / B;
+      PKV_REQUIRE(m <= max_blocks, PKV_ERR_INVALID_ARG,
+                  "sequence %d needs %lld blocks > max_blocks %d", seqs[i],
+                  static_cast<long long>(m), max_blocks);
+      tables[i].resize(static_cast<size_t>(m));
+      need += m;
+    }
+    PKV_REQUIRE(need <= static_cast<int64_t>(a->free_stack.size()), PKV_ERR_OUT_OF_BLOCKS,
+                "eviction needs %lld blocks, %zu free", static_cast<long long>(need),
+                a->free_stack.size());
+    for (int32_t i = 0; i < k; ++i) {
+      int32_t* row = tables_out + static_cast<int64_t>(i) * max_blocks;
+      for (int32_t j = 0; j < max_blocks; ++j)
+        row[j] = j < static_cast<int32_t>(tables[i].size()) ? (tables[i][j] = a->pop()) : 0;
+    }
+    for (int32_t i = 0; i < k; ++i) {
+      auto& s = a->seqs[seqs[i]];
+      for (auto it = s.table.rbegin(); it != s.table.rend(); ++it) a->decref(*it);
+      s.table.swap(tables[i]);
+      s.len = std::min(s.len, new_lens[i]);
+    }
     return pkv::ok();
   });
 }

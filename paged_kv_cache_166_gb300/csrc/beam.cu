@@ -12,15 +12,15 @@
 // CTA that finishes a row last merges the row's chunks, and the one that finishes a
 // request's rows last merges its beams.  Nobody waits: tickets say who is last.
 //
-// Best N of a set spread over a block's threads: with t the N-th best of the threads' own
-// best entries, at least N entries are as good as t, and those that are lie in N threads:
-// few, so they are collected in shared memory and each counts the entries better than
-// itself.  The order has no ties (equal values are told apart by their position), so the
-// result does not depend on the order of collection.
+// Best N of a set spread over a block's threads: with t the N-th best of the best entries
+// of small groups of threads, at least N entries are as good as t, and those that are lie
+// in N groups: few, so they are collected in shared memory and each counts the entries
+// better than itself.  Entries are compared as integer keys and no two are equal (equal
+// values are told apart by their position), so the order of collection does not matter.
 //
 // Precision: candidates of different beams may lie next to each other, so lse and the
-// scores are 64-bit: expf per logit, 32 of a thread's terms summed in fp32, everything
-// across threads in fp64.  Only the score handed out is rounded to fp32.
+// scores are 64-bit: an fp32 exponential per logit, 32 of a thread's terms summed in fp32,
+// everything across threads in fp64.  Only the score handed out is rounded to fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,6 +39,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxOut = 128;
+constexpr int kMaxRows = 65535;    // num_seqs * num_beams
 constexpr int kMaxEntries = 8192;  // entries a merge takes: chunks * N, beams * N
 constexpr int kLargeChunk = 32;    // elements a thread holds
 constexpr int kSmallChunk = 8;
@@ -50,104 +51,139 @@ struct BeamArgs {
   float* scores;
   int32_t* beams;
   int32_t* tokens;
-  // workspace: per (row, chunk), then per row, then the tickets
-  float* chunk_max;
-  double* chunk_sum;
-  float* chunk_val;
-  int32_t* chunk_tok;
-  double* row_lse;
-  float* row_val;
-  int32_t* row_tok;
+  // workspace: the tickets, zero between launches, then per (row, chunk) and per row
   int32_t* row_ticket;
   int32_t* seq_ticket;
+  float* chunk_max;
+  double* chunk_sum;
+  uint64_t* chunk_top;  // keys of a chunk's best N
+  double* row_lse;
+  uint64_t* row_top;    // keys of a row's best N
   int32_t K, V, N, chunks;
 };
 
-// a before b: larger value, equal values by position.  Position INT_MAX: no entry.
-template <typename V>
-__device__ __forceinline__ bool better(V av, int ai, V bv, int bi) {
-  return av > bv || (av == bv && ai < bi);
+// Keys: larger is better, 0 is no entry, and no two entries of a set have the same one.
+// A token of a row: its logit's bits in the order of the values (-0 as 0), then the token,
+// lower first.
+__device__ __forceinline__ uint64_t token_key(float x, int token) {
+  uint32_t u = __float_as_uint(x + 0.f);
+  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<uint64_t>(u) << 32) | static_cast<uint32_t>(~token);
+}
+__device__ __forceinline__ int key_token(uint64_t key) {
+  return static_cast<int>(~static_cast<uint32_t>(key));
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  const uint32_t u = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+// A candidate of a request: its 64-bit score's bits in the order of the values, then its
+// place in the list of beams' lists.  (Compared as integers: fp64 comparisons run at a
+// 64th of their rate.)
+struct ScoreKey {
+  uint64_t score;
+  uint32_t at;  // ~place
+  __device__ __forceinline__ bool operator>(const ScoreKey& o) const {
+    return score > o.score || (score == o.score && at > o.at);
+  }
+  __device__ __forceinline__ bool none() const { return score == 0; }
+};
+__device__ __forceinline__ ScoreKey score_key(double x, int place) {
+  uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  u = (u >> 63) ? ~u : (u | (uint64_t(1) << 63));
+  return ScoreKey{u, ~static_cast<uint32_t>(place)};
+}
+__device__ __forceinline__ double key_score(const ScoreKey& k) {
+  const uint64_t u = k.score;
+  return __longlong_as_double(static_cast<long long>((u >> 63) ? (u & ~(uint64_t(1) << 63)) : ~u));
+}
+__device__ __forceinline__ bool none(uint64_t k) { return k == 0; }
+__device__ __forceinline__ bool none(const ScoreKey& k) { return k.none(); }
+
+__device__ __forceinline__ uint64_t shfl_xor(uint64_t k, int o) {
+  return __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(k), o);
+}
+__device__ __forceinline__ ScoreKey shfl_xor(const ScoreKey& k, int o) {
+  return ScoreKey{shfl_xor(k.score, o), __shfl_xor_sync(0xffffffffu, k.at, o)};
 }
 
+// Threads whose best entries are merged before the threshold is sought: about four
+// groups of them for each entry wanted, in 32 to 256 groups.
+__host__ __device__ constexpr int group_of(int n) {
+  return n <= 8 ? 8 : (n <= 16 ? 4 : (n <= 32 ? 2 : 1));
+}
+
+template <typename Key>
 struct TopShared {
   int count;
-  int thr_id;
-  double thr_val;
-  int best_id[kThreads];
-  alignas(8) unsigned char best_val[kThreads * sizeof(double)];
+  Key threshold;
+  Key best[kThreads];
 };
 
-// Threshold: the n-th best of the threads' best entries (v, id), or "everything" if
-// fewer threads have one.
-template <typename V>
-__device__ __forceinline__ void threshold(V v, int id, int n, TopShared& sh, V* tv, int* ti) {
-  V* const bv = reinterpret_cast<V*>(sh.best_val);
+// Threshold of the block's entries, `mine` the thread's best: the n-th best of the groups'
+// best, so that at least n entries are as good as it and those that are lie in n groups;
+// an empty key ("everything") if fewer groups have an entry.
+template <typename Key>
+__device__ __forceinline__ Key threshold_of(Key mine, int n, TopShared<Key>& sh) {
+  const int g = group_of(n), groups = kThreads / g;
+  for (int o = 1; o < g; o <<= 1) {
+    const Key other = shfl_xor(mine, o);
+    if (other > mine) mine = other;
+  }
   __syncthreads();
-  bv[threadIdx.x] = v;
-  sh.best_id[threadIdx.x] = id;
+  if (threadIdx.x % g == 0) sh.best[threadIdx.x / g] = mine;
   if (threadIdx.x == 0) {
     sh.count = 0;
-    sh.thr_val = -INFINITY;
-    sh.thr_id = INT_MAX;
+    sh.threshold = Key{};
   }
   __syncthreads();
-  int rank = 0;
+  if (static_cast<int>(threadIdx.x) < groups) {
+    const Key k = sh.best[threadIdx.x];
+    int rank = 0;
 #pragma unroll 8
-  for (int i = 0; i < kThreads; ++i) rank += better(bv[i], sh.best_id[i], v, id);
-  if (rank == n - 1 && id != INT_MAX) {
-    sh.thr_val = static_cast<double>(v);
-    sh.thr_id = id;
+    for (int i = 0; i < groups; ++i) rank += sh.best[i] > k;
+    if (rank == n - 1 && !none(k)) sh.threshold = k;
   }
   __syncthreads();
-  *tv = static_cast<V>(sh.thr_val);
-  *ti = sh.thr_id;
+  return sh.threshold;
 }
 
-// The collected entries in their order: put(rank, value, position) for rank < n.
-template <typename V, typename Put>
-__device__ __forceinline__ void ranked(const V* cv, const int* ci, int n, const TopShared& sh,
-                                       Put put) {
+// The collected entries in their order: put(rank, key) for rank < n, empty keys behind them.
+template <typename Key, typename Put>
+__device__ __forceinline__ void ranked(const Key* list, int n, const TopShared<Key>& sh, Put put) {
   __syncthreads();
   const int count = sh.count;
   for (int i = threadIdx.x; i < count; i += kThreads) {
-    const V v = cv[i];
-    const int id = ci[i];
+    const Key k = list[i];
     int rank = 0;
-    for (int j = 0; j < count; ++j) rank += better(cv[j], ci[j], v, id);
-    if (rank < n) put(rank, v, id);
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) rank += list[j] > k;
+    if (rank < n) put(rank, k);
   }
-  for (int i = count + threadIdx.x; i < n; i += kThreads)
-    put(i, static_cast<V>(-INFINITY), INT_MAX);
+  for (int i = count + threadIdx.x; i < n; i += kThreads) put(i, Key{});
 }
 
-// The best n of entries get(i), i < M (value and position), M <= kMaxEntries; buf holds
-// n * ceil(M / kThreads) entries.
-template <typename V, typename Get, typename Put>
-__device__ __forceinline__ void merge_top(int M, int n, Get get, unsigned char* buf, int cap,
-                                          TopShared& sh, Put put) {
-  V best = static_cast<V>(-INFINITY), v;
-  int best_id = INT_MAX, id;
-  for (int i = threadIdx.x; i < M; i += kThreads) {
-    get(i, &v, &id);
-    if (id != INT_MAX && better(v, id, best, best_id)) {
-      best = v;
-      best_id = id;
+// The best n of the entries get(i), i < M, M <= kMaxEntries.
+template <typename Key, typename Get, typename Put>
+__device__ __forceinline__ void merge_top(int M, int n, Get get, Key* list, TopShared<Key>& sh,
+                                          Put put) {
+  Key best{}, t{};
+  if (M > kThreads) {
+    for (int i = threadIdx.x; i < M; i += kThreads) {
+      const Key k = get(i);
+      if (k > best) best = k;
     }
+    t = threshold_of(best, n, sh);
+  } else {  // few enough to be ranked as they are
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
   }
-  V tv;
-  int ti;
-  threshold(best, best_id, n, sh, &tv, &ti);
-  V* const cv = reinterpret_cast<V*>(buf);
-  int* const ci = reinterpret_cast<int*>(cv + cap);
   for (int i = threadIdx.x; i < M; i += kThreads) {
-    get(i, &v, &id);
-    if (id != INT_MAX && !better(tv, ti, v, id)) {
-      const int at = atomicAdd(&sh.count, 1);
-      cv[at] = v;
-      ci[at] = id;
-    }
+    const Key k = get(i);
+    if (!none(k) && !(t > k)) list[atomicAdd(&sh.count, 1)] = k;
   }
-  ranked(cv, ci, n, sh, put);
+  ranked(list, n, sh, put);
 }
 
 __device__ __forceinline__ double block_sum(double x, double* warp) {
@@ -162,15 +198,15 @@ __device__ __forceinline__ double block_sum(double x, double* warp) {
   return y;
 }
 
-__device__ __forceinline__ float block_max(float x, double* warp) {
+__device__ __forceinline__ float block_max(float x, float* warp) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = static_cast<double>(x);
+  if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = x;
   __syncthreads();
   float y = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) y = fmaxf(y, static_cast<float>(warp[i]));
+  for (int i = 0; i < kThreads / 32; ++i) y = fmaxf(y, warp[i]);
   return y;
 }
 
@@ -179,7 +215,7 @@ __device__ __forceinline__ float logit(T x) {
   float y;
   if constexpr (std::is_same<T, float>::value) y = x;
   else y = ptx::to_float(x);
-  return y != y ? -INFINITY : y;  // NaN: a banned token
+  return fmaxf(y, -INFINITY);  // NaN: a banned token
 }
 
 // The 16 bytes at p, which lies `skew` bytes past a 16-byte boundary: the two aligned
@@ -223,8 +259,12 @@ __device__ __forceinline__ bool last_to_come(int32_t* ticket, int of, int* flag)
 template <typename T, int E>
 __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char buf[];
-  __shared__ TopShared sh;
-  __shared__ double warp[kThreads / 32];
+  __shared__ union {
+    TopShared<uint64_t> row;
+    TopShared<ScoreKey> seq;
+  } sh;
+  __shared__ double warp_sum[kThreads / 32];
+  __shared__ float warp_max[kThreads / 32];
   __shared__ int flag;
   constexpr int W = 16 / static_cast<int>(sizeof(T));
   constexpr int kVecs = E / W;
@@ -232,10 +272,10 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
   const int tid = threadIdx.x, chunk = blockIdx.x;
   const int row = blockIdx.y, N = a.N, V = a.V;
   const int s = row / a.K, b = row - s * a.K;
+  uint64_t* const list = reinterpret_cast<uint64_t*>(buf);
 
   const float bs = a.beam_scores[row];
   const bool alive = isfinite(bs);  // a dead beam's logits are not read
-  float top = -INFINITY;
   const int64_t slot = static_cast<int64_t>(row) * a.chunks + chunk;
   if (alive) {
     const T* const x = static_cast<const T*>(a.logits) + s * a.seq_stride + b * a.beam_stride;
@@ -257,49 +297,38 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
         for (int w = 0; w < W; ++w) v[j * W + w] = p + w < V ? logit(x[p + w]) : -INFINITY;
       }
     }
-    // element j * W + w of the thread: its token, INT_MAX past the row
-    auto token = [&](int i) {
-      const int p = base + ((i / W) * kThreads + tid) * W + i % W;
-      return p < V ? p : INT_MAX;
-    };
-    float best = -INFINITY;
-    int best_id = INT_MAX;
+    // element j * W + w of the thread is token base + (j * kThreads + tid) * W + w: ascending,
+    // so the first of the largest is the best
+    auto token = [&](int i) { return base + ((i / W) * kThreads + tid) * W + i % W; };
+    float best = v[0];
+    int at = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if (better(v[i], token(i), best, best_id)) {
+    for (int i = 1; i < E; ++i) {
+      if (v[i] > best) {
         best = v[i];
-        best_id = token(i);
+        at = i;
       }
     }
-    top = block_max(best, warp);
+    const float top = block_max(best, warp_max);
     float part = 0.f;
     if (isfinite(top)) {
+      // e^d as 2^(d log2 e): the product is off by 2^-24 |d| log2 e, a term by 2^-20 of
+      // itself where it counts (d > -17)
 #pragma unroll
-      for (int i = 0; i < E; ++i) part += expf(v[i] - top);
+      for (int i = 0; i < E; ++i) part += ptx::ex2((v[i] - top) * 1.4426950408889634f);
     }
-    const double sum = block_sum(static_cast<double>(part), warp);
-    float tv;
-    int ti;
-    threshold(best, best_id, N, sh, &tv, &ti);
-    float* const cv = reinterpret_cast<float*>(buf);
-    int* const ci = reinterpret_cast<int*>(cv + N * E);
-    if (!better(tv, ti, best, best_id)) {
+    const double sum = block_sum(static_cast<double>(part), warp_sum);
+    const uint64_t mine = token(0) < V ? token_key(best, token(at)) : 0;
+    const uint64_t t = threshold_of(mine, N, sh.row);
+    if (mine != 0 && !(t > mine)) {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const int id = token(i);
-        if (id != INT_MAX && !better(tv, ti, v[i], id)) {
-          const int at = atomicAdd(&sh.count, 1);
-          cv[at] = v[i];
-          ci[at] = id;
-        }
+        const uint64_t k = token_key(v[i], token(i));
+        if (token(i) < V && !(t > k)) list[atomicAdd(&sh.row.count, 1)] = k;
       }
     }
-    float* const ov = a.chunk_val + slot * N;
-    int32_t* const ot = a.chunk_tok + slot * N;
-    ranked(cv, ci, N, sh, [&](int rank, float val, int id) {
-      ov[rank] = val;
-      ot[rank] = id;
-    });
+    uint64_t* const out = a.chunk_top + slot * N;
+    ranked(list, N, sh.row, [&](int rank, uint64_t k) { out[rank] = k; });
     if (tid == 0) {
       a.chunk_max[slot] = top;
       a.chunk_sum[slot] = sum;
@@ -312,73 +341,60 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamArgs a)
     const int64_t first = static_cast<int64_t>(row) * a.chunks;
     float m = -INFINITY;
     for (int c = tid; c < a.chunks; c += kThreads) m = fmaxf(m, __ldcg(a.chunk_max + first + c));
-    m = block_max(m, warp);
+    m = block_max(m, warp_max);
     double sum = 0.0;
     if (isfinite(m))
       for (int c = tid; c < a.chunks; c += kThreads)
         sum += __ldcg(a.chunk_sum + first + c) *
                exp(static_cast<double>(__ldcg(a.chunk_max + first + c)) - m);
-    sum = block_sum(sum, warp);
+    sum = block_sum(sum, warp_sum);
     if (tid == 0) a.row_lse[row] = isfinite(m) ? m + log(sum) : INFINITY;
-    const int M = a.chunks * N;
-    float* const ov = a.row_val + static_cast<int64_t>(row) * N;
-    int32_t* const ot = a.row_tok + static_cast<int64_t>(row) * N;
-    merge_top<float>(
-        M, N,
-        [&](int i, float* v, int* id) {
-          *v = __ldcg(a.chunk_val + first * N + i);
-          *id = __ldcg(a.chunk_tok + first * N + i);
+    const uint64_t* const in = a.chunk_top + first * N;
+    uint64_t* const out = a.row_top + static_cast<int64_t>(row) * N;
+    merge_top<uint64_t>(
+        a.chunks * N, N,
+        [&](int i) {
+          return static_cast<uint64_t>(__ldcg(reinterpret_cast<const unsigned long long*>(in + i)));
         },
-        buf, N * ((M + kThreads - 1) / kThreads), sh,
-        [&](int rank, float val, int id) {
-          ov[rank] = val;
-          ot[rank] = id;
-        });
+        list, sh.row, [&](int rank, uint64_t k) { out[rank] = k; });
   } else if (tid == 0) {
     a.row_lse[row] = INFINITY;
   }
   if (!last_to_come(a.seq_ticket + s, a.K, &flag)) return;
 
-  // The request: candidate j of beam b is entry b * N + j, so equal scores go by beam and
+  // The request: candidate j of beam b has place b * N + j, so equal scores go by beam and
   // then by the beam's own order.  A beam without a finite score or lse has candidates of
   // score -infinity, its first tokens in order.
-  const int M = a.K * N;
   const int64_t r0 = static_cast<int64_t>(s) * a.K;
-  merge_top<double>(
-      M, N,
-      [&](int i, double* v, int* id) {
-        const int bb = i / N, j = i - bb * N;
+  auto row_key = [&](int i) {
+    return static_cast<uint64_t>(
+        __ldcg(reinterpret_cast<const unsigned long long*>(a.row_top + r0 * N + i)));
+  };
+  merge_top<ScoreKey>(
+      a.K * N, N,
+      [&](int i) {
+        const int bb = i / N;
         const double lse = __ldcg(a.row_lse + r0 + bb);
-        *id = i;
-        if (lse == INFINITY) {
-          *v = -INFINITY;
-          if (j >= V) *id = INT_MAX;
-          return;
-        }
-        if (__ldcg(a.row_tok + r0 * N + i) == INT_MAX) {
-          *v = -INFINITY;
-          *id = INT_MAX;
-          return;
-        }
-        *v = static_cast<double>(__ldg(a.beam_scores + r0 + bb)) +
-             (static_cast<double>(__ldcg(a.row_val + r0 * N + i)) - lse);
+        if (lse == INFINITY) return i - bb * N < V ? score_key(-INFINITY, i) : ScoreKey{};
+        const uint64_t k = row_key(i);
+        if (k == 0) return ScoreKey{};
+        const double x = key_logit(k);
+        return score_key(static_cast<double>(__ldg(a.beam_scores + r0 + bb)) + (x - lse), i);
       },
-      buf, N * ((M + kThreads - 1) / kThreads), sh,
-      [&](int rank, double val, int i) {
-        const int bb = i / N, j = i - bb * N;
+      reinterpret_cast<ScoreKey*>(buf), sh.seq,
+      [&](int rank, const ScoreKey& k) {
+        const int i = static_cast<int>(~k.at), bb = i / N;
         const int64_t at = static_cast<int64_t>(s) * N + rank;
-        a.scores[at] = static_cast<float>(val);
+        a.scores[at] = static_cast<float>(key_score(k));
         a.beams[at] = bb;
-        a.tokens[at] =
-            __ldcg(a.row_lse + r0 + bb) == INFINITY ? j : __ldcg(a.row_tok + r0 * N + i);
+        a.tokens[at] = __ldcg(a.row_lse + r0 + bb) == INFINITY ? i - bb * N : key_token(row_key(i));
       });
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct BeamLayout {
-  size_t row_ticket, seq_ticket, tickets_end, chunk_max, chunk_sum, chunk_val, chunk_tok, row_lse,
-      row_val, row_tok, total;
+  size_t row_ticket, seq_ticket, chunk_max, chunk_sum, chunk_top, row_lse, row_top, total;
 };
 
 // Chunks of E * kThreads elements that cover a row.
@@ -397,6 +413,7 @@ int elements_per_thread(int64_t rows, int32_t V, int32_t N, int sms) {
   return kLargeChunk;
 }
 
+// The tickets lie where they are whatever the sizes, so one workspace serves every call.
 BeamLayout beam_layout(int32_t S, int32_t K, int32_t N, int chunks) {
   BeamLayout L;
   const size_t rows = static_cast<size_t>(S) * K, slots = rows * chunks;
@@ -406,19 +423,17 @@ BeamLayout beam_layout(int32_t S, int32_t K, int32_t N, int chunks) {
     off += round256(bytes);
     return at;
   };
-  L.row_ticket = take(rows * 4);
-  L.seq_ticket = take(static_cast<size_t>(S) * 4);
-  L.tickets_end = off;
+  L.row_ticket = take(PKV_BEAM_TICKET_BYTES / 2);
+  L.seq_ticket = take(PKV_BEAM_TICKET_BYTES / 2);
   L.chunk_max = take(slots * 4);
   L.chunk_sum = take(slots * 8);
-  L.chunk_val = take(slots * N * 4);
-  L.chunk_tok = take(slots * N * 4);
+  L.chunk_top = take(slots * N * 8);
   L.row_lse = take(rows * 8);
-  L.row_val = take(rows * N * 4);
-  L.row_tok = take(rows * N * 4);
+  L.row_top = take(rows * N * 8);
   L.total = off;
   return L;
 }
+static_assert(PKV_BEAM_TICKET_BYTES / 2 >= (kMaxRows + 1) * 4, "a ticket for every row");
 
 int beam_sizes(int32_t S, int32_t K, int32_t V, int32_t N, int32_t dtype, int* elements,
                BeamLayout* L) {
@@ -430,8 +445,8 @@ int beam_sizes(int32_t S, int32_t K, int32_t V, int32_t N, int32_t dtype, int* e
               "num_beams %d above %d or num_out %d above %d", K, kMaxBeams, N, kMaxOut);
   PKV_REQUIRE(static_cast<int64_t>(N) <= static_cast<int64_t>(K) * V, PKV_ERR_INVALID_ARG,
               "num_out %d above num_beams * vocab", N);
-  PKV_REQUIRE(static_cast<int64_t>(S) * K <= 65535, PKV_ERR_UNSUPPORTED,
-              "num_seqs * num_beams above 65535");
+  PKV_REQUIRE(static_cast<int64_t>(S) * K <= kMaxRows, PKV_ERR_UNSUPPORTED,
+              "num_seqs * num_beams above %d", kMaxRows);
   PKV_REQUIRE(V <= INT_MAX - 65536 &&
                   static_cast<int64_t>(chunks_of(V, kLargeChunk)) * N <= kMaxEntries,
               PKV_ERR_UNSUPPORTED, "vocab %d with num_out %d: more than %d candidates of a row", V,
@@ -446,10 +461,15 @@ int beam_sizes(int32_t S, int32_t K, int32_t V, int32_t N, int32_t dtype, int* e
 
 template <typename T, int E>
 int launch_beam(const BeamArgs& a, int32_t S, cudaStream_t st) {
-  const int N = a.N;
-  auto entries = [&](int m) { return static_cast<size_t>(N) * ((m + kThreads - 1) / kThreads); };
-  size_t smem = static_cast<size_t>(N) * E * 8;  // a chunk's: value and token
-  const size_t rows = entries(a.chunks * N) * 8, seqs = entries(a.K * N) * 12;
+  // a list holds the entries of the N groups that reach a threshold, or all of a small set
+  auto listed = [&](int per_thread) {
+    const size_t n = static_cast<size_t>(a.N) * group_of(a.N) * per_thread;
+    return n < kThreads ? static_cast<size_t>(kThreads) : n;
+  };
+  auto per_thread = [](int m) { return (m + kThreads - 1) / kThreads; };
+  size_t smem = listed(E) * sizeof(uint64_t);
+  const size_t rows = listed(per_thread(a.chunks * a.N)) * sizeof(uint64_t);
+  const size_t seqs = listed(per_thread(a.K * a.N)) * sizeof(ScoreKey);
   smem = smem < rows ? rows : smem;
   smem = smem < seqs ? seqs : smem;
   PKV_CUDA(cudaFuncSetAttribute(beam_select_kernel<T, E>,
@@ -517,18 +537,14 @@ int pkv_beam_select(const void* logits, int64_t seq_stride, int64_t beam_stride,
   a.seq_ticket = reinterpret_cast<int32_t*>(ws + L.seq_ticket);
   a.chunk_max = reinterpret_cast<float*>(ws + L.chunk_max);
   a.chunk_sum = reinterpret_cast<double*>(ws + L.chunk_sum);
-  a.chunk_val = reinterpret_cast<float*>(ws + L.chunk_val);
-  a.chunk_tok = reinterpret_cast<int32_t*>(ws + L.chunk_tok);
+  a.chunk_top = reinterpret_cast<uint64_t*>(ws + L.chunk_top);
   a.row_lse = reinterpret_cast<double*>(ws + L.row_lse);
-  a.row_val = reinterpret_cast<float*>(ws + L.row_val);
-  a.row_tok = reinterpret_cast<int32_t*>(ws + L.row_tok);
+  a.row_top = reinterpret_cast<uint64_t*>(ws + L.row_top);
   a.K = num_beams;
   a.V = vocab;
   a.N = num_out;
   a.chunks = chunks_of(vocab, elements);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // the tickets start each call at zero, so no layout of an earlier call matters
-  PKV_CUDA(cudaMemsetAsync(ws, 0, L.tickets_end, st));
   rc = dtype == PKV_F32   ? launch_beam_as<float>(a, num_seqs, elements, st)
        : dtype == PKV_F16 ? launch_beam_as<__half>(a, num_seqs, elements, st)
                           : launch_beam_as<__nv_bfloat16>(a, num_seqs, elements, st);

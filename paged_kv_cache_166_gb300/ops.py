@@ -812,7 +812,8 @@ def paged_evict_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table
 
 
 def beam_workspace_bytes(num_seqs: int, num_beams: int, vocab: int, num_out: int, dtype) -> int:
-    """Workspace bytes of ``beam_select``."""
+    """Workspace bytes of ``beam_select``; the first PKV_BEAM_TICKET_BYTES of a workspace are
+    zero before its first use."""
     n = ctypes.c_size_t(0)
     N.check(N.lib().pkv_beam_workspace_size(num_seqs, num_beams, vocab, num_out, _DTYPES[dtype],
                                             ctypes.byref(n)))
@@ -846,7 +847,7 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.T
     code, n = dtype_code(logits), scores.shape[1]
     with _current(dev):
         need = beam_workspace_bytes(S, K, V, n, logits.dtype)
-        ws = _scratch(dev, need, 0, ("beam",)) if workspace is None else workspace
+        ws = _scratch(dev, need, N.PKV_BEAM_TICKET_BYTES, ("beam",)) if workspace is None else workspace
         if ws.device != dev or ws.numel() * ws.element_size() < need:
             raise ValueError(f"workspace smaller than the {need} bytes needed")
         N.check(N.lib().pkv_beam_select(

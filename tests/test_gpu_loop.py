@@ -115,10 +115,7 @@ def test_budgeted_decode_loop(dtype, tol):
         new_lens = i32(np.zeros(S))
         m.paged_evict_select(sums, i32(ctx), i32([budget] * S), kept, new_sums, new_lens,
                              first=first, recent=recent)
-        new = np.zeros((S, -(-budget // B)), dtype=np.int32)
-        for s in range(S):
-            ids = alloc.evict(seqs[s], budget)
-            new[s, :len(ids)] = ids
+        new = alloc.evict(seqs, [budget] * S, -(-budget // B))
         m.paged_evict_gather(kc, vc, i32(tables), kept, new_lens, i32(new))
         x, k = np64(sums), kept.cpu().numpy()
         for s in range(S):

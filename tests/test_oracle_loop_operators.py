@@ -174,14 +174,16 @@ def test_evict_and_reorder_bit_exact(seed):
             s = live.pop(r.integers(len(live)))
             c.free(s), o.free(s)
         elif op < 8:
-            s, n = live[r.integers(len(live))], int(r.integers(0, 4 * B))
+            seqs = [int(x) for x in r.permutation(live)[:int(r.integers(0, 4))]]
+            lens = [int(x) for x in r.integers(0, 4 * B, len(seqs))]
             try:
-                want = o.evict(s, n)
+                want = o.evict(seqs, lens)
             except OracleOOB:
                 with pytest.raises(N.OutOfBlocks):
-                    c.evict(s, n)
+                    c.evict(seqs, lens, 4)
             else:
-                assert c.evict(s, n) == want
+                got = c.evict(seqs, lens, 4)
+                assert got.tolist() == [t + [0] * (4 - len(t)) for t in want]
         else:
             seqs = [int(x) for x in r.permutation(live)[:int(r.integers(0, len(live) + 1))]]
             parents = [int(x) for x in r.integers(0, max(1, len(seqs)), len(seqs))]
@@ -197,15 +199,15 @@ def test_evict_and_reorder_refusals_leave_the_state():
     s, t = a.create(), a.create()
     a.append(s, 16)
     with pytest.raises(N.OutOfBlocks):
-        a.evict(s, 12)  # three fresh blocks beside the four held, two free
+        a.evict([s], [12], 3)  # three fresh blocks beside the four held, two free
     assert a.length(s) == 16 and a.num_free() == 2
-    with pytest.raises(N.PkvError):
-        a.evict(s, -1)
-    with pytest.raises(N.PkvError):
-        a.evict(99, 1)
-    n = ctypes.c_int32()
-    ids = (ctypes.c_int32 * 1)()
-    assert N.lib().pkv_seq_evict(a._h, s, 8, ids, 1, ctypes.byref(n)) == N.PKV_ERR_INVALID_ARG
+    for seqs, lens, mb in (([s], [-1], 4), ([99], [1], 4), ([s, s], [1, 1], 4), ([s], [8], 1)):
+        with pytest.raises(N.PkvError):
+            a.evict(seqs, lens, mb)
+    with pytest.raises(ValueError):
+        a.evict([s, t], [1], 4)
+    assert N.lib().pkv_seq_evict(a._h, None, 1, None, 1, None) == N.PKV_ERR_INVALID_ARG
+    assert a.evict([], [], 4).shape == (0, 4)
     for seqs, parents in (([s, s], [0, 0]), ([s, 7], [0, 0]), ([s, t], [0, 2]), ([s, t], [-1, 0])):
         with pytest.raises(N.PkvError):
             a.reorder(seqs, parents)
@@ -214,12 +216,24 @@ def test_evict_and_reorder_refusals_leave_the_state():
     assert a.length(s) == 16 and a.length(t) == 0 and a.num_free() == 2
     out = a.swap_out(s)
     with pytest.raises(N.PkvError):
-        a.evict(s, 4)
+        a.evict([s], [4], 4)
     with pytest.raises(N.PkvError):
         a.reorder([s], [0])
     assert len(out) == 4
     with pytest.raises(InvalidOperation):
         BlockManager(4, 4).reorder([0], [0])
+
+
+def test_evict_takes_every_new_block_before_it_gives_any_back():
+    """One gather moves all the rows: no new block is an old block of the list."""
+    a = pkv.BlockAllocator(12, 4)
+    seqs = [a.create() for _ in range(2)]
+    for s in seqs:
+        a.append(s, 16)
+    old = {b for s in seqs for b in a.table(s)}
+    new = a.evict(seqs, [8, 5], 2)
+    assert not old & set(new.ravel().tolist()) and len(set(new.ravel().tolist())) == 4
+    assert [a.length(s) for s in seqs] == [8, 5] and a.num_free() == 8
 
 
 # --- refusals of the device entry points (checked before anything is launched) -------
