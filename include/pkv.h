@@ -725,7 +725,7 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
  * The log-sum-exp and the scores are 64-bit, scores rounded to fp32 at the end; equal
  * rows of logits have equal log-sum-exps, wherever they lie.
  * Supported: num_beams <= 64, num_out <= min(128, num_beams * vocab), num_seqs *
- * num_beams <= 65535, ceil(vocab / 8192) * num_out <= 8192.
+ * num_beams <= 65535, vocab <= 2^31 - 8193.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  */
 #define PKV_BEAM_TICKET_BYTES (512u << 10)

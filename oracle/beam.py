@@ -20,8 +20,8 @@ def candidate_scores(logits, beam_scores) -> np.ndarray:
     for b in range(x.shape[0]):
         top = x[b].max()
         if np.isfinite(top) and np.isfinite(beam_scores[b]):
-            lse = top + np.log(np.exp(x[b] - top).sum())
-            out[b] = float(beam_scores[b]) + (x[b] - lse)
+            # not x - (top + log sum): a large top would swallow the log
+            out[b] = float(beam_scores[b]) + ((x[b] - top) - np.log(np.exp(x[b] - top).sum()))
     return out
 
 

@@ -52,5 +52,7 @@ def __getattr__(name):
                 "decode_status", "workspace_bytes", "default_num_warps", "get_workspace",
                 "wait_timeout_selftest"):
         from . import ops
-        return getattr(ops, name)
+        # found here from now on: a decode step's calls do not come through this function
+        value = globals()[name] = getattr(ops, name)
+        return value
     raise AttributeError(name)

@@ -54,6 +54,19 @@ int cuda_fail(cudaError_t e, const char* what) {
               cudaGetErrorString(e));
 }
 
+int allow_dynamic_smem(SmemOnce& once, const void* kernel, int bytes) {
+  int dev = 0;
+  PKV_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(PKV_ERR_UNSUPPORTED, "device ordinal %d", dev);
+  std::call_once(once.flags[dev], [&] {
+    once.results[dev] =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+  if (once.results[dev] != cudaSuccess)
+    return cuda_fail(once.results[dev], "cudaFuncSetAttribute");
+  return PKV_OK;
+}
+
 int device_sm_count(int* sms, int* device) {
   static std::once_flag flags[64];
   static int counts[64];

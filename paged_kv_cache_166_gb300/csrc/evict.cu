@@ -494,9 +494,10 @@ int launch_select(SelectArgs a, int64_t rows, cudaStream_t st) {
   const int slice = (a.cols + cluster - 1) / cluster;
   a.slots = slice <= 40960 ? slice : 0;
   const size_t smem = static_cast<size_t>(a.slots) * sizeof(float);
-  PKV_CUDA(cudaFuncSetAttribute(evict_select_long_kernel,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                40960 * static_cast<int>(sizeof(float))));
+  static SmemOnce once;
+  const int rc = allow_dynamic_smem(once, reinterpret_cast<const void*>(evict_select_long_kernel),
+                                    40960 * static_cast<int>(sizeof(float)));
+  if (rc != PKV_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
   cfg.blockDim = dim3(kLongThreads);

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "pkv.h"
 #include "status.h"
@@ -34,6 +35,14 @@ int cuda_fail(cudaError_t e, const char* what);
 // Layers one pkv_copy_blocks_layers launch takes (their cache pointers travel as
 // kernel parameters: 2 x 128 x 8 bytes).
 constexpr int kMaxCopyLayers = 128;
+
+// Raises a kernel's dynamic shared-memory limit, once per device; `once` belongs to the
+// kernel and `bytes` is the most it is ever launched with.
+struct SmemOnce {
+  std::once_flag flags[64];
+  cudaError_t results[64];
+};
+int allow_dynamic_smem(SmemOnce& once, const void* kernel, int bytes);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count(int* sms, int* device);

@@ -27,7 +27,9 @@ def dtype_code(t: torch.Tensor) -> int:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)  # the same, without a Stream object
 
 
 def _check_cuda(*ts) -> torch.device:
@@ -89,8 +91,7 @@ def get_workspace(device: torch.device, group: int, head_dim: int, num_warps: in
     """A zero-filled device workspace of ``nbytes`` for one layout (group size,
     head_dim, warp count, cache kind), cached per device and stream: one workspace
     must not serve two launches that may overlap, nor two layouts."""
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream, group, head_dim,
-           num_warps, kind)
+    key = (device.index, _stream(device), group, head_dim, num_warps, kind)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -513,14 +514,16 @@ def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor,
 # ---------------------------------------------------------------------------------
 # Operators of a decode loop around the attention: rotary positions, eviction, beams
 # ---------------------------------------------------------------------------------
+_HERE = contextlib.nullcontext()
+_SIZES: dict = {}   # workspace bytes by device and call
+
+
 def _current(dev: torch.device):
     """A context in which ``dev`` is the current device (the library launches there)."""
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _check_status(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
+def _status_ptr(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
     if status is None:
         return None
     if status.device != dev or status.dtype != torch.int32 or status.numel() < 1:
@@ -528,21 +531,19 @@ def _check_status(status: Optional[torch.Tensor], dev: torch.device) -> Optional
     return status.data_ptr()
 
 
-def _scratch(dev: torch.device, nbytes: int, zeroed: int, key: tuple) -> torch.Tensor:
-    """Workspace of ``nbytes`` whose first ``zeroed`` bytes start at zero: cached per device
-    and stream, or, while a graph is captured, the graph's own (two graphs, or a graph and
-    eager calls, never share one)."""
+def _scratch(dev: torch.device, nbytes: int, zeroed: int, *layout) -> torch.Tensor:
+    """Workspace of ``nbytes`` whose first ``zeroed`` bytes start at zero: cached per device,
+    stream and layout, or, while a graph is captured, the graph's own (two graphs, or a
+    graph and eager calls, never share one)."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        if zeroed:
-            ws[:zeroed].zero_()
+        ws[:zeroed].zero_()
         return ws
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream) + key
+    key = (dev.index, _stream(dev)) + layout
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        if zeroed:
-            ws[:zeroed].zero_()
+        ws[:zeroed].zero_()
         _WORKSPACES[key] = ws
     return ws
 
@@ -583,50 +584,55 @@ def rotary_table(max_positions: int, inv_freq: torch.Tensor, magnitude: float = 
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements from token to token of [T, H, D] whose heads are contiguous."""
     T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}'s heads must be contiguous [H, D] for every token")
-    return t.stride(0) if T > 1 else H * D
+    return st if T > 1 else H * D
+
+
+_ROTARY_WRITES = {"": "pkv_rotary_write", "fp8": "pkv_rotary_write_fp8",
+                  "int8": "pkv_rotary_write_int8"}
 
 
 def _rotary_write(kind, q, k, v, positions, table, slot_mapping, k_cache, v_cache, k_scale,
                   v_scale, q_out, interleaved, status):
-    kc, vc = _q8_caches(k_cache, v_cache, kind) if kind else (k_cache, v_cache)
-    dev = _check_cuda(positions, table, slot_mapping, kc, vc, *((k_scale, v_scale) if kind else ()))
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
-        if t.device != dev:
-            raise ValueError(f"{name} must be on the caches' device")
-        if t.dim() != 3:
-            raise ValueError("expected q, q_out [T, Hq, D] and k, v [T, Hkv, D]")
+    if kind:
+        kc, vc = _q8_caches(k_cache, v_cache, kind)
+        dev = _check_cuda(positions, table, slot_mapping, kc, vc, k_scale, v_scale)
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+    else:
+        kc, vc, scales = k_cache, v_cache, ()
+        dev = _check_cuda(positions, table, slot_mapping, kc, vc)
+    if not (q.device == k.device == v.device == q_out.device == dev):
+        raise ValueError("q, k, v and q_out must be on the caches' device")
+    if not (q.dim() == k.dim() == v.dim() == q_out.dim() == 3) or kc.dim() != 4 or vc.dim() != 4:
+        raise ValueError("expected q, q_out [T, Hq, D], k, v [T, Hkv, D] and 4-dimensional caches")
+    dt = q.dtype
+    if not (k.dtype == v.dtype == q_out.dtype == dt) or (not kind and not (
+            kc.dtype == vc.dtype == dt)):
+        raise TypeError("q, k, v, q_out" + ("" if kind else " and caches") + " must share a dtype")
     _check_index(positions, "positions")
     _check_index(slot_mapping, "slot_mapping")
     T, Hq, D = q.shape
-    if kc.dim() != 4 or vc.dim() != 4:
-        raise ValueError("caches must be [NB, Hkv, B, D]")
     NB, Hkv, B, D2 = kc.shape
-    if D2 != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or q_out.shape != q.shape \
+    rows = (T, Hkv, D)
+    if D2 != D or k.shape != rows or v.shape != rows or q_out.shape != (T, Hq, D) \
             or vc.shape != ((NB, Hkv, D, B) if kind else (NB, Hkv, B, D)):
         raise ValueError("shape mismatch between q, k, v, q_out and caches")
     if positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("positions and slot_mapping must be [T]")
     if table.dim() != 2 or table.dtype != torch.float32:
         raise ValueError("table must be float32 [max_positions, rotary_dim]")
-    if not (q.dtype == k.dtype == v.dtype == q_out.dtype) or (not kind and not (
-            kc.dtype == vc.dtype == q.dtype)):
-        raise TypeError("q, k, v, q_out" + ("" if kind else " and caches") + " must share a dtype")
     if kind:
         _check_scales(k_scale, v_scale, Hkv)
-    st = _check_status(status, dev)
-    L = N.lib()
-    fn = {"": L.pkv_rotary_write, "fp8": L.pkv_rotary_write_fp8,
-          "int8": L.pkv_rotary_write_int8}[kind]
-    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else ()
+    P, rot = table.shape
     with _current(dev):
-        N.check(fn(q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
-                   v.data_ptr(), _token_stride(v, "v"), positions.data_ptr(), table.data_ptr(),
-                   table.shape[0], table.shape[1], 1 if interleaved else 0,
-                   slot_mapping.data_ptr(), T, kc.data_ptr(), vc.data_ptr(), *scales, NB, Hq, Hkv,
-                   B, D, q_out.data_ptr(), _token_stride(q_out, "q_out"), st, dtype_code(q),
-                   _stream(dev)))
+        N.check(getattr(N.lib(), _ROTARY_WRITES[kind])(
+            q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
+            v.data_ptr(), _token_stride(v, "v"), positions.data_ptr(), table.data_ptr(), P, rot,
+            1 if interleaved else 0, slot_mapping.data_ptr(), T, kc.data_ptr(), vc.data_ptr(),
+            *scales, NB, Hq, Hkv, B, D, q_out.data_ptr(), _token_stride(q_out, "q_out"),
+            _status_ptr(status, dev), dtype_code(q), _stream(dev)))
     return q_out
 
 
@@ -679,6 +685,10 @@ def weights_workspace_bytes(num_seqs: int, max_blocks: int, block_size: int, num
     return n.value
 
 
+_WEIGHTS = {"": "pkv_decode_attention_weights", "fp8": "pkv_decode_attention_weights_fp8",
+            "int8": "pkv_decode_attention_weights_int8"}
+
+
 def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                     scale, out, weight_sums, workspace, num_warps):
     if kind:
@@ -693,24 +703,28 @@ def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, c
     if weight_sums.dtype != torch.float32 or weight_sums.dim() != 3 \
             or weight_sums.shape[:2] != (S, Hkv):
         raise ValueError(f"weight_sums must be float32 [{S}, {Hkv}, columns]")
-    code = dtype_code(q)
     scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else ()
-    L = N.lib()
-    fn = {"": L.pkv_decode_attention_weights, "fp8": L.pkv_decode_attention_weights_fp8,
-          "int8": L.pkv_decode_attention_weights_int8}[kind]
+    element = kind or q.dtype
     with _current(dev):
-        need = weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, kind or q.dtype, num_warps)
+        key = (dev.index, S, MAXB, B, Hq, Hkv, D, element, num_warps)
+        sizes = _SIZES.get(key)
+        if sizes is None:
+            sizes = _SIZES[key] = (weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, element,
+                                                           num_warps),
+                                   workspace_bytes(Hq, Hkv, D, element, num_warps))
+        need, head = sizes
         if workspace is None:
-            head = workspace_bytes(Hq, Hkv, D, kind or q.dtype, num_warps)
-            ws = _scratch(dev, need, head, (Hq // Hkv, D, num_warps, "weights" + kind))
+            ws = _scratch(dev, need, head, "weights" + kind, Hq // Hkv, D, num_warps)
+            have = ws.numel()
         else:
-            ws = workspace
-            if ws.device != dev or ws.numel() * ws.element_size() < need:
+            ws, have = workspace, workspace.numel() * workspace.element_size()
+            if ws.device != dev or have < need:
                 raise ValueError(f"workspace smaller than the {need} bytes needed")
-        N.check(fn(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), *scales, block_tables.data_ptr(),
-                   MAXB, context_lens.data_ptr(), S, Hq, Hkv, D, B, NB, float(scale),
-                   out.data_ptr(), weight_sums.data_ptr(), weight_sums.shape[2], ws.data_ptr(),
-                   ws.numel() * ws.element_size(), num_warps, code, _stream(dev)))
+        N.check(getattr(N.lib(), _WEIGHTS[kind])(
+            q.data_ptr(), kc.data_ptr(), vc.data_ptr(), *scales, block_tables.data_ptr(), MAXB,
+            context_lens.data_ptr(), S, Hq, Hkv, D, B, NB, float(scale), out.data_ptr(),
+            weight_sums.data_ptr(), weight_sums.shape[2], ws.data_ptr(), have, num_warps,
+            dtype_code(q), _stream(dev)))
     return out
 
 
@@ -773,7 +787,7 @@ def paged_evict_select(weight_sums: torch.Tensor, context_lens: torch.Tensor,
         if t.shape != (S,):
             raise ValueError(f"{name} must be [{S}]")
     _check_index(kept, "kept")
-    st = _check_status(status, dev)
+    st = _status_ptr(status, dev)
     with _current(dev):
         N.check(N.lib().pkv_evict_select(
             weight_sums.data_ptr(), weight_sums.shape[2], context_lens.data_ptr(),
@@ -803,7 +817,7 @@ def paged_evict_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table
     if block_tables.dim() != 2 or new_tables.dim() != 2 or kept.dim() != 3 \
             or block_tables.shape[0] != S or new_tables.shape[0] != S or kept.shape[:2] != (S, Hkv):
         raise ValueError("block_tables, new_tables [S, blocks], kept [S, Hkv, columns], new_lens [S]")
-    st = _check_status(status, dev)
+    st = _status_ptr(status, dev)
     with _current(dev):
         N.check(N.lib().pkv_evict_gather(
             kc.data_ptr(), vc.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
@@ -836,7 +850,8 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.T
     if scores.dim() != 2 or scores.shape[0] != S or beams.shape != scores.shape \
             or tokens.shape != scores.shape:
         raise ValueError("scores, beams and tokens must be [S, N]")
-    if V > 1 and logits.stride(2) != 1:
+    seq_stride, beam_stride, token_stride = logits.stride()
+    if V > 1 and token_stride != 1:
         raise ValueError("logits' vocabulary must be contiguous")
     if beam_scores.dtype != torch.float32 or scores.dtype != torch.float32:
         raise TypeError("beam_scores and scores must be float32")
@@ -846,11 +861,14 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.T
     _check_index(tokens, "tokens")
     code, n = dtype_code(logits), scores.shape[1]
     with _current(dev):
-        need = beam_workspace_bytes(S, K, V, n, logits.dtype)
-        ws = _scratch(dev, need, N.PKV_BEAM_TICKET_BYTES, ("beam",)) if workspace is None else workspace
+        key = (dev.index, S, K, V, n, code)
+        need = _SIZES.get(key)
+        if need is None:
+            need = _SIZES[key] = beam_workspace_bytes(S, K, V, n, logits.dtype)
+        ws = _scratch(dev, need, N.PKV_BEAM_TICKET_BYTES, "beam") if workspace is None else workspace
         if ws.device != dev or ws.numel() * ws.element_size() < need:
             raise ValueError(f"workspace smaller than the {need} bytes needed")
         N.check(N.lib().pkv_beam_select(
-            logits.data_ptr(), logits.stride(0) if S > 1 else 0, logits.stride(1) if K > 1 else 0,
+            logits.data_ptr(), seq_stride if S > 1 else 0, beam_stride if K > 1 else 0,
             beam_scores.data_ptr(), S, K, V, n, scores.data_ptr(), beams.data_ptr(),
             tokens.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), code, _stream(dev)))

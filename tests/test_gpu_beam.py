@@ -1,9 +1,10 @@
 """GPU parity of beam search's selection.
 
-Scores: lse is a sum of fp32 exponentials 2^(d log2 e) (the exponent's two roundings are
-2^-23 |d| log2 e, so 2^-19.4 of a term where it counts, |d| < 17; the function 2^-22), 32 of
-a thread's terms added in fp32 (on average half of 32 roundings a term), the rest in fp64:
-below 2^-18 relative, so 2^-18 absolute in the log; the score is rounded to fp32 once.  Beams
+Scores: lse is a sum of fp32 exponentials 2^(d log2 e) (the exponent's rounding is 2^-24 |d|
+log2 e, so 2^-20.4 of a term where it counts, |d| < 17; the function 2^-22), 16 of a thread's
+terms added in fp32 (16 roundings, 2^-20), rescaled when its maximum grows (2^-22 each), the
+rest carried or in fp64: below 2^-18 relative, so 2^-18 absolute in the log; the score is
+rounded to fp32 once.  Beams
 and tokens: equal to the oracle's where candidates of different beams lie further apart
 than that; within a beam the order is exact whatever the distance.
 """
@@ -76,7 +77,7 @@ def make(S, K, V, dtype, seed=0, scale=2.5, banned=0.02):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("S,K,V,N", [(1, 1, 1, 1), (1, 2, 3, 6), (2, 4, 100, 8), (3, 4, 2047, 8),
+@pytest.mark.parametrize("S,K,V,N", [(1, 1, 1, 1), (1, 2, 3, 6), (1, 1, 700001, 128), (3, 3, 4097, 5), (2, 4, 100, 8), (3, 4, 2047, 8),
                                      (1, 4, 2049, 4), (2, 3, 8191, 7), (5, 8, 8193, 16),
                                      (1, 64, 1000, 128), (2, 16, 32000, 32), (40, 2, 20011, 4),
                                      (1, 1, 200003, 1)])
@@ -147,6 +148,28 @@ def test_dead_beams_banned_tokens_and_strange_values():
         check(x, bs, N)
     for dt in (torch.float16, torch.bfloat16):
         check(x.to(dt), bs, 5)
+
+
+def test_logits_whose_maximum_grows_to_huge_values():
+    """A part's sums rescaled from tile to tile, across magnitudes that overflow times log2 e."""
+    V = 30000
+    x = torch.randn((4, 2, V), device="cuda")
+    x[3, 0] += 1048575.0  # steps of 1/16, around the border of the two ways
+    x[3, 1, 12000:] += 1048570.0
+    x[0, 0, 9000:] += 60
+    x[0, 0, 25000:] += 60
+    x[1, 0, :] = -3.3e38
+    x[1, 0, 12000:] = -1e30
+    x[1, 0, 24000:] = torch.randn(6000, device="cuda")
+    x[2, 0, 12000:] = 3e38
+    x[2, 0, 29999] = 3.2e38
+    bs = torch.zeros((4, 2), device="cuda")
+    check(x, bs, 8)
+    check(x.repeat(30, 4, 1), bs.repeat(30, 4), 8)
+    bs[:, 1] = -100.0  # other beams' candidates are far away: the order is exact
+    check(x, bs, 8)
+    many = x.repeat(30, 4, 1)  # enough rows for parts of several tiles
+    check(many, bs.repeat(30, 4) - 0.25 * torch.arange(8, device="cuda"), 8)
 
 
 def test_every_candidate():
@@ -270,7 +293,7 @@ def test_python_refusals():
     with pytest.raises(ValueError, match="beam_scores"):
         m.beam_select(x, three, three, i3, i3.clone())
     for S, K, V, N in ((1, 65, 100, 4), (1, 4, 100, 129), (1, 2, 3, 7), (2000, 40, 100, 4),
-                       (1, 1, 600000, 128)):
+                       (1, 1, (1 << 31) - 8192, 1)):
         with pytest.raises(m.PkvError):
             m.beam_workspace_bytes(S, K, V, N, torch.float32)
     empty = torch.empty((0, 3, 50), device="cuda")
