@@ -36,23 +36,27 @@ from .allocator import BlockAllocator, DecodeStepTables  # noqa: F401
 from ._native import OutOfBlocks, PkvError  # noqa: F401
 
 
+_OPS = frozenset((
+    "paged_kv_write", "paged_decode_attention", "paged_decode_step", "paged_copy_blocks",
+    "paged_copy_blocks_layers", "paged_kv_write_fp8", "paged_decode_attention_fp8",
+    "paged_decode_step_fp8", "paged_kv_write_int8", "paged_decode_attention_int8",
+    "paged_decode_step_int8", "paged_swap_out", "paged_swap_in", "paged_swap_out_layers",
+    "paged_swap_in_layers", "paged_prefill_attention", "rotary_frequencies", "rotary_table",
+    "paged_rotary_write", "paged_rotary_write_fp8", "paged_rotary_write_int8",
+    "paged_decode_attention_weights", "paged_decode_attention_weights_fp8",
+    "paged_decode_attention_weights_int8", "weights_workspace_bytes", "paged_evict_select",
+    "paged_evict_gather", "beam_select", "beam_workspace_bytes", "decode_status",
+    "workspace_bytes", "default_num_warps", "get_workspace", "wait_timeout_selftest"))
+_ops = None
+
+
 def __getattr__(name):
     # torch-facing ops are imported lazily so that host-only users (the block
     # manager, the workload generators) do not need torch's CUDA runtime.
-    if name in ("paged_kv_write", "paged_decode_attention", "paged_decode_step",
-                "paged_copy_blocks", "paged_copy_blocks_layers", "paged_kv_write_fp8", "paged_decode_attention_fp8",
-                "paged_decode_step_fp8", "paged_kv_write_int8", "paged_decode_attention_int8",
-                "paged_decode_step_int8", "paged_swap_out", "paged_swap_in", "paged_swap_out_layers", "paged_swap_in_layers",
-                "paged_prefill_attention",
-                "rotary_frequencies", "rotary_table", "paged_rotary_write",
-                "paged_rotary_write_fp8", "paged_rotary_write_int8",
-                "paged_decode_attention_weights", "paged_decode_attention_weights_fp8",
-                "paged_decode_attention_weights_int8", "weights_workspace_bytes",
-                "paged_evict_select", "paged_evict_gather", "beam_select", "beam_workspace_bytes",
-                "decode_status", "workspace_bytes", "default_num_warps", "get_workspace",
-                "wait_timeout_selftest"):
-        from . import ops
-        # found here from now on: a decode step's calls do not come through this function
-        value = globals()[name] = getattr(ops, name)
-        return value
+    global _ops
+    if name in _OPS:
+        if _ops is None:
+            from . import ops
+            _ops = ops
+        return getattr(_ops, name)
     raise AttributeError(name)
