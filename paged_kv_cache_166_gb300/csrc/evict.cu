@@ -11,9 +11,9 @@
 //
 // Select is exact: the m-th largest sum is found by its bits, and the tokens above it, plus
 // the lowest positions equal to it, are compacted with prefix counts.  A row of sums is read
-// from memory once.  A short row's keys stay in a warp's registers; a long row lies in the
-// shared memory of a cluster of CTAs, one slice each, whose histograms of the keys' digits
-// are added over distributed shared memory.  Gather is a copy, bound by memory.
+// from memory once: a short row's keys stay in a warp's registers, a long row's in those of
+// a cluster of CTAs, a slice each, whose histograms of the keys' digits are added over
+// distributed shared memory.  Gather is a copy, bound by memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kDigitBins = 2048;  // 11, 11 and 10 bits of a key
 constexpr int kPasses = 3;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8;    // eight threads add a bin's shares
 
 struct SelectArgs {
   const float* sums;
@@ -42,7 +42,6 @@ struct SelectArgs {
   int32_t* new_lens;
   int32_t* status;  // or NULL
   int32_t Hkv, cols, kept_cols, new_cols, first, recent;
-  int32_t slots;  // floats of a row slice that shared memory holds
 };
 
 // Unsigned key in the order of the values: larger sum, larger key.  NaN counts as
@@ -189,11 +188,18 @@ __global__ void __launch_bounds__(kShortWarps * 32)
   else select_short<kShortCols / 32>(w, lane);
 }
 
-// ---- long rows: a cluster each, the sums in shared memory -------------------------
+// ---- long rows: a cluster of CTAs each, the keys in registers ----------------------
 
-// Exclusive prefix sum of v over the block's threads.
-template <int kThreads>
-__device__ __forceinline__ int block_prefix(int v, int* warp_sums) {
+constexpr int kLongThreads = 512;
+constexpr int kLongKeys = 32;                           // keys of a thread
+constexpr int kRound = kLongThreads * kLongKeys;        // and of a CTA at once
+constexpr int kWarps = kLongThreads / 32;
+constexpr int kCoarse = 64;                             // sums of 32 bins each
+constexpr int kTailKeys = 4;
+constexpr int kTail = kLongThreads * kTailKeys;         // keys resolved without histograms
+
+// Exclusive prefix sum of v over the block's threads; the sum of all in *total.
+__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -204,54 +210,62 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums) {
   __syncthreads();  // warp_sums may still be read from the call before
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  int base = 0;
+  int base = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) base += i < w ? warp_sums[i] : 0;
+  for (int i = 0; i < kWarps; ++i) {
+    const int y = warp_sums[i];
+    base += i < w ? y : 0;
+    all += y;
+  }
+  *total = all;
   return base + x - v;
 }
 
-constexpr int kLongThreads = 512;
-constexpr int kLongSlice = 16384;  // sums of a CTA: 64 KB, so that two CTAs share an SM
-
-__global__ void __launch_bounds__(kLongThreads) evict_select_long_kernel(const SelectArgs a) {
-  constexpr int kWarps = kLongThreads / 32;
-  extern __shared__ float slice_s[];
+// The keys are looked at in the CTA's slice order: element i * kLongThreads + tid of a round
+// is thread tid's i-th key, so a warp's i-th keys are 32 consecutive elements, and word
+// i * kWarps + warp of a bit mask over the round holds their bits.
+__global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(const SelectArgs a) {
   __shared__ __align__(16) int hist[kPasses][kDigitBins];
+  __shared__ int coarse[kPasses][kCoarse];
+  __shared__ uint32_t tail[kTail];       // this CTA's keys in the threshold's bin
+  __shared__ uint32_t mask_gt[kLongThreads], mask_eq[kLongThreads];
   __shared__ int warp_sums[kWarps];
-  __shared__ int counts[2];  // this CTA's tokens above the threshold, and equal to it
-  __shared__ int warp_gt[kWarps], warp_eq[kWarps];
-  __shared__ uint32_t found_bin;
-  __shared__ int found_above;
+  __shared__ int bins[kCoarse];          // the cluster's sums of the bins looked at
+  __shared__ int tail_count;
+  __shared__ int found_bin, found_above, found_count;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Row w = row_of(a, blockIdx.x / C, rank == 0 && tid == 0);
 
-  // this CTA's slice of the candidates
+  // this CTA's slice of the candidates, in rounds of kRound
   const int per = (w.M + C - 1) / C;
   const int lo = w.f + min(w.M, rank * per), len = max(0, min(per, w.f + w.M - lo));
-  const float* vals = w.sums + lo;
-  if (len <= a.slots) {
-    constexpr int U = 8;  // loads in flight
-    for (int i0 = tid; i0 < len; i0 += U * kLongThreads) {
-      float x[U];
+  const int rounds = (per + kRound - 1) / kRound;
+  const float* const vals = w.sums + lo;
+  uint32_t key[kLongKeys];
+  auto load = [&](int round) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u * kLongThreads < len) x[u] = vals[i0 + u * kLongThreads];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u * kLongThreads < len) slice_s[i0 + u * kLongThreads] = x[u];
+    for (int i = 0; i < kLongKeys; ++i) {
+      const int p = round * kRound + i * kLongThreads + tid;
+      key[i] = p < len ? __float_as_uint(__ldg(vals + p)) : 0u;
     }
-    vals = slice_s;
-  }
+#pragma unroll
+    for (int i = 0; i < kLongKeys; ++i) {
+      const int p = round * kRound + i * kLongThreads + tid;
+      key[i] = p < len ? key_of(__uint_as_float(key[i])) : 0u;  // 0: no token
+    }
+  };
+  if (rounds == 1) load(0);  // the usual row: read once
   for (int i = tid; i < kPasses * kDigitBins; i += kLongThreads) (&hist[0][0])[i] = 0;
-  if (tid < 2) counts[tid] = 0;
+  if (tid == 0) tail_count = 0;
   keep_ends(w, rank * kLongThreads + tid, C * kLongThreads);
   __syncthreads();
 
-  // The threshold: the m-th largest key, digit by digit; `above` keys are larger.
-  uint32_t prefix = 0;
+  // The threshold t: the m-th largest key; `above` keys are larger.  m == M: everything is
+  // above 0.
+  uint32_t t = 0;
   int above = 0;
   if (w.m > 0 && w.m < w.M) {
     int shift = 32;
@@ -259,92 +273,178 @@ __global__ void __launch_bounds__(kLongThreads) evict_select_long_kernel(const S
       const int bits = pass < 2 ? 11 : 10;
       const uint32_t fixed = shift == 32 ? 0u : ~0u << shift;
       shift -= bits;
-#pragma unroll 4
-      for (int i = tid; i < len; i += kLongThreads) {
-        const uint32_t k = key_of(vals[i]);
-        if ((k & fixed) == prefix) atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
+      for (int round = 0; round < rounds; ++round) {
+        if (rounds > 1) load(round);
+#pragma unroll
+        for (int i = 0; i < kLongKeys; ++i)
+          if (key[i] != 0 && (key[i] & fixed) == t)
+            atomicAdd(&hist[pass][(key[i] >> shift) & ((1u << bits) - 1)], 1);
+      }
+      __syncthreads();
+      {
+        const int4 h = *reinterpret_cast<const int4*>(&hist[pass][4 * tid]);
+        int n = h.x + h.y + h.z + h.w;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if ((tid & 7) == 0) coarse[pass][tid >> 3] = n;
       }
       cluster.sync();
-      // bins from the top: thread t holds those from (kLongThreads - 1 - t) * 4 on
-      static_assert(kDigitBins == 4 * kLongThreads, "four bins a thread");
-      const int b0 = (kLongThreads - 1 - tid) * 4;
-      int4 part[kMaxCluster];
+      // the cluster's sums of 64 runs of 32 bins, then of the bins of the run that counts:
+      // eight threads a sum, a CTA's share each
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q)
-        if (q < C)
-          part[q] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&hist[pass][b0], q));
-      int n[4] = {0, 0, 0, 0};
+      for (int level = 0; level < 2; ++level) {
+        const int width = level == 0 ? kCoarse : 32, first = level == 0 ? 0 : 32 * found_bin;
+        const int q = tid & 7, at = tid >> 3;
+        int n = 0;
+        if (q < C && at < width)
+          n = *cluster.map_shared_rank(level == 0 ? &coarse[pass][at] : &hist[pass][first + at], q);
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {
-        if (q < C) {
-          n[0] += part[q].x;
-          n[1] += part[q].y;
-          n[2] += part[q].z;
-          n[3] += part[q].w;
+        for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (q == 0) bins[at] = at < width ? n : 0;
+        __syncthreads();
+        if (warp == 0) {  // from the top: lane l holds bins 63 - 2 l and 62 - 2 l
+          const int hi = bins[kCoarse - 1 - 2 * lane], lw = bins[kCoarse - 2 - 2 * lane];
+          int x = hi + lw;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          const int before = above + x - hi - lw;  // keys in the bins above this lane's
+          __syncwarp();
+          if (before < w.m && before + hi >= w.m) {
+            found_bin = first + kCoarse - 1 - 2 * lane;
+            found_above = before;
+            found_count = hi;
+          } else if (before + hi < w.m && before + hi + lw >= w.m) {
+            found_bin = first + kCoarse - 2 - 2 * lane;
+            found_above = before + hi;
+            found_count = lw;
+          }
+        }
+        __syncthreads();
+        above = found_above;
+      }
+      t |= static_cast<uint32_t>(found_bin) << shift;
+      const int left = found_count;  // keys in the bin
+      if (shift == 0) break;
+      if (left > kTail) {
+        __syncthreads();  // found_* may be written again
+        continue;
+      }
+      // Few keys in the bin: every CTA takes them all and finds the rest of the threshold's
+      // bits by counting, from the highest; done early once the count is the number wanted.
+      const uint32_t prefix = ~0u << shift;
+      for (int round = 0; round < rounds; ++round) {
+        if (rounds > 1) load(round);
+#pragma unroll
+        for (int i = 0; i < kLongKeys; ++i)
+          if (key[i] != 0 && (key[i] & prefix) == t) tail[atomicAdd(&tail_count, 1)] = key[i];
+      }
+      cluster.sync();
+      uint32_t k[kTailKeys] = {};
+      int begin = 0;
+      for (int q = 0; q < C; ++q) {
+        const int n = *cluster.map_shared_rank(&tail_count, q);
+        const uint32_t* const from = cluster.map_shared_rank(&tail[0], q);
+#pragma unroll
+        for (int i = 0; i < kTailKeys; ++i) {
+          const int at = i * kLongThreads + tid - begin;
+          if (at >= 0 && at < n) k[i] = from[at];
+        }
+        begin += n;
+      }
+      const int want = w.m - above;
+      int have = left;
+      for (int bit = shift - 1; bit >= 0 && have != want; --bit) {
+        const uint32_t u = t | (1u << bit);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kTailKeys; ++i)
+          if (i * kLongThreads < left) n += __syncthreads_count(k[i] >= u);
+        if (n >= want) {
+          t = u;
+          have = n;
         }
       }
-      int before = above + block_prefix<kLongThreads>(n[0] + n[1] + n[2] + n[3], warp_sums);
+      if (have == want) {
+        t -= 1;  // all keys of at least t stay: those above t - 1, and none equal to it
+        above = w.m;
+      } else {
+        int n = 0;
 #pragma unroll
-      for (int i = 3; i >= 0; --i) {
-        if (before < w.m && before + n[i] >= w.m) {
-          found_bin = static_cast<uint32_t>(b0 + i);
-          found_above = before;
-        }
-        before += n[i];
+        for (int i = 0; i < kTailKeys; ++i)
+          if (i * kLongThreads < left) n += __syncthreads_count(k[i] > t);
+        above += n;
       }
-      __syncthreads();
-      prefix |= found_bin << shift;
-      above = found_above;
-      __syncthreads();
+      break;
     }
   }
-  // m == M: everything is above a threshold of 0 (no key is 0); m == 0: nothing stays
-  const bool all = w.m == w.M;
-  const uint32_t t = all ? 0u : prefix;
-  const int ties = all ? 0 : w.m - above;
+  const int ties = w.m == w.M ? 0 : w.m - above;  // keys equal to t that stay
 
-  // Compaction, ascending: warps take consecutive parts of the slice.
-  const int part = ((len + kWarps - 1) / kWarps + 31) & ~31;
-  const int p0 = min(len, warp * part), p1 = min(len, p0 + part);
-  int gt = 0, eq = 0;
-  if (w.m > 0) {
-#pragma unroll 4
-    for (int i = p0 + lane; i < p1; i += 32) {
-      const uint32_t k = key_of(vals[i]);
-      gt += k > t;
-      eq += k == t;
+  // Bit masks of a round's keys above t, and equal to it if some of those stay.
+  auto masks = [&] {
+    uint32_t g = 0, e = 0;  // lane i keeps the words of the warp's i-th keys
+#pragma unroll
+    for (int i = 0; i < kLongKeys; ++i) {
+      const uint32_t x = __ballot_sync(0xffffffffu, key[i] > t);
+      const uint32_t y = __ballot_sync(0xffffffffu, ties > 0 && key[i] == t);
+      g = lane == i ? x : g;
+      e = lane == i ? y : e;
     }
-  }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) {
-    warp_gt[warp] = gt;
-    warp_eq[warp] = eq;
-    atomicAdd(&counts[0], gt);
-    atomicAdd(&counts[1], eq);
+    mask_gt[lane * kWarps + warp] = g;
+    mask_eq[lane * kWarps + warp] = e;
+    __syncthreads();
+  };
+  // How many of each the CTAs before have.
+  int gt0 = 0, eq0 = 0;
+  if (w.m > 0) {
+    int total_gt = 0, total_eq = 0;
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) load(round);
+      masks();
+      total_gt += __popc(mask_gt[tid]);
+      total_eq += __popc(mask_eq[tid]);
+      if (rounds > 1) __syncthreads();
+    }
+    int all_gt, all_eq;
+    block_prefix(total_gt, warp_sums, &all_gt);
+    block_prefix(total_eq, warp_sums, &all_eq);
+    if (tid == 0) {
+      coarse[0][0] = all_gt;
+      coarse[0][1] = all_eq;
+    }
   }
   cluster.sync();
   if (w.m > 0) {
-    int gt0 = 0, eq0 = 0;
     for (int q = 0; q < rank; ++q) {
-      const int* cq = cluster.map_shared_rank(&counts[0], q);
-      gt0 += cq[0];
-      eq0 += cq[1];
+      const int* const c = cluster.map_shared_rank(&coarse[0][0], q);
+      gt0 += c[0];
+      eq0 += c[1];
     }
-    for (int i = 0; i < warp; ++i) {
-      gt0 += warp_gt[i];
-      eq0 += warp_eq[i];
-    }
-#pragma unroll 4
-    for (int i0 = p0; i0 < p1; i0 += 32) {
-      const int i = i0 + lane;
-      const float x = i < p1 ? vals[i] : 0.f;
-      const uint32_t k = key_of(x);
-      const int at = place_of(i < p1 && k > t, i < p1 && k == t, ties, lane, gt0, eq0);
-      if (at >= 0) {
-        w.kept[w.f + at] = lo + i;
-        w.out[w.f + at] = x;
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) {
+        load(round);
+        masks();
       }
+      // a thread places the tokens of one word
+      const uint32_t g = mask_gt[tid], e = mask_eq[tid];
+      int all_gt, all_eq = 0;
+      const int ng0 = gt0 + block_prefix(__popc(g), warp_sums, &all_gt);
+      const int ne0 = eq0 + (ties > 0 ? block_prefix(__popc(e), warp_sums, &all_eq) : 0);
+      for (uint32_t left = g | e; left != 0; left &= left - 1) {
+        const uint32_t bit = left & (0u - left);
+        const int ng = ng0 + __popc(g & (bit - 1)), ne = ne0 + __popc(e & (bit - 1));
+        if ((g & bit) || ne < ties) {
+          const int p = round * kRound + 32 * tid + __ffs(bit) - 1;
+          const int j = w.f + ng + min(ne, ties);
+          w.kept[j] = lo + p;
+          w.out[j] = vals[p];
+        }
+      }
+      gt0 += all_gt;
+      eq0 += all_eq;
+      if (rounds > 1) __syncthreads();
     }
   }
   cluster.sync();  // no CTA leaves while others read its counts
@@ -479,10 +579,9 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_v8_kernel(const G
   }
 }
 
-// Short rows take a warp each.  Long ones: a slice of at most 16,384 sums (64 KB, so that
-// two CTAs share an SM) a CTA, up to eight CTAs; larger slices up to 160 KB, and what does
-// not fit then is read from memory once a pass.
-int launch_select(SelectArgs a, int64_t rows, cudaStream_t st) {
+// Short rows take a warp each.  Long ones: as many CTAs, up to eight, as hold the row in
+// registers, 16,384 keys each; a longer row is read from memory once a pass.
+int launch_select(const SelectArgs& a, int64_t rows, cudaStream_t st) {
   if (a.cols <= kShortCols) {
     const int64_t ctas = (rows + kShortWarps - 1) / kShortWarps;
     evict_select_short_kernel<<<static_cast<unsigned>(ctas), kShortWarps * 32, 0, st>>>(a, rows);
@@ -490,18 +589,10 @@ int launch_select(SelectArgs a, int64_t rows, cudaStream_t st) {
     return PKV_OK;
   }
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kLongSlice < a.cols) cluster *= 2;
-  const int slice = (a.cols + cluster - 1) / cluster;
-  a.slots = slice <= 40960 ? slice : 0;
-  const size_t smem = static_cast<size_t>(a.slots) * sizeof(float);
-  static SmemOnce once;
-  const int rc = allow_dynamic_smem(once, reinterpret_cast<const void*>(evict_select_long_kernel),
-                                    40960 * static_cast<int>(sizeof(float)));
-  if (rc != PKV_OK) return rc;
+  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kRound < a.cols) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
   cfg.blockDim = dim3(kLongThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
