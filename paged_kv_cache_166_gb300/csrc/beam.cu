@@ -351,26 +351,6 @@ struct ExpSum {
   static constexpr float kLag = 16.f;
   float base = -INFINITY, ref = 0.f, sum = 0.f, carry = 0.f;
 
-  // Pairs of fp32 values, operated on at once.
-  static __device__ __forceinline__ uint64_t pair(float x, float y) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-  }
-  static __device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-  }
-  static __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-  }
-  static __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-  }
-
   static __device__ __forceinline__ bool huge(float x) { return fabsf(x) > kHuge; }
   // What a sum's unit is short of 2^(x log2 e), as an exponent: exact.
   static __device__ __forceinline__ float lost(float x, float r) {
@@ -390,16 +370,16 @@ struct ExpSum {
     if (base > -INFINITY) {
       if (!huge(base)) {
         // two terms at a time
-        const uint64_t l = pair(kLog2e, kLog2e), r = pair(-ref, -ref);
-        uint64_t sums = pair(0.f, 0.f);
+        const uint64_t l = ptx::pair(kLog2e, kLog2e), r = ptx::pair(-ref, -ref);
+        uint64_t sums = ptx::pair(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kElements; i += 2) {
           float x, y;
-          unpair(fma2(pair(v[i], v[i + 1]), l, r), x, y);
-          sums = add2(sums, pair(ptx::ex2(x), ptx::ex2(y)));
+          ptx::unpair(ptx::fma2(ptx::pair(v[i], v[i + 1]), l, r), x, y);
+          sums = ptx::add2(sums, ptx::pair(ptx::ex2(x), ptx::ex2(y)));
         }
         float x, y;
-        unpair(sums, x, y);
+        ptx::unpair(sums, x, y);
         part = x + y;
       }
       if (huge(base) || part != part) {  // or a NaN among them: a banned token

@@ -65,59 +65,95 @@ __device__ __forceinline__ float widen(T x) {
   else return ptx::to_float(x);
 }
 
-// Codes of N consecutive elements (kCodes 1: E4M3, 2: int8).
-template <int kCodes, int N>
-__device__ __forceinline__ Pack<uint8_t, N> codes_of(const float (&x)[N], float scale) {
-  Pack<uint8_t, N> c;
+// N consecutive values, each rounded once to T.
+template <typename T, int N>
+__device__ __forceinline__ void store_as(T* dst, const float (&y)[N]) {
+  if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+    Pack<uint32_t, N / 2> o;
 #pragma unroll
-  for (int i = 0; i < N; ++i) c.x[i] = kCodes == 1 ? e4m3_code(x[i], scale) : int8_code(x[i], scale);
-  return c;
+    for (int i = 0; i < N; i += 2) o.x[i / 2] = ptx::pack2<T>(y[i], y[i + 1]);
+    *reinterpret_cast<Pack<uint32_t, N / 2>*>(dst) = o;
+  } else {
+    Pack<T, N> o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o.x[i] = ptx::from_float<T>(y[i]);
+    *reinterpret_cast<Pack<T, N>*>(dst) = o;
+  }
 }
 
-// Turns U heads' pieces at once (loads first), heads h = h0, h0 + step, ... < H of src
-// [H, D]; put(h, first, y1, y2, x1): the turned pieces, x1 the unturned first one.
+// Codes of two elements (kCodes 1: E4M3, 2: int8), the first in the low byte.
+template <int kCodes>
+__device__ __forceinline__ uint32_t codes_of(float x, float y, const Quotients& by) {
+  if constexpr (kCodes == 1) return e4m3_codes(by(x), by(y));
+  return (static_cast<uint32_t>(int8_code_of(by(x))) & 0xffu) |
+         (static_cast<uint32_t>(int8_code_of(by(y))) & 0xffu) << 8;
+}
+
+// Codes of N consecutive elements, to dst.
+template <int kCodes, int N>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], const Quotients& by) {
+  if constexpr (N == 1) {
+    *dst = static_cast<uint8_t>(codes_of<kCodes>(x[0], x[0], by));
+  } else {
+    Pack<uint16_t, N / 2> c;
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      c.x[i / 2] = static_cast<uint16_t>(codes_of<kCodes>(x[i], x[i + 1], by));
+    *reinterpret_cast<Pack<uint16_t, N / 2>*>(dst) = c;
+  }
+}
+
+// The turned pieces: y1 = x1 c - x2 s, y2 = x2 c + x1 s (half layout: x1 and x2 are a piece
+// of either half; interleaved: elements 2i and 2i + 1 of x1), two pairs at a time.
+template <typename T, int VEC, bool kInter>
+__device__ __forceinline__ void turn(const Pack<T, VEC>& x1, const Pack<T, VEC>& x2,
+                                     const float (&c)[kInter ? VEC / 2 : VEC],
+                                     const float (&s)[kInter ? VEC / 2 : VEC], float (&y1)[VEC],
+                                     float (&y2)[VEC]) {
+  constexpr int kAng = kInter ? VEC / 2 : VEC;
+  auto a = [&](int i) { return widen(kInter ? x1.x[2 * i] : x1.x[i]); };
+  auto b = [&](int i) { return widen(kInter ? x1.x[2 * i + 1] : x2.x[i]); };
+  auto first = [&](int i) -> float& { return kInter ? y1[2 * i] : y1[i]; };
+  auto second = [&](int i) -> float& { return kInter ? y1[2 * i + 1] : y2[i]; };
+  if constexpr (kAng % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < kAng; i += 2) {
+      const uint64_t p = ptx::pair(a(i), a(i + 1)), r = ptx::pair(b(i), b(i + 1));
+      const uint64_t co = ptx::pair(c[i], c[i + 1]), si = ptx::pair(s[i], s[i + 1]);
+      const uint64_t ns = ptx::pair(-s[i], -s[i + 1]);
+      ptx::unpair(ptx::add2(ptx::mul2(p, co), ptx::mul2(r, ns)), first(i), first(i + 1));
+      ptx::unpair(ptx::add2(ptx::mul2(r, co), ptx::mul2(p, si)), second(i), second(i + 1));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kAng; ++i) {
+      const float p = a(i), r = b(i);
+      first(i) = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
+      second(i) = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
+    }
+  }
+}
+
+// A thread's pieces of heads h0, h0 + step, ... < H of src [H, D], a few heads' loads ahead
+// of put(h, x1, x2); two: there is a second piece, `half` elements on.
 template <typename T, int VEC, bool kInter, typename Put>
-__device__ __forceinline__ void turn_heads(const T* src, int H, int D, int h0, int step, int half,
-                                           bool turns,
-                                           const float (&c)[kInter ? VEC / 2 : VEC],
-                                           const float (&s)[kInter ? VEC / 2 : VEC], Put put) {
+__device__ __forceinline__ void each_head(const T* src, int H, int D, int h0, int step, int half,
+                                          bool two, Put put) {
   using P = Pack<T, VEC>;
-  constexpr int U = 4;
+  constexpr int U = kInter ? 4 : 2;
   for (int h = h0; h < H; h += U * step) {
     P x1[U], x2[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (h + u * step < H) {
-        const T* const at = src + static_cast<int64_t>(h + u * step) * D;
+        const T* const at = src + (h + u * step) * D;
         x1[u] = *reinterpret_cast<const P*>(at);
-        if (!kInter && turns) x2[u] = *reinterpret_cast<const P*>(at + half);
+        if (!kInter && two) x2[u] = *reinterpret_cast<const P*>(at + half);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (h + u * step < H) {
-        float y1[VEC], y2[VEC];
-        if (!turns) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) y1[i] = y2[i] = widen(x1[u].x[i]);
-        } else if constexpr (kInter) {
-#pragma unroll
-          for (int i = 0; i < VEC / 2; ++i) {
-            const float p = widen(x1[u].x[2 * i]), r = widen(x1[u].x[2 * i + 1]);
-            y1[2 * i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
-            y1[2 * i + 1] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float p = widen(x1[u].x[i]), r = widen(x2[u].x[i]);
-            y1[i] = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
-            y2[i] = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
-          }
-        }
-        put(h + u * step, y1, y2, x1[u]);
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      if (h + u * step < H) put(h + u * step, x1[u], x2[u]);
   }
 }
 
@@ -130,7 +166,7 @@ template <typename T, bool kPairs, int kCodes>
 __device__ __forceinline__ void write_v8(const RotaryArgs& a, int window, int part, int parts) {
   __shared__ int slot_s[48];  // tokens 16 (w - 1) .. 16 (w + 2) - 1; -1: nothing to write
   __shared__ int run_first[16], run_len[16], run_count;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
   const int64_t t0 = static_cast<int64_t>(window) * 16 - 16;
   if (tid < 48) {
     int slot = -1;
@@ -140,90 +176,82 @@ __device__ __forceinline__ void write_v8(const RotaryArgs& a, int window, int pa
   }
   __syncthreads();
   if (tid < 32) {
-    // token i goes on its predecessor's run
-    auto goes_on = [&](int i) {
-      return slot_s[i] > 0 && slot_s[i] % 16 != 0 && slot_s[i - 1] == slot_s[i] - 1;
-    };
-    const int i = 16 + tid;
-    const bool begins = tid < 16 && slot_s[i] >= 0 && !goes_on(i);
+    const int i = 16 + tid, slot = slot_s[i];
+    // a token that goes on its predecessor's run
+    const bool goes_on = slot > 0 && slot % 16 != 0 && slot_s[i - 1] == slot - 1;
+    const bool begins = tid < 16 && slot >= 0 && !goes_on;
+    const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
     const uint32_t all = __ballot_sync(0xffffffffu, begins);
-    if (begins) {
-      int n = 1;
-      while (i + n < 48 && goes_on(i + n)) ++n;  // at most 16: a run ends with its block
+    if (begins) {  // at most 16 tokens, so in the 32 looked at: a run ends with its block
       const int at = __popc(all & ((1u << tid) - 1));
       run_first[at] = i;
-      run_len[at] = n;
+      run_len[at] = __ffs(~(on >> (tid + 1)));
     }
     if (tid == 0) run_count = __popc(all);
   }
   __syncthreads();
   const int pairs = a.D / 2, per_run = a.Hkv * pairs;
   const int items = run_count * per_run;
-  for (int it = part * blockDim.x + tid; it < items; it += parts * blockDim.x) {
+  for (int it = part * threads + tid; it < items; it += parts * threads) {
     const int run = it / per_run, g = (it - run * per_run) / pairs;
     const int d = 2 * (it - run * per_run - g * pairs);
     const int first = run_first[run], n = run_len[run], slot = slot_s[first];
     const int off = slot % 16;
-    const float scale = __ldg(a.vs + g);
+    const Quotients by = quotients_by(__ldg(a.vs + g));
     const T* const src = static_cast<const T*>(a.v) + (t0 + first - off) * a.v_stride +
                          static_cast<int64_t>(g) * a.D + d;  // row of the block's token 0
-    T lo[16], hi[16];
+    // two elements a token, packed as they are loaded
+    Pack<T, 2> x[16];
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
-      lo[t] = hi[t] = ptx::from_float<T>(0.f);
+      x[t].x[0] = x[t].x[1] = ptx::from_float<T>(0.f);
       if (t >= off && t < off + n) {
         const T* const at = src + t * a.v_stride;
         if constexpr (kPairs) {
-          const Pack<T, 2> x = *reinterpret_cast<const Pack<T, 2>*>(at);
-          lo[t] = x.x[0];
-          hi[t] = x.x[1];
+          x[t] = *reinterpret_cast<const Pack<T, 2>*>(at);
         } else {
-          lo[t] = at[0];
-          hi[t] = at[1];
+          x[t].x[0] = at[0];
+          x[t].x[1] = at[1];
         }
       }
     }
+    // word j of a row: tokens 2j, 2j + 1, 2j + 8 and 2j + 9
+    uint32_t w[2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        w[r][j] = codes_of<kCodes>(widen(x[2 * j].x[r]), widen(x[2 * j + 1].x[r]), by) |
+                  codes_of<kCodes>(widen(x[2 * j + 8].x[r]), widen(x[2 * j + 9].x[r]), by) << 16;
+    }
     uint8_t* const dst = static_cast<uint8_t*>(a.vc) +
                          ((static_cast<int64_t>(slot / 16) * a.Hkv + g) * a.D + d) * 16;
-    Pack<uint8_t, 16> w0, w1;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const float x[2] = {widen(lo[t]), widen(hi[t])};
-      const Pack<uint8_t, 2> c = codes_of<kCodes, 2>(x, scale);
-      w0.x[fp8_v_pos(t)] = c.x[0];
-      w1.x[fp8_v_pos(t)] = c.x[1];
-    }
-    if (n == 16) {
-      reinterpret_cast<Pack<uint8_t, 16>*>(dst)[0] = w0;
-      reinterpret_cast<Pack<uint8_t, 16>*>(dst)[1] = w1;
-    } else {
-      // tokens 2i and 2i + 1 lie side by side
+    for (int r = 0; r < 2; ++r) {
+      uint8_t* const to = dst + 16 * r;
+      if (n == 16) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
+        continue;
+      }
 #pragma unroll
-      for (int t = 0; t < 16; t += 2) {
-        const bool x = t >= off && t < off + n, y = t + 1 >= off && t + 1 < off + n;
-        const int at = fp8_v_pos(t);
-        if (x && y) {
-          *reinterpret_cast<Pack<uint8_t, 2>*>(dst + at) = Pack<uint8_t, 2>{{w0.x[at], w0.x[at + 1]}};
-          *reinterpret_cast<Pack<uint8_t, 2>*>(dst + 16 + at) =
-              Pack<uint8_t, 2>{{w1.x[at], w1.x[at + 1]}};
-        } else if (x) {
-          dst[at] = w0.x[at];
-          dst[16 + at] = w1.x[at];
-        } else if (y) {
-          dst[at + 1] = w0.x[at + 1];
-          dst[17 + at] = w1.x[at + 1];
-        }
+      for (int p = 0; p < 8; ++p) {  // byte pairs: tokens t and t + 1
+        const int t = p % 2 == 0 ? p : p + 7;
+        const uint32_t c = w[r][p / 2] >> (16 * (p % 2));
+        const bool one = t >= off && t < off + n, two = t + 1 >= off && t + 1 < off + n;
+        if (one && two) *reinterpret_cast<uint16_t*>(to + 2 * p) = static_cast<uint16_t>(c);
+        else if (one) to[2 * p] = static_cast<uint8_t>(c);
+        else if (two) to[2 * p + 1] = static_cast<uint8_t>(c >> 8);
       }
     }
   }
 }
 
-// One CTA per token (blockIdx.x < T), its heads split over gridDim.y CTAs; 8-bit caches:
-// then those of V's windows, a.v_parts each.  VEC: elements a thread moves at once (16
+// One CTA per token (blockIdx.x < T), its heads split over gridDim.y CTAs and the CTA's rows of
+// threads; 8-bit caches: then those of V's windows, a.v_parts each.  VEC: elements a thread moves at once (16
 // bytes where rotary_dim, the strides and the addresses allow it, else the smallest piece
 // that holds whole pairs).
 template <typename T, int VEC, bool kInter, int kCodes>
-__global__ void __launch_bounds__(256) rotary_write_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(256, kCodes != 0 ? 4 : 3) rotary_write_kernel(const RotaryArgs a) {
   // a decode launch queued behind may start its prologue; it reads the caches and
   // q_out only after this grid has completed
   asm volatile("griddepcontrol.launch_dependents;");
@@ -241,95 +269,79 @@ __global__ void __launch_bounds__(256) rotary_write_kernel(const RotaryArgs a) {
     }
   }
   const int half = a.rot >> 1;
-  const int nturn = kInter ? a.rot / VEC : half / VEC;      // turning units of a row
-  const int units = nturn + (a.D - a.rot) / VEC;            // and passing ones
-  const int rows = blockDim.x / units;                      // rows in flight in the CTA
-  const int u = threadIdx.x % units, r0 = threadIdx.x / units;
+  const int nturn = kInter ? a.rot / VEC : half / VEC;  // turning units of a row, then passing ones
+  const int u = threadIdx.x;
 
   const int32_t slot = __ldg(a.slots + t);
   const bool write = slot >= 0 && static_cast<int64_t>(slot) < static_cast<int64_t>(a.NB) * a.B;
   int32_t pos = __ldg(a.positions + t);
   if (pos < 0 || pos >= a.P) {
-    if (a.status != nullptr && threadIdx.x == 0 && blockIdx.y == 0)
+    if (a.status != nullptr && threadIdx.x == 0 && threadIdx.y == 0 && blockIdx.y == 0)
       atomicOr(a.status, PKV_DEV_BAD_POSITION);
     pos = pos < 0 ? 0 : a.P - 1;
   }
-  const int32_t block = write ? slot / a.B : 0, off = write ? slot - block * a.B : 0;
-
-  if (r0 < rows) {
-    const bool turns = u < nturn;
-    float c[kAng], s[kAng];
-    if (turns) {
-      const float* row = a.table + static_cast<int64_t>(pos) * a.rot + u * kAng;
-      const Pack<float, kAng> pc = *reinterpret_cast<const Pack<float, kAng>*>(row);
-      const Pack<float, kAng> ps = *reinterpret_cast<const Pack<float, kAng>*>(row + half);
+  const bool turns = u < nturn;
+  float c[kAng], s[kAng];
+  if (turns) {
+    const float* row = a.table + static_cast<int64_t>(pos) * a.rot + u * kAng;
+    const Pack<float, kAng> pc = *reinterpret_cast<const Pack<float, kAng>*>(row);
+    const Pack<float, kAng> ps = *reinterpret_cast<const Pack<float, kAng>*>(row + half);
 #pragma unroll
-      for (int i = 0; i < kAng; ++i) {
-        c[i] = pc.x[i];
-        s[i] = ps.x[i];
-      }
-    }
-    const int d = turns ? u * VEC : a.rot + (u - nturn) * VEC;  // first element of the unit
-    const bool pair = turns && !kInter;
-    const int h0 = r0 + rows * static_cast<int>(blockIdx.y);
-    const int step = rows * static_cast<int>(gridDim.y);
-    // a turned piece, rounded to the type; a passing one keeps its bits (a NaN's too)
-    auto store = [&](T* dst, const float (&y1)[VEC], const float (&y2)[VEC], const P& x) {
-      P o1, o2;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        o1.x[i] = turns ? ptx::from_float<T>(y1[i]) : x.x[i];
-        if (!kInter) o2.x[i] = ptx::from_float<T>(y2[i]);
-      }
-      *reinterpret_cast<P*>(dst) = o1;
-      if (pair) *reinterpret_cast<P*>(dst + half) = o2;
-    };
-    T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + d;
-    turn_heads<T, VEC, kInter>(
-        static_cast<const T*>(a.q) + t * a.q_stride + d, a.Hq, a.D, h0, step, half, turns, c, s,
-        [&](int h, const float (&y1)[VEC], const float (&y2)[VEC], const P& x) {
-          store(qo + static_cast<int64_t>(h) * a.D, y1, y2, x);
-        });
-    if (write) {
-      turn_heads<T, VEC, kInter>(
-          static_cast<const T*>(a.k) + t * a.k_stride + d, a.Hkv, a.D, h0, step, half, turns, c, s,
-          [&](int g, const float (&y1)[VEC], const float (&y2)[VEC], const P& x) {
-            const int64_t row = (static_cast<int64_t>(block) * a.Hkv + g) * a.B + off;
-            if constexpr (kCodes != 0) {
-              using C = Pack<uint8_t, VEC>;
-              uint8_t* const dst = static_cast<uint8_t*>(a.kc) + row * a.D + d;
-              const float scale = __ldg(a.ks + g);
-              *reinterpret_cast<C*>(dst) = codes_of<kCodes, VEC>(y1, scale);
-              if (pair) *reinterpret_cast<C*>(dst + half) = codes_of<kCodes, VEC>(y2, scale);
-            } else {
-              store(static_cast<T*>(a.kc) + row * a.D + d, y1, y2, x);
-            }
-          });
+    for (int i = 0; i < kAng; ++i) {
+      c[i] = pc.x[i];
+      s[i] = ps.x[i];
     }
   }
-
-  // V rows, copied.
-  if constexpr (kCodes == 0) {
-    if (!write) return;
-    constexpr int U = 4;
-    const int vunits = a.D / VEC, total = a.Hkv * vunits;
-    const int step = blockDim.x * gridDim.y;
-    const P* const v = reinterpret_cast<const P*>(static_cast<const T*>(a.v) + t * a.v_stride);
-    for (int i0 = threadIdx.x + blockDim.x * blockIdx.y; i0 < total; i0 += U * step) {
-      P x[U];
-#pragma unroll
-      for (int w = 0; w < U; ++w)
-        if (i0 + w * step < total) x[w] = v[i0 + w * step];
-#pragma unroll
-      for (int w = 0; w < U; ++w) {
-        const int i = i0 + w * step;
-        if (i < total) {
-          const int g = i / vunits;
-          const int64_t row = (static_cast<int64_t>(block) * a.Hkv + g) * a.B + off;
-          *reinterpret_cast<P*>(static_cast<T*>(a.vc) + row * a.D + (i - g * vunits) * VEC) = x[w];
-        }
-      }
+  const int d = turns ? u * VEC : a.rot + (u - nturn) * VEC;  // first element of the unit
+  const bool two = turns && !kInter;
+  const int h0 = threadIdx.y + blockDim.y * blockIdx.y, step = blockDim.y * gridDim.y;
+  // a turned piece, rounded to the type; a passing one keeps its bits (a NaN's too)
+  auto turned = [&](T* dst, const P& x1, const P& x2) {
+    if (turns) {
+      float y1[VEC], y2[VEC];
+      turn<T, VEC, kInter>(x1, x2, c, s, y1, y2);
+      store_as<T, VEC>(dst, y1);
+      if (!kInter) store_as<T, VEC>(dst + half, y2);
+    } else {
+      *reinterpret_cast<P*>(dst) = x1;
     }
+  };
+  T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + d;
+  each_head<T, VEC, kInter>(static_cast<const T*>(a.q) + t * a.q_stride + d, a.Hq, a.D, h0, step,
+                            half, two, [&](int h, const P& x1, const P& x2) {
+                              turned(qo + h * a.D, x1, x2);
+                            });
+  if (!write) return;
+  const int32_t block = (a.B & (a.B - 1)) == 0 ? slot >> (31 - __clz(a.B)) : slot / a.B;
+  const int32_t off = slot - block * a.B;
+  const int64_t at = (static_cast<int64_t>(block) * a.Hkv * a.B + off) * a.D + d;  // head 0
+  const int64_t head = static_cast<int64_t>(a.B) * a.D;
+  each_head<T, VEC, kInter>(
+      static_cast<const T*>(a.k) + t * a.k_stride + d, a.Hkv, a.D, h0, step, half, two,
+      [&](int g, const P& x1, const P& x2) {
+        if constexpr (kCodes == 0) {
+          turned(static_cast<T*>(a.kc) + at + g * head, x1, x2);
+        } else {
+          float y1[VEC], y2[VEC];
+          if (turns) {
+            turn<T, VEC, kInter>(x1, x2, c, s, y1, y2);
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y1[i] = widen(x1.x[i]);
+          }
+          uint8_t* const dst = static_cast<uint8_t*>(a.kc) + at + g * head;
+          const Quotients by = quotients_by(__ldg(a.ks + g));
+          store_codes<kCodes, VEC>(dst, y1, by);
+          if (two) store_codes<kCodes, VEC>(dst + half, y2, by);
+        }
+      });
+  if constexpr (kCodes == 0) {  // V rows, copied
+    each_head<T, VEC, kInter>(static_cast<const T*>(a.v) + t * a.v_stride + d, a.Hkv, a.D, h0,
+                              step, half, two, [&](int g, const P& x1, const P& x2) {
+                                T* const dst = static_cast<T*>(a.vc) + at + g * head;
+                                *reinterpret_cast<P*>(dst) = x1;
+                                if (two) *reinterpret_cast<P*>(dst + half) = x2;
+                              });
   }
 }
 
@@ -353,7 +365,7 @@ __global__ void rotary_table_kernel(const __grid_constant__ Frequencies fr, doub
 }
 
 template <typename T, int VEC, int kCodes>
-void launch_layout(const RotaryArgs& a, bool interleaved, dim3 grid, int threads,
+void launch_layout(const RotaryArgs& a, bool interleaved, dim3 grid, dim3 threads,
                    cudaStream_t st) {
   if (interleaved) {
     // a thread's piece holds whole pairs
@@ -378,19 +390,22 @@ int launch_typed(RotaryArgs a, bool interleaved, cudaStream_t st) {
   if (rc != PKV_OK) return rc;
   const int vec = wide ? W : (interleaved ? 2 : 1);
   const int units = (interleaved ? a.rot / vec : a.rot / (2 * vec)) + (a.D - a.rot) / vec;
-  const int threads = units <= 128 ? 128 : 256;  // units < head_dim <= 256
-  const int rows = threads / units;
-  const int heads = a.Hq + a.Hkv;
+  // a row's units side by side, as many rows as 128 threads hold (units < head_dim <= 256)
+  const int rows = units < 128 ? 128 / units : 1;
+  const dim3 threads(units, rows);
   // few tokens: their heads are spread over more CTAs until the SMs have a few each
   int split = 1;
-  while (split * rows < heads && static_cast<int64_t>(a.T) * split < 4 * sms) split *= 2;
+  while (split * rows < a.Hq && static_cast<int64_t>(a.T) * split < 4 * sms) split *= 2;
   int64_t columns = a.T;
   if (kCodes != 0) {
-    // V's windows: split likewise, to one item a thread when all its runs are single tokens
+    // V's windows: an item a thread if the window is one run, and for few windows, whose
+    // runs may be single tokens, more parts until the SMs have a few CTAs each
     const int64_t windows = (a.T + 15) / 16;
-    const int64_t most = (static_cast<int64_t>(a.Hkv) * a.D * 8 + threads - 1) / threads;
+    const int64_t items = static_cast<int64_t>(a.Hkv) * a.D / 2;  // of one run
     int64_t parts = 1;
-    while (parts < most && windows * parts < 8 * sms) parts *= 2;
+    while (parts * units * rows < items ||
+           (parts * units * rows < 16 * items && windows * parts < 2 * sms))
+      parts *= 2;
     a.v_parts = static_cast<int32_t>(parts);
     columns += (windows * parts + split - 1) / split;
   }

@@ -177,6 +177,41 @@ def test_write_8bit(kind, inter, dtype, D, rot):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_codes_are_those_of_the_cache_write(kind, dtype):
+    """Every 16-bit pattern (fp32: magnitudes over the whole range, and quotients next to the
+    codes' borders) as V, over scales up to the extreme: the bytes paged_kv_write leaves."""
+    m, Hkv, D = pkv(), 8, 128
+    scales = torch.tensor([0.01, 1.0, 3.0, 448.0, 1e-30, 1e30, 2.0 ** -70, 1.7e-5], device="cuda")
+    if dtype == "f32":
+        g = torch.Generator(device="cuda")
+        g.manual_seed(0)
+        x = torch.randint(-2 ** 31, 2 ** 31, (128, Hkv, D), generator=g, device="cuda",
+                          dtype=torch.int64).to(torch.int32).view(torch.float32)
+        # k / 32 times the scale: ties of the codes among them, and their neighbours
+        k = torch.randint(-1024 * 32, 1024 * 32, (384, Hkv, D), generator=g, device="cuda") / 32.0
+        y = k * scales[:, None]
+        y = torch.nextafter(y, y + torch.randint(-1, 2, y.shape, generator=g, device="cuda") * y.abs())
+        v = torch.cat([x, y])
+    else:
+        v = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.int16)
+        v = v.view(DT[dtype]).view(512, 1, D).expand(512, Hkv, D).contiguous()
+    T = v.shape[0]
+    k = torch.zeros_like(v)
+    slots = torch.arange(T, device="cuda", dtype=torch.int32)
+    ct = torch.uint8 if kind == "fp8" else torch.int8
+    caches = [[torch.zeros((T // 16, Hkv) + s, dtype=ct, device="cuda") for s in ((16, D), (D, 16))]
+              for _ in range(2)]
+    freq = m.rotary_frequencies(D)
+    table, pos = m.rotary_table(4, freq), torch.zeros(T, dtype=torch.int32, device="cuda")
+    getattr(m, "paged_rotary_write_" + kind)(k, k, v, pos, table, slots, *caches[0], scales, scales,
+                                             torch.empty_like(k))
+    getattr(m, "paged_kv_write_" + kind)(k, v, slots, *caches[1], scales, scales)
+    torch.cuda.synchronize()
+    assert torch.equal(caches[0][1].view(torch.uint8), caches[1][1].view(torch.uint8))
+
+
 @pytest.mark.parametrize("kind", ["", "fp8", "int8"])
 @pytest.mark.parametrize("T,first", [(16, 0), (64, 0), (83, 5), (40, 15), (33, 16), (7, 9)])
 def test_prompt_order(kind, T, first):
