@@ -33,6 +33,26 @@ struct SumArgs {
   int32_t S, Hkv, limit, cols;  // limit: positions a block table holds
 };
 
+// cursor_at, by a warp: the sequence is looked for among 32 places a round, one a lane.
+__device__ __forceinline__ Cursor warp_cursor_at(const int32_t* pre, int S, int Hkv, int f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = S;  // pre[lo] <= f < pre[hi]
+  while (hi - lo > 1) {
+    const int stride = (hi - lo + 31) / 32, at = lo + lane * stride;
+    const bool below = at < hi && pre[at] <= f;  // true for lanes 0 .. n - 1
+    const int n = __popc(__ballot_sync(0xffffffffu, below));
+    lo += (n - 1) * stride;
+    hi = min(hi, lo + stride);
+  }
+  Cursor c;
+  c.s = lo;
+  const int r = f - pre[lo];
+  c.nb = (pre[lo + 1] - pre[lo]) / Hkv;
+  c.g = r / c.nb;
+  c.j = r - c.g * c.nb;
+  return c;
+}
+
 // A warp walks its run of the flat step list unit by unit: a unit's tokens, scores and sums
 // are contiguous, its G log-sum-exps stay in registers.
 template <int G>
@@ -46,7 +66,7 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const SumArgs 
   if (static_cast<int64_t>(gw) * per >= total) return;
   int f = gw * per;
   const int f1 = total - f < per ? total : f + per;
-  Cursor c = cursor_at(a.steps, a.S, a.Hkv, f);
+  Cursor c = warp_cursor_at(a.steps, a.S, a.Hkv, f);
   while (f < f1) {
     const int j1 = min(c.nb, c.j + (f1 - f));  // steps c.j .. j1 - 1 of unit (c.s, c.g)
     int end = j1 * kTok;                       // positions in the context
@@ -93,6 +113,12 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const SumArgs 
         }
       }
     }
+    // The scores are not read again: lines still in L2 need not be written to memory.
+    __syncwarp();
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(x);
+    const uintptr_t s1 = s0 + static_cast<uintptr_t>(j1 - c.j) * (kTok * G * sizeof(float));
+    for (uintptr_t l = ((s0 + 127) & ~uintptr_t(127)) + 128 * lane; l + 128 <= s1; l += 128 * 32)
+      ptx::discard_line(reinterpret_cast<const void*>(l));
     f += j1 - c.j;
     c.j = j1 - 1;
     advance(c, a.steps, a.S, a.Hkv);

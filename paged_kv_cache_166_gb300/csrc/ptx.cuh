@@ -155,6 +155,23 @@ __device__ __forceinline__ void st_global_v4_hint(void* ptr, uint4 v, uint64_t p
 }
 
 // ---- 4-byte cp.async (block-table prefetch) -------------------------------------
+__device__ __forceinline__ void st_global_f32_hint(float* ptr, float x, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(ptr), "f"(x), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void st_global_v2_f32_hint(float* ptr, float x, float y,
+                                                      uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(ptr), "f"(x), "f"(y),
+               "l"(policy)
+               : "memory");
+}
+
+// Drops a 128-byte line (aligned) from L2 without writing it back: its contents are
+// undefined afterwards.
+__device__ __forceinline__ void discard_line(const void* line) {
+  asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
