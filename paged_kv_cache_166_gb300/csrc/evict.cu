@@ -47,10 +47,8 @@ struct SelectArgs {
 // Unsigned key in the order of the values: larger sum, larger key.  NaN counts as
 // -infinity and -0 as +0.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  uint32_t u = __float_as_uint(x);
-  if (x != x) u = 0xff800000u;
-  if (x == 0.f) u = 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(x + 0.f, -INFINITY));
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
 // A row's ends, and the candidates between them.
@@ -176,7 +174,7 @@ __device__ __forceinline__ void select_short(const Row& w, int lane) {
   }
 }
 
-__global__ void __launch_bounds__(kShortWarps * 32)
+__global__ void __launch_bounds__(kShortWarps * 32, 5)
     evict_select_short_kernel(const SelectArgs a, int64_t rows) {
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + (threadIdx.x >> 5);
@@ -184,15 +182,16 @@ __global__ void __launch_bounds__(kShortWarps * 32)
   const Row w = row_of(a, row, lane == 0);
   keep_ends(w, lane, 32);
   if (w.m == 0) return;
-  if (w.M <= 512) select_short<16>(w, lane);
+  if (w.M <= 256) select_short<8>(w, lane);
+  else if (w.M <= 512) select_short<16>(w, lane);
+  else if (w.M <= 1024) select_short<32>(w, lane);
   else select_short<kShortCols / 32>(w, lane);
 }
 
 // ---- long rows: a cluster of CTAs each, the keys in registers ----------------------
 
 constexpr int kLongThreads = 512;
-constexpr int kLongKeys = 32;                           // keys of a thread
-constexpr int kRound = kLongThreads * kLongKeys;        // and of a CTA at once
+constexpr int kLongKeys = 32;                           // keys of a thread, at most
 constexpr int kWarps = kLongThreads / 32;
 constexpr int kCoarse = 64;                             // sums of 32 bins each
 constexpr int kTailKeys = 4;
@@ -224,7 +223,10 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 // The keys are looked at in the CTA's slice order: element i * kLongThreads + tid of a round
 // is thread tid's i-th key, so a warp's i-th keys are 32 consecutive elements, and word
 // i * kWarps + warp of a bit mask over the round holds their bits.
+// kKeys: keys of a thread.
+template <int kKeys>
 __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(const SelectArgs a) {
+  constexpr int kRound = kLongThreads * kKeys;  // keys of the CTA at once
   __shared__ __align__(16) int hist[kPasses][kDigitBins];
   __shared__ int coarse[kPasses][kCoarse];
   __shared__ uint32_t tail[kTail];       // this CTA's keys in the threshold's bin
@@ -244,15 +246,15 @@ __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(cons
   const int lo = w.f + min(w.M, rank * per), len = max(0, min(per, w.f + w.M - lo));
   const int rounds = (per + kRound - 1) / kRound;
   const float* const vals = w.sums + lo;
-  uint32_t key[kLongKeys];
+  uint32_t key[kKeys];
   auto load = [&](int round) {
 #pragma unroll
-    for (int i = 0; i < kLongKeys; ++i) {
+    for (int i = 0; i < kKeys; ++i) {
       const int p = round * kRound + i * kLongThreads + tid;
       key[i] = p < len ? __float_as_uint(__ldg(vals + p)) : 0u;
     }
 #pragma unroll
-    for (int i = 0; i < kLongKeys; ++i) {
+    for (int i = 0; i < kKeys; ++i) {
       const int p = round * kRound + i * kLongThreads + tid;
       key[i] = p < len ? key_of(__uint_as_float(key[i])) : 0u;  // 0: no token
     }
@@ -275,10 +277,15 @@ __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(cons
       shift -= bits;
       for (int round = 0; round < rounds; ++round) {
         if (rounds > 1) load(round);
+        if (pass == 0) {  // no token counts in bin 0, which no key's digit is
 #pragma unroll
-        for (int i = 0; i < kLongKeys; ++i)
-          if (key[i] != 0 && (key[i] & fixed) == t)
-            atomicAdd(&hist[pass][(key[i] >> shift) & ((1u << bits) - 1)], 1);
+          for (int i = 0; i < kKeys; ++i) atomicAdd(&hist[0][key[i] >> 21], 1);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if ((key[i] & fixed) == t)
+              atomicAdd(&hist[pass][(key[i] >> shift) & ((1u << bits) - 1)], 1);
+        }
       }
       __syncthreads();
       {
@@ -338,8 +345,8 @@ __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(cons
       for (int round = 0; round < rounds; ++round) {
         if (rounds > 1) load(round);
 #pragma unroll
-        for (int i = 0; i < kLongKeys; ++i)
-          if (key[i] != 0 && (key[i] & prefix) == t) tail[atomicAdd(&tail_count, 1)] = key[i];
+        for (int i = 0; i < kKeys; ++i)
+          if ((key[i] & prefix) == t) tail[atomicAdd(&tail_count, 1)] = key[i];
       }
       cluster.sync();
       uint32_t k[kTailKeys] = {};
@@ -386,13 +393,18 @@ __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(cons
   auto masks = [&] {
     uint32_t g = 0, e = 0;  // lane i keeps the words of the warp's i-th keys
 #pragma unroll
-    for (int i = 0; i < kLongKeys; ++i) {
+    for (int i = 0; i < kKeys; ++i) {
       const uint32_t x = __ballot_sync(0xffffffffu, key[i] > t);
-      const uint32_t y = __ballot_sync(0xffffffffu, ties > 0 && key[i] == t);
       g = lane == i ? x : g;
-      e = lane == i ? y : e;
     }
-    mask_gt[lane * kWarps + warp] = g;
+    if (ties > 0) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        const uint32_t y = __ballot_sync(0xffffffffu, key[i] == t);
+        e = lane == i ? y : e;
+      }
+    }
+    mask_gt[lane * kWarps + warp] = g;  // empty words behind the kKeys-th
     mask_eq[lane * kWarps + warp] = e;
     __syncthreads();
   };
@@ -579,17 +591,8 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_v8_kernel(const G
   }
 }
 
-// Short rows take a warp each.  Long ones: as many CTAs, up to eight, as hold the row in
-// registers, 16,384 keys each; a longer row is read from memory once a pass.
-int launch_select(const SelectArgs& a, int64_t rows, cudaStream_t st) {
-  if (a.cols <= kShortCols) {
-    const int64_t ctas = (rows + kShortWarps - 1) / kShortWarps;
-    evict_select_short_kernel<<<static_cast<unsigned>(ctas), kShortWarps * 32, 0, st>>>(a, rows);
-    PKV_CUDA(cudaGetLastError());
-    return PKV_OK;
-  }
-  int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kRound < a.cols) cluster *= 2;
+template <int kKeys>
+int launch_long(const SelectArgs& a, int64_t rows, int cluster, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
   cfg.blockDim = dim3(kLongThreads);
@@ -601,8 +604,25 @@ int launch_select(const SelectArgs& a, int64_t rows, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_select_long_kernel, a));
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_select_long_kernel<kKeys>, a));
   return PKV_OK;
+}
+
+// Short rows take a warp each.  Long ones: as many CTAs, up to eight, as hold the row in
+// registers, up to 16,384 keys each; a longer row is read from memory once a pass.
+int launch_select(const SelectArgs& a, int64_t rows, cudaStream_t st) {
+  if (a.cols <= kShortCols) {
+    const int64_t ctas = (rows + kShortWarps - 1) / kShortWarps;
+    evict_select_short_kernel<<<static_cast<unsigned>(ctas), kShortWarps * 32, 0, st>>>(a, rows);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+  }
+  constexpr int kMost = kLongThreads * kLongKeys;
+  if (a.cols <= kMost / 4) return launch_long<kLongKeys / 4>(a, rows, 1, st);
+  if (a.cols <= kMost / 2) return launch_long<kLongKeys / 2>(a, rows, 1, st);
+  int cluster = 1;
+  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kMost < a.cols) cluster *= 2;
+  return launch_long<kLongKeys>(a, rows, cluster, st);
 }
 
 }  // namespace
