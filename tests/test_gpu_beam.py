@@ -270,6 +270,29 @@ def test_two_graphs_and_eager_calls():
             assert torch.equal(a, b)
 
 
+def test_two_streams_at_once():
+    m = pkv()
+    data = [make(16, 4, 50000, "f32", seed=s) for s in (3, 4)]
+    want = [run(x, bs, 8) for x, bs in data]
+    outs = [[torch.empty_like(t) for t in w] for w in want]
+    streams = [torch.cuda.Stream() for _ in data]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (x, bs), o, s in zip(data, outs, streams):
+            with torch.cuda.stream(s):
+                m.beam_select(x, bs, *o)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for a, b in zip(o, w):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("K,N,V", [(64, 128, 20000), (16, 128, 60000), (8, 64, 33000)])
+def test_many_candidates_are_merged_by_row(K, N, V):
+    x, bs = make(2, K, V, "bf16", seed=N + V)
+    check(x, bs, N)
+
+
 def test_python_refusals():
     m = pkv()
     x, bs = make(2, 3, 50, "f32")

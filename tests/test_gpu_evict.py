@@ -249,6 +249,50 @@ def test_weights_graphs_do_not_share_a_workspace():
         assert torch.equal(a[2], want)
 
 
+def test_weights_on_two_streams_at_once():
+    bs = [batch(32, 4, 128, "bf16", (3000, 64, 999), seed=s) for s in (7, 8)]
+    refs, sums, idx = [], [], []
+    for b in bs:
+        r = torch.zeros((3, 4, b.tables.shape[1] * 16), device="cuda")
+        attend(b, r)
+        refs.append(r)
+        sums.append(torch.zeros_like(r))
+        idx.append(b.device_index("cuda"))
+    outs = [torch.empty_like(b.q) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for b, st, s, (tables, ctx, _), out in zip(bs, streams, sums, idx, outs):
+            with torch.cuda.stream(st):
+                pkv().paged_decode_attention_weights(b.q, b.kc, b.vc, tables, ctx, b.w.scale, out, s)
+    torch.cuda.synchronize()
+    for s, r in zip(sums, refs):
+        want = torch.zeros_like(r)
+        for _ in range(4):
+            want += r
+        assert torch.equal(s, want)
+
+
+def test_empty_batches():
+    m, i = pkv(), dict(dtype=torch.int32, device="cuda")
+    kc = torch.zeros((4, 2, 16, 64), dtype=torch.float16, device="cuda")
+    q = torch.zeros((0, 4, 64), dtype=torch.float16, device="cuda")
+    none, table = torch.zeros(0, **i), torch.zeros((0, 2), **i)
+    m.paged_decode_attention_weights(q, kc, kc.clone(), table, none, 0.1, torch.empty_like(q),
+                                     torch.zeros((0, 2, 32), device="cuda"))
+    kept, sums = torch.zeros((0, 2, 8), **i), torch.zeros((0, 2, 8), device="cuda")
+    m.paged_evict_select(torch.zeros((0, 2, 32), device="cuda"), none, none, kept, sums,
+                         torch.zeros(0, **i))
+    m.paged_evict_gather(kc, kc.clone(), table, kept, none, torch.zeros((0, 1), **i))
+    # contexts that are all empty: zero rows, untouched sums
+    q = torch.ones((2, 4, 64), dtype=torch.float16, device="cuda")
+    sums = torch.full((2, 2, 32), 3.0, device="cuda")
+    out = m.paged_decode_attention_weights(q, kc, kc.clone(), torch.zeros((2, 2), **i),
+                                           torch.zeros(2, **i), 0.1, torch.empty_like(q), sums)
+    torch.cuda.synchronize()
+    assert not out.any() and bool((sums == 3.0).all())
+
+
 # --- select --------------------------------------------------------------------------
 def select(sums, ctx, keep, cols=None, first=0, recent=0, status=None, ncols=None):
     S, H, W_ = sums.shape
@@ -374,7 +418,8 @@ def pools(kind, NB, H, B, D, seed):
 
 @pytest.mark.parametrize("kind,B,D", [("bf16", 16, 128), ("f16", 8, 64), ("bf16", 32, 256),
                                       ("f32", 16, 32), ("f32", 16, 128), ("f16", 16, 96),
-                                      ("f32", 16, 1024), ("fp8", 16, 128), ("int8", 16, 256),
+                                      ("f32", 16, 1024), ("bf16", 24, 128), ("f16", 1, 64),
+                                      ("fp8", 16, 128), ("int8", 16, 256),
                                       ("int8", 16, 48)])
 def test_gather(kind, B, D):
     g = np.random.default_rng(D + B)

@@ -167,6 +167,29 @@ def test_write_shapes(inter, dtype, D, rot, B):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("B", [1, 5, 24])
+def test_block_sizes_that_are_no_power_of_two(B):
+    for inter in (False, True):
+        c = Case(50, 4, 2, 128, 128, "bf16", B=B, inter=inter, seed=B)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 4), ("bf16", 8), ("f16", 24), ("f32", 36)])
+def test_small_and_odd_heads(dtype, D):
+    for rot in sorted({2, max(2, D // 4 * 2), D}):
+        for inter in (False, True):
+            c = Case(21, 3, 1, D, rot, dtype, inter=inter, seed=D + rot)
+            c.check(c.run())
+
+
+def test_no_tokens():
+    c = Case(4, 4, 2, 64, 64, "f16")
+    c.T = 0
+    c.q, c.k, c.v, c.pos, c.slots = c.q[:0], c.k[:0], c.v[:0], c.pos[:0], c.slots[:0]
+    assert c.run().shape == (0, 4, 64)
+    assert bool((c.kc == 7.0).all())
+
+
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("dtype,D,rot", [("bf16", 128, 128), ("f16", 256, 64), ("f32", 128, 96),
