@@ -547,7 +547,7 @@ int pkv_rotary_table(const double* inv_freq, int32_t rotary_dim, float magnitude
  * multiple of 16 bytes; caches and table 16-byte aligned, q, k, v and q_out aligned
  * to their element (interleaved: strides even, addresses aligned to two elements).
  * Strides and addresses that are multiples of 16 bytes, and rotary_dim a multiple
- * of 16 bytes' elements (half layout: of 32), take the fast path.
+ * of 16 bytes' elements (half layout: of 32), take the fast path.  At most 65535 heads.
  * num_tokens == 0 is a no-op.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  */
@@ -661,6 +661,7 @@ int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_s
  * kept          device int32 [num_seqs, num_kv_heads, kept_cols].
  * new_sums      device float [num_seqs, num_kv_heads, new_cols]; overlaps no input.
  * new_lens      device int32 [num_seqs]; not context_lens.
+ * At most 2^30 columns each.
  * status        device int32 word or NULL: PKV_DEV_BAD_CONTEXT_LEN for a context
  *               length outside [0, sums_cols] or an n above kept_cols or new_cols
  *               (clamped).
@@ -686,7 +687,8 @@ int pkv_evict_select(const float* weight_sums, int32_t sums_cols, const int32_t*
  * status        device int32 word or NULL: PKV_DEV_BAD_BLOCK_ID for a position or a
  *               block id out of range (that row is not moved).
  * Requirements: head_dim * element size a multiple of 16 bytes, at most 4096; caches
- * 16-byte aligned; 8-bit caches block_size 16; num_seqs <= 65535.
+ * 16-byte aligned; 8-bit caches block_size 16; num_seqs and num_kv_heads <= 65535;
+ * kept_cols <= 2^30.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  */
 int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
@@ -717,13 +719,16 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
  *               elements, vocab contiguous elements of dtype (PKV_F32, F16, BF16), at
  *               any alignment of the element.
  * beam_scores   device float [num_seqs, num_beams]; scores must not be this array.
- * scores        device float [num_seqs, num_out]; beams, tokens device int32 likewise.
+ * scores        device float [num_seqs, num_out]; beams, tokens device int32 likewise
+ *               (three arrays).
  * workspace     >= pkv_beam_workspace_size(...) bytes, 256-byte aligned; its first
  *               PKV_BEAM_TICKET_BYTES zero before its first use, and left so by every
  *               call, so one workspace serves calls of any sizes.  Calls that may
  *               overlap need their own.
- * The log-sum-exp and the scores are 64-bit, scores rounded to fp32 at the end; equal
- * rows of logits have equal log-sum-exps, wherever they lie.
+ * The log-sum-exp and the scores that order the candidates are pairs of fp32 values (some
+ * 48 bits; the exponentials are fp32 ones, so a log-sum-exp is off by less than 2^-18),
+ * rounded to fp32 at the end; a score beyond fp32's range
+ * counts as -infinity.  Equal rows of logits have equal log-sum-exps, wherever they lie.
  * Supported: num_beams <= 64, num_out <= min(128, num_beams * vocab), num_seqs *
  * num_beams <= 65535, vocab <= 2^31 - 8193.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.

@@ -678,8 +678,7 @@ BeamLayout beam_layout(int32_t S, int32_t K, int32_t N, int parts) {
 }
 static_assert(PKV_BEAM_TICKET_BYTES / 2 >= (kMaxRows + 1) * 4, "a ticket for every row");
 
-int beam_sizes(int32_t S, int32_t K, int32_t V, int32_t N, int32_t dtype, int* parts,
-               BeamLayout* L) {
+int beam_check(int32_t S, int32_t K, int32_t V, int32_t N, int32_t dtype) {
   PKV_REQUIRE(dtype == PKV_F32 || dtype == PKV_F16 || dtype == PKV_BF16, PKV_ERR_DTYPE,
               "dtype %d is not f32, f16 or bf16", dtype);
   PKV_REQUIRE(S >= 0 && K > 0 && V > 0 && N > 0, PKV_ERR_INVALID_ARG,
@@ -692,6 +691,10 @@ int beam_sizes(int32_t S, int32_t K, int32_t V, int32_t N, int32_t dtype, int* p
               "num_seqs * num_beams above %d", kMaxRows);
   PKV_REQUIRE(V <= INT_MAX - 2 * kTile, PKV_ERR_UNSUPPORTED, "vocab %d above %d", V,
               INT_MAX - 2 * kTile);
+  return PKV_OK;
+}
+
+int beam_sizes(int32_t S, int32_t K, int32_t V, int32_t N, int* parts, BeamLayout* L) {
   int sms = 0, dev = 0;
   const int rc = device_sm_count(&sms, &dev);
   if (rc != PKV_OK) return rc;
@@ -732,9 +735,11 @@ extern "C" {
 int pkv_beam_workspace_size(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_out,
                             int32_t dtype, size_t* bytes) {
   PKV_REQUIRE(bytes != nullptr, PKV_ERR_INVALID_ARG, "bytes is NULL");
+  int rc = beam_check(num_seqs, num_beams, vocab, num_out, dtype);
+  if (rc != PKV_OK) return rc;
   int parts = 0;
   BeamLayout L;
-  const int rc = beam_sizes(num_seqs, num_beams, vocab, num_out, dtype, &parts, &L);
+  rc = beam_sizes(num_seqs, num_beams, vocab, num_out, &parts, &L);
   if (rc != PKV_OK) return rc;
   *bytes = L.total;
   return ok();
@@ -744,9 +749,7 @@ int pkv_beam_select(const void* logits, int64_t seq_stride, int64_t beam_stride,
                     const float* beam_scores, int32_t num_seqs, int32_t num_beams, int32_t vocab,
                     int32_t num_out, float* scores, int32_t* beams, int32_t* tokens,
                     void* workspace, size_t workspace_bytes, int32_t dtype, void* stream) {
-  int parts = 0;
-  BeamLayout L;
-  int rc = beam_sizes(num_seqs, num_beams, vocab, num_out, dtype, &parts, &L);
+  int rc = beam_check(num_seqs, num_beams, vocab, num_out, dtype);
   if (rc != PKV_OK) return rc;
   PKV_REQUIRE(seq_stride >= 0 && beam_stride >= 0, PKV_ERR_INVALID_ARG, "negative stride");
   if (num_seqs == 0) return ok();
@@ -758,6 +761,12 @@ int pkv_beam_select(const void* logits, int64_t seq_stride, int64_t beam_stride,
               PKV_ERR_INVALID_ARG, "a pointer is not aligned to its element");
   PKV_REQUIRE(workspace != nullptr && aligned(workspace, 256), PKV_ERR_INVALID_ARG,
               "workspace must be non-NULL and 256-byte aligned");
+  PKV_REQUIRE(scores != beam_scores && beams != tokens, PKV_ERR_INVALID_ARG,
+              "scores must not be beam_scores, nor beams tokens");
+  int parts = 0;
+  BeamLayout L;
+  rc = beam_sizes(num_seqs, num_beams, vocab, num_out, &parts, &L);
+  if (rc != PKV_OK) return rc;
   PKV_REQUIRE(workspace_bytes >= L.total, PKV_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed",
               workspace_bytes, L.total);
   char* ws = static_cast<char*>(workspace);

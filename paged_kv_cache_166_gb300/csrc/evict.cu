@@ -29,6 +29,7 @@ namespace {
 
 // ---- select ---------------------------------------------------------------------
 
+constexpr int kMaxCols = 1 << 30;  // of sums and positions: indices stay within 32 bits
 constexpr int kDigitBins = 2048;  // 11, 11 and 10 bits of a key
 constexpr int kPasses = 3;
 constexpr int kMaxCluster = 8;    // eight threads add a bin's shares
@@ -639,6 +640,8 @@ int pkv_evict_select(const float* weight_sums, int32_t sums_cols, const int32_t*
                      void* stream) {
   PKV_REQUIRE(num_seqs >= 0 && num_kv_heads > 0 && sums_cols > 0 && kept_cols > 0 && new_cols > 0,
               PKV_ERR_INVALID_ARG, "sizes must be positive (num_seqs >= 0)");
+  PKV_REQUIRE(sums_cols <= kMaxCols && kept_cols <= kMaxCols && new_cols <= kMaxCols,
+              PKV_ERR_UNSUPPORTED, "more than %d columns", kMaxCols);
   PKV_REQUIRE(first >= 0 && recent >= 0, PKV_ERR_INVALID_ARG, "negative first or recent");
   PKV_REQUIRE(static_cast<int64_t>(num_seqs) * num_kv_heads * kMaxCluster < (int64_t(1) << 31),
               PKV_ERR_UNSUPPORTED, "num_seqs * num_kv_heads * %d >= 2^31", kMaxCluster);
@@ -684,6 +687,7 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
               PKV_ERR_INVALID_ARG, "sizes must be positive (num_seqs >= 0)");
   PKV_REQUIRE(num_seqs <= 65535 && num_kv_heads <= 65535, PKV_ERR_UNSUPPORTED,
               "num_seqs %d or num_kv_heads %d above 65535", num_seqs, num_kv_heads);
+  PKV_REQUIRE(kept_cols <= kMaxCols, PKV_ERR_UNSUPPORTED, "more than %d columns", kMaxCols);
   PKV_REQUIRE(!codes || block_size == 16, PKV_ERR_UNSUPPORTED,
               "8-bit caches use block_size 16, not %d", block_size);
   const int64_t row_bytes = static_cast<int64_t>(head_dim) * elt;

@@ -434,6 +434,8 @@ int rotary_entry(int32_t codes, const void* q, int64_t q_stride, const void* k, 
               rotary_dim, head_dim);
   PKV_REQUIRE(head_dim <= 2 * kMaxRotaryPairs, PKV_ERR_UNSUPPORTED, "head_dim %d above %d",
               head_dim, 2 * kMaxRotaryPairs);
+  PKV_REQUIRE(num_q_heads <= 65535 && num_kv_heads <= 65535, PKV_ERR_UNSUPPORTED,
+              "num_q_heads %d or num_kv_heads %d above 65535", num_q_heads, num_kv_heads);
   PKV_REQUIRE(max_positions > 0, PKV_ERR_INVALID_ARG, "max_positions must be positive");
   const int elt = element_bytes(dtype);
   if (codes != 0) {

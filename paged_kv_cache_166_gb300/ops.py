@@ -515,7 +515,14 @@ def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor,
 # Operators of a decode loop around the attention: rotary positions, eviction, beams
 # ---------------------------------------------------------------------------------
 _HERE = contextlib.nullcontext()
-_SIZES: dict = {}   # workspace bytes by device and call
+_SIZES: dict = {}   # workspace bytes by device and call, forgotten when there are many
+
+
+def _remember(key, sizes):
+    if len(_SIZES) >= 4096:
+        _SIZES.clear()
+    _SIZES[key] = sizes
+    return sizes
 
 
 def _current(dev: torch.device):
@@ -709,9 +716,9 @@ def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, c
         key = (dev.index, S, MAXB, B, Hq, Hkv, D, element, num_warps)
         sizes = _SIZES.get(key)
         if sizes is None:
-            sizes = _SIZES[key] = (weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, element,
-                                                           num_warps),
-                                   workspace_bytes(Hq, Hkv, D, element, num_warps))
+            sizes = _remember(key, (
+                weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, element, num_warps),
+                workspace_bytes(Hq, Hkv, D, element, num_warps)))
         need, head = sizes
         if workspace is None:
             ws = _scratch(dev, need, head, "weights" + kind, Hq // Hkv, D, num_warps)
@@ -864,7 +871,7 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.T
         key = (dev.index, S, K, V, n, code)
         need = _SIZES.get(key)
         if need is None:
-            need = _SIZES[key] = beam_workspace_bytes(S, K, V, n, logits.dtype)
+            need = _remember(key, beam_workspace_bytes(S, K, V, n, logits.dtype))
         ws = _scratch(dev, need, N.PKV_BEAM_TICKET_BYTES, "beam") if workspace is None else workspace
         if ws.device != dev or ws.numel() * ws.element_size() < need:
             raise ValueError(f"workspace smaller than the {need} bytes needed")

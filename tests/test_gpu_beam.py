@@ -3,7 +3,7 @@
 Scores: lse is a sum of fp32 exponentials 2^(d log2 e) (the exponent's rounding is 2^-24 |d|
 log2 e, so 2^-20.4 of a term where it counts, |d| < 17; the function 2^-22), 16 of a thread's
 terms added in fp32 (16 roundings, 2^-20), rescaled when its maximum grows (2^-22 each), the
-rest carried or in fp64: below 2^-18 relative, so 2^-18 absolute in the log; the score is
+rest carried or in 64-bit integers: below 2^-18 relative, so 2^-18 absolute in the log; the score is
 rounded to fp32 once.  Beams
 and tokens: equal to the oracle's where candidates of different beams lie further apart
 than that; within a beam the order is exact whatever the distance.

@@ -273,6 +273,36 @@ def test_weights_on_two_streams_at_once():
         assert torch.equal(s, want)
 
 
+def test_weights_beyond_32_bit_offsets():
+    """2^31 scores and more: 2048 blocks shared by long tables; all sequences alike, so every
+    row of sums is the first one's, the pieces' order of summing aside."""
+    S, G, D, nb = 260, 8, 64, 65536
+    t = nb * 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    kc, vc = (torch.randn((2048, 1, 16, D), generator=g, device="cuda").to(torch.bfloat16)
+              for _ in range(2))
+    q = torch.randn((1, G, D), generator=g, device="cuda").to(torch.bfloat16).expand(S, G, D)
+    tables = (torch.arange(nb, dtype=torch.int32, device="cuda") % 2048).expand(S, nb)
+    sums = torch.zeros((S, 1, t), device="cuda")
+    q = q.contiguous()
+    pkv().paged_decode_attention_weights(q, kc, vc, tables.contiguous(),
+                                         torch.full((S,), t, dtype=torch.int32, device="cuda"),
+                                         0.125, torch.empty_like(q), sums)
+    x = 0.125 * q[0].double() @ kc[:, 0].reshape(-1, D).double().T  # [G, 2048 * 16]
+    w = (torch.softmax(x, 1).sum(0) / (t // (2048 * 16))).float()
+    A = D * 2.0 ** -23 * 0.125 * (kc.abs().reshape(-1, D).double()
+                                  @ q[0].abs().double().T).max().item()
+    rel = 2 * A + (t / 16 + 64 + 2 * G) * 2.0 ** -24 + 2.0 ** -23
+    for s in (0, 1, 130, S - 1):
+        got = sums[s, 0].view(-1, 2048 * 16)
+        assert bool(((got - w).abs() <= rel * w).all()), s
+    torch.cuda.synchronize()
+    del sums
+    pkv().ops._WORKSPACES.clear()
+    torch.cuda.empty_cache()
+
+
 def test_empty_batches():
     m, i = pkv(), dict(dtype=torch.int32, device="cuda")
     kc = torch.zeros((4, 2, 16, 64), dtype=torch.float16, device="cuda")
@@ -341,7 +371,8 @@ def test_fast_select_is_the_oracle():
 
 @pytest.mark.parametrize("cols,first,recent", [(1, 0, 0), (33, 4, 5), (500, 0, 0), (2048, 4, 64),
                                                (2049, 0, 32), (16384, 4, 0), (16385, 1, 7),
-                                               (40000, 4, 128), (131072, 4, 256)])
+                                               (40000, 4, 128), (131072, 4, 256),
+                                               (131073, 0, 9), (300000, 4, 128)])
 def test_select_sizes(cols, first, recent):
     g = np.random.default_rng(cols)
     S, H = (6, 3) if cols <= 2049 else (5, 2)
@@ -352,7 +383,7 @@ def test_select_sizes(cols, first, recent):
     check_select(sums, ctx, keep, first, recent, cols=cols)
 
 
-@pytest.mark.parametrize("cols", [700, 5000, 70000])
+@pytest.mark.parametrize("cols", [700, 5000, 70000, 140001])
 def test_select_ties_and_strange_values(cols):
     g = np.random.default_rng(cols)
     rows = [np.zeros(cols), np.full(cols, 2.5), g.integers(0, 3, cols),  # few values
@@ -460,6 +491,28 @@ def test_gather(kind, B, D):
     torch.cuda.synchronize()
     assert int(st) == 0
     assert np.array_equal(k.float().cpu().numpy(), kw) and np.array_equal(v.float().cpu().numpy(), vw)
+
+
+@pytest.mark.parametrize("kind,NB", [("bf16", 140000), ("int8", 140000)])
+def test_gather_beyond_32_bit_offsets(kind, NB):
+    H, B, D = 8, 16, 128
+    dt = torch.bfloat16 if kind == "bf16" else torch.int8
+    k = torch.zeros((NB, H, B, D), dtype=dt, device="cuda")
+    v = torch.zeros((NB, H, B, D) if kind == "bf16" else (NB, H, D, B), dtype=dt, device="cuda")
+    src, dst = NB - 1, NB - 3
+    k[src], v[src] = torch.randint(1, 100, k[src].shape, device="cuda").to(dt), 5
+    kept = i32(np.tile([3, 7, 9], (1, H, 1)))
+    pkv().paged_evict_gather(k, v, i32([[src]]), kept, i32([3]), i32([[dst]]))
+    torch.cuda.synchronize()
+    assert torch.equal(k[dst, :, :3], k[src][:, [3, 7, 9]]) and not k[dst, :, 3:].any()
+    if kind == "bf16":
+        assert bool((v[dst, :, :3] == 5).all()) and not v[dst, :, 3:].any()
+    else:
+        at = torch.tensor(ofp8.V_POS[:3].copy(), device="cuda")
+        assert bool((v[dst][:, :, at] == 5).all()) and int(v[dst].sum()) == 5 * 3 * H * D
+    assert not k[:NB - 3].any() and not v[:NB - 3].any()
+    del k, v
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("kind", ["bf16", "int8"])

@@ -254,6 +254,8 @@ def _rotary_args(**kw):
     (dict(rot=3), N.PKV_ERR_INVALID_ARG), (dict(rot=130), N.PKV_ERR_INVALID_ARG),
     (dict(rot=0), N.PKV_ERR_INVALID_ARG), (dict(maxp=0), N.PKV_ERR_INVALID_ARG),
     (dict(D=512, rot=64, qs=4096, ks=1024, vs=1024, qos=4096), N.PKV_ERR_UNSUPPORTED),
+    (dict(Hq=65536, qs=1 << 23, qos=1 << 23), N.PKV_ERR_UNSUPPORTED),
+    (dict(Hkv=1 << 24, ks=1 << 31, vs=1 << 31), N.PKV_ERR_UNSUPPORTED),
     (dict(D=4, rot=4), N.PKV_ERR_INVALID_ARG), (dict(qs=1023), N.PKV_ERR_INVALID_ARG),
     (dict(vs=8), N.PKV_ERR_INVALID_ARG), (dict(qos=0), N.PKV_ERR_INVALID_ARG),
     (dict(q=None), N.PKV_ERR_INVALID_ARG), (dict(table=None), N.PKV_ERR_INVALID_ARG),
@@ -317,6 +319,8 @@ def test_evict_refusals():
                dict(recent=-1), dict(sums=None), dict(new=P), dict(lens=P), dict(kept=P + 2)):
         assert lib.pkv_evict_select(*sel(**kw)) == N.PKV_ERR_INVALID_ARG, kw
     assert lib.pkv_evict_select(*sel(S=1 << 20, H=1 << 10)) == N.PKV_ERR_UNSUPPORTED
+    for kw in (dict(cols=(1 << 30) + 1), dict(kc=(1 << 31) - 1), dict(nc=(1 << 31) - 1)):
+        assert lib.pkv_evict_select(*sel(**kw)) == N.PKV_ERR_UNSUPPORTED, kw
     assert lib.pkv_evict_select(*sel(S=0, sums=None)) == N.PKV_OK
 
     def gat(**kw):
@@ -329,8 +333,39 @@ def test_evict_refusals():
                      (dict(nt=P), N.PKV_ERR_INVALID_ARG), (dict(kc=P + 4), N.PKV_ERR_INVALID_ARG),
                      (dict(newb=0), N.PKV_ERR_INVALID_ARG), (dict(lens=None), N.PKV_ERR_INVALID_ARG),
                      (dict(dt=N.PKV_INT8, B=8), N.PKV_ERR_UNSUPPORTED),
+                     (dict(cols=(1 << 31) - 1), N.PKV_ERR_UNSUPPORTED),
                      (dict(maxb=1 << 28), N.PKV_ERR_INVALID_ARG)):
         assert lib.pkv_evict_gather(*gat(**kw)) == code, kw
+
+
+def test_beam_refusals():
+    lib = N.lib()
+
+    def args(**kw):
+        a = dict(logits=P, ss=400, bs=100, scores_in=P, S=2, K=4, V=100, N=8, scores=P + 256,
+                 beams=P + 512, tokens=P + 768, ws=P, wsb=1 << 30, dt=N.PKV_F32, stream=None)
+        a.update(kw)
+        return list(a.values())
+    for kw, code in ((dict(dt=N.PKV_INT8), N.PKV_ERR_DTYPE), (dict(S=-1), N.PKV_ERR_INVALID_ARG),
+                     (dict(K=0), N.PKV_ERR_INVALID_ARG), (dict(V=0), N.PKV_ERR_INVALID_ARG),
+                     (dict(N=0), N.PKV_ERR_INVALID_ARG), (dict(K=65), N.PKV_ERR_UNSUPPORTED),
+                     (dict(N=129), N.PKV_ERR_UNSUPPORTED), (dict(V=1, N=5), N.PKV_ERR_INVALID_ARG),
+                     (dict(S=20000), N.PKV_ERR_UNSUPPORTED),
+                     (dict(V=(1 << 31) - 8192), N.PKV_ERR_UNSUPPORTED),
+                     (dict(ss=-1), N.PKV_ERR_INVALID_ARG), (dict(bs=-4), N.PKV_ERR_INVALID_ARG),
+                     (dict(logits=None), N.PKV_ERR_INVALID_ARG),
+                     (dict(logits=P + 2), N.PKV_ERR_INVALID_ARG),
+                     (dict(tokens=P + 2), N.PKV_ERR_INVALID_ARG),
+                     (dict(scores=P), N.PKV_ERR_INVALID_ARG),
+                     (dict(beams=P + 768), N.PKV_ERR_INVALID_ARG),
+                     (dict(ws=None), N.PKV_ERR_INVALID_ARG),
+                     (dict(ws=P + 128), N.PKV_ERR_INVALID_ARG)):
+        assert lib.pkv_beam_select(*args(**kw)) == code, kw
+    assert lib.pkv_beam_select(*args(S=0, logits=None)) == N.PKV_OK
+    n = ctypes.c_size_t()
+    assert lib.pkv_beam_workspace_size(1, 65, 100, 4, N.PKV_F32, ctypes.byref(n)) \
+        == N.PKV_ERR_UNSUPPORTED
+    assert lib.pkv_beam_workspace_size(1, 4, 100, 4, N.PKV_F32, None) == N.PKV_ERR_INVALID_ARG
 
 
 def test_python_refusals_of_host_tensors():
