@@ -11,9 +11,9 @@
 //
 // Select is exact: the m-th largest sum is found by its bits, and the tokens above it, plus
 // the lowest positions equal to it, are compacted with prefix counts.  A row of sums is read
-// from memory once: a short row's keys stay in a warp's registers, a long row's in those of
-// a cluster of CTAs, a slice each, whose histograms of the keys' digits are added over
-// distributed shared memory.  Gather is a copy, bound by memory.
+// from memory once: a short row's keys stay in a warp's registers, a long row's upper halves
+// in the shared memory of a cluster of CTAs, a slice each, whose histograms of the keys'
+// digits are added over distributed shared memory.  Gather is a copy, bound by memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -30,8 +30,8 @@ namespace {
 // ---- select ---------------------------------------------------------------------
 
 constexpr int kMaxCols = 1 << 30;  // of sums and positions: indices stay within 32 bits
-constexpr int kDigitBins = 2048;  // 11, 11 and 10 bits of a key
-constexpr int kPasses = 3;
+constexpr int kDigitBins = 2048;  // 11, 5, 11 and 5 bits of a key
+constexpr int kPasses = 4;
 constexpr int kMaxCluster = 8;    // eight threads add a bin's shares
 
 struct SelectArgs {
@@ -189,14 +189,27 @@ __global__ void __launch_bounds__(kShortWarps * 32, 5)
   else select_short<kShortCols / 32>(w, lane);
 }
 
-// ---- long rows: a cluster of CTAs each, the keys in registers ----------------------
+// ---- long rows: a cluster of CTAs each, the keys' upper halves in shared memory -----
+//
+// The threshold is found by its digits, 11, 5, 11 and 5 bits, from histograms of the keys
+// that agree with it so far; once few are left, every CTA of the cluster takes them all and
+// goes on alone.  Halves take 2 bytes a key, so a CTA holds 32,768 of them, two CTAs fit an
+// SM and 64 rows of 131,072 are worked on at once; with whole keys in registers (16,384 a
+// CTA) they took a second round of CTAs: 41.7 us against 26.1 (33.5 MB, of which reading
+// them takes 5.2).  The loops over eight keys a thread are short code run many times: the
+// same keys unrolled in registers took 31.9 us, much of it waiting for instructions.  What is
+// left is latency: of some 38,000 cycles the loads and first histogram take 12,000 (6.5 TB/s),
+// the bin's keys 5,000, the cluster's sums and barriers 8,000, the output 5,000.
 
 constexpr int kLongThreads = 512;
-constexpr int kLongKeys = 32;                           // keys of a thread, at most
+constexpr int kLongKeys = 32768;                        // keys of a CTA at once, at most
+constexpr int kSlice = 4096;                            // keys a CTA is left with, if possible
+constexpr int kSmallSlice = 8192;                       // keys of a CTA of which four fit an SM
 constexpr int kWarps = kLongThreads / 32;
 constexpr int kCoarse = 64;                             // sums of 32 bins each
 constexpr int kTailKeys = 4;
 constexpr int kTail = kLongThreads * kTailKeys;         // keys resolved without histograms
+constexpr int kTailBins = 128;
 
 // Exclusive prefix sum of v over the block's threads; the sum of all in *total.
 __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
@@ -221,91 +234,146 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   return base + x - v;
 }
 
-// The keys are looked at in the CTA's slice order: element i * kLongThreads + tid of a round
-// is thread tid's i-th key, so a warp's i-th keys are 32 consecutive elements, and word
-// i * kWarps + warp of a bit mask over the round holds their bits.
-// kKeys: keys of a thread.
-template <int kKeys>
-__global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(const SelectArgs a) {
-  constexpr int kRound = kLongThreads * kKeys;  // keys of the CTA at once
-  __shared__ __align__(16) int hist[kPasses][kDigitBins];
-  __shared__ int coarse[kPasses][kCoarse];
-  __shared__ uint32_t tail[kTail];       // this CTA's keys in the threshold's bin
-  __shared__ uint32_t mask_gt[kLongThreads], mask_eq[kLongThreads];
+// Bits of eight keys whose upper halves, masked, are above u (over) or u itself (same).
+__device__ __forceinline__ void compare8(const uint4& q, uint32_t mask, uint32_t u, uint32_t& over,
+                                         uint32_t& same) {
+  const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+  over = same = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = h[i] & mask, b = (h[i] >> 16) & mask;
+    over |= (a > u ? 1u << (2 * i) : 0u) | (b > u ? 2u << (2 * i) : 0u);
+    same |= (a == u ? 1u << (2 * i) : 0u) | (b == u ? 2u << (2 * i) : 0u);
+  }
+}
+
+// The few keys whose lower half matters, those with the threshold's upper half, are read
+// again (from L2).  cap: keys of the CTA at once, a multiple of 32.  kCtas: CTAs of an SM.
+template <int kCtas>
+__global__ void __launch_bounds__(kLongThreads, kCtas)
+    evict_select_long_kernel(const SelectArgs a, int cap) {
+  extern __shared__ uint4 eights[];
+  __shared__ __align__(16) int hist[kDigitBins];  // of 11 bits
+  __shared__ int coarse[kCoarse], low[32];        // its sums; of 5 bits
+  __shared__ uint32_t tail[kTail];                // this CTA's keys in the threshold's bin
+  __shared__ int tail_at[kTail];                  // and where they are
+  __shared__ __align__(16) int tail_hist[3][kTailBins];  // of seven bits
+  __shared__ uint32_t mask_gt[kLongKeys / 32], mask_eq[kLongKeys / 32];
   __shared__ int warp_sums[kWarps];
-  __shared__ int bins[kCoarse];          // the cluster's sums of the bins looked at
-  __shared__ int tail_count;
+  __shared__ int bins[kCoarse];                   // the cluster's sums of the bins looked at
+  __shared__ int tail_count, counts[2];
   __shared__ int found_bin, found_above, found_count;
+  uint16_t* const halves = reinterpret_cast<uint16_t*>(eights);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Row w = row_of(a, blockIdx.x / C, rank == 0 && tid == 0);
 
-  // this CTA's slice of the candidates, in rounds of kRound
+  // this CTA's slice of the candidates, in rounds of cap
   const int per = (w.M + C - 1) / C;
   const int lo = w.f + min(w.M, rank * per), len = max(0, min(per, w.f + w.M - lo));
-  const int rounds = (per + kRound - 1) / kRound;
+  const int rounds = (per + cap - 1) / cap;
   const float* const vals = w.sums + lo;
-  uint32_t key[kKeys];
-  auto load = [&](int round) {
+  auto load = [&](int round, bool count) {
+    constexpr int U = kCtas == 2 ? 16 : 8;  // loads in flight
+    const float* const at = vals + static_cast<int64_t>(round) * cap;
+    const int n = min(len - round * cap, cap), n8 = (n + 7) & ~7;
+    for (int p0 = tid; p0 < n8; p0 += U * kLongThreads) {
+      float x[U];
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int p = round * kRound + i * kLongThreads + tid;
-      key[i] = p < len ? __float_as_uint(__ldg(vals + p)) : 0u;
-    }
+      for (int i = 0; i < U; ++i) {
+        const int p = p0 + i * kLongThreads;
+        x[i] = p < n ? __ldg(at + p) : 0.f;
+      }
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int p = round * kRound + i * kLongThreads + tid;
-      key[i] = p < len ? key_of(__uint_as_float(key[i])) : 0u;  // 0: no token
+      for (int i = 0; i < U; ++i) {
+        const int p = p0 + i * kLongThreads;
+        const uint32_t k = p < n ? key_of(x[i]) : 0u;  // 0: no token
+        if (p < n8) halves[p] = static_cast<uint16_t>(k >> 16);
+        if (count && p < n) atomicAdd(&hist[k >> 21], 1);
+      }
     }
+    __syncthreads();
   };
-  if (rounds == 1) load(0);  // the usual row: read once
-  for (int i = tid; i < kPasses * kDigitBins; i += kLongThreads) (&hist[0][0])[i] = 0;
+  auto eights_of = [&](int round) { return (max(0, min(len - round * cap, cap)) + 7) / 8; };
+  // use(bit, key) for each key of `same` of the eight at v: all of them read at once
+  auto each = [&](int round, int v, uint32_t same, auto use) {
+    const float* const at = vals + static_cast<int64_t>(round) * cap + 8 * v;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = same >> i & 1 ? __ldg(at + i) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (same >> i & 1) use(i, key_of(x[i]));
+  };
+  for (int i = tid; i < kDigitBins; i += kLongThreads) hist[i] = 0;
+  for (int i = tid; i < kLongKeys / 32; i += kLongThreads) mask_gt[i] = mask_eq[i] = 0;
+  if (tid < 32) low[tid] = 0;
+  if (tid < 3 * kTailBins) (&tail_hist[0][0])[tid] = 0;
   if (tid == 0) tail_count = 0;
-  keep_ends(w, rank * kLongThreads + tid, C * kLongThreads);
   __syncthreads();
+  // a row of one round is read from memory once
+  const bool cuts = w.m > 0 && w.m < w.M;
+  if (rounds == 1) load(0, cuts);
+  keep_ends(w, rank * kLongThreads + tid, C * kLongThreads);
 
   // The threshold t: the m-th largest key; `above` keys are larger.  m == M: everything is
   // above 0.
   uint32_t t = 0;
   int above = 0;
-  if (w.m > 0 && w.m < w.M) {
+  bool masked = false;  // the masks are there
+  if (cuts) {
     int shift = 32;
     for (int pass = 0; pass < kPasses; ++pass) {
-      const int bits = pass < 2 ? 11 : 10;
-      const uint32_t fixed = shift == 32 ? 0u : ~0u << shift;
+      const int bits = pass % 2 == 0 ? 11 : 5;
       shift -= bits;
+      if (pass == 2) {  // every CTA is past its reads of the first two passes
+        for (int i = tid; i < kDigitBins; i += kLongThreads) hist[i] = 0;
+      }
+      if (pass == 3 && tid < 32) low[tid] = 0;
+      __syncthreads();
       for (int round = 0; round < rounds; ++round) {
-        if (rounds > 1) load(round);
-        if (pass == 0) {  // no token counts in bin 0, which no key's digit is
+        if (rounds > 1) load(round, pass == 0);
+        if (pass == 0) continue;
+        for (int v = tid; v < eights_of(round); v += kLongThreads) {
+          uint32_t over, same;
+          const uint4 q = eights[v];
+          compare8(q, pass == 1 ? 0xffe0u : 0xffffu, t >> 16, over, same);
+          if (pass == 1) {
+            const uint32_t h[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) atomicAdd(&hist[0][key[i] >> 21], 1);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if ((key[i] & fixed) == t)
-              atomicAdd(&hist[pass][(key[i] >> shift) & ((1u << bits) - 1)], 1);
+            for (int i = 0; i < 8; ++i)
+              if (same >> i & 1) atomicAdd(&low[h[i / 2] >> (16 * (i % 2)) & 31], 1);
+          } else if (same != 0) {
+            each(round, v, same, [&](int, uint32_t k) {
+              if (pass == 2) atomicAdd(&hist[k >> 5 & 2047], 1);
+              else if (k >> 5 == t >> 5) atomicAdd(&low[k & 31], 1);
+            });
+          }
         }
+        if (rounds > 1) __syncthreads();
       }
       __syncthreads();
-      {
-        const int4 h = *reinterpret_cast<const int4*>(&hist[pass][4 * tid]);
+      if (bits == 11) {
+        const int4 h = *reinterpret_cast<const int4*>(&hist[4 * tid]);
         int n = h.x + h.y + h.z + h.w;
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        if ((tid & 7) == 0) coarse[pass][tid >> 3] = n;
+        if ((tid & 7) == 0) coarse[tid >> 3] = n;
       }
       cluster.sync();
       // the cluster's sums of 64 runs of 32 bins, then of the bins of the run that counts:
       // eight threads a sum, a CTA's share each
-#pragma unroll
-      for (int level = 0; level < 2; ++level) {
-        const int width = level == 0 ? kCoarse : 32, first = level == 0 ? 0 : 32 * found_bin;
+      for (int level = bits == 11 ? 0 : 1; level < 2; ++level) {
+        const int width = level == 0 ? kCoarse : 32;
+        const int first = level == 0 || bits == 5 ? 0 : 32 * found_bin;
         const int q = tid & 7, at = tid >> 3;
         int n = 0;
         if (q < C && at < width)
-          n = *cluster.map_shared_rank(level == 0 ? &coarse[pass][at] : &hist[pass][first + at], q);
+          n = *cluster.map_shared_rank(bits == 5    ? &low[at]
+                                       : level == 0 ? &coarse[at]
+                                                    : &hist[first + at], q);
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         if (q == 0) bins[at] = at < width ? n : 0;
@@ -334,21 +402,29 @@ __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(cons
         above = found_above;
       }
       t |= static_cast<uint32_t>(found_bin) << shift;
-      const int left = found_count;  // keys in the bin
+      int left = found_count;  // keys in the bin
       if (shift == 0) break;
-      if (left > kTail) {
+      if (left > kTail || shift < 16) {
         __syncthreads();  // found_* may be written again
         continue;
       }
       // Few keys in the bin: every CTA takes them all and finds the rest of the threshold's
       // bits by counting, from the highest; done early once the count is the number wanted.
-      const uint32_t prefix = ~0u << shift;
       for (int round = 0; round < rounds; ++round) {
-        if (rounds > 1) load(round);
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i)
-          if ((key[i] & prefix) == t) tail[atomicAdd(&tail_count, 1)] = key[i];
+        if (rounds > 1) load(round, false);
+        for (int v = tid; v < eights_of(round); v += kLongThreads) {
+          uint32_t over, same;
+          compare8(eights[v], 0xffffu << (shift - 16) & 0xffffu, t >> 16, over, same);
+          if (rounds == 1) reinterpret_cast<uint8_t*>(mask_gt)[v] = static_cast<uint8_t>(over);
+          for (; same != 0; same &= same - 1)
+            tail_at[atomicAdd(&tail_count, 1)] = round * cap + 8 * v + __ffs(same) - 1;
+        }
+        if (rounds > 1) __syncthreads();
       }
+      masked = rounds == 1;
+      __syncthreads();
+      const int mine = tail_count;
+      for (int i = tid; i < mine; i += kLongThreads) tail[i] = key_of(__ldg(vals + tail_at[i]));
       cluster.sync();
       uint32_t k[kTailKeys] = {};
       int begin = 0;
@@ -362,98 +438,136 @@ __global__ void __launch_bounds__(kLongThreads, 2) evict_select_long_kernel(cons
         }
         begin += n;
       }
-      const int want = w.m - above;
-      int have = left;
-      for (int bit = shift - 1; bit >= 0 && have != want; --bit) {
-        const uint32_t u = t | (1u << bit);
-        int n = 0;
+      // The rest of the threshold, seven bits at a time, until all keys of a bin stay.
+      for (int i = 0; shift > 0 && above + left != w.m; ++i) {
+        const int bits7 = shift < 7 ? shift : 7;
+        const uint32_t fixed = ~0u << shift;
+        shift -= bits7;
 #pragma unroll
-        for (int i = 0; i < kTailKeys; ++i)
-          if (i * kLongThreads < left) n += __syncthreads_count(k[i] >= u);
-        if (n >= want) {
-          t = u;
-          have = n;
+        for (int j = 0; j < kTailKeys; ++j)
+          if ((k[j] & fixed) == t) atomicAdd(&tail_hist[i][k[j] >> shift & ((1u << bits7) - 1)], 1);
+        __syncthreads();
+        if (warp == 0) {  // from the top: lane l holds bins 127 - 4 l .. 124 - 4 l
+          const int4 h = *reinterpret_cast<const int4*>(&tail_hist[i][kTailBins - 4 - 4 * lane]);
+          const int sum = h.x + h.y + h.z + h.w;
+          int x = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          int before = above + x - sum;
+          const int n[4] = {h.w, h.z, h.y, h.x};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (before < w.m && before + n[j] >= w.m) {
+              found_bin = kTailBins - 1 - 4 * lane - j;
+              found_above = before;
+              found_count = n[j];
+            }
+            before += n[j];
+          }
         }
+        __syncthreads();
+        t |= static_cast<uint32_t>(found_bin) << shift;
+        above = found_above;
+        left = found_count;
       }
-      if (have == want) {
+      if (above + left == w.m) {
         t -= 1;  // all keys of at least t stay: those above t - 1, and none equal to it
         above = w.m;
-      } else {
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < kTailKeys; ++i)
-          if (i * kLongThreads < left) n += __syncthreads_count(k[i] > t);
-        above += n;
+      }
+      if (masked) {  // the keys of the bin join those above it
+        for (int i = tid; i < mine; i += kLongThreads) {
+          const int p = tail_at[i];
+          if (tail[i] > t) atomicOr(&mask_gt[p >> 5], 1u << (p & 31));
+          else if (tail[i] == t) atomicOr(&mask_eq[p >> 5], 1u << (p & 31));
+        }
+        __syncthreads();
       }
       break;
     }
   }
   const int ties = w.m == w.M ? 0 : w.m - above;  // keys equal to t that stay
 
-  // Bit masks of a round's keys above t, and equal to it if some of those stay.
-  auto masks = [&] {
-    uint32_t g = 0, e = 0;  // lane i keeps the words of the warp's i-th keys
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const uint32_t x = __ballot_sync(0xffffffffu, key[i] > t);
-      g = lane == i ? x : g;
+  // Bit masks of a round's keys above t, and equal to it; words behind the round's keys are
+  // not used.
+  auto masks = [&](int round) {
+    const uint32_t th = t >> 16;
+    for (int v = tid; v < eights_of(round); v += kLongThreads) {
+      uint32_t over, same, equal = 0;
+      compare8(eights[v], 0xffffu, th, over, same);
+      if (th == 0) same = 0;  // no tokens
+      if (same != 0)
+        each(round, v, same, [&](int i, uint32_t k) {
+          if (k > t) over |= 1u << i;
+          if (k == t) equal |= 1u << i;
+        });
+      reinterpret_cast<uint8_t*>(mask_gt)[v] = static_cast<uint8_t>(over);
+      reinterpret_cast<uint8_t*>(mask_eq)[v] = static_cast<uint8_t>(equal);
     }
-    if (ties > 0) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        const uint32_t y = __ballot_sync(0xffffffffu, key[i] == t);
-        e = lane == i ? y : e;
-      }
-    }
-    mask_gt[lane * kWarps + warp] = g;  // empty words behind the kKeys-th
-    mask_eq[lane * kWarps + warp] = e;
     __syncthreads();
+  };
+  // A thread has `words` (one or two) consecutive words of a round's masks.
+  const int words = (cap / 32 + kLongThreads - 1) / kLongThreads;
+  auto bits_of = [&](const uint32_t* mask, int round) {
+    const int i = words * tid, left = 8 * eights_of(round) - 32 * i;  // bits from there on
+    uint64_t x = left > 0 ? mask[i] : 0u;
+    if (words == 2 && left > 32) x |= static_cast<uint64_t>(mask[i + 1]) << 32;
+    const int n = min(left, 32 * words);
+    return n <= 0 || n == 64 ? x : x & ((1ull << n) - 1);
   };
   // How many of each the CTAs before have.
   int gt0 = 0, eq0 = 0;
   if (w.m > 0) {
     int total_gt = 0, total_eq = 0;
     for (int round = 0; round < rounds; ++round) {
-      if (rounds > 1) load(round);
-      masks();
-      total_gt += __popc(mask_gt[tid]);
-      total_eq += __popc(mask_eq[tid]);
+      if (rounds > 1) load(round, false);
+      if (!masked) masks(round);
+      total_gt += __popcll(bits_of(mask_gt, round));
+      total_eq += __popcll(bits_of(mask_eq, round));
       if (rounds > 1) __syncthreads();
     }
     int all_gt, all_eq;
     block_prefix(total_gt, warp_sums, &all_gt);
     block_prefix(total_eq, warp_sums, &all_eq);
     if (tid == 0) {
-      coarse[0][0] = all_gt;
-      coarse[0][1] = all_eq;
+      counts[0] = all_gt;
+      counts[1] = all_eq;
     }
   }
   cluster.sync();
   if (w.m > 0) {
     for (int q = 0; q < rank; ++q) {
-      const int* const c = cluster.map_shared_rank(&coarse[0][0], q);
+      const int* const c = cluster.map_shared_rank(&counts[0], q);
       gt0 += c[0];
       eq0 += c[1];
     }
     for (int round = 0; round < rounds; ++round) {
       if (rounds > 1) {
-        load(round);
-        masks();
+        load(round, false);
+        masks(round);
       }
-      // a thread places the tokens of one word
-      const uint32_t g = mask_gt[tid], e = mask_eq[tid];
+      const uint64_t g = bits_of(mask_gt, round), e = bits_of(mask_eq, round);
       int all_gt, all_eq = 0;
-      const int ng0 = gt0 + block_prefix(__popc(g), warp_sums, &all_gt);
-      const int ne0 = eq0 + (ties > 0 ? block_prefix(__popc(e), warp_sums, &all_eq) : 0);
-      for (uint32_t left = g | e; left != 0; left &= left - 1) {
-        const uint32_t bit = left & (0u - left);
-        const int ng = ng0 + __popc(g & (bit - 1)), ne = ne0 + __popc(e & (bit - 1));
-        if ((g & bit) || ne < ties) {
-          const int p = round * kRound + 32 * tid + __ffs(bit) - 1;
-          const int j = w.f + ng + min(ne, ties);
-          w.kept[j] = lo + p;
-          w.out[j] = vals[p];
-        }
+      const int ng0 = gt0 + block_prefix(__popcll(g), warp_sums, &all_gt);
+      const int ne0 = eq0 + (ties > 0 ? block_prefix(__popcll(e), warp_sums, &all_eq) : 0);
+      // the round's tokens in order, in the keys' place, then copied side by side
+      const int at0 = gt0 + min(eq0, ties);
+      const int count = gt0 + all_gt + min(eq0 + all_eq, ties) - at0;
+      for (uint64_t left = g | e; left != 0; left &= left - 1) {
+        const uint64_t bit = left & (0ull - left);
+        const int ng = ng0 + __popcll(g & (bit - 1)), ne = ne0 + __popcll(e & (bit - 1));
+        if ((g & bit) || ne < ties)
+          halves[ng + min(ne, ties) - at0] =
+              static_cast<uint16_t>(32 * words * tid + 63 - __clzll(static_cast<long long>(bit)));
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int j = tid; j < count; j += kLongThreads) {
+        const int p = round * cap + halves[j];
+        w.kept[w.f + at0 + j] = lo + p;
+        w.out[w.f + at0 + j] = __ldg(vals + p);
       }
       gt0 += all_gt;
       eq0 += all_eq;
@@ -592,11 +706,17 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_v8_kernel(const G
   }
 }
 
-template <int kKeys>
-int launch_long(const SelectArgs& a, int64_t rows, int cluster, cudaStream_t st) {
+template <int kCtas>
+int launch_long(const SelectArgs& a, int64_t rows, int cluster, int cap, cudaStream_t st) {
+  static SmemOnce once;
+  const int rc = allow_dynamic_smem(
+      once, reinterpret_cast<const void*>(evict_select_long_kernel<kCtas>),
+      kLongKeys * sizeof(uint16_t));
+  if (rc != PKV_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
   cfg.blockDim = dim3(kLongThreads);
+  cfg.dynamicSmemBytes = cap * sizeof(uint16_t);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -605,12 +725,15 @@ int launch_long(const SelectArgs& a, int64_t rows, int cluster, cudaStream_t st)
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_select_long_kernel<kKeys>, a));
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_select_long_kernel<kCtas>, a, cap));
   return PKV_OK;
 }
 
-// Short rows take a warp each.  Long ones: as many CTAs, up to eight, as hold the row in
-// registers, up to 16,384 keys each; a longer row is read from memory once a pass.
+// Rows of up to 2,048 columns take a warp each: 2,560 rows of 2,048 took 33 us so, against 54
+// with a CTA's histograms.  A longer row takes a cluster of as many CTAs, up to eight, as
+// leave no SM idle (two on each): 8 rows of 131,072 took 20.4 us with the four CTAs that hold
+// one, 15.3 with eight; 64 rows of 32,768 20.8 with one and 15.8 with four.  A row that eight
+// CTAs do not hold is read once a pass.
 int launch_select(const SelectArgs& a, int64_t rows, cudaStream_t st) {
   if (a.cols <= kShortCols) {
     const int64_t ctas = (rows + kShortWarps - 1) / kShortWarps;
@@ -618,12 +741,21 @@ int launch_select(const SelectArgs& a, int64_t rows, cudaStream_t st) {
     PKV_CUDA(cudaGetLastError());
     return PKV_OK;
   }
-  constexpr int kMost = kLongThreads * kLongKeys;
-  if (a.cols <= kMost / 4) return launch_long<kLongKeys / 4>(a, rows, 1, st);
-  if (a.cols <= kMost / 2) return launch_long<kLongKeys / 2>(a, rows, 1, st);
+  int sms = 0, dev = 0;
+  const int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kMost < a.cols) cluster *= 2;
-  return launch_long<kLongKeys>(a, rows, cluster, st);
+  while (cluster < kMaxCluster &&
+         (static_cast<int64_t>(cluster) * kLongKeys < a.cols ||
+          (a.cols / cluster > kSlice && rows * cluster <= sms)))
+    cluster *= 2;
+  const int per = static_cast<int>((static_cast<int64_t>(a.cols) + cluster - 1) / cluster);
+  const int cap = per < kLongKeys ? (per + 31) / 32 * 32 : kLongKeys;
+  // few keys a CTA and more CTAs than two an SM: four, with half the loads in flight each
+  // (2,048 rows of 8,192: 111 us with two, 92 with four; 64 of 32,768: 17.4 and 19.2)
+  return cap <= kSmallSlice && rows * cluster > 2 * sms
+             ? launch_long<4>(a, rows, cluster, cap, st)
+             : launch_long<2>(a, rows, cluster, cap, st);
 }
 
 }  // namespace
