@@ -18,6 +18,11 @@
 // better than itself.  Entries are compared as integer keys and no two are equal (equal
 // values are told apart by their position), so the order of collection does not matter.
 //
+// What bounds it: many rows of large vocabularies the memory (64 x 8 rows of 131,072 fp32
+// logits, 268 MB: 53.5 us, 5.0 TB/s), small calls the chain of steps of which each waits for
+// the one before: a tile's loads, its threshold, the list and its ranking, a ticket, the merge
+// (4 rows of 32,000: 9.5 us; 32 x 4 of 65,537 fp16: 20.2 us, 17 MB).
+//
 // Precision: candidates of different beams may lie next to each other, so a thread's sums
 // carry their rounding errors, sums across threads are 64-bit integers, and lse and the
 // scores are pairs of fp32 values (48 bits).  Only the score handed out is rounded to fp32.
@@ -46,7 +51,6 @@ constexpr int kMaxEntries = 8192;  // entries a merge takes: parts * N, beams * 
 constexpr int kOneMerge = 2048;
 constexpr int kElements = 16;      // logits of a tile a thread holds
 constexpr int kTile = kElements * kThreads;
-constexpr int kFew = 64;           // threads whose candidates are listed without a threshold
 constexpr int kMaxSmem = 128 << 10;  // above kMaxOut threads' 64 entries of 24 bytes (2 kMaxEntries dealt)
 constexpr int kList = kMaxOut + kMaxOut * kElements;  // entries of the list
 
@@ -156,7 +160,8 @@ __device__ __forceinline__ ScoreKey shfl_xor(const ScoreKey& k, int o) {
 }
 
 // Threads whose best entries are merged before the threshold is sought: about four
-// groups of them for each entry wanted, in 32 to 256 groups.
+// groups of them for each entry wanted, in 32 to 256 groups.  (Ranking all 256 threads' best
+// for 8 wanted of one request: 19.1 us a call against 9.5.)
 __host__ __device__ constexpr int group_of(int n) {
   return n <= 8 ? 8 : (n <= 16 ? 4 : (n <= 32 ? 2 : 1));
 }
@@ -525,14 +530,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
       if (care) {
 #pragma unroll
         for (int i = 0; i < kElements; ++i) v[i] = fmaxf(v[i], -INFINITY);  // NaN: banned
-        const int listing = __syncthreads_count(lists);
-        if (listing > kFew) {
-          // the thread's best: the lowest token of its largest logit
-          const uint32_t same = lists ? at_least(v, most) : 0u;
-          const int token = Tile<T>::token(at, __ffs(same) - 1);
-          t = threshold_of(same != 0 && token < V ? token_key(most, token) : 0, N, sh.row);
-          if (t != 0) floor = fmaxf(floor, key_logit(t));
-        }
+        // the thread's best: the lowest token of its largest logit
+        const uint32_t same = lists ? at_least(v, most) : 0u;
+        const int token = Tile<T>::token(at, __ffs(same) - 1);
+        t = threshold_of(same != 0 && token < V ? token_key(most, token) : 0, N, sh.row);
+        if (t != 0) floor = fmaxf(floor, key_logit(t));
       }
       if (lists) {
         for (uint32_t left = at_least(v, floor); left != 0; left &= left - 1) {
@@ -667,10 +669,13 @@ struct BeamLayout {
   size_t row_ticket, seq_ticket, part_max, part_sum, part_top, row_top, total;
 };
 
-// Parts a row is cut into: as many as fill the SMs once, at four CTAs each.
+// Parts a row is cut into: as many as fill the SMs once, at three CTAs each.  Two, three, four:
+// 50 x 4 rows of 128,256 fp32 logits 33.3, 27.6, 27.1 us (too few CTAs to hide their steps from
+// one another); 64 x 4 of 32,000 bf16 17.1, 17.1, 19.2 and 32 x 4 of 65,537 fp16 19.8, 20.2,
+// 22.0 (every part has its first tile, its list and its place in the merge).
 int parts_of(int64_t rows, int32_t V, int32_t N, int sms) {
   const int64_t tiles = (static_cast<int64_t>(V) + kTile - 1) / kTile;
-  int64_t parts = rows > 0 ? 4 * static_cast<int64_t>(sms) / rows : 1;
+  int64_t parts = rows > 0 ? 3 * static_cast<int64_t>(sms) / rows : 1;
   parts = parts < kMaxEntries / N ? parts : kMaxEntries / N;
   parts = parts < tiles ? parts : tiles;
   parts = parts > 1 ? parts : 1;
