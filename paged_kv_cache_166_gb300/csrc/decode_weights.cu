@@ -14,10 +14,10 @@
 // The kernel below reads the scores once, and reads and writes the sums once.  Most scores come
 // from L2, where the attention's stores ask to be kept ahead of the K and V that stream
 // through, and a line that has been read is dropped: nothing of it need go to memory.  70B
-// shape (256 sequences, 451,896 tokens, 1.85 GB of K and V, 116 MB of scores): both kernels 336
-// us, of which the attention without the weights takes 286; 13B shape (509 MB, 4 MB) 95 of 87;
+// shape (256 sequences, 451,896 tokens, 1.85 GB of K and V, 116 MB of scores): both kernels 332
+// us, of which the attention without the weights takes 286; 13B shape (509 MB, 4 MB) 94 of 87;
 // 8 sequences to 131,072 tokens over an fp8 cache (1.75 GB, 219 MB of scores, more than L2
-// holds) 389 of 281.
+// holds) 381 of 281.
 // Every sum belongs to one thread and its heads are added in order: no atomics, the same
 // bits on every run.
 #define PKV_DECODE_TEMPLATES_ONLY
@@ -179,7 +179,7 @@ int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
   int sms = 0, dev = 0;
   rc = device_sm_count(&sms, &dev);
   if (rc != PKV_OK) return rc;
-  // eight CTAs on an SM (four: 70B shape 338 us against 336), but no more warps than a batch
+  // eight CTAs on an SM (four: 70B shape 338 us, then 336 with eight), but no more warps than a batch
   // this wide can have steps
   const int64_t most = (static_cast<int64_t>(h.S) * h.Hkv *
                             ((static_cast<int64_t>(h.MAXB) * h.block_size + kTok - 1) / kTok) +
