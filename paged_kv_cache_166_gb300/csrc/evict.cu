@@ -594,6 +594,11 @@ struct GatherArgs {
   int32_t tokens;  // kept tokens of one CTA, at most kGatherThreads
 };
 
+// New V tiles of one CTA: a thread has one of the D rows of one.
+__host__ __device__ __forceinline__ int v8_tiles(int D) {
+  return D < kGatherThreads ? kGatherThreads / D : 1;
+}
+
 // Slot row (in rows of the cache) of position p of a table row, or -1.
 __device__ __forceinline__ int64_t cache_row(const int32_t* table, int max_blocks, int p, int B,
                                              int NB, int Hkv, int h) {
@@ -659,51 +664,67 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Gath
   }
 }
 
-// V of 8-bit caches: tiles [D x 16 bytes], a token one byte of every row.  A CTA fills
-// one new tile, a thread whole 16-byte rows of it; consecutive kept tokens often come
-// from one old tile, whose row is then read once.
-__global__ void __launch_bounds__(kGatherThreads) evict_gather_v8_kernel(const GatherArgs a) {
+// V of 8-bit caches: tiles [D x 16 bytes], a token one byte of every row.  A thread fills a
+// 16-byte row of a new tile (a CTA as many tiles as it has rows for); consecutive kept tokens
+// often come from one old tile, whose row is then read once, and eight tokens' rows are on
+// their way together (select and gather of 82 sequences of 1,334 tokens cut to 207, 16 heads:
+// 181 us with one row read behind the other and one tile a CTA, 133 now; of 8 to 131,072 cut to
+// 4,096, 8 heads: 242 and 144).
+__global__ void __launch_bounds__(kGatherThreads, 3) evict_gather_v8_kernel(const GatherArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int64_t src_tile[16];
-  __shared__ int src_byte[16];
+  __shared__ int64_t src_tile[kGatherThreads];  // of 16 tokens a tile, 16 tiles at most
+  __shared__ int src_byte[kGatherThreads];
   const int s = blockIdx.z, h = blockIdx.y;
   const int n = min(max(a.new_lens[s], 0), a.kept_cols);
-  const int j0 = blockIdx.x * 16;
-  if (j0 >= n) return;
-  const int count = min(16, n - j0);
-  const int64_t to = cache_row(a.new_tables + static_cast<int64_t>(s) * a.NEWB, a.NEWB, j0, 16,
-                               a.NB, a.Hkv, h);
-  if (threadIdx.x < 16) {
+  const int tiles = v8_tiles(a.D), first = blockIdx.x * tiles * 16;  // of the CTA; its first token
+  if (first >= n) return;
+  if (static_cast<int>(threadIdx.x) < 16 * tiles) {
+    const int j = first + threadIdx.x;
     int64_t row = -1;
-    if (static_cast<int>(threadIdx.x) < count)
+    if (j < n)
       row = cache_row(a.tables + static_cast<int64_t>(s) * a.MAXB, a.MAXB,
-                      __ldg(a.kept + (static_cast<int64_t>(s) * a.Hkv + h) * a.kept_cols + j0 +
-                            threadIdx.x),
-                      16, a.NB, a.Hkv, h);
+                      __ldg(a.kept + (static_cast<int64_t>(s) * a.Hkv + h) * a.kept_cols + j), 16,
+                      a.NB, a.Hkv, h);
     src_tile[threadIdx.x] = row < 0 ? -1 : row >> 4;
     src_byte[threadIdx.x] = row < 0 ? 0 : fp8_v_pos(static_cast<int>(row & 15));
   }
   __syncthreads();
+  const int mine = tiles == 1 ? 0 : threadIdx.x / a.D, j0 = first + 16 * mine;
+  if (mine >= tiles || j0 >= n) return;
+  const int64_t to = cache_row(a.new_tables + static_cast<int64_t>(s) * a.NEWB, a.NEWB, j0, 16,
+                               a.NB, a.Hkv, h);
   if (to < 0) return;  // reported by the K rows' kernel
-  for (int d = threadIdx.x; d < a.D; d += kGatherThreads) {
+  const int64_t* const tile_of = src_tile + 16 * mine;
+  const int* const byte_of = src_byte + 16 * mine;
+  for (int d = threadIdx.x - mine * a.D; d < a.D; d += kGatherThreads) {
     uint4* const dst = a.vc + (to >> 4) * a.D + d;
     // bytes of tokens that do not move (past n, or from a bad block) stay as they are
-    uint4 w = count < 16 ? *dst : make_uint4(0u, 0u, 0u, 0u);
-    uint8_t* const wb = reinterpret_cast<uint8_t*>(&w);
-    int64_t have = -1;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    bool whole = true;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const int64_t tile = src_tile[t];
-      if (tile < 0) continue;
-      if (tile != have) {
-        x = a.vc[tile * a.D + d];
-        have = tile;
+    for (int t = 0; t < 16; ++t) whole &= tile_of[t] >= 0;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (!whole) w = *dst;
+    uint8_t* const wb = reinterpret_cast<uint8_t*>(&w);
+#pragma unroll
+    for (int t0 = 0; t0 < 16; t0 += 8) {
+      uint4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int64_t tile = tile_of[t0 + u];
+        if (tile >= 0 && (u == 0 || tile != tile_of[t0 + u - 1])) x[u] = a.vc[tile * a.D + d];
       }
-      const int b = src_byte[t];
-      const uint32_t word = (b >> 2) == 0 ? x.x : (b >> 2) == 1 ? x.y : (b >> 2) == 2 ? x.z : x.w;
-      const int at = t < 8 ? 4 * (t >> 1) + (t & 1) : 4 * ((t - 8) >> 1) + 2 + (t & 1);
-      wb[at] = static_cast<uint8_t>(word >> (8 * (b & 3)));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int t = t0 + u;
+        const int64_t tile = tile_of[t];
+        if (tile < 0) continue;
+        if (u > 0 && tile == tile_of[t - 1]) x[u] = x[u > 0 ? u - 1 : 0];
+        const int b = byte_of[t];
+        const uint32_t word =
+            (b >> 2) == 0 ? x[u].x : (b >> 2) == 1 ? x[u].y : (b >> 2) == 2 ? x[u].z : x[u].w;
+        const int at = t < 8 ? 4 * (t >> 1) + (t & 1) : 4 * ((t - 8) >> 1) + 2 + (t & 1);
+        wb[at] = static_cast<uint8_t>(word >> (8 * (b & 3)));
+      }
     }
     *dst = w;
   }
@@ -881,7 +902,8 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
     return ok();
   }
   PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_gather_kernel<false>, a));
-  cfg.gridDim = dim3((kept_cols + 15) / 16, num_kv_heads, num_seqs);
+  const int span = 16 * v8_tiles(head_dim);
+  cfg.gridDim = dim3((kept_cols + span - 1) / span, num_kv_heads, num_seqs);
   PKV_CUDA(cudaLaunchKernelEx(&cfg, evict_gather_v8_kernel, a));
   return ok();
 }

@@ -493,6 +493,27 @@ def test_gather(kind, B, D):
     assert np.array_equal(k.float().cpu().numpy(), kw) and np.array_equal(v.float().cpu().numpy(), vw)
 
 
+@pytest.mark.parametrize("D", [16, 48, 64, 128, 256, 512])
+def test_gather_v8_leaves_the_slots_of_bad_places(D):
+    """A whole tile one of whose tokens cannot be moved: its slot keeps its bytes."""
+    k, v = pools("int8", 12, 2, 16, D, 5)
+    k0, v0 = k.cpu().numpy(), v.cpu().numpy()
+    n = 40
+    kept = np.tile(np.arange(n) * 2, (1, 2, 1))
+    kept[0, :, 5] = 4000
+    kept[0, 1, 33] = -2
+    pkv().paged_evict_gather(k, v, i32([[1, 9, 2, 7, 0]]), i32(kept), i32([n]), i32([[4, 11, 5]]))
+    torch.cuda.synchronize()
+    want = v0.copy()
+    for h in range(2):
+        for j in range(n):
+            p = kept[0, h, j]
+            if 0 <= p < 80:
+                src, dst = [1, 9, 2, 7, 0][p // 16], [4, 11, 5][j // 16]
+                want[dst, h, :, ofp8.V_POS[j % 16]] = v0[src, h, :, ofp8.V_POS[p % 16]]
+    assert np.array_equal(v.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("kind,NB", [("bf16", 140000), ("int8", 140000)])
 def test_gather_beyond_32_bit_offsets(kind, NB):
     H, B, D = 8, 16, 128
