@@ -424,8 +424,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Pairs of f32 values in one 64-bit register, operated on at once (each operation rounded
-// to nearest by itself).
+// Pairs of f32 values in one 64-bit register, operated on at once, rounded to nearest.  (No
+// product alone: one that is added to something comes out fused with the addition.)
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t p;
   asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
@@ -437,11 +437,6 @@ __device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {

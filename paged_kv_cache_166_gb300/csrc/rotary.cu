@@ -11,7 +11,7 @@
 //
 // Arithmetic: fp32 with every product and sum rounded once (no contraction), then one
 // rounding to q's type, or one quantisation straight from fp32 for an 8-bit cache: the
-// results are those of the written formula whatever the compiler does.  cos and sin
+// results are those of the written formula, the same bits on every path.  cos and sin
 // come from a table of fp32 values computed in 64 bits: an angle p * f_i near 131,072
 // has only 2^-7 left of its fraction in fp32.
 //
@@ -107,7 +107,10 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], c
 }
 
 // The turned pieces: y1 = x1 c - x2 s, y2 = x2 c + x1 s (half layout: x1 and x2 are a piece
-// of either half; interleaved: elements 2i and 2i + 1 of x1), two pairs at a time.
+// of either half; interleaved: elements 2i and 2i + 1 of x1).  One pair at a time: products
+// and sums of two pairs packed in 64-bit registers (mul and add .f32x2) come out fused, so that
+// a token's bits would depend on the path that its alignment allows.  They were little
+// faster: a step of 256 tokens 3.6 us against 3.7, an fp8 prompt 25.8 against 26.0.
 template <typename T, int VEC, bool kInter>
 __device__ __forceinline__ void turn(const Pack<T, VEC>& x1, const Pack<T, VEC>& x2,
                                      const float (&c)[kInter ? VEC / 2 : VEC],
@@ -118,22 +121,11 @@ __device__ __forceinline__ void turn(const Pack<T, VEC>& x1, const Pack<T, VEC>&
   auto b = [&](int i) { return widen(kInter ? x1.x[2 * i + 1] : x2.x[i]); };
   auto first = [&](int i) -> float& { return kInter ? y1[2 * i] : y1[i]; };
   auto second = [&](int i) -> float& { return kInter ? y1[2 * i + 1] : y2[i]; };
-  if constexpr (kAng % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < kAng; i += 2) {
-      const uint64_t p = ptx::pair(a(i), a(i + 1)), r = ptx::pair(b(i), b(i + 1));
-      const uint64_t co = ptx::pair(c[i], c[i + 1]), si = ptx::pair(s[i], s[i + 1]);
-      const uint64_t ns = ptx::pair(-s[i], -s[i + 1]);
-      ptx::unpair(ptx::add2(ptx::mul2(p, co), ptx::mul2(r, ns)), first(i), first(i + 1));
-      ptx::unpair(ptx::add2(ptx::mul2(r, co), ptx::mul2(p, si)), second(i), second(i + 1));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kAng; ++i) {
-      const float p = a(i), r = b(i);
-      first(i) = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
-      second(i) = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
-    }
+  for (int i = 0; i < kAng; ++i) {
+    const float p = a(i), r = b(i);
+    first(i) = __fsub_rn(__fmul_rn(p, c[i]), __fmul_rn(r, s[i]));
+    second(i) = __fadd_rn(__fmul_rn(r, c[i]), __fmul_rn(p, s[i]));
   }
 }
 
