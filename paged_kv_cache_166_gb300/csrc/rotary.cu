@@ -245,8 +245,8 @@ __device__ __forceinline__ void write_v8(const RotaryArgs& a, int window, int pa
 // 8-bit caches: then V's windows, a.v_parts CTAs each.  VEC: elements a thread moves at once.
 template <typename T, int VEC, bool kInter, int kCodes>
 __global__ void __launch_bounds__(256, kCodes != 0 ? 4 : 3) rotary_write_kernel(const RotaryArgs a) {
-  // a decode launch queued behind may start its prologue; it reads the caches and
-  // q_out only after this grid has completed
+  // a decode launch queued behind may start its prologue; it reads the caches and q_out, and
+  // writes anything that this grid may still read, only after this grid has completed
   asm volatile("griddepcontrol.launch_dependents;");
   using P = Pack<T, VEC>;
   constexpr int kAng = kInter ? VEC / 2 : VEC;  // pairs a thread turns at once
