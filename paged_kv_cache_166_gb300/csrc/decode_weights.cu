@@ -20,6 +20,8 @@
 // holds) 381 of 281.
 // Every sum belongs to one thread and its heads are added in order: no atomics, the same
 // bits on every run.
+#include <mutex>
+
 #define PKV_DECODE_TEMPLATES_ONLY
 #include "decode_attention.cu"
 
@@ -163,8 +165,6 @@ int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
   h.steps = reinterpret_cast<int32_t*>(ws + L.steps);
   h.lse = reinterpret_cast<float*>(ws + L.lse);
   h.scores = reinterpret_cast<float*>(ws + L.scores);
-  rc = dispatch<true>(h, W);
-  if (rc != PKV_OK) return rc;
   SumArgs a{};
   a.scores = h.scores;
   a.lse = h.lse;
@@ -193,6 +193,12 @@ int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // The two launches hand the scores over through the workspace: they are queued one behind
+  // the other, whatever other host threads queue on the stream with the same workspace.
+  static std::mutex queue;
+  const std::lock_guard<std::mutex> both(queue);
+  rc = dispatch<true>(h, W);
+  if (rc != PKV_OK) return rc;
   switch (h.Hq / h.Hkv) {
     case 1: PKV_CUDA(cudaLaunchKernelEx(&cfg, weight_sums_kernel<1>, a)); break;
     case 2: PKV_CUDA(cudaLaunchKernelEx(&cfg, weight_sums_kernel<2>, a)); break;
