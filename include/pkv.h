@@ -514,6 +514,14 @@ int pkv_rotary_frequencies(int32_t rotary_dim, float base, int32_t scaling, floa
                            double* inv_freq);
 
 /*
+ * pkv_rotary_frequencies_f64 — the same with base, factor and the turns in 64 bits: at
+ * position 131,072 a factor of 1.1 rounded to fp32 turns the first pair 0.003 too far.
+ * settings   host double [4]: base, factor, low_turns, high_turns.
+ */
+int pkv_rotary_frequencies_f64(int32_t rotary_dim, const double* settings, int32_t scaling,
+                               int32_t original_length, double* inv_freq);
+
+/*
  * pkv_rotary_table — fills a table of cos and sin for positions 0 .. max_positions-1:
  *   table[p, i] = magnitude * cos(p f_i),  table[p, rotary_dim / 2 + i] = magnitude * sin(p f_i),
  * i < rotary_dim / 2, angles and functions in 64 bits, rounded once to fp32.

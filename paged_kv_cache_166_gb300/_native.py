@@ -83,6 +83,7 @@ SIGNATURES = {
                                             _i32, _i32, _i32, _i32, _f, _p, _p, _sz, _i32, _i32,
                                             _p]),
     "pkv_rotary_frequencies": (ctypes.c_int, [_i32, _f, _i32, _f, _i32, _f, _f, _p]),
+    "pkv_rotary_frequencies_f64": (ctypes.c_int, [_i32, _p, _i32, _i32, _p]),
     "pkv_rotary_table": (ctypes.c_int, [_p, _i32, _f, _i32, _p, _p]),
     "pkv_rotary_write": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _i32, _i32, _p,
                                         _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _i64, _p,

@@ -508,30 +508,39 @@ extern "C" {
 int pkv_rotary_frequencies(int32_t rotary_dim, float base, int32_t scaling, float factor,
                            int32_t original_length, float low_turns, float high_turns,
                            double* inv_freq) {
+  const double settings[4] = {base, factor, low_turns, high_turns};
+  return pkv_rotary_frequencies_f64(rotary_dim, settings, scaling, original_length, inv_freq);
+}
+
+int pkv_rotary_frequencies_f64(int32_t rotary_dim, const double* settings, int32_t scaling,
+                               int32_t original_length, double* inv_freq) {
+  PKV_REQUIRE(settings != nullptr, PKV_ERR_INVALID_ARG, "settings is NULL");
+  const double base = settings[0], factor = settings[1];
+  const double low_turns = settings[2], high_turns = settings[3];
   PKV_REQUIRE(rotary_dim > 0 && rotary_dim % 2 == 0 && rotary_dim <= 2 * kMaxRotaryPairs,
               PKV_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, %d]", rotary_dim,
               2 * kMaxRotaryPairs);
   PKV_REQUIRE(inv_freq != nullptr, PKV_ERR_INVALID_ARG, "inv_freq is NULL");
-  PKV_REQUIRE(std::isfinite(base) && base > 1.f, PKV_ERR_INVALID_ARG, "base must be above 1");
+  PKV_REQUIRE(std::isfinite(base) && base > 1.0, PKV_ERR_INVALID_ARG, "base must be above 1");
   PKV_REQUIRE(scaling >= PKV_ROTARY_PLAIN && scaling <= PKV_ROTARY_BANDS, PKV_ERR_INVALID_ARG,
               "unknown scaling %d", scaling);
-  PKV_REQUIRE(scaling == PKV_ROTARY_PLAIN || (std::isfinite(factor) && factor >= 1.f),
+  PKV_REQUIRE(scaling == PKV_ROTARY_PLAIN || (std::isfinite(factor) && factor >= 1.0),
               PKV_ERR_INVALID_ARG, "factor must be finite and at least 1");
   PKV_REQUIRE(scaling != PKV_ROTARY_BANDS ||
                   (original_length > 0 && std::isfinite(low_turns) && std::isfinite(high_turns) &&
-                   low_turns >= 0.f && high_turns > low_turns),
+                   low_turns >= 0.0 && high_turns > low_turns),
               PKV_ERR_INVALID_ARG,
               "bands need original_length > 0 and 0 <= low_turns < high_turns");
   const double pi = 3.14159265358979323846;
   double b = base;
   if (scaling == PKV_ROTARY_NTK && rotary_dim > 2)
-    b *= std::pow(static_cast<double>(factor), rotary_dim / (rotary_dim - 2.0));
+    b *= std::pow(factor, rotary_dim / (rotary_dim - 2.0));
   for (int32_t i = 0; i < rotary_dim / 2; ++i) {
     double f = std::pow(b, -2.0 * i / rotary_dim);
     if (scaling == PKV_ROTARY_LINEAR) f /= factor;
     if (scaling == PKV_ROTARY_BANDS) {
       const double turns = original_length * f / (2.0 * pi);
-      double t = (turns - low_turns) / (static_cast<double>(high_turns) - low_turns);
+      double t = (turns - low_turns) / (high_turns - low_turns);
       t = t < 0.0 ? 0.0 : (t > 1.0 ? 1.0 : t);
       f *= (1.0 - t) / factor + t;
     }

@@ -564,9 +564,10 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "n
     if scaling not in N.ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(N.ROTARY_SCALINGS)}")
     out = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
-    N.check(N.lib().pkv_rotary_frequencies(rotary_dim, base, N.ROTARY_SCALINGS[scaling], factor,
-                                           original_length, low_turns, high_turns,
-                                           out.data_ptr()))
+    settings = torch.tensor([base, factor, low_turns, high_turns], dtype=torch.float64)
+    N.check(N.lib().pkv_rotary_frequencies_f64(rotary_dim, settings.data_ptr(),
+                                               N.ROTARY_SCALINGS[scaling], original_length,
+                                               out.data_ptr()))
     return out
 
 

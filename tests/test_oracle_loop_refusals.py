@@ -1,0 +1,36 @@
+"""Host-side properties of the decode loop's operators (no GPU): frequencies of settings that
+fp32 does not hold, and arguments that the library's 32-bit integers do not."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import paged_kv_cache_166_gb300 as pkv
+from oracle import rotary as orot
+from paged_kv_cache_166_gb300 import _native as N
+
+
+@pytest.mark.parametrize("kw", [
+    dict(base=10000.1), dict(base=500000.3, scaling="linear", factor=1.1),
+    dict(scaling="ntk", factor=1.3),
+    dict(scaling="bands", factor=2.7, original_length=4000, low_turns=0.9, high_turns=30.1)])
+def test_frequencies_of_settings_in_64_bits(kw):
+    got, want = pkv.rotary_frequencies(128, **kw).numpy(), orot.frequencies(128, **kw)
+    # pow twice (ntk's base is raised to at most -1), a band's weight t of a difference that
+    # is at least 2^-3 of its terms or else multiplies little: some 16 units in the last place
+    assert np.all(np.abs(got - want) <= 16 * 2.0 ** -52 * want)
+
+
+def test_frequencies_f64_refusals_and_agreement():
+    lib = N.lib()
+    out, ref = (ctypes.c_double * 8)(), (ctypes.c_double * 8)()
+    four = ctypes.c_double * 4
+    assert lib.pkv_rotary_frequencies_f64(16, None, 0, 0, out) == N.PKV_ERR_INVALID_ARG
+    for bad in ((1.0, 1, 1, 4), (float("nan"), 1, 1, 4), (float("inf"), 1, 1, 4)):
+        assert lib.pkv_rotary_frequencies_f64(16, four(*bad), 0, 0, out) == N.PKV_ERR_INVALID_ARG
+    assert lib.pkv_rotary_frequencies_f64(16, four(1e4, 0.5, 1, 4), 1, 0, out) == N.PKV_ERR_INVALID_ARG
+    assert lib.pkv_rotary_frequencies_f64(16, four(1e4, 2, 4, 4), 3, 9, out) == N.PKV_ERR_INVALID_ARG
+    for scaling in range(4):
+        assert lib.pkv_rotary_frequencies_f64(16, four(1e4, 2, 1, 4), scaling, 4096, out) == 0
+        assert lib.pkv_rotary_frequencies(16, 1e4, scaling, 2.0, 4096, 1.0, 4.0, ref) == 0
+        assert list(out) == list(ref)
