@@ -525,6 +525,13 @@ def _remember(key, sizes):
     return sizes
 
 
+def _fits(name: str, *values: int) -> None:
+    """The library's sizes are 32-bit; ctypes would cut a larger one off without a word."""
+    for v in values:
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{name} {v} does not fit 32 bits")
+
+
 def _current(dev: torch.device):
     """A context in which ``dev`` is the current device (the library launches there)."""
     return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
@@ -563,6 +570,7 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "n
     ``original_length``, between ``low_turns`` and ``high_turns``)."""
     if scaling not in N.ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(N.ROTARY_SCALINGS)}")
+    _fits("rotary_dim or original_length", rotary_dim, original_length)
     out = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
     settings = torch.tensor([base, factor, low_turns, high_turns], dtype=torch.float64)
     N.check(N.lib().pkv_rotary_frequencies_f64(rotary_dim, settings.data_ptr(),
@@ -580,6 +588,7 @@ def rotary_table(max_positions: int, inv_freq: torch.Tensor, magnitude: float = 
         raise ValueError("inv_freq must be a contiguous float64 [rotary_dim / 2] host tensor")
     if max_positions <= 0:
         raise ValueError("max_positions must be positive")
+    _fits("max_positions", max_positions)
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     rot = 2 * inv_freq.numel()
     table = torch.empty((max_positions, rot), dtype=torch.float32, device=dev)
@@ -711,6 +720,7 @@ def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, c
     if weight_sums.dtype != torch.float32 or weight_sums.dim() != 3 \
             or weight_sums.shape[:2] != (S, Hkv):
         raise ValueError(f"weight_sums must be float32 [{S}, {Hkv}, columns]")
+    _fits("num_warps or columns", num_warps, weight_sums.shape[2])
     scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else ()
     element = kind or q.dtype
     with _current(dev):
@@ -782,6 +792,7 @@ def paged_evict_select(weight_sums: torch.Tensor, context_lens: torch.Tensor,
     min(keep_lens, context_lens) in all.  Their ascending positions go to kept
     [S, Hkv, kept columns] (int32), their sums to new_sums [S, Hkv, new columns], n to
     new_lens [S]."""
+    _fits("first or recent", first, recent)
     dev = _check_cuda(weight_sums, context_lens, keep_lens, kept, new_sums, new_lens)
     if weight_sums.dim() != 3 or kept.dim() != 3 or new_sums.dim() != 3 \
             or weight_sums.shape[:2] != kept.shape[:2] or weight_sums.shape[:2] != new_sums.shape[:2]:
@@ -795,6 +806,7 @@ def paged_evict_select(weight_sums: torch.Tensor, context_lens: torch.Tensor,
         if t.shape != (S,):
             raise ValueError(f"{name} must be [{S}]")
     _check_index(kept, "kept")
+    _fits("columns", weight_sums.shape[2], kept.shape[2], new_sums.shape[2])
     st = _status_ptr(status, dev)
     with _current(dev):
         N.check(N.lib().pkv_evict_select(
@@ -825,6 +837,7 @@ def paged_evict_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table
     if block_tables.dim() != 2 or new_tables.dim() != 2 or kept.dim() != 3 \
             or block_tables.shape[0] != S or new_tables.shape[0] != S or kept.shape[:2] != (S, Hkv):
         raise ValueError("block_tables, new_tables [S, blocks], kept [S, Hkv, columns], new_lens [S]")
+    _fits("columns", kept.shape[2])
     st = _status_ptr(status, dev)
     with _current(dev):
         N.check(N.lib().pkv_evict_gather(
@@ -867,6 +880,7 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.T
         raise ValueError("scores must not be beam_scores")
     _check_index(beams, "beams")
     _check_index(tokens, "tokens")
+    _fits("vocabulary", V)
     code, n = dtype_code(logits), scores.shape[1]
     with _current(dev):
         key = (dev.index, S, K, V, n, code)

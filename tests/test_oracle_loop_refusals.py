@@ -34,3 +34,19 @@ def test_frequencies_f64_refusals_and_agreement():
         assert lib.pkv_rotary_frequencies_f64(16, four(1e4, 2, 1, 4), scaling, 4096, out) == 0
         assert lib.pkv_rotary_frequencies(16, 1e4, scaling, 2.0, 4096, 1.0, 4.0, ref) == 0
         assert list(out) == list(ref)
+
+
+def test_sizes_that_32_bits_do_not_hold_are_refused():
+    """Cut to 32 bits, these would be small valid values."""
+    import torch
+    x, i = torch.zeros(1, 1, 8), torch.zeros(1, dtype=torch.int32)
+    kept = torch.zeros((1, 1, 8), dtype=torch.int32)
+    for kw in (dict(first=1 << 32), dict(recent=(1 << 32) + 3), dict(first=-(1 << 40))):
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.paged_evict_select(x, i, i.clone(), kept, x.clone(), i.clone(), **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.rotary_frequencies((1 << 32) + 16)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.rotary_frequencies(16, scaling="bands", factor=2.0, original_length=(1 << 32) + 4096)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.rotary_table((1 << 32) + 8, pkv.rotary_frequencies(16))
