@@ -75,7 +75,8 @@ enum pkv_device_status {
   PKV_DEV_BAD_BLOCK_ID = 2,    /* a block-table entry was outside [0, num_blocks); read as zeros */
   PKV_DEV_WAIT_TIMEOUT = 4,    /* a copy into shared memory did not complete within ~1 s; unit skipped */
   PKV_DEV_WORKSPACE_MISMATCH = 8,/* the workspace was last used with another (num_warps, group, head_dim) */
-  PKV_DEV_BAD_POSITION = 16      /* a token's position was outside the rotary table; clamped */
+  PKV_DEV_BAD_POSITION = 16,     /* a token's position was outside the rotary table; clamped */
+  PKV_DEV_TOO_MANY_TOKENS = 32   /* a batch had more tokens than its max_tokens; no weights were added */
 };
 
 /* Message of the last failure in this thread ("" if none).  Never NULL. */
@@ -654,6 +655,33 @@ int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_s
                                       int32_t block_size, int32_t num_q_heads,
                                       int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
                                       int32_t num_warps, size_t* bytes);
+
+/*
+ * pkv_decode_attention_weights_tokens — the three calls above with a bound on the batch's
+ * tokens: the scores take room for max_tokens in place of every position the tables can hold.
+ * (256 sequences of 64 query heads under tables for 131,072 tokens each: 8.6 GB, and 117 MB
+ * for the 451,896 tokens of a batch of the usual lengths.)
+ * codes       0 (caches of dtype), PKV_FP8_E4M3 or PKV_INT8; k_scale and v_scale only there.
+ * max_tokens  at least the sum of context_lens; negative: no bound.  A batch that needs more
+ *             room sets PKV_DEV_TOO_MANY_TOKENS: out is computed, the sums stay as they are.
+ * workspace   >= pkv_decode_weights_workspace_size_tokens(..., max_tokens) bytes.
+ */
+int pkv_decode_attention_weights_tokens(int32_t codes, const void* q, const void* k_cache,
+                                        const void* v_cache, const float* k_scale,
+                                        const float* v_scale, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                        int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t num_blocks, float scale,
+                                        void* out, float* weight_sums, int32_t sums_cols,
+                                        int64_t max_tokens, void* workspace,
+                                        size_t workspace_bytes, int32_t num_warps, int32_t dtype,
+                                        void* stream);
+int pkv_decode_weights_workspace_size_tokens(int32_t num_seqs, int32_t max_blocks_per_seq,
+                                             int32_t block_size, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t dtype, int32_t num_warps,
+                                             int64_t max_tokens, size_t* bytes);
 
 /*
  * pkv_evict_select — which cached tokens stay, for every sequence and KV head.

@@ -26,6 +26,7 @@ PKV_DEV_BAD_BLOCK_ID = 2
 PKV_DEV_WAIT_TIMEOUT = 4
 PKV_DEV_WORKSPACE_MISMATCH = 8
 PKV_DEV_BAD_POSITION = 16
+PKV_DEV_TOO_MANY_TOKENS = 32
 
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
 
@@ -105,6 +106,13 @@ SIGNATURES = {
                                                          _i32, _p, _sz, _i32, _i32, _p]),
     "pkv_decode_weights_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                                          _i32, ctypes.POINTER(_sz)]),
+    "pkv_decode_attention_weights_tokens": (ctypes.c_int, [_i32, _p, _p, _p, _p, _p, _p, _i32, _p,
+                                                           _i32, _i32, _i32, _i32, _i32, _i32, _f,
+                                                           _p, _p, _i32, _i64, _p, _sz, _i32, _i32,
+                                                           _p]),
+    "pkv_decode_weights_workspace_size_tokens": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _i32,
+                                                                _i32, _i32, _i64,
+                                                                ctypes.POINTER(_sz)]),
     "pkv_evict_select": (ctypes.c_int, [_p, _i32, _p, _p, _i32, _i32, _i32, _i32, _p, _i32, _p,
                                         _i32, _p, _p, _p]),
     "pkv_evict_gather": (ctypes.c_int, [_p, _p, _p, _i32, _p, _i32, _p, _p, _i32, _i32, _i32, _i32,

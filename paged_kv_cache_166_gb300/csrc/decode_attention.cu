@@ -140,6 +140,7 @@ struct DecodeArgs {
   float* scores;
   float* lse;
   int32_t* steps;
+  int32_t score_steps;  // steps that scores has room for
 };
 
 // Cache element tags of the 8-bit caches, fp8 (E4M3) and int8 codes with
@@ -354,11 +355,11 @@ struct ScoreLane {
   float* at;
   int32_t stride;  // floats of a step
   bool writes;
-  __device__ __forceinline__ ScoreLane(float* step0, int G, int lane) {
+  __device__ __forceinline__ ScoreLane(float* step0, int G, int lane, bool fits) {
     const int h = 2 * (lane & 3);
     at = step0 + (lane >> 2) * G + h;
     stride = 16 * G;
-    writes = h < G;
+    writes = h < G && fits;
   }
   __device__ __forceinline__ void store(const float (&x)[4], uint64_t policy) {
     if (!writes) return;
@@ -1136,8 +1137,10 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     a.status[3] = D;
   }
   if constexpr (kWeights) {
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
       for (int s = threadIdx.x; s <= a.S; s += blockDim.x) a.steps[s] = pre[s];
+      if (threadIdx.x == 0 && pre[a.S] > a.score_steps) atomicOr(a.status, PKV_DEV_TOO_MANY_TOKENS);
+    }
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1342,7 +1345,8 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     cc = cursor_at(pre, S, Hkv, f0);
   }
   int first_j = cc.j;
-  ScoreLane sc(kWeights ? a.scores + static_cast<int64_t>(f0) * (kTok * a.G) : nullptr, a.G, lane);
+  const bool fits = kWeights && total <= a.score_steps;
+  ScoreLane sc(fits ? a.scores + static_cast<int64_t>(f0) * (kTok * a.G) : nullptr, a.G, lane, fits);
   const uint64_t score_policy = kWeights ? ptx::policy_evict_last() : 0;
   CutUnit cut[2];
   int ncut = 0;
@@ -1385,7 +1389,8 @@ __global__ void __launch_bounds__(Shape<C, D>::kWarpsPerCta * 32, 1)
     } else {
       const uint8_t* ktp = base + (kt - base_s);
       float* step_sc = nullptr;
-      if constexpr (kWeights) step_sc = a.scores + static_cast<int64_t>(f0 + n) * (kTok * a.G);
+      if constexpr (kWeights)  // no room: all in the first step's place, where nobody reads them
+        step_sc = a.scores + (fits ? static_cast<int64_t>(f0 + n) : 0) * (kTok * a.G);
       st_.template step<kWeights>(ktp, ktp + Sh::kTileBytes, valid, a.scale_log2, a.G, lane,
                                   step_sc);
     }
@@ -1470,6 +1475,7 @@ struct HostArgs {
   float* scores = nullptr;  // kWeights: as in DecodeArgs
   float* lse = nullptr;
   int32_t* steps = nullptr;
+  int32_t score_steps = 0;
 };
 
 bool supported_head_dim(int32_t dtype, int32_t D) {
@@ -1638,6 +1644,7 @@ DecodeArgs device_args(const HostArgs& h, int W) {
   a.scores = h.scores;
   a.lse = h.lse;
   a.steps = h.steps;
+  a.score_steps = h.score_steps;
   return a;
 }
 

@@ -39,6 +39,7 @@ struct SumArgs {
   float* sums;
   int32_t* status;
   int32_t S, Hkv, limit, cols;  // limit: positions a block table holds
+  int32_t score_steps;          // steps that scores has room for
 };
 
 // cursor_at, by a warp: the sequence is looked for among 32 places a round, one a lane.
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const SumArgs 
   const int warps = gridDim.x * (kSumThreads / 32);
   const int gw = blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
   const int total = a.steps[a.S];
+  if (total > a.score_steps) return;  // reported by the attention, which left no scores
   const int per = (total + warps - 1) / warps;
   if (static_cast<int64_t>(gw) * per >= total) return;
   int f = gw * per;
@@ -135,27 +137,33 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const SumArgs 
 
 struct WeightsLayout {
   size_t steps, lse, scores, total;
+  int32_t score_steps;
 };
 
-// The decode workspace, then what the weights need.  steps a sequence can have:
-// ceil(max_blocks * block_size / 16) per KV head.
+// The decode workspace, then what the weights need.  A sequence has at most ceil(max_blocks *
+// block_size / 16) steps per KV head, and S of at most max_tokens (if not negative) together
+// no more than max_tokens / 16 + S.
 WeightsLayout weights_layout(int32_t S, int32_t MAXB, int32_t B, int32_t Hq, int32_t Hkv,
-                             int32_t D, int32_t W) {
+                             int32_t D, int32_t W, int64_t max_tokens) {
   WeightsLayout L;
   L.steps = round256(workspace_bytes_for(Hq / Hkv, D, W));
   L.lse = L.steps + round256((static_cast<size_t>(S) + 1) * sizeof(int32_t));
   L.scores = L.lse + round256(static_cast<size_t>(S) * Hq * sizeof(float));
-  const size_t steps = (static_cast<size_t>(MAXB) * B + kTok - 1) / kTok;
-  L.total = L.scores + static_cast<size_t>(S) * Hq * steps * kTok * sizeof(float);
+  int64_t steps = S * ((static_cast<int64_t>(MAXB) * B + kTok - 1) / kTok);
+  if (max_tokens >= 0 && max_tokens / kTok < steps - S) steps = max_tokens / kTok + S;
+  L.total = L.scores + static_cast<size_t>(steps) * Hq * kTok * sizeof(float);
+  steps *= Hkv;
+  L.score_steps = steps < INT32_MAX ? static_cast<int32_t>(steps) : INT32_MAX;
   return L;
 }
 
-int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
+int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols, int64_t max_tokens = -1) {
   int W = 0;
   int rc = validate(h, &W);
   if (rc != PKV_OK) return rc;
   PKV_REQUIRE(sums_cols > 0, PKV_ERR_INVALID_ARG, "weight_sums must have columns");
-  const WeightsLayout L = weights_layout(h.S, h.MAXB, h.block_size, h.Hq, h.Hkv, h.D, W);
+  const WeightsLayout L =
+      weights_layout(h.S, h.MAXB, h.block_size, h.Hq, h.Hkv, h.D, W, max_tokens);
   PKV_REQUIRE(h.workspace_bytes >= L.total, PKV_ERR_INVALID_ARG,
               "workspace of %zu bytes < %zu needed", h.workspace_bytes, L.total);
   if (h.S == 0) return ok();
@@ -165,6 +173,7 @@ int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
   h.steps = reinterpret_cast<int32_t*>(ws + L.steps);
   h.lse = reinterpret_cast<float*>(ws + L.lse);
   h.scores = reinterpret_cast<float*>(ws + L.scores);
+  h.score_steps = L.score_steps;
   SumArgs a{};
   a.scores = h.scores;
   a.lse = h.lse;
@@ -176,6 +185,7 @@ int weights_entry(HostArgs h, float* weight_sums, int32_t sums_cols) {
   a.Hkv = h.Hkv;
   a.limit = h.MAXB * h.block_size;
   a.cols = sums_cols;
+  a.score_steps = L.score_steps;
   int sms = 0, dev = 0;
   rc = device_sm_count(&sms, &dev);
   if (rc != PKV_OK) return rc;
@@ -215,10 +225,11 @@ using namespace pkv;
 
 extern "C" {
 
-int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_seq,
-                                      int32_t block_size, int32_t num_q_heads,
-                                      int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
-                                      int32_t num_warps, size_t* bytes) {
+int pkv_decode_weights_workspace_size_tokens(int32_t num_seqs, int32_t max_blocks_per_seq,
+                                             int32_t block_size, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t dtype, int32_t num_warps,
+                                             int64_t max_tokens, size_t* bytes) {
   PKV_REQUIRE(bytes != nullptr, PKV_ERR_INVALID_ARG, "bytes is NULL");
   PKV_REQUIRE(element_bytes(dtype) != 0, PKV_ERR_DTYPE, "unknown dtype %d", dtype);
   PKV_REQUIRE(num_seqs >= 0 && max_blocks_per_seq > 0 && block_size > 0, PKV_ERR_INVALID_ARG,
@@ -234,8 +245,17 @@ int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_s
     if (W < 0) return W;
   }
   *bytes = weights_layout(num_seqs, max_blocks_per_seq, block_size, num_q_heads, num_kv_heads,
-                          head_dim, W).total;
+                          head_dim, W, max_tokens).total;
   return ok();
+}
+
+int pkv_decode_weights_workspace_size(int32_t num_seqs, int32_t max_blocks_per_seq,
+                                      int32_t block_size, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                                      int32_t num_warps, size_t* bytes) {
+  return pkv_decode_weights_workspace_size_tokens(num_seqs, max_blocks_per_seq, block_size,
+                                                  num_q_heads, num_kv_heads, head_dim, dtype,
+                                                  num_warps, -1, bytes);
 }
 
 int pkv_decode_attention_weights(const void* q, const void* k_cache, const void* v_cache,
@@ -288,6 +308,28 @@ int pkv_decode_attention_weights_int8(const void* q, const void* k_cache, const 
   h.k_scale = k_scale;
   h.v_scale = v_scale;
   return weights_entry(h, weight_sums, sums_cols);
+}
+
+int pkv_decode_attention_weights_tokens(int32_t codes, const void* q, const void* k_cache,
+                                        const void* v_cache, const float* k_scale,
+                                        const float* v_scale, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                        int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t num_blocks, float scale,
+                                        void* out, float* weight_sums, int32_t sums_cols,
+                                        int64_t max_tokens, void* workspace,
+                                        size_t workspace_bytes, int32_t num_warps, int32_t dtype,
+                                        void* stream) {
+  PKV_REQUIRE(codes == 0 || codes == PKV_FP8_E4M3 || codes == PKV_INT8, PKV_ERR_DTYPE,
+              "codes %d are not 0, PKV_FP8_E4M3 or PKV_INT8", codes);
+  HostArgs h = host_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                         num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         scale, out, workspace, workspace_bytes, num_warps, dtype, stream);
+  h.codes = codes;
+  h.k_scale = k_scale;
+  h.v_scale = v_scale;
+  return weights_entry(h, weight_sums, sums_cols, max_tokens);
 }
 
 }  // extern "C"

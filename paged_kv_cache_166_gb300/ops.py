@@ -691,23 +691,28 @@ def paged_rotary_write_int8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 
 def weights_workspace_bytes(num_seqs: int, max_blocks: int, block_size: int, num_q_heads: int,
-                            num_kv_heads: int, head_dim: int, dtype, num_warps: int = 0) -> int:
+                            num_kv_heads: int, head_dim: int, dtype, num_warps: int = 0,
+                            max_tokens: Optional[int] = None) -> int:
     """Workspace bytes of ``paged_decode_attention_weights``; ``dtype`` as in
-    ``workspace_bytes``."""
+    ``workspace_bytes``, ``max_tokens`` as there."""
     code = _CODES[dtype] if isinstance(dtype, str) else _DTYPES[dtype]
     n = ctypes.c_size_t(0)
-    N.check(N.lib().pkv_decode_weights_workspace_size(num_seqs, max_blocks, block_size,
-                                                      num_q_heads, num_kv_heads, head_dim, code,
-                                                      num_warps, ctypes.byref(n)))
+    N.check(N.lib().pkv_decode_weights_workspace_size_tokens(
+        num_seqs, max_blocks, block_size, num_q_heads, num_kv_heads, head_dim, code, num_warps,
+        _bound(max_tokens), ctypes.byref(n)))
     return n.value
 
 
-_WEIGHTS = {"": "pkv_decode_attention_weights", "fp8": "pkv_decode_attention_weights_fp8",
-            "int8": "pkv_decode_attention_weights_int8"}
+def _bound(max_tokens: Optional[int]) -> int:
+    if max_tokens is None:
+        return -1
+    if not 0 <= max_tokens < 1 << 62:
+        raise ValueError(f"max_tokens {max_tokens} must not be negative")
+    return max_tokens
 
 
 def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                    scale, out, weight_sums, workspace, num_warps):
+                    scale, out, weight_sums, workspace, num_warps, max_tokens):
     if kind:
         kc, vc = _q8_caches(k_cache, v_cache, kind)
         dev = _check_cuda(q, kc, vc, k_scale, v_scale, block_tables, context_lens, out, weight_sums)
@@ -721,14 +726,14 @@ def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, c
             or weight_sums.shape[:2] != (S, Hkv):
         raise ValueError(f"weight_sums must be float32 [{S}, {Hkv}, columns]")
     _fits("num_warps or columns", num_warps, weight_sums.shape[2])
-    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else ()
-    element = kind or q.dtype
+    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if kind else (None, None)
+    element, bound = kind or q.dtype, _bound(max_tokens)
     with _current(dev):
-        key = (dev.index, S, MAXB, B, Hq, Hkv, D, element, num_warps)
+        key = (dev.index, S, MAXB, B, Hq, Hkv, D, element, num_warps, bound)
         sizes = _SIZES.get(key)
         if sizes is None:
             sizes = _remember(key, (
-                weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, element, num_warps),
+                weights_workspace_bytes(S, MAXB, B, Hq, Hkv, D, element, num_warps, max_tokens),
                 workspace_bytes(Hq, Hkv, D, element, num_warps)))
         need, head = sizes
         if workspace is None:
@@ -738,11 +743,11 @@ def _decode_weights(kind, q, k_cache, v_cache, k_scale, v_scale, block_tables, c
             ws, have = workspace, workspace.numel() * workspace.element_size()
             if ws.device != dev or have < need:
                 raise ValueError(f"workspace smaller than the {need} bytes needed")
-        N.check(getattr(N.lib(), _WEIGHTS[kind])(
-            q.data_ptr(), kc.data_ptr(), vc.data_ptr(), *scales, block_tables.data_ptr(), MAXB,
-            context_lens.data_ptr(), S, Hq, Hkv, D, B, NB, float(scale), out.data_ptr(),
-            weight_sums.data_ptr(), weight_sums.shape[2], ws.data_ptr(), have, num_warps,
-            dtype_code(q), _stream(dev)))
+        N.check(N.lib().pkv_decode_attention_weights_tokens(
+            _CODES[kind] if kind else 0, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), *scales,
+            block_tables.data_ptr(), MAXB, context_lens.data_ptr(), S, Hq, Hkv, D, B, NB,
+            float(scale), out.data_ptr(), weight_sums.data_ptr(), weight_sums.shape[2], bound,
+            ws.data_ptr(), have, num_warps, dtype_code(q), _stream(dev)))
     return out
 
 
@@ -751,12 +756,15 @@ def paged_decode_attention_weights(q: torch.Tensor, k_cache: torch.Tensor,
                                    context_lens: torch.Tensor, scale: float, out: torch.Tensor,
                                    weight_sums: torch.Tensor,
                                    workspace: Optional[torch.Tensor] = None,
-                                   num_warps: int = 0) -> torch.Tensor:
+                                   num_warps: int = 0,
+                                   max_tokens: Optional[int] = None) -> torch.Tensor:
     """paged_decode_attention that also adds each cached position's attention weight, summed
     over the query heads of its KV group, to weight_sums [S, Hkv, columns] (float32, in
-    place); writes and returns out, the same bits as paged_decode_attention's."""
+    place); writes and returns out, the same bits as paged_decode_attention's.  The scores take
+    workspace for every position that the tables can hold, or for ``max_tokens``, at least the
+    sum of context_lens (a batch of more sets PKV_DEV_TOO_MANY_TOKENS and adds nothing)."""
     return _decode_weights("", q, k_cache, v_cache, None, None, block_tables, context_lens,
-                           scale, out, weight_sums, workspace, num_warps)
+                           scale, out, weight_sums, workspace, num_warps, max_tokens)
 
 
 def paged_decode_attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor,
@@ -765,10 +773,11 @@ def paged_decode_attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor,
                                        context_lens: torch.Tensor, scale: float,
                                        out: torch.Tensor, weight_sums: torch.Tensor,
                                        workspace: Optional[torch.Tensor] = None,
-                                       num_warps: int = 0) -> torch.Tensor:
+                                       num_warps: int = 0,
+                                       max_tokens: Optional[int] = None) -> torch.Tensor:
     """paged_decode_attention_weights over fp8 caches."""
     return _decode_weights("fp8", q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                           context_lens, scale, out, weight_sums, workspace, num_warps)
+                           context_lens, scale, out, weight_sums, workspace, num_warps, max_tokens)
 
 
 def paged_decode_attention_weights_int8(q: torch.Tensor, k_cache: torch.Tensor,
@@ -777,10 +786,11 @@ def paged_decode_attention_weights_int8(q: torch.Tensor, k_cache: torch.Tensor,
                                         context_lens: torch.Tensor, scale: float,
                                         out: torch.Tensor, weight_sums: torch.Tensor,
                                         workspace: Optional[torch.Tensor] = None,
-                                        num_warps: int = 0) -> torch.Tensor:
+                                        num_warps: int = 0,
+                                        max_tokens: Optional[int] = None) -> torch.Tensor:
     """paged_decode_attention_weights over int8 caches."""
     return _decode_weights("int8", q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                           context_lens, scale, out, weight_sums, workspace, num_warps)
+                           context_lens, scale, out, weight_sums, workspace, num_warps, max_tokens)
 
 
 def paged_evict_select(weight_sums: torch.Tensor, context_lens: torch.Tensor,

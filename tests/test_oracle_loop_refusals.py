@@ -50,3 +50,38 @@ def test_sizes_that_32_bits_do_not_hold_are_refused():
         pkv.rotary_frequencies(16, scaling="bands", factor=2.0, original_length=(1 << 32) + 4096)
     with pytest.raises(ValueError, match="32 bits"):
         pkv.rotary_table((1 << 32) + 8, pkv.rotary_frequencies(16))
+
+
+def test_weights_workspace_of_bounded_tokens():
+    import torch
+    size = lambda **kw: pkv.weights_workspace_bytes(256, 8192, 16, 64, 8, 128,  # noqa: E731
+                                                    torch.bfloat16, num_warps=608, **kw)
+    base = size(max_tokens=0) - 256 * 64 * 16 * 4  # no tokens: a step for each sequence's rest
+    assert base < 20 << 20
+    assert size() - base == 256 * 64 * 131072 * 4
+    # 451,896 tokens: their scores and a step of 16 more a sequence
+    assert size(max_tokens=451896) - base == (451896 // 16 + 256) * 16 * 64 * 4
+    assert size(max_tokens=256 * 131072) == size(max_tokens=1 << 60) == size()
+    with pytest.raises(ValueError):
+        size(max_tokens=-1)
+
+
+def test_bounded_weights_refusals():
+    lib, P = N.lib(), 1 << 20
+
+    def call(**kw):
+        a = dict(codes=0, q=P, kc=P, vc=P, ks=None, vs=None, bt=P, maxb=4, ctx=P, S=2, Hq=8, Hkv=2,
+                 D=128, B=16, NB=8, scale=0.1, out=P, sums=P, cols=64, tokens=20, ws=P, wsb=1 << 30,
+                 warps=8, dt=N.PKV_BF16, stream=None)
+        a.update(kw)
+        return lib.pkv_decode_attention_weights_tokens(*a.values())
+    n = ctypes.c_size_t()
+    assert lib.pkv_decode_weights_workspace_size_tokens(2, 4, 16, 8, 2, 128, N.PKV_BF16, 8, 20,
+                                                        ctypes.byref(n)) == N.PKV_OK
+    for kw, code in ((dict(wsb=n.value - 1), N.PKV_ERR_INVALID_ARG), (dict(codes=5), N.PKV_ERR_DTYPE),
+                     (dict(codes=N.PKV_INT8), N.PKV_ERR_INVALID_ARG),
+                     (dict(sums=None), N.PKV_ERR_INVALID_ARG), (dict(cols=0), N.PKV_ERR_INVALID_ARG),
+                     (dict(tokens=21 * 16, wsb=n.value), N.PKV_ERR_INVALID_ARG)):
+        assert call(**kw) == code, kw
+    assert lib.pkv_decode_weights_workspace_size_tokens(2, 4, 16, 8, 2, 128, N.PKV_BF16, 8, 20,
+                                                        None) == N.PKV_ERR_INVALID_ARG
