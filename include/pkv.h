@@ -607,6 +607,10 @@ int pkv_rotary_write_int8(const void* q, int64_t q_stride, const void* k, int64_
  *               of the batch and KV head, updated in place (zero it for a new
  *               sequence).  A context longer than sums_cols is reported as
  *               PKV_DEV_BAD_CONTEXT_LEN; its positions from sums_cols on are dropped.
+ * Only these calls add weights: pkv_prefill_attention adds none, so a prompt's sums are 0
+ * until they are called.  To weigh a prompt's tokens by its last queries, give those as
+ * sequences of their own, query i under the prompt's table with the context that it sees, and
+ * add their rows of sums.
  * workspace     >= pkv_decode_weights_workspace_size(...) bytes: the decode workspace
  *               (same zero-filling and layout rules), then the fp32 scores of every
  *               position a table of max_blocks_per_seq blocks can hold.
@@ -688,7 +692,8 @@ int pkv_decode_weights_workspace_size_tokens(int32_t num_seqs, int32_t max_block
  * With t = context_lens[s] and n = min(keep_lens[s], t): r = min(recent, n) last
  * positions stay, then f = min(first, n - r) first ones, and of the positions
  * f .. t - r - 1 between them the n - r - f with the largest weight_sums[s, h, :]
- * (equal sums: the lower position; NaN counts as -infinity, -0 as 0).
+ * (equal sums: the lower position, so of a prompt whose tokens have no weights yet the first;
+ * NaN counts as -infinity, -0 as 0).
  *   kept[s, h, j]     = the j-th kept position, ascending in j < n
  *   new_sums[s, h, j] = weight_sums[s, h, kept[s, h, j]]
  *   new_lens[s]       = n

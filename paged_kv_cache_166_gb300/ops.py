@@ -801,7 +801,8 @@ def paged_evict_select(weight_sums: torch.Tensor, context_lens: torch.Tensor,
     ``recent`` and those with the largest weight_sums [S, Hkv, columns] between, n =
     min(keep_lens, context_lens) in all.  Their ascending positions go to kept
     [S, Hkv, kept columns] (int32), their sums to new_sums [S, Hkv, new columns], n to
-    new_lens [S]."""
+    new_lens [S].  Of equal sums the lower position stays: a prompt whose tokens have no
+    weights yet (prefill adds none) keeps its first ones."""
     _fits("first or recent", first, recent)
     dev = _check_cuda(weight_sums, context_lens, keep_lens, kept, new_sums, new_lens)
     if weight_sums.dim() != 3 or kept.dim() != 3 or new_sums.dim() != 3 \
