@@ -16,7 +16,8 @@
 //     host memory) and keeps its length; swap-in gives it ceil(len / B) fresh
 //     blocks, all or nothing;
 //   * eviction gives sequences fresh blocks for the tokens that stay, all of them before
-//     any old one is handed back (one launch moves all their rows); reordering makes each listed sequence the continuation of another.
+//     any old one is handed back (one launch moves all their rows); reordering makes each
+//     listed sequence the continuation of another.
 // Every public call validates first and mutates only once it cannot fail, so a
 // failing call leaves the state unchanged.
 #include <algorithm>

@@ -51,7 +51,7 @@ constexpr int kMaxEntries = 8192;  // entries a merge takes: parts * N, beams * 
 constexpr int kOneMerge = 2048;
 constexpr int kElements = 16;      // logits of a tile a thread holds
 constexpr int kTile = kElements * kThreads;
-constexpr int kMaxSmem = 128 << 10;  // above kMaxOut threads' 64 entries of 24 bytes (2 kMaxEntries dealt)
+constexpr int kMaxSmem = 128 << 10;  // the most is 96 KB: kMaxOut x 32 entries of 24 bytes, dealt from 64 lists
 constexpr int kList = kMaxOut + kMaxOut * kElements;  // entries of the list
 
 struct BeamArgs {

@@ -472,7 +472,9 @@ struct MmaState {
         o[mt][3] *= al1;
       }
     }
-    // transpose the (tokens x heads) halves in registers
+    // transpose the (tokens x heads) halves in registers; the probabilities are rounded to V's
+    // type, since the matrix instruction takes both operands in one 16-bit type (2^-8 of a
+    // weight in bf16, 2^-11 in f16); their sums above stay fp32
     pb0 = ptx::movmatrix_trans(ptx::pack2<T>(p0, p1));
     pb1 = ptx::movmatrix_trans(ptx::pack2<T>(p2, p3));
   }
@@ -716,6 +718,7 @@ struct Q8State {
         o[mt][3] *= al1;
       }
     }
+    // f16, as the codes are widened to (2^-11 of a weight); the sums above stay fp32
     const uint32_t pb0 = ptx::movmatrix_trans(ptx::pack2<__half>(p0, p1));
     const uint32_t pb1 = ptx::movmatrix_trans(ptx::pack2<__half>(p2, p3));
     // masks of the V lanes: a word's f16 pairs hold tokens (2 tig, 2 tig + 1) and

@@ -15,9 +15,9 @@
 // from L2, where the attention's stores ask to be kept ahead of the K and V that stream
 // through, and a line that has been read is dropped: nothing of it need go to memory.  70B
 // shape (256 sequences, 451,896 tokens, 1.85 GB of K and V, 116 MB of scores): both kernels 332
-// us, of which the attention without the weights takes 286; 13B shape (509 MB, 4 MB) 94 of 87;
+// us, of which the attention without the weights takes 286; 13B shape (509 MB, 4 MB) 95 of 87;
 // 8 sequences to 131,072 tokens over an fp8 cache (1.75 GB, 219 MB of scores, more than L2
-// holds) 381 of 281.
+// holds) 384 of 281.
 // Every sum belongs to one thread and its heads are added in order: no atomics, the same
 // bits on every run.
 #include <mutex>

@@ -762,7 +762,8 @@ def paged_decode_attention_weights(q: torch.Tensor, k_cache: torch.Tensor,
     over the query heads of its KV group, to weight_sums [S, Hkv, columns] (float32, in
     place); writes and returns out, the same bits as paged_decode_attention's.  The scores take
     workspace for every position that the tables can hold, or for ``max_tokens``, at least the
-    sum of context_lens (a batch of more sets PKV_DEV_TOO_MANY_TOKENS and adds nothing)."""
+    sum of context_lens (a batch of more sets PKV_DEV_TOO_MANY_TOKENS and adds nothing; a
+    workspace of the caller's own lets ``decode_status`` read that)."""
     return _decode_weights("", q, k_cache, v_cache, None, None, block_tables, context_lens,
                            scale, out, weight_sums, workspace, num_warps, max_tokens)
 
