@@ -616,8 +616,9 @@ int pkv_rotary_write_int8(const void* q, int64_t q_stride, const void* k, int64_
  *               position a table of max_blocks_per_seq blocks can hold.
  * The sums are fp32, a position's heads added in order by one thread: the same bits
  * on every run.  Two launches, queued one behind the other: host threads that call on one
- * stream may share a workspace (calls on other streams need their own).  After PKV_DEV_WAIT_TIMEOUT or PKV_DEV_BAD_BLOCK_ID
- * the affected sums are not to be trusted.  Everything else as pkv_decode_attention.
+ * stream may share a workspace (calls on other streams need their own).  After
+ * PKV_DEV_WAIT_TIMEOUT or PKV_DEV_BAD_BLOCK_ID the affected sums are not to be trusted.
+ * Everything else as pkv_decode_attention.
  * Errors: as pkv_decode_attention.
  */
 int pkv_decode_attention_weights(const void* q, const void* k_cache, const void* v_cache,

@@ -28,8 +28,9 @@ __device__ __forceinline__ int int8_code(float x, float scale) {
 // elementary functions on the IBM RISC System/6000 processor", 1990), three operations in
 // place of a division each.  A q0 beyond any code's range is cut off first, so that the
 // remainder of an infinity stays one; quotients so small that the remainder could
-// underflow are coded 0 either way.  (Beside the theorem: next to every border of the codes, for
-// every 24-bit scale, the five nearest dividends give the quotients that a division gives.)  Scales of extreme magnitude are divided by.
+// underflow are coded 0 either way.  Scales of extreme magnitude are divided by.  (Beside the
+// theorem: for every 24-bit scale, the five dividends nearest to every border of the codes
+// give the quotients that a division gives.)
 struct Quotients {
   float scale, r;
   bool divides;
