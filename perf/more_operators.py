@@ -460,8 +460,8 @@ def own_adjust(st):
 
 def own_commit(st):
     import paged_kv_cache_166_gb300 as pkv
-    pkv.paged_tree_commit(list(st["kc"].unbind(0)), list(st["vc"].unbind(0)), st["tables"],
-                          st["ctx"], st["starts"], st["path"], st["lens"])
+    pkv.paged_tree_commit(st["kc"], st["vc"], st["tables"], st["ctx"], st["starts"], st["path"],
+                          st["lens"])
     return _cache_out(st)
 
 
