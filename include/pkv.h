@@ -15,7 +15,10 @@
  * prefill attention over the paged cache on the 5th-generation tensor cores, and
  * the operators of a decode loop around the attention: rotary positions joined to
  * the cache write, attention weights accumulated per cached token and eviction by
- * them, and beam search's selection with the reordering of the beams' tables.
+ * them, and beam search's selection with the reordering of the beams' tables; and those
+ * of a speculative step: norms and rotary positions joined to the cache write, attention
+ * of a tree of drafted tokens, penalties and masks on logits, and the accepted path moved
+ * together in the caches.
  *
  * Conventions (all entry points):
  *   - Every function returns an int status: PKV_OK (0) or a negative PKV_ERR_*.
@@ -742,6 +745,173 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
                      void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* A speculative step: drafted tokens verified over the cache                  */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * A sequence's step appends c drafted tokens to its cache (pkv_seq_append), a chain or a
+ * tree: drafted token i follows its parent, another drafted token before it or the end of
+ * the context.  Their K and V are written (pkv_norm_rotary_write or pkv_rotary_write),
+ * pkv_tree_attention attends with all of them at once, the model's logits are adjusted
+ * (pkv_adjust_logits), and the accepted tokens, a path of the tree, are moved to the front
+ * (pkv_tree_commit) before pkv_seq_truncate gives the rest back.  (The pages do not treat
+ * drafting; the formulas stand here in full.)
+ */
+
+/*
+ * pkv_norm_rotary_write — pkv_rotary_write with norms of q and k in front and positions on
+ * one to four axes: for each head x of q and of k
+ *   y_d = (x_d * r) * w_d,   r = 1 / sqrt(sum_e x_e^2 / head_dim + eps),
+ * then its pairs are turned, pair i by the table's row at the token's position on axis
+ * pair_axes[i]; v as it is.  fp32, each operation rounded once, one rounding to dtype (or
+ * one quantisation from fp32) at the end.
+ * codes         0 (caches of dtype), PKV_FP8_E4M3 or PKV_INT8 (k_scale and v_scale only
+ *               there; layouts and quantisation as pkv_kv_write_fp8 / _int8).
+ * q_weight, k_weight  device, [head_dim], or with weight_per_head [num_heads, head_dim],
+ *               contiguous, of weight_dtype (dtype or PKV_F32); NULL: ones.
+ * eps           at least 0; negative: no norm (both weights NULL).
+ * positions     device int32 [num_axes, num_tokens], each in [0, max_positions) as in
+ *               pkv_rotary_write.
+ * pair_axes     HOST int32 [rotary_dim / 2], each in [0, num_axes); NULL with one axis;
+ *               read before the call returns.
+ * Everything else, requirements included, as pkv_rotary_write / _fp8 / _int8.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_norm_rotary_write(int32_t codes, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const void* q_weight,
+                          const void* k_weight, int32_t weight_dtype, int32_t weight_per_head,
+                          float eps, const int32_t* positions, const int32_t* pair_axes,
+                          int32_t num_axes, const float* table, int32_t max_positions,
+                          int32_t rotary_dim, int32_t interleaved, const int32_t* slot_mapping,
+                          int32_t num_tokens, void* k_cache, void* v_cache, const float* k_scale,
+                          const float* v_scale, int32_t num_blocks, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+                          int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream);
+
+/*
+ * pkv_tree_attention — attention of every sequence's drafted tokens over its cache.
+ *
+ * Sequence s has t = context_lens[s] cached tokens, the last c = query_start[s+1] -
+ * query_start[s] of them drafted (their K and V written before); base = t - c.  Query row
+ * query_start[s] + i is drafted token i.  It sees every key p < base, and drafted token j
+ * (key base + j) if bit j % 32 of word j / 32 of its row of tree_mask is set (without a
+ * mask: if j <= i).  With pos(p) = p for p < base and base + depths[...] for a drafted
+ * token (without depths: base + its number), and h a query head of KV group g = h / G:
+ *   x_p = scale * q[row, h] . K[slot(p), g];
+ *   cap > 0:     x_p = cap * tanh(x_p / cap);
+ *   slopes:      x_p = x_p + slopes[h] * (pos(p) - pos(row));
+ *   window > 0:  only keys with pos(row) - pos(p) < window are seen;
+ *   out[row, h] = sum_p e^(x_p - max) V[slot(p), g] / sum_p e^(x_p - max) over the keys seen,
+ * zero for a row that sees nothing.  Keys that a row does not see do not reach it, whatever
+ * they hold (a mask may hide a drafted token from itself); for depths above c - 1 together
+ * with a window that holds for finite values.  Without mask, depths, cap, slopes and window
+ * it is pkv_prefill_attention's definition.
+ * tree_mask     device int32 [num_tokens, mask_words] or NULL (mask_words then unused); a
+ *               sequence of more than 32 * mask_words drafted tokens is clamped and reported.
+ *               pkv_tree_masks makes masks and depths of parents.
+ * depths        device int32 [num_tokens] or NULL; negative ones count as 0
+ *               (PKV_DEV_BAD_POSITION).
+ * slopes        device float [num_q_heads] or NULL.  cap 0: none.  window 0: none.
+ * q, out        device [num_tokens, num_q_heads, head_dim], contiguous; rows of no sequence
+ *               are left as they were.  out is not q.
+ * block_tables, caches, context_lens, query_start, status: as pkv_prefill_attention.
+ * workspace     >= pkv_tree_workspace_size(head_dim) bytes, 256-byte aligned, any contents;
+ *               calls that may overlap need their own.
+ * Supported: F16 and BF16, head_dim 64, 128 or 256, up to 16 query heads per KV head,
+ * block_size 8, 16 or 32, num_seqs <= 2048, max_blocks_per_seq * block_size < 2^30.
+ * Scores, softmax and sums are fp32, probabilities rounded to dtype for the product with V.
+ * Two launches; the same bits on every run, and on any blocks that hold the same data.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* query_start,
+                       const int32_t* tree_mask, int32_t mask_words, const int32_t* depths,
+                       const float* slopes, float cap, int32_t window, int32_t num_seqs,
+                       int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                       void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+                       int32_t dtype, void* stream);
+
+/* pkv_tree_workspace_size — workspace bytes of pkv_tree_attention on the current device. */
+int pkv_tree_workspace_size(int32_t head_dim, size_t* bytes);
+
+/*
+ * pkv_tree_masks — masks and depths of trees, on the host.  Drafted token i of sequence s
+ * sees itself and what its parent sees; its depth is one more than its parent's (0 at the
+ * context's end).
+ * parents       host int32 [num_tokens]: at query_start[s] + i the number within the
+ *               sequence of drafted token i's parent, less than i, or -1.
+ * query_start   host int32 [num_seqs + 1], non-decreasing.
+ * tree_mask     host int32 [num_tokens, mask_words]; depths host int32 [num_tokens].
+ * Errors: PKV_ERR_INVALID_ARG (nothing written).
+ */
+int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int32_t num_seqs,
+                   int32_t mask_words, int32_t* tree_mask, int32_t* depths);
+
+/*
+ * pkv_tree_commit — the accepted path of every sequence's drafted tokens moved to the front:
+ * with t, c and base as in pkv_tree_attention and n = path_lens[s], for j < n the K and V rows
+ * at position base + path[s, j] go to position base + j, in the caches of num_layers layers
+ * (8-bit V tiles byte by byte).  Other rows are left as they were.
+ * path          device int32 [num_seqs, path_cols]: numbers within the sequence's drafted
+ *               tokens, path[s, j] >= j (as the numbers of a path from the context's end, each
+ *               after its parent, are); another one is not moved and sets PKV_DEV_BAD_POSITION.
+ * path_lens     device int32 [num_seqs], in [0, min(c, path_cols)]: others are clamped and
+ *               reported likewise.
+ * k_caches, v_caches  HOST arrays as in pkv_copy_blocks_layers; the blocks of the drafted
+ *               positions belong to one sequence alone (pkv_seq_append has seen to that).
+ * block_tables, context_lens, query_start: as pkv_tree_attention; a sequence whose lengths
+ *               do not fit is left alone (PKV_DEV_BAD_CONTEXT_LEN).
+ * status        device int32 word or NULL; bits are ORed in (PKV_DEV_BAD_BLOCK_ID too).
+ * Requirements: head_dim * element size a multiple of 16 bytes; caches 16-byte aligned; 8-bit
+ * caches block_size 16; 1 <= num_layers <= 128.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_tree_commit(void* const* k_caches, void* const* v_caches, int32_t num_layers,
+                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                    const int32_t* context_lens, const int32_t* query_start, const int32_t* path,
+                    int32_t path_cols, const int32_t* path_lens, int32_t num_seqs,
+                    int32_t num_blocks, int32_t num_kv_heads, int32_t block_size,
+                    int32_t head_dim, int32_t* status, int32_t dtype, void* stream);
+
+/*
+ * pkv_adjust_logits — penalties for repeated tokens, biases and masks on rows of logits.
+ * Rows row_start[s] .. row_start[s+1] - 1 belong to request s (NULL: row s does).  For row r,
+ * token v: n = how often v comes in history[s, prompt_lens[s] .. history_lens[s] - 1] and in
+ * path[r, :]; seen: n > 0, or v comes in history[s, 0 .. prompt_lens[s] - 1].
+ *   x = logits[r, v];
+ *   seen:   x = x > 0 ? x / repetition[s] : x * repetition[s];
+ *   n > 0:  x = (x - frequency[s] * n) - presence[s];
+ *   v among bias_tokens[s, :]:  x = x + bias_values[s, the last such entry];
+ *   bit v % 32 of word v / 32 of allowed[r, :] clear:  x = -infinity;
+ *   out[r, v] = x,
+ * fp32, each operation rounded, then rounded to dtype; a logit that nothing of this touches
+ * keeps its bits.  Tokens outside [0, vocab) (padding: -1) count for nothing.
+ * logits, out   device, row r at r * row_stride (out_stride) elements, vocab contiguous
+ *               elements, at any alignment of the element.  out may be logits (same stride):
+ *               then only what changes is written.  Otherwise they do not overlap.
+ * history       device int32 [num_requests, history_cols]; history_lens, prompt_lens (NULL:
+ *               0) device int32 [num_requests]; lengths are clamped to the columns.
+ * repetition, frequency, presence  device float [num_requests] each, or NULL (1, 0, 0).
+ * path          device int32 [num_rows, path_cols] or NULL: a drafted token's ancestors.
+ * bias_tokens, bias_values  device int32 and float [num_requests, bias_cols], or both NULL.
+ * allowed       device int32 [num_rows, allowed_words] or NULL; allowed_words * 32 >= vocab.
+ * row_start     device int32 [num_requests + 1], non-decreasing, within [0, num_rows]; rows of
+ *               no request are left as they were.
+ * Supported: vocab <= 2^30, num_requests <= 65535, under 2^24 columns of history and path.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+int pkv_adjust_logits(const void* logits, int64_t row_stride, void* out, int64_t out_stride,
+                      int32_t num_rows, int32_t vocab, const int32_t* row_start,
+                      int32_t num_requests, const int32_t* history, int32_t history_cols,
+                      const int32_t* history_lens, const int32_t* prompt_lens,
+                      const float* repetition, const float* frequency, const float* presence,
+                      const int32_t* path, int32_t path_cols, const int32_t* bias_tokens,
+                      const float* bias_values, int32_t bias_cols, const int32_t* allowed,
+                      int32_t allowed_words, int32_t dtype, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Beam search                                                                */
 /* ------------------------------------------------------------------------- */
 
@@ -957,6 +1127,18 @@ int pkv_seq_swap_in(pkv_allocator_t* a, int32_t seq, int32_t* ids_out, int32_t c
  */
 int pkv_seq_evict(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int32_t* new_lens,
                   int32_t max_blocks, int32_t* tables_out);
+
+/*
+ * pkv_seq_truncate — sequences cut down to their first new_lens[i] tokens: the blocks past
+ * ceil(new_lens[i] / block_size) are decremented, in list order, each table from its end (as
+ * pkv_seq_free does).  The rest of the table stays, a last block that is shared included: the
+ * next append reports its copy-on-write pair.
+ * seqs      host int32 [k], resident sequence ids, no id twice.
+ * new_lens  host int32 [k], each in [0, the sequence's length].
+ * Errors: PKV_ERR_INVALID_ARG (state unchanged).  k = 0 is a no-op.
+ */
+int pkv_seq_truncate(pkv_allocator_t* a, const int32_t* seqs, int32_t k,
+                     const int32_t* new_lens);
 
 /*
  * pkv_seq_reorder — beam search's reordering of states: sequence seqs[i] becomes a

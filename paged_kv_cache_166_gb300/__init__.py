@@ -25,6 +25,12 @@ Public API (all device work runs in libpkv.so's sm_103a kernels):
   ``BlockAllocator.evict``)
 * beam search: ``beam_select`` — the best continuations over beams and vocabulary (with
   ``BlockAllocator.reorder``)
+* a speculative step: ``paged_norm_rotary_write`` (and ``_fp8``, ``_int8``) — norms of q and k
+  for each head, positions on one or several axes, the cache write, one launch;
+  ``paged_tree_attention`` — attention of drafted tokens (a tree, ``tree_masks``, or a chunk)
+  over the cache, with capped scores, a bias or a window by distance; ``adjust_logits`` —
+  penalties, biases and masks of allowed tokens; ``paged_tree_commit`` — the accepted path's
+  rows moved together in every layer (with ``BlockAllocator.truncate``)
 * ``BlockAllocator`` — host block manager (free list, refcounts, fork, CoW, free);
   ``DecodeStepTables`` — one decode step's appends and table export, pre-bound
 * ``decode_status(workspace)`` — the device-side status bits of the decode kernels;
@@ -45,7 +51,9 @@ _OPS = frozenset((
     "paged_rotary_write", "paged_rotary_write_fp8", "paged_rotary_write_int8",
     "paged_decode_attention_weights", "paged_decode_attention_weights_fp8",
     "paged_decode_attention_weights_int8", "weights_workspace_bytes", "paged_evict_select",
-    "paged_evict_gather", "beam_select", "beam_workspace_bytes", "decode_status",
+    "paged_evict_gather", "paged_norm_rotary_write", "paged_norm_rotary_write_fp8",
+    "paged_norm_rotary_write_int8", "paged_tree_attention", "tree_workspace_bytes", "tree_masks",
+    "adjust_logits", "paged_tree_commit", "beam_select", "beam_workspace_bytes", "decode_status",
     "workspace_bytes", "default_num_warps", "get_workspace", "wait_timeout_selftest"))
 _ops = None
 

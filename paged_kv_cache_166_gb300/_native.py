@@ -120,6 +120,21 @@ SIGNATURES = {
     "pkv_beam_select": (ctypes.c_int, [_p, _i64, _i64, _p, _i32, _i32, _i32, _i32, _p, _p, _p, _p,
                                        _sz, _i32, _p]),
     "pkv_beam_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "pkv_tree_attention": (ctypes.c_int, [_p, _p, _p, _p, _i32, _p, _p, _p, _i32, _p, _p, _f, _i32,
+                                          _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f, _p, _p, _p,
+                                          _sz, _i32, _p]),
+    "pkv_tree_workspace_size": (ctypes.c_int, [_i32, ctypes.POINTER(_sz)]),
+    "pkv_tree_masks": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p]),
+    "pkv_tree_commit": (ctypes.c_int, [_p, _p, _i32, _p, _i32, _p, _p, _p, _i32, _p, _i32, _i32,
+                                       _i32, _i32, _i32, _p, _i32, _p]),
+    "pkv_norm_rotary_write": (ctypes.c_int, [_i32, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i32,
+                                             _i32, _f, _p, _p, _i32, _p, _i32, _i32, _i32, _p,
+                                             _i32, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32,
+                                             _p, _i64, _p, _i32, _p]),
+    "pkv_adjust_logits": (ctypes.c_int, [_p, _i64, _p, _i64, _i32, _i32, _p, _i32, _p, _i32, _p,
+                                         _p, _p, _p, _p, _p, _i32, _p, _p, _i32, _p, _i32, _i32,
+                                         _p]),
+    "pkv_seq_truncate": (ctypes.c_int, [_p, _pi32, _i32, _pi32]),
     "pkv_seq_evict": (ctypes.c_int, [_p, _pi32, _i32, _pi32, _i32, _pi32]),
     "pkv_seq_reorder": (ctypes.c_int, [_p, _pi32, _i32, _pi32]),
     "pkv_allocator_create": (ctypes.c_int, [_i32, _i32, _pi32, ctypes.POINTER(_p)]),

@@ -145,6 +145,16 @@ class BlockAllocator:
                                         _ptr(out)))
         return out
 
+    def truncate(self, seqs: Sequence[int], new_lens: Sequence[int]) -> None:
+        """Cut each seqs[i] down to its first new_lens[i] tokens (at most its length): the
+        blocks behind them go back, last one first (to the pool, or to their other holders).
+        What drafted tokens that were not accepted leave behind; all or nothing."""
+        ids = np.ascontiguousarray(seqs, dtype=np.int32)
+        lens = np.ascontiguousarray(new_lens, dtype=np.int32)
+        if ids.ndim != 1 or ids.shape != lens.shape:
+            raise ValueError("seqs and new_lens must be lists of one length")
+        N.check(self._lib.pkv_seq_truncate(self._h, _ptr(ids), len(ids), _ptr(lens)))
+
     def reorder(self, seqs: Sequence[int], parents: Sequence[int]) -> None:
         """Beam search: each seqs[i] becomes the continuation of what seqs[parents[i]] was
         (table and length), all at once; distinct ids, parents in [0, len(seqs))."""

@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "decode_attention.cu", "decode_weights.cu", "prefill_attention.cu",
-           "prefill_tcgen05.cu", "kv_ops.cu", "rotary.cu", "evict.cu", "beam.cu", "allocator.cpp"]
+           "prefill_tcgen05.cu", "kv_ops.cu", "rotary.cu", "evict.cu", "beam.cu", "tree_attention.cu",
+           "tree_commit.cu", "norm_rotary.cu", "logits.cu", "allocator.cpp"]
 
 
 def nvcc() -> str:

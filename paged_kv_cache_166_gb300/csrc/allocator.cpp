@@ -307,6 +307,37 @@ int pkv_seq_evict(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int3
   });
 }
 
+int pkv_seq_truncate(pkv_allocator_t* a, const int32_t* seqs, int32_t k,
+                     const int32_t* new_lens) {
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL handle");
+  PKV_REQUIRE(k >= 0, PKV_ERR_INVALID_ARG, "negative sequence count");
+  PKV_REQUIRE(k == 0 || (seqs && new_lens), PKV_ERR_INVALID_ARG, "NULL array");
+  return guarded([&] {
+    const uint32_t epoch = a->next_epoch();
+    for (int32_t i = 0; i < k; ++i) {
+      PKV_REQUIRE(a->resident_seq(seqs[i]), PKV_ERR_INVALID_ARG,
+                  "unknown or swapped-out sequence %d", seqs[i]);
+      PKV_REQUIRE(a->seqs[seqs[i]].mark != epoch, PKV_ERR_INVALID_ARG,
+                  "sequence %d listed twice", seqs[i]);
+      a->seqs[seqs[i]].mark = epoch;
+      PKV_REQUIRE(new_lens[i] >= 0 && new_lens[i] <= a->seqs[seqs[i]].len, PKV_ERR_INVALID_ARG,
+                  "sequence %d has %d tokens, cannot be cut down to %d", seqs[i],
+                  a->seqs[seqs[i]].len, new_lens[i]);
+    }
+    const int64_t B = a->block_size;
+    for (int32_t i = 0; i < k; ++i) {
+      auto& s = a->seqs[seqs[i]];
+      const size_t stay = static_cast<size_t>((new_lens[i] + B - 1) / B);
+      while (s.table.size() > stay) {
+        a->decref(s.table.back());
+        s.table.pop_back();
+      }
+      s.len = new_lens[i];
+    }
+    return pkv::ok();
+  });
+}
+
 int pkv_seq_reorder(pkv_allocator_t* a, const int32_t* seqs, int32_t k, const int32_t* parents) {
   PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL handle");
   PKV_REQUIRE(k >= 0, PKV_ERR_INVALID_ARG, "negative sequence count");

@@ -1,0 +1,419 @@
+// Norms of q and k for each head, rotary positions on one or several axes, and the write of k
+// and v into the paged cache, in one pass.
+//
+// A head x of D elements is first normed (unless the call asks for none),
+//   y_d = (x_d * r) * w_d,   r = 1 / sqrt(sum_e x_e^2 / D + eps),
+// then its first rotary_dim elements are turned in pairs as rotary.cu does, pair i by the row
+// of the table at the token's position on the pair's axis.  q goes to q_out, k and v to their
+// slots, so q, k and v are read once and nothing between is written.
+//
+// Arithmetic: fp32, each product and sum rounded once (squares are added as they are formed;
+// the reciprocal square root is one rounding), then one rounding to the type, or one
+// quantisation straight from fp32.  A head's squares are summed in an order that depends on its
+// layout alone (D, rotary_dim, pairing, type), so a token's bits do not depend on strides or
+// alignment.
+//
+// A group of up to 32 lanes takes a head: a lane's pieces of 16 bytes (both halves' ones of a
+// turned pair), the sum of squares by shuffles; then the next head with the cos, sin and
+// weights that the lane has loaded once.  Bound by memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "internal.h"
+#include "rotary_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kMaxAxes = 4;
+constexpr int kNormThreads = 128;
+
+struct NormArgs : RotaryArgs {
+  const void* qw;  // weights [D] or [heads, D], or NULL: ones
+  const void* kw;
+  float eps;
+  int32_t norm, axes, per_head, w_f32;
+  int32_t wide, w_wide, v_pairs;  // addresses that allow 16 bytes (or a pair) at once
+  uint32_t axis_bits[kMaxRotaryPairs / 16];  // two bits a pair
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_piece(const T* p, bool wide) {
+  Pack<T, N> x;
+  if (wide) {
+    x = *reinterpret_cast<const Pack<T, N>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x.x[i] = p[i];
+  }
+  return x;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_piece(T* p, const float (&y)[N], bool wide) {
+  if (wide) {
+    store_as<T, N>(p, y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = ptx::from_float<T>(y[i]);
+  }
+}
+
+// A lane's pieces of one head.
+template <typename T, int VEC, int NU>
+struct Pieces {
+  Pack<T, VEC> one[NU], two[NU];  // two: the second half's, of turned pieces (half layout)
+};
+
+// blockIdx.x < T: a token, its heads split over gridDim.y CTAs and the CTA's groups of lanes;
+// 8-bit caches: then V's windows, a.v_parts CTAs each.
+template <typename T, int VEC, bool kInter, int kCodes, int NU>
+__global__ void __launch_bounds__(kNormThreads, 5)
+    norm_rotary_kernel(const __grid_constant__ NormArgs a) {
+  // as rotary_write_kernel: a launch queued behind reads and writes nothing of this one's
+  // before this grid has completed
+  asm volatile("griddepcontrol.launch_dependents;");
+  using P = Pack<T, VEC>;
+  constexpr int kAng = kInter ? VEC / 2 : VEC;  // pairs of a piece
+  const int64_t t = blockIdx.x;
+  if constexpr (kCodes != 0) {
+    if (t >= a.T) {
+      const int64_t i = (t - a.T) * gridDim.y + blockIdx.y;
+      const int64_t window = i / a.v_parts;
+      if (window * 16 < a.T) {
+        const int part = static_cast<int>(i - window * a.v_parts);
+        if (a.v_pairs) write_v8<T, true, kCodes>(a, static_cast<int>(window), part, a.v_parts);
+        else write_v8<T, false, kCodes>(a, static_cast<int>(window), part, a.v_parts);
+      }
+      return;
+    }
+  }
+  const int half = a.rot >> 1;
+  const int nturn = kInter ? a.rot / VEC : half / VEC;
+  const int units = nturn + (a.D - a.rot) / VEC;
+  const int L = blockDim.x;  // lanes of a head: a power of two
+  const int lane = (threadIdx.y * L + threadIdx.x) & 31;
+  const uint32_t group = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
+
+  const int32_t slot = __ldg(a.slots + t);
+  const bool write = slot >= 0 && static_cast<int64_t>(slot) < static_cast<int64_t>(a.NB) * a.B;
+  int32_t pos[kMaxAxes];
+#pragma unroll
+  for (int x = 0; x < kMaxAxes; ++x) {
+    pos[x] = 0;
+    if (x < a.axes) {
+      pos[x] = __ldg(a.positions + static_cast<int64_t>(x) * a.T + t);
+      if (pos[x] < 0 || pos[x] >= a.P) {
+        if (a.status != nullptr && threadIdx.x == 0 && threadIdx.y == 0 && blockIdx.y == 0)
+          atomicOr(a.status, PKV_DEV_BAD_POSITION);
+        pos[x] = pos[x] < 0 ? 0 : a.P - 1;
+      }
+    }
+  }
+  int at[NU];  // first element of the lane's unit; D: none
+  float c[NU][kAng], s[NU][kAng];
+#pragma unroll
+  for (int j = 0; j < NU; ++j) {
+    const int u = threadIdx.x + j * L;
+    at[j] = u < nturn ? u * VEC : (u < units ? a.rot + (u - nturn) * VEC : a.D);
+    if (u >= nturn) continue;
+    const int i0 = u * kAng;
+    if (a.axes == 1) {
+      const float* const row = a.table + static_cast<int64_t>(pos[0]) * a.rot + i0;
+      const Pack<float, kAng> pc = *reinterpret_cast<const Pack<float, kAng>*>(row);
+      const Pack<float, kAng> ps = *reinterpret_cast<const Pack<float, kAng>*>(row + half);
+#pragma unroll
+      for (int i = 0; i < kAng; ++i) {
+        c[j][i] = pc.x[i];
+        s[j][i] = ps.x[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kAng; ++i) {
+        const uint32_t x = (a.axis_bits[(i0 + i) >> 4] >> (2 * ((i0 + i) & 15))) & 3u;
+        const int32_t p = x == 0 ? pos[0] : (x == 1 ? pos[1] : (x == 2 ? pos[2] : pos[3]));
+        const float* const row = a.table + static_cast<int64_t>(p) * a.rot + i0 + i;
+        c[j][i] = __ldg(row);
+        s[j][i] = __ldg(row + half);
+      }
+    }
+  }
+  auto turns = [&](int j) { return static_cast<int>(threadIdx.x) + j * L < nturn; };
+  const bool wide = a.wide != 0;
+
+  float w1[NU][VEC], w2[NU][VEC];
+  auto weights = [&](const void* w, int h) {  // of head h, or of all
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) w1[j][i] = w2[j][i] = 1.f;
+      if (w == nullptr || !a.norm || at[j] >= a.D) continue;
+      const int64_t d = (a.per_head ? static_cast<int64_t>(h) * a.D : 0) + at[j];
+      const bool second = !kInter && turns(j);
+      if (a.w_f32) {
+        const float* const p = static_cast<const float*>(w) + d;
+        const Pack<float, VEC> x = load_piece<float, VEC>(p, a.w_wide != 0);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w1[j][i] = x.x[i];
+        if (second) {
+          const Pack<float, VEC> y = load_piece<float, VEC>(p + half, a.w_wide != 0);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) w2[j][i] = y.x[i];
+        }
+      } else {
+        const T* const p = static_cast<const T*>(w) + d;
+        const P x = load_piece<T, VEC>(p, a.w_wide != 0);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w1[j][i] = widen(x.x[i]);
+        if (second) {
+          const P y = load_piece<T, VEC>(p + half, a.w_wide != 0);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) w2[j][i] = widen(y.x[i]);
+        }
+      }
+    }
+  };
+  using Own = Pieces<T, VEC, NU>;
+  auto load = [&](const T* src, Own& x) {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      if (at[j] >= a.D) continue;
+      x.one[j] = load_piece<T, VEC>(src + at[j], wide);
+      if (!kInter && turns(j)) x.two[j] = load_piece<T, VEC>(src + at[j] + half, wide);
+    }
+  };
+  // norm and turn of a head; put(j, element, values) for each of the lane's pieces
+  auto work = [&](const Own& x, auto put) {
+    float r = 1.f;
+    if (a.norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        if (at[j] >= a.D) continue;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x.one[j].x[i]), widen(x.one[j].x[i]), ss);
+        if (!kInter && turns(j)) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x.two[j].x[i]), widen(x.two[j].x[i]), ss);
+        }
+      }
+      for (int o = L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+      r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(a.D)), a.eps));
+    }
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      if (at[j] >= a.D) continue;
+      float x1[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        x1[i] = widen(x.one[j].x[i]);
+        if (a.norm) x1[i] = __fmul_rn(__fmul_rn(x1[i], r), w1[j][i]);
+      }
+      if (!turns(j)) {
+        put(j, at[j], x1);
+        continue;
+      }
+      float y1[VEC];
+      if constexpr (kInter) {
+#pragma unroll
+        for (int i = 0; i < kAng; ++i) {
+          const float p = x1[2 * i], q = x1[2 * i + 1];
+          y1[2 * i] = __fsub_rn(__fmul_rn(p, c[j][i]), __fmul_rn(q, s[j][i]));
+          y1[2 * i + 1] = __fadd_rn(__fmul_rn(q, c[j][i]), __fmul_rn(p, s[j][i]));
+        }
+        put(j, at[j], y1);
+      } else {
+        float x2[VEC], y2[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          x2[i] = widen(x.two[j].x[i]);
+          if (a.norm) x2[i] = __fmul_rn(__fmul_rn(x2[i], r), w2[j][i]);
+          y1[i] = __fsub_rn(__fmul_rn(x1[i], c[j][i]), __fmul_rn(x2[i], s[j][i]));
+          y2[i] = __fadd_rn(__fmul_rn(x2[i], c[j][i]), __fmul_rn(x1[i], s[j][i]));
+        }
+        put(j, at[j], y1);
+        put(j, at[j] + half, y2);
+      }
+    }
+  };
+  const int h0 = threadIdx.y + blockDim.y * blockIdx.y, step = blockDim.y * gridDim.y;
+  constexpr int U = NU > 1 ? 1 : (kInter ? 4 : 2);  // heads whose loads go out together
+  auto each = [&](const T* src, int H, auto put) {
+    for (int h = h0; h < H; h += U * step) {
+      Own x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < H) load(src + static_cast<int64_t>(h + u * step) * a.D, x[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < H) put(h + u * step, x[u]);
+    }
+  };
+  // a piece that neither norm nor turn touches keeps its bits (a NaN's too)
+  auto put_same = [&](T* row, int j, int d, const float (&y)[VEC], const Own& x, bool w) {
+    if (!a.norm && !turns(j)) {
+      if (w) {
+        *reinterpret_cast<P*>(row + d) = x.one[j];
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) row[d + i] = x.one[j].x[i];
+      }
+    } else {
+      store_piece<T, VEC>(row + d, y, w);
+    }
+  };
+  if (!a.per_head) weights(a.qw, 0);
+  T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride;
+  each(static_cast<const T*>(a.q) + t * a.q_stride, a.Hq, [&](int h, const Own& x) {
+    if (a.per_head) weights(a.qw, h);
+    T* const row = qo + static_cast<int64_t>(h) * a.D;
+    work(x, [&](int j, int d, const float (&y)[VEC]) { put_same(row, j, d, y, x, wide); });
+  });
+  if (!write) return;
+  const int32_t block = (a.B & (a.B - 1)) == 0 ? slot >> (31 - __clz(a.B)) : slot / a.B;
+  const int32_t off = slot - block * a.B;
+  const int64_t row0 = (static_cast<int64_t>(block) * a.Hkv * a.B + off) * a.D;  // of head 0
+  const int64_t head = static_cast<int64_t>(a.B) * a.D;
+  if (!a.per_head) weights(a.kw, 0);
+  each(static_cast<const T*>(a.k) + t * a.k_stride, a.Hkv, [&](int g, const Own& x) {
+    if (a.per_head) weights(a.kw, g);
+    if constexpr (kCodes == 0) {
+      T* const row = static_cast<T*>(a.kc) + row0 + g * head;
+      work(x, [&](int j, int d, const float (&y)[VEC]) { put_same(row, j, d, y, x, true); });
+    } else {
+      uint8_t* const row = static_cast<uint8_t*>(a.kc) + row0 + g * head;
+      const Quotients by = quotients_by(__ldg(a.ks + g));
+      work(x, [&](int, int d, const float (&y)[VEC]) { store_codes<kCodes, VEC>(row + d, y, by); });
+    }
+  });
+  if constexpr (kCodes == 0) {  // V rows, copied
+    each(static_cast<const T*>(a.v) + t * a.v_stride, a.Hkv, [&](int g, const Own& x) {
+      T* const row = static_cast<T*>(a.vc) + row0 + g * head;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        if (at[j] >= a.D) continue;
+        *reinterpret_cast<P*>(row + at[j]) = x.one[j];
+        if (!kInter && turns(j)) *reinterpret_cast<P*>(row + at[j] + half) = x.two[j];
+      }
+    });
+  }
+}
+
+int lanes_of(int units) {
+  int l = 1;
+  while (l < units && l < 32) l *= 2;
+  return l;
+}
+
+template <typename T, int kCodes>
+int launch_norm(NormArgs a, bool interleaved, cudaStream_t st) {
+  constexpr int W = 16 / sizeof(T);
+  // pieces of 16 bytes where head_dim and rotary_dim allow them, else the smallest that
+  // hold whole pairs
+  const bool whole = a.rot % (interleaved ? W : 2 * W) == 0 && a.D % W == 0;
+  const int vec = whole ? W : (interleaved ? 2 : 1);
+  const bool strides = a.q_stride % W == 0 && a.k_stride % W == 0 && a.v_stride % W == 0 &&
+                       a.qo_stride % W == 0 && aligned(a.q, 16) && aligned(a.k, 16) &&
+                       aligned(a.v, 16) && aligned(a.q_out, 16);
+  // (interleaved pairs are aligned to their two elements, single elements to themselves)
+  a.wide = !whole || strides;
+  a.w_wide = vec == 1 || (aligned(a.qw, 16) && aligned(a.kw, 16));
+  a.v_pairs = (a.v_stride % 2 == 0 && aligned(a.v, 2 * sizeof(T))) ? 1 : 0;
+  const int units = (interleaved ? a.rot / vec : a.rot / (2 * vec)) + (a.D - a.rot) / vec;
+  const int lanes = lanes_of(units), rows = kNormThreads / lanes;
+  int sms = 0, dev = 0;
+  const int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  // few tokens: their heads are spread over more CTAs until the SMs have a few each
+  int split = 1;
+  while (split * rows < a.Hq && static_cast<int64_t>(a.T) * split < 4 * sms) split *= 2;
+  int64_t columns = a.T;
+  if (kCodes != 0) {  // V's windows: an item a thread if the window is one run
+    const int64_t windows = (static_cast<int64_t>(a.T) + 15) / 16;
+    const int64_t items = static_cast<int64_t>(a.Hkv) * a.D / 2;
+    const int64_t parts = (items + kNormThreads - 1) / kNormThreads;
+    a.v_parts = static_cast<int32_t>(parts);
+    columns += (windows * parts + split - 1) / split;
+  }
+  PKV_REQUIRE(columns < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED, "too many tokens");
+  const dim3 grid(static_cast<unsigned>(columns), split), threads(lanes, rows);
+  if (whole && interleaved)
+    norm_rotary_kernel<T, W, true, kCodes, W == 4 ? 2 : 1><<<grid, threads, 0, st>>>(a);
+  else if (whole)
+    norm_rotary_kernel<T, W, false, kCodes, W == 4 ? 2 : 1><<<grid, threads, 0, st>>>(a);
+  else if (interleaved)
+    norm_rotary_kernel<T, 2, true, kCodes, 4><<<grid, threads, 0, st>>>(a);
+  else
+    norm_rotary_kernel<T, 1, false, kCodes, 8><<<grid, threads, 0, st>>>(a);
+  PKV_CUDA(cudaGetLastError());
+  return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int pkv_norm_rotary_write(
+    int32_t codes, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int32_t weight_dtype,
+    int32_t weight_per_head, float eps, const int32_t* positions, const int32_t* pair_axes,
+    int32_t num_axes, const float* table, int32_t max_positions, int32_t rotary_dim,
+    int32_t interleaved, const int32_t* slot_mapping, int32_t num_tokens, void* k_cache,
+    void* v_cache, const float* k_scale, const float* v_scale, int32_t num_blocks,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t block_size, int32_t head_dim, void* q_out,
+    int64_t q_out_stride, int32_t* status, int32_t dtype, void* stream) {
+  PKV_REQUIRE(codes == 0 || codes == PKV_FP8_E4M3 || codes == PKV_INT8, PKV_ERR_DTYPE,
+              "cache code %d is not 0, PKV_FP8_E4M3 or PKV_INT8", codes);
+  RotaryArgs base;
+  int rc = rotary_args(codes, q, q_stride, k, k_stride, v, v_stride, positions, table,
+                       max_positions, rotary_dim, interleaved, slot_mapping, num_tokens, k_cache,
+                       v_cache, k_scale, v_scale, num_blocks, num_q_heads, num_kv_heads,
+                       block_size, head_dim, q_out, q_out_stride, status, dtype, base);
+  if (rc != PKV_OK) return rc;
+  PKV_REQUIRE(std::isfinite(eps), PKV_ERR_INVALID_ARG, "eps must be finite (negative: no norm)");
+  const bool norm = eps >= 0.f;
+  PKV_REQUIRE(norm || (!q_weight && !k_weight), PKV_ERR_INVALID_ARG,
+              "weights without a norm (eps is negative)");
+  PKV_REQUIRE(weight_dtype == dtype || weight_dtype == PKV_F32, PKV_ERR_DTYPE,
+              "weights have q's dtype or f32 (dtype %d)", weight_dtype);
+  PKV_REQUIRE(num_axes >= 1 && num_axes <= kMaxAxes, PKV_ERR_UNSUPPORTED,
+              "num_axes %d outside [1, %d]", num_axes, kMaxAxes);
+  PKV_REQUIRE(num_axes == 1 || pair_axes != nullptr, PKV_ERR_INVALID_ARG,
+              "several axes need pair_axes");
+  const int welt = element_bytes(weight_dtype);
+  PKV_REQUIRE(aligned(q_weight, welt) && aligned(k_weight, welt), PKV_ERR_INVALID_ARG,
+              "a weight is not aligned to its element");
+  NormArgs a{};
+  static_cast<RotaryArgs&>(a) = base;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.eps = eps;
+  a.norm = norm;
+  a.axes = num_axes;
+  a.per_head = weight_per_head != 0;
+  a.w_f32 = weight_dtype == PKV_F32;
+  if (num_axes > 1) {
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+      PKV_REQUIRE(pair_axes[i] >= 0 && pair_axes[i] < num_axes, PKV_ERR_INVALID_ARG,
+                  "axis %d of pair %d outside [0, %d)", pair_axes[i], i, num_axes);
+      a.axis_bits[i / 16] |= static_cast<uint32_t>(pair_axes[i]) << (2 * (i % 16));
+    }
+  }
+  if (num_tokens == 0) return ok();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define PKV_NORM(C)                                                            \
+  rc = dtype == PKV_F32   ? launch_norm<float, C>(a, interleaved != 0, st)     \
+       : dtype == PKV_F16 ? launch_norm<__half, C>(a, interleaved != 0, st)    \
+                          : launch_norm<__nv_bfloat16, C>(a, interleaved != 0, st)
+  if (codes == 0) PKV_NORM(0);
+  else if (codes == PKV_FP8_E4M3) PKV_NORM(1);
+  else PKV_NORM(2);
+#undef PKV_NORM
+  return rc == PKV_OK ? ok() : rc;
+}

@@ -1,0 +1,1198 @@
+// Attention of drafted tokens over the paged cache on the 5th-generation tensor cores.
+//
+// Sequence s has t cached tokens, the last c of them drafted (their K and V written before):
+// a tree, or a plain chunk.  Query row q0 + i is drafted token i; with base = t - c it sees
+// every key p < base and of the drafted keys base + j those of its row of the mask (no mask:
+// j <= i), both only within the window:
+//   x = scale * q . K[p];  cap > 0: x = cap * tanh(x / cap);  x += slope_h * (pos(p) - pos(i));
+//   out = softmax_p(x) . V[p], zero where a row sees nothing,
+// pos(p) = p for p < base, base + depth_j for drafted token j; window: pos(i) - pos(p) < window.
+//
+// How.  A unit is a tile of up to 128 rows of one (sequence, KV head): row r is drafted token
+// i0 + r / G, head g * G + r % G.  Its keys come in tiles of 128 (64 at head_dim 256, where
+// the output alone takes half of the tensor memory): S = Q K^T (tcgen05, operands in
+// 128-byte-swizzled shared memory, S in tensor memory, two buffers), softmax by two threads a
+// row with a running maximum, P rounded to the input type in tensor memory, O += P V with O in
+// tensor memory.  The layout of the tiles is the paged prefill's (prefill_tcgen05.cu).
+//
+// Split: the key tiles of all units, one after the other, are cut into one run of equal cost
+// for each CTA (one CTA an SM), so that few long contexts use every SM.  A unit that a run's
+// border cuts leaves each piece's unnormalised O, maximum and sum in the workspace (fp32); a
+// second kernel, its launch overlapped, joins the pieces in order.  The same bits on every run.
+//
+// Bound: up to 128 rows read K and V once, 512 bytes a key and KV head at head_dim 128 for
+// 4 * 128 * 128 operations: memory, if the softmax of a tile (16,384 exponentials) stays below
+// the 1.5 us that its 64 KB take.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kTrMaxSeqs = 2048;
+constexpr int kTrMaxGroup = 16;
+constexpr uint64_t kTrWaitNs = 1000000000ull;  // 1 s per wait before giving up
+constexpr int kTrRows = 128;                   // rows of a unit = tensor-memory lanes = MMA M
+constexpr int kTrRowWarps = 8;                 // softmax warps 2 .. 9: a lane quarter, a half of the keys
+constexpr int kTrVWarp = 10, kTrQWarp = 11;    // producers of V and of the query tiles
+constexpr int kTrThreads = 12 * 32;
+constexpr int kTrChunk = 128 * 128;            // one [128 rows x 128 B] swizzled chunk of Q
+constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximum that moves the reference
+
+// What a CTA leaves behind of the unit that its run begins and another one ends.
+struct TreeCut {
+  long long P, C;   // cost before the unit; of all units
+  int32_t n;        // key tiles of the unit; 0: no such unit
+  int32_t row0;     // row of q and out of the unit's row 0
+  int32_t rows, g;  // rows of the unit, KV head
+};
+
+struct TreeArgs {
+  const void* q;
+  void* out;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;
+  const uint32_t* mask;   // [T, W] or NULL: drafted tokens that each row sees
+  const int32_t* depths;  // [T] or NULL
+  const float* slopes;    // [Hq] or NULL
+  const void* v_cache;
+  int32_t* status;        // or NULL
+  TreeCut* cuts;          // [grid]
+  float* part_o;          // [2 * grid][128][D]: O of cut pieces
+  float2* part_ml;        // [2 * grid][128]: reference (log2 units) and sum
+  int32_t S, T, Hq, Hkv, G, MAXB, NB, bs, W, window;
+  int32_t nodes, box;     // drafted tokens of a unit and of one TMA box of q
+  float scale_log2;       // without cap: x in log2 units is S * scale_log2
+  float cap_log2, cap_z;  // with cap: cap_log2 * tanh, 2^(S * cap_z) = e^(2 x / cap)
+};
+
+__device__ __forceinline__ void tr_flag(const TreeArgs& a, int bits) {
+  if (a.status) atomicOr(a.status, bits);
+}
+
+// Context t, drafted tokens c and first row q0 of sequence s, clamped to 0 <= c <= t <= MAXB *
+// bs (with a mask c <= 32 W) and 0 <= q0, q0 + c <= T.
+__device__ __forceinline__ void tr_seq(const TreeArgs& a, int s, int& t, int& c, int& q0,
+                                       bool report) {
+  t = __ldg(a.context_lens + s);
+  q0 = __ldg(a.query_start + s);
+  const int q1 = __ldg(a.query_start + s + 1);
+  const int limit = a.MAXB * a.bs;
+  const int most = a.mask != nullptr && static_cast<int64_t>(a.W) * 32 < limit ? a.W * 32 : limit;
+  const bool fine = t >= 0 && t <= limit && q0 >= 0 && q1 >= q0 && q1 <= a.T && q1 - q0 <= t &&
+                    q1 - q0 <= most;
+  c = q1 - q0;
+  if (!fine) {
+    if (report) tr_flag(a, PKV_DEV_BAD_CONTEXT_LEN);
+    t = t < 0 ? 0 : (t > limit ? limit : t);
+    q0 = q0 < 0 ? 0 : (q0 > a.T ? a.T : q0);
+    const int end = q1 > a.T ? a.T : q1;
+    c = end > q0 ? end - q0 : 0;
+    c = c > t ? t : c;
+    c = c > most ? most : c;
+  }
+}
+
+__device__ __forceinline__ int tr_depth(const TreeArgs& a, int q0, int i) {
+  if (a.depths == nullptr) return i;
+  const int d = __ldg(a.depths + q0 + i);
+  return d < 0 ? 0 : d;
+}
+
+__device__ __forceinline__ int tr_units(const TreeArgs& a, int c) {
+  return (c + a.nodes - 1) / a.nodes;
+}
+
+// Keys [lo, hi) that some row of unit `tile` may see.
+__device__ __forceinline__ void tr_keys(const TreeArgs& a, int t, int c, int tile, int& lo,
+                                        int& hi) {
+  const int base = t - c, i0 = tile * a.nodes;
+  hi = a.mask != nullptr ? t : base + min(c, i0 + a.nodes);
+  lo = 0;
+  if (a.window > 0) {  // depths are not negative
+    const int p = base + (a.depths != nullptr ? 0 : i0);
+    lo = p >= a.window ? p - a.window + 1 : 0;
+  }
+}
+
+template <int KT>
+__device__ __forceinline__ int tr_tiles(const TreeArgs& a, int t, int c, int tile, int& j0) {
+  int lo, hi;
+  tr_keys(a, t, c, tile, lo, hi);
+  j0 = lo / KT;
+  return (hi - 1) / KT + 1 - j0;
+}
+
+// A unit of n key tiles costs n + 1: its first tile lies at cost P, tile k > 0 at P + k + 1.
+// First tile at or after cost x.
+__device__ __forceinline__ int tr_first_tile(long long P, int n, long long x) {
+  if (x <= P) return 0;
+  const long long k = x - P - 1;
+  return k < 1 ? (n < 1 ? n : 1) : (k < n ? static_cast<int>(k) : n);
+}
+
+template <int KT>
+__device__ __forceinline__ long long tr_seq_cost(const TreeArgs& a, int s, bool report) {
+  int t, c, q0, j0;
+  tr_seq(a, s, t, c, q0, report);
+  long long cost = 0;
+  const int nu = tr_units(a, c);
+  for (int u = 0; u < nu; ++u) cost += tr_tiles<KT>(a, t, c, u, j0) + 1;
+  return cost * a.Hkv;
+}
+
+// A CTA's place in the list of units, and the part of the unit there that is its own.
+struct TreeWalk {
+  int32_t s, g, tile;
+  long long P, lo, hi;  // cost before the unit; the CTA's run of costs
+  int32_t t, c, q0;     // of sequence s
+  int32_t j0, n;        // the unit's first key tile and how many
+  int32_t ka, kb;       // of those, the CTA's
+};
+
+// Fills in the unit at (s, g, tile); false behind the CTA's last one.
+template <int KT>
+__device__ __forceinline__ bool tr_unit(const TreeArgs& a, TreeWalk& w) {
+  for (;;) {
+    if (w.s >= a.S || w.P >= w.hi) return false;
+    tr_seq(a, w.s, w.t, w.c, w.q0, false);
+    if (w.tile >= tr_units(a, w.c)) {
+      w.tile = 0;
+      if (w.c == 0 || ++w.g >= a.Hkv) {
+        w.g = 0;
+        ++w.s;
+      }
+      continue;
+    }
+    w.n = tr_tiles<KT>(a, w.t, w.c, w.tile, w.j0);
+    w.ka = tr_first_tile(w.P, w.n, w.lo);
+    w.kb = tr_first_tile(w.P, w.n, w.hi);
+    if (w.kb > w.ka) return true;
+    w.P += w.n + 1;
+    ++w.tile;
+  }
+}
+template <int KT>
+__device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeWalk& w) {
+  w.P += w.n + 1;
+  ++w.tile;
+  return tr_unit<KT>(a, w);
+}
+
+enum {
+  kTrKFull = 0,     // [4] K stage landed (TMA bytes)
+  kTrKEmpty = 4,    // [4] K stage consumed (commit after S)
+  kTrVFull = 8,     // [4] V stage landed
+  kTrVEmpty = 12,   // [4] V stage consumed (commit after P V)
+  kTrQFull = 16,    // [2] query tile landed
+  kTrQEmpty = 18,   // [2] query tile consumed (commit after the piece's last S)
+  kTrSFull = 20,    // [2] S in tensor memory (commit)
+  kTrSEmpty = 22,   // [2] S read by the row warps
+  kTrPFull = 24,    // [2] P in tensor memory (row warps)
+  kTrPvDone = 26,   // [2] P V done (commit)
+  kTrOEmpty = 28,   // the piece's O read out by the row warps
+  kTrDrain = 29,    // every MMA of the CTA done (final commit)
+  kTrBars = 30
+};
+constexpr uint32_t kTrSlotOff = 8 * kTrBars;       // tensor-memory base address
+constexpr uint32_t kTrDeadOff = kTrSlotOff + 8;    // [4] give-up bits of the row-warp pairs
+constexpr uint32_t kTrOddOff = kTrDeadOff + 16;    // [2] a piece met values of V that are not finite
+constexpr uint32_t kTrWalkOff = kTrOddOff + 8;     // the CTA's first TreeWalk
+constexpr uint32_t kTrBarArea = 512;
+static_assert(kTrWalkOff % 8 == 0 && kTrWalkOff + sizeof(TreeWalk) <= kTrBarArea, "barrier area");
+
+template <typename T, int D>
+struct TreeShape {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  static constexpr int KT = D == 256 ? 64 : 128;      // keys of a tile
+  static constexpr int kHalfKeys = KT / 2;            // a row thread's
+  static constexpr int kChunks = D * 2 / 128;         // 128-byte column chunks of a row
+  static constexpr uint32_t kQTile = kTrRows * D * 2;
+  static constexpr uint32_t kTile = KT * D * 2;       // K or V tile
+  static constexpr uint32_t kGroup = kChunks * 1024;  // 8 keys of a tile, every chunk
+  static constexpr int kQ = D == 256 ? 1 : 2;         // query tiles
+  static constexpr int kK = D == 64 ? 3 : 2;          // K ring
+  static constexpr int kV = D == 64 ? 4 : 3;          // V ring
+  static constexpr uint32_t kQOff = 0;
+  static constexpr uint32_t kKOff = kQ * kQTile;
+  static constexpr uint32_t kVOff = kKOff + kK * kTile;
+  static constexpr uint32_t kBarOff = kVOff + kV * kTile;
+  static constexpr uint32_t kXchOff = kBarOff + kTrBarArea;           // [2 halves][128] floats
+  static constexpr uint32_t kBytes = kXchOff + 2 * kTrRows * 4 + 1024;  // + alignment slack
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kOCol = 256;                              // O: D columns
+  static constexpr uint32_t kPCol = D == 256 ? 2 * KT : 384;          // P[b]: KT / 2 columns each
+  static constexpr uint32_t kIdQK = ptx::idesc_f16(kTrRows, KT, kBf16, false);
+  static constexpr uint32_t kIdPV = ptx::idesc_f16(kTrRows, D, kBf16, true);
+  static constexpr int kHalfD = D / 2;                                // O columns of a row thread
+  // P = 2^(x - m + shift): f16 loses values below 2^-24, so its P uses the range above 1 too
+  static constexpr float kShift = kBf16 ? 0.f : 7.f;
+  static_assert(2 * KT <= kOCol && kBytes <= 232448, "tensor and shared memory");
+  static_assert(D == 256 ? kPCol + KT <= kOCol : (kOCol + D <= kPCol && kPCol + KT <= kTmemCols),
+                "tensor memory");
+};
+
+// 16 consecutive 32-bit columns of this thread's lane, waited for.  Whole warp.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 1 / x, one instruction.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
+}
+
+// Bits [at, at + 64) of a row of W words (at >= 0; bits past the words are 0).
+__device__ __forceinline__ uint64_t bits_of(const uint32_t* row, int W, int at) {
+  const int w = at >> 5, sh = at & 31;
+  const uint32_t x0 = w < W ? __ldg(row + w) : 0u;
+  const uint32_t x1 = w + 1 < W ? __ldg(row + w + 1) : 0u;
+  const uint32_t x2 = w + 2 < W ? __ldg(row + w + 2) : 0u;
+  const uint32_t lo = __funnelshift_r(x0, x1, sh), hi = __funnelshift_r(x1, x2, sh);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// Which of the keys k0 .. k0 + n - 1 (n <= 64) drafted token i sees, bit by bit.
+__device__ __forceinline__ uint64_t tr_sees(const TreeArgs& a, const TreeWalk& w, int i, int depth,
+                                            int k0, int n) {
+  const int base = w.t - w.c;
+  uint64_t vis;
+  if (a.mask == nullptr) {
+    vis = low_bits(base + i + 1 - k0);
+  } else {
+    vis = low_bits(base - k0);
+    if (k0 + n > base) {
+      const uint32_t* const row = a.mask + static_cast<int64_t>(w.q0 + i) * a.W;
+      const int at = k0 - base;  // drafted token of bit 0
+      const uint64_t m = at >= 0 ? bits_of(row, a.W, at) : bits_of(row, a.W, 0) << -at;
+      vis |= m & low_bits(w.t - k0);
+    }
+  }
+  if (a.window > 0) {
+    const int pos = base + depth;
+    if (a.depths == nullptr) {
+      vis &= ~low_bits(pos - a.window + 1 - k0);
+    } else {
+      vis &= ~low_bits(min(pos - a.window + 1, base) - k0);
+      if (depth >= a.window) {
+        for (int e = max(0, base - k0); e < n && k0 + e < w.t; ++e)
+          if (depth - tr_depth(a, w.q0, k0 + e - base) >= a.window) vis &= ~(1ull << e);
+      }
+    }
+  }
+  return n >= 64 ? vis : vis & low_bits(n);
+}
+
+// Keys that one row of a unit may see and another not, as up to two ranges: values of V there
+// that are not finite must not reach the rows that do not see them (0 * infinity).
+__device__ __forceinline__ void tr_mixed(const TreeArgs& a, const TreeWalk& w, int (&from)[2],
+                                         int (&to)[2]) {
+  const int base = w.t - w.c, i0 = w.tile * a.nodes, last = min(w.c, i0 + a.nodes) - 1;
+  int lo, hi;
+  tr_keys(a, w.t, w.c, w.tile, lo, hi);
+  from[1] = a.mask != nullptr ? base : base + i0 + 1;
+  to[1] = hi;
+  from[0] = lo;
+  to[0] = lo;
+  if (a.window > 0)
+    to[0] = min(base + (a.depths != nullptr ? w.c - 1 : last) - a.window + 1, from[1]);
+}
+
+template <typename T>
+__device__ __forceinline__ bool odd_pair(uint32_t x) {  // one of two 16-bit values not finite
+  constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  return (x & e) == e || (x & (e << 16)) == (e << 16);
+}
+
+template <typename T, int D, bool kBias>
+__global__ void __launch_bounds__(kTrThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap qmap,
+                          const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
+  using Sh = TreeShape<T, D>;
+  constexpr int KT = Sh::KT, HK = Sh::kHalfKeys, HD = Sh::kHalfD;
+  constexpr uint32_t NQ = Sh::kQ, NK = Sh::kK, NV = Sh::kV;
+  // the joining kernel may be launched: it waits for the whole of this grid
+  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base_s = (raw + 1023u) & ~1023u;
+  uint8_t* const base_p = smem_raw + (base_s - raw);
+  const uint32_t bars = base_s + Sh::kBarOff;
+  const int BS = a.bs, bs_log = 31 - __clz(a.bs);
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(base_p + Sh::kBarOff + kTrSlotOff);
+  TreeWalk* const first = reinterpret_cast<TreeWalk*>(base_p + Sh::kBarOff + kTrWalkOff);
+  volatile int* const odd_seen = reinterpret_cast<volatile int*>(base_p + Sh::kBarOff + kTrOddOff);
+
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+    for (int st = 0; st < 4; ++st) {
+      ptx::mbar_init(bar(kTrKFull + st), 1);
+      ptx::mbar_init(bar(kTrKEmpty + st), 1);
+      ptx::mbar_init(bar(kTrVFull + st), 1);
+      ptx::mbar_init(bar(kTrVEmpty + st), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar(kTrQFull + b), 1);
+      ptx::mbar_init(bar(kTrQEmpty + b), 1);
+      ptx::mbar_init(bar(kTrSFull + b), 1);
+      ptx::mbar_init(bar(kTrSEmpty + b), kTrRowWarps);
+      ptx::mbar_init(bar(kTrPFull + b), kTrRowWarps);
+      ptx::mbar_init(bar(kTrPvDone + b), 1);
+      odd_seen[b] = 0;
+    }
+    ptx::mbar_init(bar(kTrOEmpty), kTrRowWarps);
+    ptx::mbar_init(bar(kTrDrain), 1);
+    ptx::fence_barrier_init();
+    for (int i = 0; i < 4; ++i) reinterpret_cast<int*>(base_p + Sh::kBarOff + kTrDeadOff)[i] = 0;
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(slot), Sh::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+
+  // ---- the CTA's run: costs of all sequences summed up (in the K ring, free until the first
+  // load), then the unit in which the run begins ------------------------------------------
+  {
+    long long* const cpre = reinterpret_cast<long long*>(base_p + Sh::kKOff);
+    long long* const wsum = cpre + a.S + 1;
+    const int tid = threadIdx.x;
+    const int per = (a.S + kTrThreads - 1) / kTrThreads;
+    const int b0 = min(a.S, tid * per), b1 = min(a.S, b0 + per);
+    long long local = 0;
+    for (int s = b0; s < b1; ++s) local += tr_seq_cost<KT>(a, s, blockIdx.x == 0);
+    long long x = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    long long run = x - local;
+    for (int w = 0; w < warp; ++w) run += wsum[w];
+    for (int s = b0; s < b1; ++s) {
+      cpre[s] = run;
+      if (per > 1) run += tr_seq_cost<KT>(a, s, false);
+      else run += local;
+    }
+    if (tid == kTrThreads - 1) cpre[a.S] = run;
+    ptx::fence_proxy_async_smem();  // the rings' copies come after these stores
+    __syncthreads();
+    if (tid == 0) {
+      const long long C = cpre[a.S];
+      TreeWalk w{};
+      w.lo = C * blockIdx.x / gridDim.x;
+      w.hi = C * (blockIdx.x + 1) / gridDim.x;
+      w.s = a.S;
+      if (w.lo < C) {
+        int l = 0, h = a.S;  // the last sequence with cpre <= lo: it has units, and lo is in one
+        while (h - l > 1) {
+          const int mid = (l + h) >> 1;
+          if (cpre[mid] <= w.lo) l = mid; else h = mid;
+        }
+        int j0;
+        tr_seq(a, l, w.t, w.c, w.q0, false);
+        const long long cost_g = (cpre[l + 1] - cpre[l]) / a.Hkv;
+        w.s = l;
+        w.g = static_cast<int>((w.lo - cpre[l]) / cost_g);
+        w.P = cpre[l] + w.g * cost_g;
+        for (;;) {
+          const int n = tr_tiles<KT>(a, w.t, w.c, w.tile, j0);
+          if (w.P + n + 1 > w.lo) break;
+          w.P += n + 1;
+          ++w.tile;
+        }
+      }
+      // the unit that this run begins and another ends, for the joining kernel
+      TreeCut cut{0, C, 0, 0, 0, 0};
+      if (w.hi > w.lo && w.hi < C) {
+        int l = 0, h = a.S;  // the unit that holds cost hi - 1 ...
+        while (h - l > 1) {
+          const int mid = (l + h) >> 1;
+          if (cpre[mid] <= w.hi - 1) l = mid; else h = mid;
+        }
+        int t, c, q0, j0, n = 0, u = 0;
+        tr_seq(a, l, t, c, q0, false);
+        const long long cost_g = (cpre[l + 1] - cpre[l]) / a.Hkv;
+        const int g = static_cast<int>((w.hi - 1 - cpre[l]) / cost_g);
+        long long P = cpre[l] + g * cost_g;
+        for (;; ++u) {
+          n = tr_tiles<KT>(a, t, c, u, j0);
+          if (P + n + 1 > w.hi - 1) break;
+          P += n + 1;
+        }
+        // ... if its first tile is this run's and its last is not
+        if (P >= w.lo && tr_first_tile(P, n, w.hi) < n) {
+          cut.P = P;
+          cut.n = n;
+          cut.row0 = q0 + u * a.nodes;
+          cut.rows = min(a.nodes, c - u * a.nodes) * a.G;
+          cut.g = g;
+        }
+      }
+      a.cuts[blockIdx.x] = cut;
+      *first = w;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();  // (the prefix sums have been read: the rings may be filled)
+  ptx::tc_fence_after();
+  const uint32_t tmem = *slot;
+  TreeWalk w = *first;
+  bool more = tr_unit<KT>(a, w);
+
+  if (warp == kTrQWarp) {
+    // ---- TMA producer of the query tiles ---------------------------------------------
+    uint32_t un = 0;
+    bool alive = true;
+    const uint64_t policy = ptx::policy_evict_first();
+    for (; more; more = tr_next<KT>(a, w)) {
+      const uint32_t qb = un % NQ;
+      const int here = min(a.nodes, w.c - w.tile * a.nodes);
+      const int boxes = (here + a.box - 1) / a.box;
+      const uint32_t box_bytes = static_cast<uint32_t>(a.box * a.G) * 128u;
+      bool ok = true;
+      if (lane == 0) {
+        ok = ptx::mbar_wait(bar(kTrQEmpty + qb), ((un / NQ) & 1u) ^ 1u, kTrWaitNs);
+        if (ok) ptx::mbar_arrive_expect_tx(bar(kTrQFull + qb), boxes * box_bytes * Sh::kChunks);
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) { alive = false; break; }
+      __syncwarp();
+      for (int i = lane; i < boxes * Sh::kChunks; i += 32) {
+        const int bx = i / Sh::kChunks, cc = i - bx * Sh::kChunks;
+        ptx::tma_load_3d(base_s + Sh::kQOff + qb * Sh::kQTile + cc * kTrChunk + bx * box_bytes,
+                         &qmap, cc * 64, w.g * a.G, w.q0 + w.tile * a.nodes + bx * a.box,
+                         bar(kTrQFull + qb), policy);
+      }
+      ++un;
+    }
+    if (lane == 0) {
+      if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+      for (uint32_t k = un > NQ ? un - NQ : 0u; k < un; ++k)  // copies in flight land first
+        ptx::mbar_wait(bar(kTrQFull + k % NQ), (k / NQ) & 1u, kTrWaitNs / 8);
+    }
+  } else if (warp == 0 || warp == kTrVWarp) {
+    // ---- TMA producers of K (warp 0) and V (warp 10) ---------------------------------
+    const bool is_k = warp == 0;
+    const uint64_t policy = ptx::policy_evict_normal();
+    const int32_t groups_total = a.NB * a.Hkv * (BS / 8);  // 8-row groups of the cache
+    const int nblk = KT >> bs_log;                         // cache blocks of a tile
+    const CUtensorMap* const map = is_k ? &kmap : &vmap;
+    const int full0 = is_k ? kTrKFull : kTrVFull, empty0 = is_k ? kTrKEmpty : kTrVEmpty;
+    const uint32_t ring = base_s + (is_k ? Sh::kKOff : Sh::kVOff);
+    const uint32_t NS = is_k ? NK : NV;
+    uint32_t it = 0;
+    bool alive = true;
+    for (; alive && more; more = tr_next<KT>(a, w)) {
+      int lo, hi;
+      tr_keys(a, w.t, w.c, w.tile, lo, hi);
+      for (int k = w.ka; k < w.kb; ++k, ++it) {
+        const uint32_t st = it % NS;
+        const int bi = nblk * (w.j0 + k) + (lane & (nblk - 1));
+        int32_t y = groups_total;  // a box wholly past the end: zero-filled
+        // blocks behind the last key, and those that the window has left behind, are not read
+        if (lane < nblk && bi * BS < hi && (bi + 1) * BS > lo) {
+          const int id = __ldg(a.block_tables + static_cast<int64_t>(w.s) * a.MAXB + bi);
+          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(a.NB))
+            y = (id * a.Hkv + w.g) * (BS / 8);
+          else if (is_k)
+            tr_flag(a, PKV_DEV_BAD_BLOCK_ID);
+        }
+        bool ok = true;
+        if (lane == 0) {
+          ok = ptx::mbar_wait(bar(empty0 + st), ((it / NS) & 1u) ^ 1u, kTrWaitNs);
+          if (ok) ptx::mbar_arrive_expect_tx(bar(full0 + st), Sh::kTile);
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) { alive = false; break; }
+        __syncwarp();
+        if (lane < nblk)
+          ptx::tma_load_4d(ring + st * Sh::kTile + lane * (BS / 8) * Sh::kGroup, map, 0, 0, 0, y,
+                           bar(full0 + st), policy);
+      }
+      if (!alive) break;
+    }
+    if (lane == 0) {
+      if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+      for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k)  // copies in flight land first
+        ptx::mbar_wait(bar(full0 + k % NS), (k / NS) & 1u, kTrWaitNs / 8);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer: S of a tile ahead of P V of the one before, across units too --------
+    uint32_t it = 0, un = 0;
+    bool alive = true;
+    auto wait1 = [&](uint32_t b, uint32_t parity) {
+      return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, kTrWaitNs)) != 0;
+    };
+    // address of 16 bytes of V: key row, piece of the row
+    auto v_at = [&](uint32_t vt, int row, int piece) {
+      return vt + (row >> 3) * Sh::kGroup + (piece >> 3) * 1024 + (row & 7) * 128 +
+             (piece & 7) * 16;
+    };
+    constexpr int kPieces = 8 * Sh::kChunks;  // 16-byte pieces of a key's V
+    // O (+)= P V for tile k of piece n (the x-th tile of the CTA)
+    auto pv = [&](uint32_t x, const TreeWalk& u, int k, uint32_t n) {
+      const int b = static_cast<int>(x & 1u);
+      const uint32_t st = x % NV;
+      if (k == u.ka) {
+        if (!wait1(bar(kTrOEmpty), (n & 1u) ^ 1u)) return false;
+        if (lane == 0) odd_seen[n & 1u] = 0;  // the piece before the last one has been read out
+      }
+      if (!wait1(bar(kTrVFull + st), (x / NV) & 1u)) return false;
+      const uint32_t vt = base_s + Sh::kVOff + st * Sh::kTile;
+      const int k0 = (u.j0 + k) * KT;
+      int lo, hi;
+      tr_keys(a, u.t, u.c, u.tile, lo, hi);
+      bool wrote = false;
+      // rows of V that no query of the unit sees may hold anything, and P is 0 there: zeroed
+      // (blocks that were not read are zero already)
+      auto clear = [&](int r0, int r1) {
+        for (int i = lane; i < (r1 - r0) * kPieces; i += 32)
+          ptx::st_shared_v4(v_at(vt, r0 + i / kPieces, i % kPieces), 0u, 0u, 0u, 0u);
+        wrote = true;
+      };
+      if (k0 + KT > hi) clear(max(0, hi - k0), min(KT, ((hi + BS - 1) >> bs_log << bs_log) - k0));
+      if (lo > k0) clear(max(0, (lo >> bs_log << bs_log) - k0), min(KT, lo - k0));
+      // rows that some queries see: values that are not finite are taken out and added to
+      // the rows that see them at the end
+      int from[2], to[2];
+      tr_mixed(a, u, from, to);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r0 = max(0, from[e] - k0), r1 = min(KT, to[e] - k0);
+        for (int i = lane; i < (r1 - r0) * kPieces; i += 32) {
+          const uint32_t at = v_at(vt, r0 + i / kPieces, i % kPieces);
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(at)
+                       : "memory");
+          if (odd_pair<T>(v[0]) || odd_pair<T>(v[1]) || odd_pair<T>(v[2]) || odd_pair<T>(v[3])) {
+            constexpr uint32_t m = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if ((v[q] & m) == m) v[q] &= 0xffff0000u;
+              if ((v[q] & (m << 16)) == (m << 16)) v[q] &= 0xffffu;
+            }
+            ptx::st_shared_v4(at, v[0], v[1], v[2], v[3]);
+            odd_seen[n & 1u] = 1;
+            wrote = true;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, wrote)) {
+        __threadfence_block();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!wait1(bar(kTrPFull + b), (x >> 1) & 1u)) return false;
+      ptx::tc_fence_after();
+      const uint32_t pt = tmem + Sh::kPCol + b * (KT / 2);
+#pragma unroll
+      for (int ks = 0; ks < KT / 16; ++ks)  // 16 keys = 8 packed columns of P
+        ptx::umma_f16_ta_elect(tmem + Sh::kOCol, pt + ks * 8,
+                               ptx::smem_desc_sw128(vt + ks * 2 * Sh::kGroup, 1024, Sh::kGroup),
+                               Sh::kIdPV, k > u.ka || ks > 0);
+      ptx::umma_commit_elect(bar(kTrPvDone + b));
+      ptx::umma_commit_elect(bar(kTrVEmpty + st));
+      __syncwarp();
+      return true;
+    };
+    bool pending = false;  // a P V not issued yet: tile pk of pu, the px-th, in piece pn
+    uint32_t px = 0, pn = 0;
+    int pk = 0;
+    TreeWalk pu = w;
+    for (; alive && more; more = tr_next<KT>(a, w)) {
+      const uint32_t qb = un % NQ;
+      if (!wait1(bar(kTrQFull + qb), (un / NQ) & 1u)) { alive = false; break; }
+      const uint32_t n = un++;
+      ptx::tc_fence_after();
+      for (int k = w.ka; k < w.kb; ++k, ++it) {
+        const uint32_t st = it % NK;
+        const int b = static_cast<int>(it & 1u);
+        if (!wait1(bar(kTrKFull + st), (it / NK) & 1u) ||
+            !wait1(bar(kTrSEmpty + b), ((it >> 1) & 1u) ^ 1u)) {
+          alive = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t qa = base_s + Sh::kQOff + qb * Sh::kQTile;
+        const uint32_t kb = base_s + Sh::kKOff + st * Sh::kTile;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t kin = (ks & 3) * 32;  // 16 columns inside a 128-byte chunk
+          ptx::umma_f16_elect(tmem + b * KT,
+                              ptx::smem_desc_sw128(qa + (ks >> 2) * kTrChunk + kin, 16, 1024),
+                              ptx::smem_desc_sw128(kb + (ks >> 2) * 1024 + kin, 16, Sh::kGroup),
+                              Sh::kIdQK, ks > 0);
+        }
+        ptx::umma_commit_elect(bar(kTrSFull + b));
+        ptx::umma_commit_elect(bar(kTrKEmpty + st));
+        if (k == w.kb - 1) ptx::umma_commit_elect(bar(kTrQEmpty + qb));
+        __syncwarp();
+        if (pending && !pv(px, pu, pk, pn)) { alive = false; break; }
+        pending = true;
+        px = it;
+        pk = k;
+        pn = n;
+        if (k == w.ka) pu = w;
+      }
+      if (!alive) break;
+    }
+    if (alive && pending && !pv(px, pu, pk, pn)) alive = false;
+    if (lane == 0) {
+      if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+      ptx::umma_commit(bar(kTrDrain));  // lands once every MMA issued above is done
+      ptx::mbar_wait(bar(kTrDrain), 0, kTrWaitNs);
+    }
+    __syncwarp();
+  } else {
+    // ---- row threads: scores, softmax, output ------------------------------------------
+    // The two warps of a lane quarter meet at every exchange (named barrier); a warp whose
+    // wait ran out skips ahead to the next exchange and flags itself there, and both leave
+    // together.  A quarter without rows only keeps the hand-offs going.
+    const int q4 = warp & 3, h = (warp - 2) >> 2;
+    const int r = 32 * q4 + lane;  // tile row = tensor-memory lane
+    const int rn = r / a.G, rh = r - rn * a.G;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * q4) << 16;
+    const uint32_t pcol = tmem + lane_off + Sh::kPCol + h * (HK / 2);
+    const uint32_t oa = tmem + lane_off + Sh::kOCol + h * HD;  // this thread's half of O
+    float* const xch = reinterpret_cast<float*>(base_p + Sh::kXchOff);
+    volatile int* const dead_bits =
+        reinterpret_cast<volatile int*>(base_p + Sh::kBarOff + kTrDeadOff);
+    const uint32_t pair_bar = 1 + q4;
+    bool dead = false;       // this warp gave up a wait
+    bool pair_dead = false;  // either warp of the pair did
+    auto exchange = [&](float x) {  // the other half's x for this row
+      ptx::named_bar_sync(pair_bar, 64);
+      if (dead && lane == 0) dead_bits[q4] = dead_bits[q4] | (1 << h);
+      xch[h * kTrRows + r] = x;
+      ptx::named_bar_sync(pair_bar, 64);
+      pair_dead = dead_bits[q4] != 0;
+      return xch[(1 - h) * kTrRows + r];
+    };
+    uint32_t it = 0, un = 0;
+    auto wait_all = [&](uint32_t b, uint32_t parity) {
+      if (dead) return;
+      dead = !__all_sync(0xffffffffu, ptx::mbar_wait(b, parity, kTrWaitNs));
+    };
+    // A piece's output is written after the first tile of the next (its last P V is done by
+    // then), so that the tensor cores are not left waiting on it.
+    bool pend = false, pend_live = false, pend_valid = false;
+    TreeWalk pu = w;
+    float pend_m = 0.f, pend_l = 0.f;
+    uint32_t pend_x = 0, pend_n = 0;
+    auto epilogue = [&]() {
+      pend = false;
+      float lt = pend_l;
+      if (pend_live) lt += exchange(pend_l);
+      if (pair_dead) return;
+      wait_all(bar(kTrPvDone + (pend_x & 1u)), (pend_x >> 1) & 1u);
+      if (dead) return;
+      if (pend_live) {
+        ptx::tc_fence_after();
+        const bool whole = pu.ka == 0 && pu.kb == pu.n;
+        // a piece that begins its unit is the run's last one, another its first
+        const int64_t cut_row =
+            (2 * static_cast<int64_t>(blockIdx.x) + (pu.ka == 0 ? 1 : 0)) * kTrRows + r;
+        const int node = pu.tile * a.nodes + rn;
+        T* const out_row = static_cast<T*>(a.out) +
+                           (static_cast<int64_t>(pu.q0 + node) * a.Hq + pu.g * a.G + rh) * D +
+                           h * HD;
+        float* const part_row = a.part_o + cut_row * D + h * HD;
+        if (!whole && pend_valid && h == 0) a.part_ml[cut_row] = make_float2(pend_m, lt);
+        const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
+        const bool odd = odd_seen[pend_n & 1u] != 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld32(oa + c0, o);
+          if (!pend_valid) continue;
+          if (odd) {  // values of V that are not finite, for the rows that see them
+            int from[2], to[2];
+            tr_mixed(a, pu, from, to);
+            const int first_key = (pu.j0 + pu.ka) * KT, last_key = (pu.j0 + pu.kb) * KT;
+            const int depth = tr_depth(a, pu.q0, node);
+            for (int e = 0; e < 2; ++e) {
+              for (int p = max(from[e], first_key); p < min(to[e], last_key); ++p) {
+                if (tr_sees(a, pu, node, depth, p, 1) == 0) continue;
+                const int id =
+                    __ldg(a.block_tables + static_cast<int64_t>(pu.s) * a.MAXB + (p >> bs_log));
+                if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.NB)) continue;
+                const T* const vr =
+                    static_cast<const T*>(a.v_cache) +
+                    ((static_cast<int64_t>(id) * a.Hkv + pu.g) * BS + (p & (BS - 1))) * D +
+                    h * HD + c0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float v = ptx::to_float(vr[i]);
+                  if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+                }
+              }
+            }
+          }
+          if (whole) {
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              y[i] = ptx::pack2<T>(__uint_as_float(o[2 * i]) * inv,
+                                   __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(out_row + c0 + 2 * i) =
+                  make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(part_row + c0 + i) =
+                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        ptx::tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(kTrOEmpty));
+    };
+    for (; more && !pair_dead; more = tr_next<KT>(a, w)) {
+      const int here = min(a.nodes, w.c - w.tile * a.nodes);
+      const bool live = 32 * q4 < here * a.G;  // a row of this quarter
+      const bool valid = rn < here;
+      const int node = w.tile * a.nodes + (valid ? rn : 0);
+      const int base = w.t - w.c;
+      const int depth = live ? tr_depth(a, w.q0, node) : 0;
+      float slope = 0.f;
+      if constexpr (kBias) {
+        if (live && a.slopes != nullptr)
+          slope = __ldg(a.slopes + w.g * a.G + rh) * 1.4426950408889634f;
+      }
+      if (live && a.depths != nullptr && h == 0 && valid && w.ka == 0 &&
+          __ldg(a.depths + w.q0 + node) < 0)
+        tr_flag(a, PKV_DEV_BAD_POSITION);
+      float m = -INFINITY, l = 0.f;
+      for (int k = w.ka; k < w.kb; ++k, ++it) {
+        const int b = static_cast<int>(it & 1u);
+        wait_all(bar(kTrSFull + b), (it >> 1) & 1u);
+        if (live) {
+          uint32_t v[HK];
+          const int k0 = (w.j0 + k) * KT + h * HK;
+          float mx = -INFINITY;
+          if (!dead) {
+            ptx::tc_fence_after();
+            const uint32_t sa = tmem + lane_off + b * KT + h * HK;
+#pragma unroll
+            for (int i = 0; i < HK; i += 32)
+              ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
+            ptx::tmem_wait_ld();
+            if constexpr (kBias) {  // scores in log2 units
+              if (a.cap_log2 > 0.f) {
+                // tanh z = 1 - 2 / (1 + e^2z): off by some 1e-7 of the cap
+#pragma unroll
+                for (int i = 0; i < HK; ++i)
+                  v[i] = __float_as_uint(
+                      fmaf(-2.f * a.cap_log2,
+                           rcp_approx(1.f + ptx::ex2(__uint_as_float(v[i]) * a.cap_z)), a.cap_log2));
+              } else {
+#pragma unroll
+                for (int i = 0; i < HK; ++i)
+                  v[i] = __float_as_uint(__uint_as_float(v[i]) * a.scale_log2);
+              }
+              if (slope != 0.f) {
+                if (a.depths == nullptr || k0 + HK <= base) {
+                  const float d0 = static_cast<float>(k0 - base - depth);
+#pragma unroll
+                  for (int i = 0; i < HK; ++i)
+                    v[i] = __float_as_uint(
+                        fmaf(slope, d0 + static_cast<float>(i), __uint_as_float(v[i])));
+                } else {
+#pragma unroll
+                  for (int i = 0; i < HK; ++i) {
+                    const int j = k0 + i - base;  // drafted token, or a cached one
+                    const int pos = j < 0 ? j : (j < w.c ? tr_depth(a, w.q0, j) : 0);
+                    v[i] = __float_as_uint(
+                        fmaf(slope, static_cast<float>(pos - depth), __uint_as_float(v[i])));
+                  }
+                }
+              }
+            }
+            // keys that the row does not see score -inf
+            const uint64_t vis = valid ? tr_sees(a, w, node, depth, k0, HK) : 0ull;
+            const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
+            if (!__all_sync(0xffffffffu, vis == low_bits(HK))) {
+#pragma unroll
+              for (int i = 0; i < HK; ++i)
+                if (!((i < 32 ? v0 >> (i & 31) : v1 >> (i & 31)) & 1u))
+                  v[i] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int i = 0; i < HK; i += 2)
+              asm("max.f32 %0, %0, %1, %2;"
+                  : "+f"(mx)
+                  : "f"(__uint_as_float(v[i])), "f"(__uint_as_float(v[i + 1])));
+          }
+          mx = fmaxf(mx, exchange(mx));
+          if (pair_dead) break;
+          const float sc = kBias ? 1.f : a.scale_log2;
+          const float mt = mx * sc;  // the row's maximum over this tile, log2 units
+          // this P buffer is free once the product of two tiles ago is done
+          wait_all(bar(kTrPvDone + b), ((it >> 1) & 1u) ^ 1u);
+          // The reference m moves only when the maximum grows by more than 2^8 (at first from
+          // -inf): O and l are scaled once the product before has landed.  The accesses are
+          // warp-wide: the whole warp takes the branch, the other rows scale by 1.
+          const bool move = mt > m + kTrRescale;
+          if (k > w.ka && __any_sync(0xffffffffu, move)) {
+            const float al = move ? ptx::ex2(m - mt) : 1.f;  // 2^-inf = 0
+            wait_all(bar(kTrPvDone + (b ^ 1)), ((it - 1) >> 1) & 1u);
+            if (!dead) {
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < HD; c0 += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld32(oa + c0, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                ptx::tmem_st32(oa + c0, o);
+              }
+            }
+            l *= al;
+          }
+          if (move) m = mt;
+          if (dead) continue;  // on to the next exchange
+          // a row that has seen nothing yet: every exponent is -inf whatever the reference
+          const float ref = m == -INFINITY ? 0.f : m - Sh::kShift;
+          float s0 = 0.f, s1 = 0.f;
+          uint32_t pk[HK / 2];
+#pragma unroll
+          for (int i = 0; i < HK / 2; ++i) {  // keys 2i, 2i + 1 of the half
+            const float x0 = ptx::ex2(fmaf(__uint_as_float(v[2 * i]), sc, -ref));
+            const float x1 = ptx::ex2(fmaf(__uint_as_float(v[2 * i + 1]), sc, -ref));
+            pk[i] = ptx::pack2<T>(x0, x1);
+            s0 += x0;
+            s1 += x1;
+          }
+          if constexpr (HK == 64) ptx::tmem_st32(pcol + b * (KT / 2), pk);
+          else tmem_st16(pcol + b * (KT / 2), pk);
+          l += s0 + s1;
+          ptx::tc_fence_before();
+        }
+        if (dead) continue;
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(kTrSEmpty + b));
+          ptx::mbar_arrive(bar(kTrPFull + b));
+        }
+        if (k == w.ka && pend) {  // the previous piece's output
+          epilogue();
+          if (pair_dead) break;
+        }
+      }
+      if (pair_dead) break;
+      if (pend) epilogue();  // only if a wait ran out: the flags go on to the next exchange
+      if (pair_dead) break;
+      pend = true;
+      pend_live = live;
+      pend_valid = valid;
+      pend_m = m == -INFINITY ? m : m - Sh::kShift;
+      pend_l = l;
+      pend_x = it - 1;
+      pend_n = un++;
+      pu = w;
+    }
+    if (pend && !pair_dead) epilogue();
+    if ((dead || pair_dead) && lane == 0) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc(tmem, Sh::kTmemCols);
+}
+
+// Joins the pieces of the units that runs' borders cut: CTA x looks after the unit that run x
+// begins, a warp a row.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in order.
+constexpr int kJoinWarps = 4, kJoinRows = 16;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeArgs a, int runs) {
+  constexpr int E = D / 32;  // elements of a lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeCut cut = a.cuts[blockIdx.x];
+  if (cut.n == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the runs that hold the unit's first and last tile; those between hold a tile or none
+  const int x0 = blockIdx.x;
+  const long long end = cut.P + cut.n;
+  const int x1 = static_cast<int>(((end + 1) * runs - 1) / cut.C);
+  auto holds = [&](int x) {
+    const long long lo = cut.C * x / runs, hi = cut.C * (x + 1) / runs;
+    return tr_first_tile(cut.P, cut.n, hi) > tr_first_tile(cut.P, cut.n, lo);
+  };
+  for (int r = blockIdx.y * kJoinRows + warp; r < min(cut.rows, (blockIdx.y + 1) * kJoinRows);
+       r += kJoinWarps) {
+    auto row = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == x0)) * kTrRows + r; };
+    float M = -INFINITY;
+    for (int x = x0 + lane; x <= x1; x += 32)
+      if (holds(x)) M = fmaxf(M, a.part_ml[row(x)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float total = 0.f, acc[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    for (int b0 = x0; b0 <= x1; b0 += 32) {
+      const int x = b0 + lane;
+      float wt = 0.f, part = 0.f;
+      const bool here = x <= x1 && holds(x);
+      if (here) {
+        const float2 ml = a.part_ml[row(x)];
+        wt = M == -INFINITY ? 1.f : ptx::ex2(ml.x - M);
+        part = ml.y * wt;
+      }
+      const uint32_t on = __ballot_sync(0xffffffffu, here);
+      for (int i = 0; i < 32 && b0 + i <= x1; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wt, i);
+        total += __shfl_sync(0xffffffffu, part, i);
+        if (!((on >> i) & 1u)) continue;
+        const float* const src = a.part_o + row(b0 + i) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], wi, acc[e]);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const int rn = r / a.G, rh = r - rn * a.G;
+    T* const dst = static_cast<T*>(a.out) +
+                   (static_cast<int64_t>(cut.row0 + rn) * a.Hq + cut.g * a.G + rh) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+template <typename T, int D, bool kBias>
+int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, cudaStream_t st) {
+  using Sh = TreeShape<T, D>;
+  static SmemOnce once;
+  int rc = allow_dynamic_smem(
+      once, reinterpret_cast<const void*>(tree_attention_kernel<T, D, kBias>), Sh::kBytes);
+  if (rc != PKV_OK) return rc;
+  static_assert((kTrMaxSeqs + 1 + 12) * 8 <= Sh::kK * Sh::kTile, "the prefix sums' room");
+  CUtensorMap qmap, kmap, vmap;
+  const CUtensorMapDataType ty =
+      dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  // q [T, Hq, D]: boxes of 64 columns (128 B) x G heads x `box` drafted tokens, whole 8-row
+  // swizzle atoms
+  const int64_t qdims[3] = {D, a.Hq, a.T};
+  const int64_t qstrides[2] = {static_cast<int64_t>(D) * 2, static_cast<int64_t>(a.Hq) * D * 2};
+  const int32_t qbox[3] = {64, a.G, a.box};
+  rc = encode_map_3d(&qmap, a.q, ty, 2, qdims, qstrides, qbox, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != PKV_OK) return rc;
+  // K and V [rows, D] as (column in chunk, row in group, chunk, 8-row group): a box is a cache
+  // block of one KV head, landing chunk-major within each group
+  const int64_t kvdims[4] = {64, 8, Sh::kChunks, static_cast<int64_t>(a.NB) * a.Hkv * (a.bs / 8)};
+  const int64_t kvstrides[3] = {static_cast<int64_t>(D) * 2, 128, 8 * static_cast<int64_t>(D) * 2};
+  const int32_t kvbox[4] = {64, 8, Sh::kChunks, a.bs / 8};
+  rc = encode_map_4d(&kmap, k_cache, ty, kvdims, kvstrides, kvbox, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != PKV_OK) return rc;
+  rc = encode_map_4d(&vmap, a.v_cache, ty, kvdims, kvstrides, kvbox, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != PKV_OK) return rc;
+  tree_attention_kernel<T, D, kBias><<<sms, kTrThreads, Sh::kBytes, st>>>(qmap, kmap, vmap, a);
+  PKV_CUDA(cudaGetLastError());
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(sms, kTrRows / kJoinRows);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, a, sms));
+  return PKV_OK;
+}
+
+template <typename T>
+int launch_tree_d(const TreeArgs& a, const void* k_cache, int32_t dtype, int32_t head_dim,
+                  bool bias, int sms, cudaStream_t st) {
+#define PKV_TREE(D)                                                  \
+  (bias ? launch_tree<T, D, true>(a, k_cache, dtype, sms, st)        \
+        : launch_tree<T, D, false>(a, k_cache, dtype, sms, st))
+  return head_dim == 64 ? PKV_TREE(64) : (head_dim == 128 ? PKV_TREE(128) : PKV_TREE(256));
+#undef PKV_TREE
+}
+
+size_t tree_part_bytes(int sms, int head_dim) {
+  return static_cast<size_t>(2) * sms * kTrRows * head_dim * sizeof(float);
+}
+size_t tree_ml_bytes(int sms) { return static_cast<size_t>(2) * sms * kTrRows * sizeof(float2); }
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_tree_workspace_size(int32_t head_dim, size_t* bytes) {
+  PKV_REQUIRE(bytes != nullptr, PKV_ERR_INVALID_ARG, "bytes is NULL");
+  PKV_REQUIRE(head_dim == 64 || head_dim == 128 || head_dim == 256, PKV_ERR_UNSUPPORTED,
+              "head_dim %d not in {64, 128, 256}", head_dim);
+  int sms = 0, dev = 0;
+  const int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  *bytes = tree_part_bytes(sms, head_dim) + tree_ml_bytes(sms) + sms * sizeof(TreeCut);
+  return ok();
+}
+
+int pkv_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* query_start,
+                       const int32_t* tree_mask, int32_t mask_words, const int32_t* depths,
+                       const float* slopes, float cap, int32_t window, int32_t num_seqs,
+                       int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                       void* out, int32_t* status, void* workspace, size_t workspace_bytes,
+                       int32_t dtype, void* stream) {
+  PKV_REQUIRE(dtype == PKV_F16 || dtype == PKV_BF16, PKV_ERR_DTYPE,
+              "tree attention takes f16 or bf16 (dtype %d)", dtype);
+  PKV_REQUIRE(num_seqs >= 0 && num_seqs <= kTrMaxSeqs, PKV_ERR_UNSUPPORTED,
+              "num_seqs %d outside [0, %d]", num_seqs, kTrMaxSeqs);
+  PKV_REQUIRE(num_q_heads > 0 && num_kv_heads > 0 && num_q_heads % num_kv_heads == 0,
+              PKV_ERR_INVALID_ARG, "num_q_heads %d must be a positive multiple of num_kv_heads %d",
+              num_q_heads, num_kv_heads);
+  const int G = num_q_heads / num_kv_heads;
+  PKV_REQUIRE(G <= kTrMaxGroup, PKV_ERR_UNSUPPORTED, "query heads per KV head %d above %d", G,
+              kTrMaxGroup);
+  PKV_REQUIRE(head_dim == 64 || head_dim == 128 || head_dim == 256, PKV_ERR_UNSUPPORTED,
+              "head_dim %d not in {64, 128, 256}", head_dim);
+  PKV_REQUIRE(block_size == 8 || block_size == 16 || block_size == 32, PKV_ERR_UNSUPPORTED,
+              "block_size %d not in {8, 16, 32}", block_size);
+  PKV_REQUIRE(max_blocks_per_seq > 0 && num_blocks > 0, PKV_ERR_INVALID_ARG, "bad sizes");
+  PKV_REQUIRE(static_cast<int64_t>(max_blocks_per_seq) * block_size < (int64_t(1) << 30),
+              PKV_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size >= 2^30");
+  PKV_REQUIRE(static_cast<int64_t>(num_blocks) * num_kv_heads * block_size * 4 < (int64_t(1) << 31),
+              PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * block_size * 4 >= 2^31");
+  PKV_REQUIRE(num_tokens >= 0, PKV_ERR_INVALID_ARG, "negative num_tokens");
+  PKV_REQUIRE(static_cast<int64_t>(num_tokens) * num_q_heads < (int64_t(1) << 31),
+              PKV_ERR_UNSUPPORTED, "num_tokens * num_q_heads >= 2^31");
+  PKV_REQUIRE(std::isfinite(scale), PKV_ERR_INVALID_ARG, "scale must be finite");
+  PKV_REQUIRE(std::isfinite(cap) && cap >= 0.f, PKV_ERR_INVALID_ARG,
+              "cap must be finite and not negative (0: none)");
+  PKV_REQUIRE(window >= 0, PKV_ERR_INVALID_ARG, "window must not be negative (0: none)");
+  PKV_REQUIRE(tree_mask == nullptr || mask_words > 0, PKV_ERR_INVALID_ARG,
+              "a mask has at least one word a row");
+  if (num_seqs == 0 || num_tokens == 0) return ok();
+  PKV_REQUIRE(q && k_cache && v_cache && block_tables && context_lens && query_start && out,
+              PKV_ERR_INVALID_ARG, "NULL pointer");
+  PKV_REQUIRE(aligned(q, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(out, 16),
+              PKV_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned");
+  PKV_REQUIRE(aligned(block_tables, 4) && aligned(context_lens, 4) && aligned(query_start, 4) &&
+                  aligned(tree_mask, 4) && aligned(depths, 4) && aligned(slopes, 4) &&
+                  aligned(status, 4),
+              PKV_ERR_INVALID_ARG, "a pointer is not aligned to its element");
+  PKV_REQUIRE(workspace != nullptr && aligned(workspace, 256), PKV_ERR_INVALID_ARG,
+              "workspace must be a 256-byte aligned device pointer");
+  int sms = 0, dev = 0;
+  int rc = device_sm_count(&sms, &dev);
+  if (rc != PKV_OK) return rc;
+  const size_t po = tree_part_bytes(sms, head_dim), ml = tree_ml_bytes(sms);
+  PKV_REQUIRE(workspace_bytes >= po + ml + sms * sizeof(TreeCut), PKV_ERR_INVALID_ARG,
+              "workspace of %zu bytes, %zu needed", workspace_bytes,
+              po + ml + sms * sizeof(TreeCut));
+  TreeArgs a{};
+  a.q = q;
+  a.out = out;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  a.depths = depths;
+  a.slopes = slopes;
+  a.v_cache = v_cache;
+  a.status = status;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + po);
+  a.cuts = reinterpret_cast<TreeCut*>(static_cast<char*>(workspace) + po + ml);
+  a.S = num_seqs;
+  a.T = num_tokens;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.G = G;
+  a.MAXB = max_blocks_per_seq;
+  a.NB = num_blocks;
+  a.bs = block_size;
+  a.W = mask_words;
+  a.window = window;
+  // whole 8-row swizzle atoms: a box of q is 8 / gcd(G, 8) drafted tokens, a unit whole boxes
+  a.box = G % 8 == 0 ? 1 : (G % 4 == 0 ? 2 : (G % 2 == 0 ? 4 : 8));
+  a.nodes = kTrRows / G / a.box * a.box;
+  const double log2e = 1.4426950408889634;
+  a.scale_log2 = static_cast<float>(scale * log2e);
+  a.cap_log2 = static_cast<float>(cap * log2e);
+  a.cap_z = cap > 0.f ? static_cast<float>(2.0 * log2e * scale / cap) : 0.f;
+  // without cap and slopes the maximum is taken of q . k, which a positive scale keeps in order
+  const bool bias = cap > 0.f || slopes != nullptr || !(a.scale_log2 > 0.f);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = dtype == PKV_BF16
+           ? launch_tree_d<__nv_bfloat16>(a, k_cache, dtype, head_dim, bias, sms, st)
+           : launch_tree_d<__half>(a, k_cache, dtype, head_dim, bias, sms, st);
+  return rc == PKV_OK ? ok() : rc;
+}
+
+int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int32_t num_seqs,
+                   int32_t mask_words, int32_t* tree_mask, int32_t* depths) {
+  PKV_REQUIRE(num_seqs >= 0 && mask_words > 0, PKV_ERR_INVALID_ARG, "bad sizes");
+  PKV_REQUIRE(query_start && (num_seqs == 0 || (parents && tree_mask && depths)),
+              PKV_ERR_INVALID_ARG, "NULL pointer");
+  PKV_REQUIRE(num_seqs == 0 || query_start[0] >= 0, PKV_ERR_INVALID_ARG,
+              "query_start must not be negative");
+  for (int32_t s = 0; s < num_seqs; ++s) {  // all checked before anything is written
+    const int32_t q0 = query_start[s], q1 = query_start[s + 1];
+    PKV_REQUIRE(q1 >= q0, PKV_ERR_INVALID_ARG, "query_start must not decrease");
+    PKV_REQUIRE(q1 - q0 <= static_cast<int64_t>(mask_words) * 32, PKV_ERR_INVALID_ARG,
+                "sequence %d has %d drafted tokens, a mask row holds %lld", s, q1 - q0,
+                static_cast<long long>(mask_words) * 32);
+    for (int32_t i = q0; i < q1; ++i)
+      PKV_REQUIRE(parents[i] >= -1 && parents[i] < i - q0, PKV_ERR_INVALID_ARG,
+                  "parent %d of drafted token %d is not one before it (or -1)", parents[i], i - q0);
+  }
+  for (int32_t s = 0; s < num_seqs; ++s) {
+    const int32_t q0 = query_start[s], q1 = query_start[s + 1];
+    for (int32_t i = q0; i < q1; ++i) {
+      int32_t* const row = tree_mask + static_cast<int64_t>(i) * mask_words;
+      const int32_t p = parents[i];
+      for (int32_t x = 0; x < mask_words; ++x)
+        row[x] = p < 0 ? 0 : tree_mask[static_cast<int64_t>(q0 + p) * mask_words + x];
+      const int32_t j = i - q0;
+      row[j / 32] = static_cast<int32_t>(static_cast<uint32_t>(row[j / 32]) | (1u << (j % 32)));
+      depths[i] = p < 0 ? 0 : depths[q0 + p] + 1;
+    }
+  }
+  return ok();
+}
+
+}  // extern "C"

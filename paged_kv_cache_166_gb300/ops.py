@@ -906,3 +906,352 @@ def beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.T
             logits.data_ptr(), seq_stride if S > 1 else 0, beam_stride if K > 1 else 0,
             beam_scores.data_ptr(), S, K, V, n, scores.data_ptr(), beams.data_ptr(),
             tokens.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), code, _stream(dev)))
+
+
+# ---------------------------------------------------------------------------------
+# Operators of a speculative step: drafted tokens verified over the cache
+# ---------------------------------------------------------------------------------
+def _norm_rotary_write(kind, q, k, v, q_weight, k_weight, eps, positions, table, slot_mapping,
+                       k_cache, v_cache, k_scale, v_scale, q_out, interleaved, axes, status):
+    if kind:
+        kc, vc = _q8_caches(k_cache, v_cache, kind)
+        dev = _check_cuda(positions, table, slot_mapping, kc, vc, k_scale, v_scale)
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+    else:
+        kc, vc, scales = k_cache, v_cache, (None, None)
+        dev = _check_cuda(positions, table, slot_mapping, kc, vc)
+    if not (q.device == k.device == v.device == q_out.device == dev):
+        raise ValueError("q, k, v and q_out must be on the caches' device")
+    if not (q.dim() == k.dim() == v.dim() == q_out.dim() == 3) or kc.dim() != 4 or vc.dim() != 4:
+        raise ValueError("expected q, q_out [T, Hq, D], k, v [T, Hkv, D] and 4-dimensional caches")
+    dt = q.dtype
+    if not (k.dtype == v.dtype == q_out.dtype == dt) or (not kind and not (
+            kc.dtype == vc.dtype == dt)):
+        raise TypeError("q, k, v, q_out" + ("" if kind else " and caches") + " must share a dtype")
+    _check_index(positions, "positions")
+    _check_index(slot_mapping, "slot_mapping")
+    T, Hq, D = q.shape
+    NB, Hkv, B, D2 = kc.shape
+    rows = (T, Hkv, D)
+    if D2 != D or k.shape != rows or v.shape != rows or q_out.shape != (T, Hq, D) \
+            or vc.shape != ((NB, Hkv, D, B) if kind else (NB, Hkv, B, D)):
+        raise ValueError("shape mismatch between q, k, v, q_out and caches")
+    if table.dim() != 2 or table.dtype != torch.float32:
+        raise ValueError("table must be float32 [max_positions, rotary_dim]")
+    P, rot = table.shape
+    if axes is None:
+        if positions.shape != (T,):
+            raise ValueError("positions must be [T] (with axes [number of axes, T])")
+        A, axis_ptr = 1, None
+    else:
+        if positions.dim() != 2 or positions.shape[1] != T or len(axes) != rot // 2:
+            raise ValueError("with axes: positions [number of axes, T], an axis for each of the "
+                             "rotary_dim / 2 pairs")
+        A = positions.shape[0]
+        axis_ptr = (ctypes.c_int32 * len(axes))(*axes)
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    if kind:
+        _check_scales(k_scale, v_scale, Hkv)
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights need an eps")
+        eps = -1.0
+    elif not eps >= 0:
+        raise ValueError("eps must not be negative (None: no norm)")
+    own, kinds = dtype_code(q), set()
+    for w, H, name in ((q_weight, Hq, "q_weight"), (k_weight, Hkv, "k_weight")):
+        if w is None:
+            continue
+        if w.device != dev or not w.is_contiguous() or w.shape not in ((D,), (H, D)):
+            raise ValueError(f"{name} must be a contiguous [{D}] or [{H}, {D}] tensor on the "
+                             "caches' device")
+        kinds.add((dtype_code(w), w.dim() == 2))
+    wcode, per_head = kinds.pop() if kinds else (own, False)
+    if kinds or wcode not in (N.PKV_F32, own):
+        raise TypeError("weights are float32 or of q's dtype, both of one dtype and dimension")
+    with _current(dev):
+        N.check(N.lib().pkv_norm_rotary_write(
+            _CODES[kind] if kind else 0, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(),
+            _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"),
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), wcode, 1 if per_head else 0, eps,
+            positions.data_ptr(), axis_ptr, A, table.data_ptr(), P, rot, 1 if interleaved else 0,
+            slot_mapping.data_ptr(), T, kc.data_ptr(), vc.data_ptr(), *scales, NB, Hq, Hkv, B, D,
+            q_out.data_ptr(), _token_stride(q_out, "q_out"), _status_ptr(status, dev), own,
+            _stream(dev)))
+    return q_out
+
+
+def paged_norm_rotary_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                            eps: Optional[float], positions: torch.Tensor, table: torch.Tensor,
+                            slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, q_out: torch.Tensor, interleaved: bool = False,
+                            axes=None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``paged_rotary_write`` with a norm of each head of q and k in front: divided by the root
+    of their mean square (plus ``eps``), times the weights ([D], or [heads, D]; q's dtype or
+    float32; None: ones).  ``eps`` None: no norm.  ``axes``: the axis of each pair of turning
+    elements, positions then [number of axes, T] (up to four), for tokens with a time, a height
+    and a width."""
+    return _norm_rotary_write("", q, k, v, q_weight, k_weight, eps, positions, table,
+                              slot_mapping, k_cache, v_cache, None, None, q_out, interleaved, axes,
+                              status)
+
+
+def paged_norm_rotary_write_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                q_weight: Optional[torch.Tensor],
+                                k_weight: Optional[torch.Tensor], eps: Optional[float],
+                                positions: torch.Tensor, table: torch.Tensor,
+                                slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                                v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                v_scale: torch.Tensor, q_out: torch.Tensor,
+                                interleaved: bool = False, axes=None,
+                                status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_norm_rotary_write into fp8 caches: the turned k and v quantised as
+    paged_kv_write_fp8 does."""
+    return _norm_rotary_write("fp8", q, k, v, q_weight, k_weight, eps, positions, table,
+                              slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out,
+                              interleaved, axes, status)
+
+
+def paged_norm_rotary_write_int8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 q_weight: Optional[torch.Tensor],
+                                 k_weight: Optional[torch.Tensor], eps: Optional[float],
+                                 positions: torch.Tensor, table: torch.Tensor,
+                                 slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                                 v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                 v_scale: torch.Tensor, q_out: torch.Tensor,
+                                 interleaved: bool = False, axes=None,
+                                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_norm_rotary_write into int8 caches: the turned k and v quantised as
+    paged_kv_write_int8 does."""
+    return _norm_rotary_write("int8", q, k, v, q_weight, k_weight, eps, positions, table,
+                              slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out,
+                              interleaved, axes, status)
+
+
+def tree_masks(parents: torch.Tensor, query_start: torch.Tensor, words: int = 0):
+    """Masks and depths of trees of drafted tokens, on the host: ``parents`` [T] (int32; each
+    token's parent's number within its sequence, or -1 at the context's end) and
+    ``query_start`` [S + 1] give (tree_mask int32 [T, words], depths int32 [T]); ``words``: 32-bit
+    words a row, by default as many as the largest tree needs."""
+    for t, name in ((parents, "parents"), (query_start, "query_start")):
+        if t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous host tensor of one dimension")
+        _check_index(t, name)
+    S, T = query_start.shape[0] - 1, parents.shape[0]
+    if S < 0 or int(query_start[0]) != 0 or int(query_start[-1]) != T:
+        raise ValueError(f"query_start must go from 0 to {T}")
+    if words <= 0:
+        most = int((query_start[1:] - query_start[:-1]).max()) if S else 0
+        words = max(1, -(-most // 32))
+    _fits("words", words)
+    mask = torch.zeros((T, words), dtype=torch.int32)
+    depths = torch.zeros(T, dtype=torch.int32)
+    if T > 0:
+        N.check(N.lib().pkv_tree_masks(parents.data_ptr(), query_start.data_ptr(), S, words,
+                                       mask.data_ptr(), depths.data_ptr()))
+    return mask, depths
+
+
+def tree_workspace_bytes(head_dim: int) -> int:
+    """Workspace bytes of ``paged_tree_attention`` on the current device."""
+    n = ctypes.c_size_t(0)
+    N.check(N.lib().pkv_tree_workspace_size(head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def paged_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor,
+                         query_start: torch.Tensor, scale: float, out: torch.Tensor,
+                         tree_mask: Optional[torch.Tensor] = None,
+                         depths: Optional[torch.Tensor] = None, cap: float = 0.0,
+                         slopes: Optional[torch.Tensor] = None, window: int = 0,
+                         workspace: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of each sequence's drafted tokens q [T, Hq, D] (rows query_start[s] ..
+    query_start[s + 1] - 1, the last positions of context_lens[s]) over the paged caches: every
+    token before them, and of the drafted ones those of the row's bits in tree_mask [T, words]
+    (``tree_masks``; None: a chunk, each its predecessors and itself).  ``cap``: scores x become
+    cap * tanh(x / cap); ``slopes`` [Hq] (float32): a bias of slope * (key's position - query's);
+    ``window``: only the last positions are seen; a drafted token's position is the context's end
+    plus its ``depths`` [T] (None: its number).  Writes and returns out."""
+    dev = _check_cuda(q, k_cache, v_cache, block_tables, context_lens, query_start, out)
+    if q.dim() != 3 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or out.shape != q.shape:
+        raise ValueError("expected q, out [T, Hq, D] and caches [NB, Hkv, B, D]")
+    T, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    S = context_lens.shape[0] if context_lens.dim() == 1 else -1
+    if D2 != D or block_tables.dim() != 2 or block_tables.shape[0] != S \
+            or query_start.shape != (S + 1,):
+        raise ValueError("block_tables [S, max_blocks], context_lens [S], query_start [S + 1]")
+    _check_index(block_tables, "block_tables")
+    _check_index(context_lens, "context_lens")
+    _check_index(query_start, "query_start")
+    if not (q.dtype == k_cache.dtype == v_cache.dtype == out.dtype):
+        raise TypeError("q, caches and out must share a dtype")
+    if out.data_ptr() == q.data_ptr() and T > 0:
+        raise ValueError("out must not be q")
+    mask_ptr = depth_ptr = slope_ptr = None
+    words = 0
+    if tree_mask is not None:
+        _check_index(tree_mask, "tree_mask")
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] < 1:
+            raise ValueError("tree_mask must be [T, words]")
+        _check_cuda(q, tree_mask)
+        mask_ptr, words = tree_mask.data_ptr(), tree_mask.shape[1]
+    if depths is not None:
+        _check_index(depths, "depths")
+        if depths.shape != (T,):
+            raise ValueError("depths must be [T]")
+        _check_cuda(q, depths)
+        depth_ptr = depths.data_ptr()
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or slopes.shape != (Hq,):
+            raise ValueError("slopes must be float32 [Hq]")
+        _check_cuda(q, slopes)
+        slope_ptr = slopes.data_ptr()
+    _fits("window or tokens", window, T, NB, block_tables.shape[1])
+    st = _status_ptr(status, dev)
+    with _current(dev):
+        key = (dev.index, "tree", D)
+        need = _SIZES.get(key)
+        if need is None:
+            need = _remember(key, tree_workspace_bytes(D))
+        if workspace is None:
+            ws = _scratch(dev, need, 0, "tree")
+            have = ws.numel()
+        else:
+            ws, have = workspace, workspace.numel() * workspace.element_size()
+            if ws.device != dev or have < need:
+                raise ValueError(f"workspace smaller than the {need} bytes needed")
+        N.check(N.lib().pkv_tree_attention(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), mask_ptr, words,
+            depth_ptr, slope_ptr, cap, window, S, T, Hq, Hkv, D, B, NB, scale, out.data_ptr(), st,
+            ws.data_ptr(), have, dtype_code(q), _stream(dev)))
+    return out
+
+
+def _layer_pointers(caches, name):
+    """(first cache, pointers of the layers' caches) of a list of caches, or of one tensor that
+    holds the layers one after another."""
+    if isinstance(caches, torch.Tensor):
+        if caches.dim() != 5 or not caches.is_contiguous() or caches.shape[0] < 1:
+            raise ValueError(f"{name} in one tensor must be a contiguous [layers, NB, Hkv, ., .]")
+        L, p = caches.shape[0], caches.data_ptr()
+        step = caches.stride(0) * caches.element_size()
+        return caches[0], (ctypes.c_void_p * L)(*[p + i * step for i in range(L)])
+    caches = list(caches)
+    if not caches:
+        raise ValueError("at least one layer")
+    ref = caches[0]
+    shape, dt, dev = ref.shape, ref.dtype, ref.device
+    for c in caches:
+        if c.shape != shape or c.dtype != dt:
+            raise ValueError("every layer's caches must have one shape and dtype")
+        if c.device != dev or not c.is_contiguous():
+            raise ValueError("tensors must be contiguous and on one device")
+    return ref, (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+
+
+def paged_tree_commit(k_caches, v_caches, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                      query_start: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
+                      status: Optional[torch.Tensor] = None) -> None:
+    """Move the accepted path of every sequence's drafted tokens to the front: for j <
+    path_lens[s] the rows at position base + path[s, j] go to base + j, base = context_lens[s]
+    minus the drafted tokens, in every layer's caches (lists of caches, or tensors with the
+    layers in front; 16- and 32-bit, fp8 or int8).  path [S, columns] int32: numbers within the
+    sequence's drafted tokens, ascending.  ``BlockAllocator.truncate`` then gives the rest back."""
+    kc, kp = _layer_pointers(k_caches, "k_caches")
+    vc, vp = _layer_pointers(v_caches, "v_caches")
+    dev = _check_cuda(kc, vc, block_tables, context_lens, query_start, path, path_lens)
+    code = _copy_code(kc)
+    if kc.dim() != 4 or kc.dtype != vc.dtype or len(kp) != len(vp):
+        raise ValueError("one K and one V cache per layer, 4-dimensional, of one dtype")
+    NB, Hkv, B, D = kc.shape
+    if vc.shape != ((NB, Hkv, D, B) if code in _CODES.values() else kc.shape):
+        raise ValueError("v_cache must be [NB, Hkv, B, D] ([NB, Hkv, D, 16] if 8-bit)")
+    for t, name in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                    (query_start, "query_start"), (path, "path"), (path_lens, "path_lens")):
+        _check_index(t, name)
+    S = context_lens.shape[0] if context_lens.dim() == 1 else -1
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start.shape != (S + 1,) \
+            or path.dim() != 2 or path.shape[0] != S or path_lens.shape != (S,):
+        raise ValueError("block_tables [S, blocks], context_lens [S], query_start [S + 1], "
+                         "path [S, columns], path_lens [S]")
+    _fits("blocks or columns", block_tables.shape[1], path.shape[1], NB)
+    st = _status_ptr(status, dev)
+    with _current(dev):
+        N.check(N.lib().pkv_tree_commit(
+            kp, vp, len(kp), block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), query_start.data_ptr(), path.data_ptr(), path.shape[1],
+            path_lens.data_ptr(), S, NB, Hkv, B, D, st, code, _stream(dev)))
+
+
+def adjust_logits(logits: torch.Tensor, history: torch.Tensor, history_lens: torch.Tensor,
+                  prompt_lens: Optional[torch.Tensor] = None,
+                  row_start: Optional[torch.Tensor] = None,
+                  repetition: Optional[torch.Tensor] = None,
+                  frequency: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None, path: Optional[torch.Tensor] = None,
+                  bias_tokens: Optional[torch.Tensor] = None,
+                  bias_values: Optional[torch.Tensor] = None,
+                  allowed: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Penalties, biases and masks on logits [T, V] (vocabulary contiguous, any row stride), in
+    place or into ``out``; returns what it wrote.  Rows row_start[s] .. row_start[s + 1] - 1
+    (None: row s) belong to request s, whose tokens are history[s, :history_lens[s]] (int32), the
+    first prompt_lens[s] of them its prompt.  ``repetition`` divides (positive) or multiplies the
+    logits of every token that came; ``frequency`` is subtracted for each time the request has
+    written it, ``presence`` once (all [S] float32).  ``path`` [T, columns]: more tokens of a row
+    alone (a drafted token's ancestors; -1: none).  ``bias_tokens`` [S, columns] with
+    ``bias_values``: added (of entries for one token the last counts; -1: none).  ``allowed``
+    [T, words] int32, a bit a token: the others become -infinity."""
+    y = logits if out is None else out
+    dev = _check_cuda(history, history_lens)
+    if logits.device != dev or y.device != dev:
+        raise ValueError("logits and out must be on the device of history")
+    if logits.dim() != 2 or y.shape != logits.shape or y.dtype != logits.dtype:
+        raise ValueError("expected logits [T, V], and out of the same shape and dtype")
+    T, V = logits.shape
+    if V > 1 and (logits.stride(1) != 1 or y.stride(1) != 1):
+        raise ValueError("the vocabulary must be contiguous")
+    if history.dim() != 2:
+        raise ValueError("history must be [S, columns]")
+    S = history.shape[0]
+
+    def given(t, name, shape, dtype):
+        if t is None:
+            return None
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {str(dtype)[6:]}")
+        if t.shape != shape or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {list(shape)} on the logits' device")
+        return t.data_ptr()
+
+    def columns(t):
+        return 0 if t is None or t.dim() != 2 else t.shape[1]
+
+    i32, f32 = torch.int32, torch.float32
+    L, P, E, W = history.shape[1], columns(path), columns(bias_tokens), columns(allowed)
+    _fits("rows or columns", V, T, L, P, E, W)
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values come together")
+    rows, out_rows = (logits.stride(0), y.stride(0)) if T > 1 else (V, V)
+    if y.data_ptr() == logits.data_ptr() and rows != out_rows and T > 0:
+        raise ValueError("out must be logits or not overlap them")
+    with _current(dev):
+        N.check(N.lib().pkv_adjust_logits(
+            logits.data_ptr(), rows, y.data_ptr(), out_rows, T, V,
+            given(row_start, "row_start", (S + 1,), i32), S,
+            given(history, "history", (S, L), i32), L,
+            given(history_lens, "history_lens", (S,), i32),
+            given(prompt_lens, "prompt_lens", (S,), i32),
+            given(repetition, "repetition", (S,), f32), given(frequency, "frequency", (S,), f32),
+            given(presence, "presence", (S,), f32), given(path, "path", (T, P), i32), P,
+            given(bias_tokens, "bias_tokens", (S, E), i32),
+            given(bias_values, "bias_values", (S, E), f32), E,
+            given(allowed, "allowed", (T, W), i32), W, dtype_code(logits), _stream(dev)))
+    return y
