@@ -809,8 +809,7 @@ int pkv_norm_rotary_write(int32_t codes, const void* q, int64_t q_stride, const 
  * tree_mask     device int32 [num_tokens, mask_words] or NULL (mask_words then unused); a
  *               sequence of more than 32 * mask_words drafted tokens is clamped and reported.
  *               pkv_tree_masks makes masks and depths of parents.
- * depths        device int32 [num_tokens] or NULL; negative ones count as 0
- *               (PKV_DEV_BAD_POSITION).
+ * depths        device int32 [num_tokens] or NULL; clamped to [0, 2^29] (PKV_DEV_BAD_POSITION).
  * slopes        device float [num_q_heads] or NULL.  cap 0: none.  window 0: none.
  * q, out        device [num_tokens, num_q_heads, head_dim], contiguous; rows of no sequence
  *               are left as they were.  out is not q.

@@ -176,6 +176,20 @@ class BlockManager:
             self.tables[sid], self.lengths[sid] = list(table), n
         return tables
 
+    def truncate(self, seqs: Sequence[int], new_lens: Sequence[int]) -> None:
+        """Cut each ``seqs[i]`` down to its first ``new_lens[i]`` tokens; the blocks behind them
+        are given back, last one first."""
+        for sid in seqs:
+            self._check_resident(sid)
+        if len(set(seqs)) != len(seqs) or any(not 0 <= n <= self.lengths[s]
+                                              for s, n in zip(seqs, new_lens)):
+            raise InvalidOperation("a sequence listed twice or a length it does not have")
+        for sid, n in zip(seqs, new_lens):
+            table = self.tables[sid]
+            while len(table) > -(-n // self.block_size):
+                self.decref(table.pop())
+            self.lengths[sid] = n
+
     def reorder(self, seqs: Sequence[int], parents: Sequence[int]) -> None:
         """Beam search: ``seqs[i]`` becomes the continuation of what ``seqs[parents[i]]``
         was; all new tables are counted before the old ones are given back."""

@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kTrMaxSeqs = 2048;
 constexpr int kTrMaxGroup = 16;
+constexpr int kTrMaxDepth = 1 << 29;           // positions, below 2^30 + this, fit 32 bits
 constexpr uint64_t kTrWaitNs = 1000000000ull;  // 1 s per wait before giving up
 constexpr int kTrRows = 128;                   // rows of a unit = tensor-memory lanes = MMA M
 constexpr int kTrRowWarps = 8;                 // softmax warps 2 .. 9: a lane quarter, a half of the keys
@@ -106,8 +107,7 @@ __device__ __forceinline__ void tr_seq(const TreeArgs& a, int s, int& t, int& c,
 
 __device__ __forceinline__ int tr_depth(const TreeArgs& a, int q0, int i) {
   if (a.depths == nullptr) return i;
-  const int d = __ldg(a.depths + q0 + i);
-  return d < 0 ? 0 : d;
+  return min(max(__ldg(a.depths + q0 + i), 0), kTrMaxDepth);
 }
 
 __device__ __forceinline__ int tr_units(const TreeArgs& a, int c) {
@@ -294,9 +294,9 @@ __device__ __forceinline__ uint64_t tr_sees(const TreeArgs& a, const TreeWalk& w
   if (a.window > 0) {
     const int pos = base + depth;
     if (a.depths == nullptr) {
-      vis &= ~low_bits(pos - a.window + 1 - k0);
+      vis &= ~low_bits(max(pos - a.window + 1, 0) - k0);
     } else {
-      vis &= ~low_bits(min(pos - a.window + 1, base) - k0);
+      vis &= ~low_bits(min(max(pos - a.window + 1, 0), base) - k0);
       if (depth >= a.window) {
         for (int e = max(0, base - k0); e < n && k0 + e < w.t; ++e)
           if (depth - tr_depth(a, w.q0, k0 + e - base) >= a.window) vis &= ~(1ull << e);
@@ -318,7 +318,7 @@ __device__ __forceinline__ void tr_mixed(const TreeArgs& a, const TreeWalk& w, i
   from[0] = lo;
   to[0] = lo;
   if (a.window > 0)
-    to[0] = min(base + (a.depths != nullptr ? w.c - 1 : last) - a.window + 1, from[1]);
+    to[0] = min(max(base + (a.depths != nullptr ? w.c - 1 : last) - a.window + 1, 0), from[1]);
 }
 
 template <typename T>
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           slope = __ldg(a.slopes + w.g * a.G + rh) * 1.4426950408889634f;
       }
       if (live && a.depths != nullptr && h == 0 && valid && w.ka == 0 &&
-          __ldg(a.depths + w.q0 + node) < 0)
+          __ldg(a.depths + w.q0 + node) != depth)
         tr_flag(a, PKV_DEV_BAD_POSITION);
       float m = -INFINITY, l = 0.f;
       for (int k = w.ka; k < w.kb; ++k, ++it) {
@@ -1146,7 +1146,7 @@ int pkv_tree_attention(const void* q, const void* k_cache, const void* v_cache,
   a.NB = num_blocks;
   a.bs = block_size;
   a.W = mask_words;
-  a.window = window;
+  a.window = window > (1 << 30) + kTrMaxDepth ? 0 : window;  // no two positions are as far apart
   // whole 8-row swizzle atoms: a box of q is 8 / gcd(G, 8) drafted tokens, a unit whole boxes
   a.box = G % 8 == 0 ? 1 : (G % 4 == 0 ? 2 : (G % 2 == 0 ? 4 : 8));
   a.nodes = kTrRows / G / a.box * a.box;
