@@ -93,7 +93,8 @@ class Case:
                     elif dead:
                         rows[:, w] |= np.uint32((0xffffffff << (32 - dead)) & 0xffffffff)
             kw["tree_mask"] = i32(words)
-        if self.depths is not None and not kw.pop("no_depths", False):
+        no_depths = kw.pop("no_depths", False)
+        if self.depths is not None and not no_depths:
             kw["depths"] = i32(self.depths)
         if kw.get("slopes") is not None:
             kw["slopes"] = torch.tensor(kw["slopes"], dtype=torch.float32, device="cuda")
