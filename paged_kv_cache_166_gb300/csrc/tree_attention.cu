@@ -45,7 +45,7 @@ constexpr int kTrMaxDepth = 1 << 29;           // positions, below 2^30 + this, 
 constexpr uint64_t kTrWaitNs = 1000000000ull;  // 1 s per wait before giving up
 constexpr int kTrRows = 128;                   // rows of a unit = tensor-memory lanes = MMA M
 constexpr int kTrRowWarps = 8;                 // softmax warps 2 .. 9: a lane quarter, a half of the keys
-constexpr int kTrVWarp = 10, kTrQWarp = 11;    // producers of V and of the query tiles
+constexpr int kTrVWarp = 10, kTrQWarp = 11;    // producer of V; query tiles, and V looked through
 constexpr int kTrThreads = 12 * 32;
 constexpr int kTrChunk = 128 * 128;            // one [128 rows x 128 B] swizzled chunk of Q
 constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximum that moves the reference
@@ -194,7 +194,7 @@ enum {
   kTrKFull = 0,     // [4] K stage landed (TMA bytes)
   kTrKEmpty = 4,    // [4] K stage consumed (commit after S)
   kTrVFull = 8,     // [4] V stage landed
-  kTrVEmpty = 12,   // [4] V stage consumed (commit after P V)
+  kTrVEmpty = 12,   // [4] V stage consumed (commit after P V) and passed by the looking warp
   kTrQFull = 16,    // [2] query tile landed
   kTrQEmpty = 18,   // [2] query tile consumed (commit after the piece's last S)
   kTrSFull = 20,    // [2] S in tensor memory (commit)
@@ -203,12 +203,13 @@ enum {
   kTrPvDone = 26,   // [2] P V done (commit)
   kTrOEmpty = 28,   // the piece's O read out by the row warps
   kTrDrain = 29,    // every MMA of the CTA done (final commit)
-  kTrBars = 30
+  kTrVReady = 30,   // [4] V stage looked through (only tiles that need it)
+  kTrBars = 34
 };
 constexpr uint32_t kTrSlotOff = 8 * kTrBars;       // tensor-memory base address
 constexpr uint32_t kTrDeadOff = kTrSlotOff + 8;    // [4] give-up bits of the row-warp pairs
-constexpr uint32_t kTrOddOff = kTrDeadOff + 16;    // [2] a piece met values of V that are not finite
-constexpr uint32_t kTrWalkOff = kTrOddOff + 8;     // the CTA's first TreeWalk
+constexpr uint32_t kTrOddOff = kTrDeadOff + 16;    // [8] a piece met values of V that are not finite
+constexpr uint32_t kTrWalkOff = kTrOddOff + 32;    // the CTA's first TreeWalk
 constexpr uint32_t kTrBarArea = 512;
 static_assert(kTrWalkOff % 8 == 0 && kTrWalkOff + sizeof(TreeWalk) <= kTrBarArea, "barrier area");
 
@@ -306,19 +307,29 @@ __device__ __forceinline__ uint64_t tr_sees(const TreeArgs& a, const TreeWalk& w
   return n >= 64 ? vis : vis & low_bits(n);
 }
 
-// Keys that one row of a unit may see and another not, as up to two ranges: values of V there
-// that are not finite must not reach the rows that do not see them (0 * infinity).
+// Keys whose values must not reach every row of a unit, as up to two ranges: those that some row
+// sees and another does not, and the rest of the first and last cache blocks that are read.
+// There, values of V that are not finite would (0 * infinity).
 __device__ __forceinline__ void tr_mixed(const TreeArgs& a, const TreeWalk& w, int (&from)[2],
                                          int (&to)[2]) {
   const int base = w.t - w.c, i0 = w.tile * a.nodes, last = min(w.c, i0 + a.nodes) - 1;
   int lo, hi;
   tr_keys(a, w.t, w.c, w.tile, lo, hi);
   from[1] = a.mask != nullptr ? base : base + i0 + 1;
-  to[1] = hi;
-  from[0] = lo;
+  to[1] = (hi + a.bs - 1) & -a.bs;
+  from[0] = lo & -a.bs;
   to[0] = lo;
   if (a.window > 0)
-    to[0] = min(max(base + (a.depths != nullptr ? w.c - 1 : last) - a.window + 1, 0), from[1]);
+    to[0] = min(max(base + (a.depths != nullptr ? w.c - 1 : last) - a.window + 1, lo), from[1]);
+}
+
+// Whether tile k has any of them.
+template <int KT>
+__device__ __forceinline__ bool tr_special(const TreeArgs& a, const TreeWalk& w, int k) {
+  const int k0 = (w.j0 + k) * KT;
+  int from[2], to[2];
+  tr_mixed(a, w, from, to);
+  return max(from[0], k0) < min(to[0], k0 + KT) || max(from[1], k0) < min(to[1], k0 + KT);
 }
 
 template <typename T>
@@ -357,7 +368,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       ptx::mbar_init(bar(kTrKFull + st), 1);
       ptx::mbar_init(bar(kTrKEmpty + st), 1);
       ptx::mbar_init(bar(kTrVFull + st), 1);
-      ptx::mbar_init(bar(kTrVEmpty + st), 1);
+      ptx::mbar_init(bar(kTrVEmpty + st), 2);
+      ptx::mbar_init(bar(kTrVReady + st), 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bar(kTrQFull + b), 1);
@@ -366,12 +378,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       ptx::mbar_init(bar(kTrSEmpty + b), kTrRowWarps);
       ptx::mbar_init(bar(kTrPFull + b), kTrRowWarps);
       ptx::mbar_init(bar(kTrPvDone + b), 1);
-      odd_seen[b] = 0;
     }
     ptx::mbar_init(bar(kTrOEmpty), kTrRowWarps);
     ptx::mbar_init(bar(kTrDrain), 1);
     ptx::fence_barrier_init();
     for (int i = 0; i < 4; ++i) reinterpret_cast<int*>(base_p + Sh::kBarOff + kTrDeadOff)[i] = 0;
+    for (int i = 0; i < 8; ++i) odd_seen[i] = 0;
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(slot), Sh::kTmemCols);
@@ -470,13 +482,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   bool more = tr_unit<KT>(a, w);
 
   if (warp == kTrQWarp) {
-    // ---- TMA producer of the query tiles ---------------------------------------------
-    uint32_t un = 0;
+    // ---- query tiles (TMA), NQ pieces ahead; and V looked through where rows of it must not
+    // reach every query -------------------------------------------------------------------
+    uint32_t un = 0, it = 0;  // pieces whose queries are loaded; tiles
     bool alive = true;
     const uint64_t policy = ptx::policy_evict_first();
-    for (; more; more = tr_next<KT>(a, w)) {
+    TreeWalk ahead = w;  // the next piece whose queries are to be loaded
+    bool ahead_more = more;
+    auto load_q = [&]() {
       const uint32_t qb = un % NQ;
-      const int here = min(a.nodes, w.c - w.tile * a.nodes);
+      const int here = min(a.nodes, ahead.c - ahead.tile * a.nodes);
       const int boxes = (here + a.box - 1) / a.box;
       const uint32_t box_bytes = static_cast<uint32_t>(a.box * a.G) * 128u;
       bool ok = true;
@@ -484,15 +499,88 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         ok = ptx::mbar_wait(bar(kTrQEmpty + qb), ((un / NQ) & 1u) ^ 1u, kTrWaitNs);
         if (ok) ptx::mbar_arrive_expect_tx(bar(kTrQFull + qb), boxes * box_bytes * Sh::kChunks);
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) { alive = false; break; }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
       __syncwarp();
       for (int i = lane; i < boxes * Sh::kChunks; i += 32) {
         const int bx = i / Sh::kChunks, cc = i - bx * Sh::kChunks;
         ptx::tma_load_3d(base_s + Sh::kQOff + qb * Sh::kQTile + cc * kTrChunk + bx * box_bytes,
-                         &qmap, cc * 64, w.g * a.G, w.q0 + w.tile * a.nodes + bx * a.box,
-                         bar(kTrQFull + qb), policy);
+                         &qmap, cc * 64, ahead.g * a.G,
+                         ahead.q0 + ahead.tile * a.nodes + bx * a.box, bar(kTrQFull + qb), policy);
       }
       ++un;
+      ahead_more = tr_next<KT>(a, ahead);
+      return true;
+    };
+    constexpr int kPieces = 8 * Sh::kChunks;  // 16-byte pieces of a key's V
+    auto look_through = [&](uint32_t vt, const TreeWalk& u, int k, uint32_t n) {
+      const int k0 = (u.j0 + k) * KT;
+      // address of 16 bytes of V: piece i of row r0 + i / kPieces
+      auto v_at = [&](int r0, int i) {
+        const int row = r0 + i / kPieces, piece = i % kPieces;
+        return vt + (row >> 3) * Sh::kGroup + (piece >> 3) * 1024 + (row & 7) * 128 +
+               (piece & 7) * 16;
+      };
+      // values that are not finite are taken out, and added to the rows that see them at the
+      // end.  (Taking nothing out costs no fence: one between this warp's stores and the tensor
+      // cores' reads waits for the copies in flight, some 4 us a tile.)
+      int from[2], to[2];
+      bool wrote = false;
+      tr_mixed(a, u, from, to);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r0 = max(0, from[e] - k0), n16 = (min(KT, to[e] - k0) - r0) * kPieces;
+        for (int i0 = lane; i0 < n16; i0 += 128) {  // four loads on their way
+          uint32_t v[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0u;
+            if (i0 + 32 * x < n16)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v[x][0]), "=r"(v[x][1]), "=r"(v[x][2]), "=r"(v[x][3])
+                           : "r"(v_at(r0, i0 + 32 * x)));
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (!(odd_pair<T>(v[x][0]) || odd_pair<T>(v[x][1]) || odd_pair<T>(v[x][2]) ||
+                  odd_pair<T>(v[x][3])))
+              continue;
+            constexpr uint32_t m = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if ((v[x][q] & m) == m) v[x][q] &= 0xffff0000u;
+              if ((v[x][q] & (m << 16)) == (m << 16)) v[x][q] &= 0xffffu;
+            }
+            ptx::st_shared_v4(v_at(r0, i0 + 32 * x), v[x][0], v[x][1], v[x][2], v[x][3]);
+            wrote = true;
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, wrote)) {
+        if (lane == 0) odd_seen[n & 7u] = 1;
+        __threadfence_block();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      }
+    };
+    for (uint32_t i = 0; i < NQ && alive && ahead_more; ++i) alive = load_q();
+    for (uint32_t n = 0; alive && more; more = tr_next<KT>(a, w), ++n) {
+      // the flag's last user, eight pieces before, has been read out: the ring holds fewer tiles
+      if (lane == 0) odd_seen[n & 7u] = 0;
+      __syncwarp();
+      for (int k = w.ka; k < w.kb; ++k, ++it) {
+        // every tile is waited for, so that no phase of its barrier is missed
+        const uint32_t st = it % NV;
+        alive = __all_sync(0xffffffffu,
+                           ptx::mbar_wait(bar(kTrVFull + st), (it / NV) & 1u, kTrWaitNs));
+        if (!alive) break;
+        const bool special = tr_special<KT>(a, w, k);
+        if (special) look_through(base_s + Sh::kVOff + st * Sh::kTile, w, k, n);
+        if (lane == 0) {
+          if (special) ptx::mbar_arrive(bar(kTrVReady + st));
+          ptx::mbar_arrive(bar(kTrVEmpty + st));
+        }
+      }
+      if (alive && ahead_more) alive = load_q();
     }
     if (lane == 0) {
       if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
@@ -551,67 +639,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     auto wait1 = [&](uint32_t b, uint32_t parity) {
       return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, kTrWaitNs)) != 0;
     };
-    // address of 16 bytes of V: key row, piece of the row
-    auto v_at = [&](uint32_t vt, int row, int piece) {
-      return vt + (row >> 3) * Sh::kGroup + (piece >> 3) * 1024 + (row & 7) * 128 +
-             (piece & 7) * 16;
-    };
-    constexpr int kPieces = 8 * Sh::kChunks;  // 16-byte pieces of a key's V
+    uint32_t ready = 0;  // phases of the V stages' kTrVReady
     // O (+)= P V for tile k of piece n (the x-th tile of the CTA)
     auto pv = [&](uint32_t x, const TreeWalk& u, int k, uint32_t n) {
       const int b = static_cast<int>(x & 1u);
       const uint32_t st = x % NV;
-      if (k == u.ka) {
-        if (!wait1(bar(kTrOEmpty), (n & 1u) ^ 1u)) return false;
-        if (lane == 0) odd_seen[n & 1u] = 0;  // the piece before the last one has been read out
-      }
+      if (k == u.ka && !wait1(bar(kTrOEmpty), (n & 1u) ^ 1u)) return false;
       if (!wait1(bar(kTrVFull + st), (x / NV) & 1u)) return false;
+      if (tr_special<KT>(a, u, k)) {
+        if (!wait1(bar(kTrVReady + st), (ready >> st) & 1u)) return false;
+        ready ^= 1u << st;
+      }
       const uint32_t vt = base_s + Sh::kVOff + st * Sh::kTile;
-      const int k0 = (u.j0 + k) * KT;
-      int lo, hi;
-      tr_keys(a, u.t, u.c, u.tile, lo, hi);
-      bool wrote = false;
-      // rows of V that no query of the unit sees may hold anything, and P is 0 there: zeroed
-      // (blocks that were not read are zero already)
-      auto clear = [&](int r0, int r1) {
-        for (int i = lane; i < (r1 - r0) * kPieces; i += 32)
-          ptx::st_shared_v4(v_at(vt, r0 + i / kPieces, i % kPieces), 0u, 0u, 0u, 0u);
-        wrote = true;
-      };
-      if (k0 + KT > hi) clear(max(0, hi - k0), min(KT, ((hi + BS - 1) >> bs_log << bs_log) - k0));
-      if (lo > k0) clear(max(0, (lo >> bs_log << bs_log) - k0), min(KT, lo - k0));
-      // rows that some queries see: values that are not finite are taken out and added to
-      // the rows that see them at the end
-      int from[2], to[2];
-      tr_mixed(a, u, from, to);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r0 = max(0, from[e] - k0), r1 = min(KT, to[e] - k0);
-        for (int i = lane; i < (r1 - r0) * kPieces; i += 32) {
-          const uint32_t at = v_at(vt, r0 + i / kPieces, i % kPieces);
-          uint32_t v[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                       : "r"(at)
-                       : "memory");
-          if (odd_pair<T>(v[0]) || odd_pair<T>(v[1]) || odd_pair<T>(v[2]) || odd_pair<T>(v[3])) {
-            constexpr uint32_t m = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if ((v[q] & m) == m) v[q] &= 0xffff0000u;
-              if ((v[q] & (m << 16)) == (m << 16)) v[q] &= 0xffffu;
-            }
-            ptx::st_shared_v4(at, v[0], v[1], v[2], v[3]);
-            odd_seen[n & 1u] = 1;
-            wrote = true;
-          }
-        }
-      }
-      if (__any_sync(0xffffffffu, wrote)) {
-        __threadfence_block();
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-      }
       if (!wait1(bar(kTrPFull + b), (x >> 1) & 1u)) return false;
       ptx::tc_fence_after();
       const uint32_t pt = tmem + Sh::kPCol + b * (KT / 2);
@@ -631,6 +670,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     TreeWalk pu = w;
     for (; alive && more; more = tr_next<KT>(a, w)) {
       const uint32_t qb = un % NQ;
+      if (NQ == 1 && pending) {  // the queries come once the piece before has no use for theirs
+        if (!pv(px, pu, pk, pn)) { alive = false; break; }
+        pending = false;
+      }
       if (!wait1(bar(kTrQFull + qb), (un / NQ) & 1u)) { alive = false; break; }
       const uint32_t n = un++;
       ptx::tc_fence_after();
@@ -729,7 +772,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         float* const part_row = a.part_o + cut_row * D + h * HD;
         if (!whole && pend_valid && h == 0) a.part_ml[cut_row] = make_float2(pend_m, lt);
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
-        const bool odd = odd_seen[pend_n & 1u] != 0;
+        const bool odd = odd_seen[pend_n & 7u] != 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += 32) {
           uint32_t o[32];
