@@ -229,8 +229,8 @@ struct TreeShape {
   static constexpr uint32_t kKOff = kQ * kQTile;
   static constexpr uint32_t kVOff = kKOff + kK * kTile;
   static constexpr uint32_t kBarOff = kVOff + kV * kTile;
-  static constexpr uint32_t kXchOff = kBarOff + kTrBarArea;           // [2 halves][128] floats
-  static constexpr uint32_t kBytes = kXchOff + 2 * kTrRows * 4 + 1024;  // + alignment slack
+  static constexpr uint32_t kXchOff = kBarOff + kTrBarArea;  // [2 turns][2 halves][128] floats
+  static constexpr uint32_t kBytes = kXchOff + 4 * kTrRows * 4;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 256;                              // O: D columns
   static constexpr uint32_t kPCol = D == 256 ? 2 * KT : 384;          // P[b]: KT / 2 columns each
@@ -255,6 +255,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// max(a, b, c), one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // 1 / x, one instruction.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -332,10 +338,28 @@ __device__ __forceinline__ bool tr_special(const TreeArgs& a, const TreeWalk& w,
   return max(from[0], k0) < min(to[0], k0 + KT) || max(from[1], k0) < min(to[1], k0 + KT);
 }
 
+// Two 16-bit values.
 template <typename T>
-__device__ __forceinline__ bool odd_pair(uint32_t x) {  // one of two 16-bit values not finite
+using PairOf = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+template <typename T>
+__device__ __forceinline__ PairOf<T> as_pair(uint32_t x) {
+  return *reinterpret_cast<PairOf<T>*>(&x);
+}
+template <typename P>
+__device__ __forceinline__ uint32_t pair_bits(P x) {
+  return *reinterpret_cast<uint32_t*>(&x);
+}
+template <typename T>
+__device__ __forceinline__ bool odd_pair(uint32_t x) {  // one of the two is not finite
   constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
   return (x & e) == e || (x & (e << 16)) == (e << 16);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {  // 0 in place of what is not finite
+  constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  if ((x & e) == e) x &= 0xffff0000u;
+  if ((x & (e << 16)) == (e << 16)) x &= 0xffffu;
+  return x;
 }
 
 template <typename T, int D, bool kBias>
@@ -348,11 +372,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   constexpr uint32_t NQ = Sh::kQ, NK = Sh::kK, NV = Sh::kV;
   // the joining kernel may be launched: it waits for the whole of this grid
   asm volatile("griddepcontrol.launch_dependents;");
-  extern __shared__ uint8_t smem_raw[];
+  // swizzled tiles lie on 1,024-byte boundaries (head_dim 256 leaves no room to look for one)
+  extern __shared__ __align__(1024) uint8_t base_p[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t raw = ptx::smem_addr(smem_raw);
-  const uint32_t base_s = (raw + 1023u) & ~1023u;
-  uint8_t* const base_p = smem_raw + (base_s - raw);
+  const uint32_t base_s = ptx::smem_addr(base_p);
+  if ((base_s & 1023u) != 0) {
+    if (threadIdx.x == 0) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+    return;
+  }
   const uint32_t bars = base_s + Sh::kBarOff;
   const int BS = a.bs, bs_log = 31 - __clz(a.bs);
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -511,48 +538,50 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       ahead_more = tr_next<KT>(a, ahead);
       return true;
     };
-    constexpr int kPieces = 8 * Sh::kChunks;  // 16-byte pieces of a key's V
     auto look_through = [&](uint32_t vt, const TreeWalk& u, int k, uint32_t n) {
-      const int k0 = (u.j0 + k) * KT;
-      // address of 16 bytes of V: piece i of row r0 + i / kPieces
-      auto v_at = [&](int r0, int i) {
-        const int row = r0 + i / kPieces, piece = i % kPieces;
-        return vt + (row >> 3) * Sh::kGroup + (piece >> 3) * 1024 + (row & 7) * 128 +
-               (piece & 7) * 16;
-      };
       // values that are not finite are taken out, and added to the rows that see them at the
-      // end.  (Taking nothing out costs no fence: one between this warp's stores and the tensor
-      // cores' reads waits for the copies in flight, some 4 us a tile.)
+      // end.  Products with 0, summed up, show whether there are any: one instruction for two
+      // values.  (Taking nothing out costs no fence: one between this warp's stores and the
+      // tensor cores' reads waits for the copies in flight, some microseconds.)
+      const int k0 = (u.j0 + k) * KT;
       int from[2], to[2];
-      bool wrote = false;
       tr_mixed(a, u, from, to);
+      bool wrote = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r0 = max(0, from[e] - k0), n16 = (min(KT, to[e] - k0) - r0) * kPieces;
-        for (int i0 = lane; i0 < n16; i0 += 128) {  // four loads on their way
-          uint32_t v[4][4];
+        const int r0 = max(0, from[e] - k0), r1 = min(KT, to[e] - k0);
+        PairOf<T> sum = as_pair<T>(0u);
+        for (int g = r0 >> 3; g < (r1 + 7) >> 3; ++g) {  // 8 rows: 2 * kChunks pieces a lane
+          uint32_t v[2 * Sh::kChunks][4];
+          const uint32_t at = vt + g * Sh::kGroup + lane * 16;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0u;
-            if (i0 + 32 * x < n16)
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v[x][0]), "=r"(v[x][1]), "=r"(v[x][2]), "=r"(v[x][3])
-                           : "r"(v_at(r0, i0 + 32 * x)));
+          for (int x = 0; x < 2 * Sh::kChunks; ++x)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[x][0]), "=r"(v[x][1]), "=r"(v[x][2]), "=r"(v[x][3])
+                         : "r"(at + 512 * x));
+#pragma unroll
+          for (int x = 0; x < 2 * Sh::kChunks; ++x) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum = __hfma2(as_pair<T>(v[x][q]), as_pair<T>(0u), sum);
           }
+        }
+        if (r1 <= r0 || !__any_sync(0xffffffffu, odd_pair<T>(pair_bits(sum)))) continue;
+        for (uint32_t i = lane; i < static_cast<uint32_t>((r1 + 7) >> 3) * (Sh::kGroup / 16); i += 32) {
+          const int row = 8 * (i / (Sh::kGroup / 16)) + ((i >> 3) & 7);
+          if (row < r0 || row >= r1) continue;
+          const uint32_t at = vt + 16 * i;
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(at));
+          bool any = false;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (!(odd_pair<T>(v[x][0]) || odd_pair<T>(v[x][1]) || odd_pair<T>(v[x][2]) ||
-                  odd_pair<T>(v[x][3])))
-              continue;
-            constexpr uint32_t m = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if ((v[x][q] & m) == m) v[x][q] &= 0xffff0000u;
-              if ((v[x][q] & (m << 16)) == (m << 16)) v[x][q] &= 0xffffu;
-            }
-            ptx::st_shared_v4(v_at(r0, i0 + 32 * x), v[x][0], v[x][1], v[x][2], v[x][3]);
-            wrote = true;
+          for (int q = 0; q < 4; ++q) {
+            any |= odd_pair<T>(v[q]);
+            v[q] = finite_pair<T>(v[q]);
           }
+          if (any) ptx::st_shared_v4(at, v[0], v[1], v[2], v[3]);
+          wrote |= any;
         }
       }
       if (__any_sync(0xffffffffu, wrote)) {
@@ -728,18 +757,20 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const uint32_t pcol = tmem + lane_off + Sh::kPCol + h * (HK / 2);
     const uint32_t oa = tmem + lane_off + Sh::kOCol + h * HD;  // this thread's half of O
     float* const xch = reinterpret_cast<float*>(base_p + Sh::kXchOff);
-    volatile int* const dead_bits =
-        reinterpret_cast<volatile int*>(base_p + Sh::kBarOff + kTrDeadOff);
+    int* const dead_bits = reinterpret_cast<int*>(base_p + Sh::kBarOff + kTrDeadOff);
     const uint32_t pair_bar = 1 + q4;
     bool dead = false;       // this warp gave up a wait
     bool pair_dead = false;  // either warp of the pair did
-    auto exchange = [&](float x) {  // the other half's x for this row
+    // the other half's x for this row; two buffers in turn: a value has been read once its
+    // reader comes to the next exchange
+    uint32_t turn = 0;
+    auto exchange = [&](float x) {
+      float* const at = xch + (turn ^= 2 * kTrRows);
+      if (dead && lane == 0) atomicOr(dead_bits + q4, 1 << h);
+      at[h * kTrRows + r] = x;
       ptx::named_bar_sync(pair_bar, 64);
-      if (dead && lane == 0) dead_bits[q4] = dead_bits[q4] | (1 << h);
-      xch[h * kTrRows + r] = x;
-      ptx::named_bar_sync(pair_bar, 64);
-      pair_dead = dead_bits[q4] != 0;
-      return xch[(1 - h) * kTrRows + r];
+      pair_dead = *reinterpret_cast<volatile int*>(dead_bits + q4) != 0;
+      return at[(1 - h) * kTrRows + r];
     };
     uint32_t it = 0, un = 0;
     auto wait_all = [&](uint32_t b, uint32_t parity) {
@@ -893,11 +924,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (!((i < 32 ? v0 >> (i & 31) : v1 >> (i & 31)) & 1u))
                   v[i] = __float_as_uint(-INFINITY);
             }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < HK; i += 2)
-              asm("max.f32 %0, %0, %1, %2;"
-                  : "+f"(mx)
-                  : "f"(__uint_as_float(v[i])), "f"(__uint_as_float(v[i + 1])));
+              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
           }
           mx = fmaxf(mx, exchange(mx));
           if (pair_dead) break;
