@@ -190,28 +190,39 @@ __device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeWalk& w) {
   return tr_unit<KT>(a, w);
 }
 
+// What the roles of a CTA need of a piece, handed out ahead of its use.
+struct TreePiece {
+  int32_t s, g, tile, t, c, q0, j0, n, ka, kb;  // as in TreeWalk; n = 0: no more
+  int32_t pad[2];
+};
+constexpr int kTrAhead = 2;   // pieces handed out ahead of the one whose V is looked through
+// ... and kept: when piece n is looked through, P V of the tile four (the V ring's most) before
+// is done, so the pieces up to n - 6 are read out, and the slot of piece n + 2 is free.
+constexpr int kTrPieces = 8;
+
 enum {
-  kTrKFull = 0,     // [4] K stage landed (TMA bytes)
-  kTrKEmpty = 4,    // [4] K stage consumed (commit after S)
-  kTrVFull = 8,     // [4] V stage landed
-  kTrVEmpty = 12,   // [4] V stage consumed (commit after P V) and passed by the looking warp
-  kTrQFull = 16,    // [2] query tile landed
-  kTrQEmpty = 18,   // [2] query tile consumed (commit after the piece's last S)
-  kTrSFull = 20,    // [2] S in tensor memory (commit)
-  kTrSEmpty = 22,   // [2] S read by the row warps
-  kTrPFull = 24,    // [2] P in tensor memory (row warps)
-  kTrPvDone = 26,   // [2] P V done (commit)
-  kTrOEmpty = 28,   // the piece's O read out by the row warps
-  kTrDrain = 29,    // every MMA of the CTA done (final commit)
-  kTrVReady = 30,   // [4] V stage looked through (only tiles that need it)
-  kTrBars = 34
+  kTrKFull = 0,     // [6] K stage landed (TMA bytes)
+  kTrKEmpty = 6,    // [6] K stage consumed (commit after S)
+  kTrVFull = 12,    // [6] V stage landed
+  kTrVEmpty = 18,   // [6] V stage consumed (commit after P V) and passed by the looking warp
+  kTrVReady = 24,   // [6] V stage looked through (only tiles that need it)
+  kTrQFull = 30,    // query tile landed
+  kTrQEmpty = 31,   // query tile consumed (commit after the piece's last S)
+  kTrSFull = 32,    // [2] S in tensor memory (commit)
+  kTrSEmpty = 34,   // [2] S read by the row warps
+  kTrPFull = 36,    // [2] P in tensor memory (row warps)
+  kTrPvDone = 38,   // [2] P V done (commit)
+  kTrOEmpty = 40,   // the piece's O read out by the row warps
+  kTrDrain = 41,    // every MMA of the CTA done (final commit)
+  kTrPiece = 42,    // [8] piece handed out
+  kTrBars = 50
 };
 constexpr uint32_t kTrSlotOff = 8 * kTrBars;       // tensor-memory base address
 constexpr uint32_t kTrDeadOff = kTrSlotOff + 8;    // [4] give-up bits of the row-warp pairs
 constexpr uint32_t kTrOddOff = kTrDeadOff + 16;    // [8] a piece met values of V that are not finite
-constexpr uint32_t kTrWalkOff = kTrOddOff + 32;    // the CTA's first TreeWalk
-constexpr uint32_t kTrBarArea = 512;
-static_assert(kTrWalkOff % 8 == 0 && kTrWalkOff + sizeof(TreeWalk) <= kTrBarArea, "barrier area");
+constexpr uint32_t kTrPieceOff = (kTrOddOff + 32 + 15) / 16 * 16;
+constexpr uint32_t kTrBarArea = 1024;
+static_assert(kTrPieceOff + kTrPieces * sizeof(TreePiece) <= kTrBarArea, "barrier area");
 
 template <typename T, int D>
 struct TreeShape {
@@ -222,11 +233,10 @@ struct TreeShape {
   static constexpr uint32_t kQTile = kTrRows * D * 2;
   static constexpr uint32_t kTile = KT * D * 2;       // K or V tile
   static constexpr uint32_t kGroup = kChunks * 1024;  // 8 keys of a tile, every chunk
-  static constexpr int kQ = D == 256 ? 1 : 2;         // query tiles
-  static constexpr int kK = D == 64 ? 3 : 2;          // K ring
-  static constexpr int kV = D == 64 ? 4 : 3;          // V ring
+  static constexpr int kK = D == 64 ? 6 : (D == 128 ? 3 : 2);  // K ring
+  static constexpr int kV = D == 64 ? 4 : 3;                   // V ring
   static constexpr uint32_t kQOff = 0;
-  static constexpr uint32_t kKOff = kQ * kQTile;
+  static constexpr uint32_t kKOff = kQTile;
   static constexpr uint32_t kVOff = kKOff + kK * kTile;
   static constexpr uint32_t kBarOff = kVOff + kV * kTile;
   static constexpr uint32_t kXchOff = kBarOff + kTrBarArea;  // [2 turns][2 halves][128] floats
@@ -239,6 +249,7 @@ struct TreeShape {
   static constexpr int kHalfD = D / 2;                                // O columns of a row thread
   // P = 2^(x - m + shift): f16 loses values below 2^-24, so its P uses the range above 1 too
   static constexpr float kShift = kBf16 ? 0.f : 7.f;
+  static_assert(kV <= 4 && kK <= 6, "barriers, and the pieces kept");
   static_assert(2 * KT <= kOCol && kBytes <= 232448, "tensor and shared memory");
   static_assert(D == 256 ? kPCol + KT <= kOCol : (kOCol + D <= kPCol && kPCol + KT <= kTmemCols),
                 "tensor memory");
@@ -255,6 +266,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// N consecutive 32-bit words (16-byte aligned), 32 bytes a store where the address allows it.
+template <int N>
+__device__ __forceinline__ void st_row(void* to, const uint32_t* y) {
+  uint32_t* const p = static_cast<uint32_t*>(to);
+  if ((reinterpret_cast<uintptr_t>(to) & 31u) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + i),
+                   "r"(y[i]), "r"(y[i + 1]), "r"(y[i + 2]), "r"(y[i + 3]), "r"(y[i + 4]),
+                   "r"(y[i + 5]), "r"(y[i + 6]), "r"(y[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+  }
+}
 // max(a, b, c), one instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -369,45 +397,36 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                           const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
   using Sh = TreeShape<T, D>;
   constexpr int KT = Sh::KT, HK = Sh::kHalfKeys, HD = Sh::kHalfD;
-  constexpr uint32_t NQ = Sh::kQ, NK = Sh::kK, NV = Sh::kV;
+  constexpr uint32_t NK = Sh::kK, NV = Sh::kV;
   // the joining kernel may be launched: it waits for the whole of this grid
   asm volatile("griddepcontrol.launch_dependents;");
-  // swizzled tiles lie on 1,024-byte boundaries (head_dim 256 leaves no room to look for one)
+  // swizzled tiles lie on 1,024-byte boundaries (there is no room to look for one)
   extern __shared__ __align__(1024) uint8_t base_p[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base_s = ptx::smem_addr(base_p);
   if ((base_s & 1023u) != 0) {
-    if (threadIdx.x == 0) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+    if (threadIdx.x == 0) {
+      tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+      a.cuts[blockIdx.x] = TreeCut{0, 0, 0, 0, 0, 0};
+    }
     return;
   }
   const uint32_t bars = base_s + Sh::kBarOff;
   const int BS = a.bs, bs_log = 31 - __clz(a.bs);
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   uint32_t* const slot = reinterpret_cast<uint32_t*>(base_p + Sh::kBarOff + kTrSlotOff);
-  TreeWalk* const first = reinterpret_cast<TreeWalk*>(base_p + Sh::kBarOff + kTrWalkOff);
   volatile int* const odd_seen = reinterpret_cast<volatile int*>(base_p + Sh::kBarOff + kTrOddOff);
+  TreePiece* const pieces = reinterpret_cast<TreePiece*>(base_p + Sh::kBarOff + kTrPieceOff);
 
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
-    for (int st = 0; st < 4; ++st) {
-      ptx::mbar_init(bar(kTrKFull + st), 1);
-      ptx::mbar_init(bar(kTrKEmpty + st), 1);
-      ptx::mbar_init(bar(kTrVFull + st), 1);
-      ptx::mbar_init(bar(kTrVEmpty + st), 2);
-      ptx::mbar_init(bar(kTrVReady + st), 1);
+    for (int i = 0; i < kTrBars; ++i) {
+      const bool rows = i == kTrOEmpty || (i >= kTrSEmpty && i < kTrPvDone);
+      const bool two = i >= kTrVEmpty && i < kTrVReady;
+      ptx::mbar_init(bar(i), rows ? kTrRowWarps : (two ? 2 : 1));
     }
-    for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(bar(kTrQFull + b), 1);
-      ptx::mbar_init(bar(kTrQEmpty + b), 1);
-      ptx::mbar_init(bar(kTrSFull + b), 1);
-      ptx::mbar_init(bar(kTrSEmpty + b), kTrRowWarps);
-      ptx::mbar_init(bar(kTrPFull + b), kTrRowWarps);
-      ptx::mbar_init(bar(kTrPvDone + b), 1);
-    }
-    ptx::mbar_init(bar(kTrOEmpty), kTrRowWarps);
-    ptx::mbar_init(bar(kTrDrain), 1);
     ptx::fence_barrier_init();
     for (int i = 0; i < 4; ++i) reinterpret_cast<int*>(base_p + Sh::kBarOff + kTrDeadOff)[i] = 0;
     for (int i = 0; i < 8; ++i) odd_seen[i] = 0;
@@ -417,10 +436,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     ptx::tmem_relinquish();
   }
 
-  // ---- the CTA's run: costs of all sequences summed up (in the K ring, free until the first
-  // load), then the unit in which the run begins ------------------------------------------
+  // ---- costs of all sequences summed up (in the K ring, free until the first load) --------
+  long long* const cpre = reinterpret_cast<long long*>(base_p + Sh::kKOff);
   {
-    long long* const cpre = reinterpret_cast<long long*>(base_p + Sh::kKOff);
     long long* const wsum = cpre + a.S + 1;
     const int tid = threadIdx.x;
     const int per = (a.S + kTrThreads - 1) / kTrThreads;
@@ -439,103 +457,112 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (int w = 0; w < warp; ++w) run += wsum[w];
     for (int s = b0; s < b1; ++s) {
       cpre[s] = run;
-      if (per > 1) run += tr_seq_cost<KT>(a, s, false);
-      else run += local;
+      run += per > 1 ? tr_seq_cost<KT>(a, s, false) : local;
     }
     if (tid == kTrThreads - 1) cpre[a.S] = run;
     ptx::fence_proxy_async_smem();  // the rings' copies come after these stores
-    __syncthreads();
-    if (tid == 0) {
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *slot;
+  auto read_piece = [&](uint32_t n, TreeWalk& w) {
+    const int4* const p = reinterpret_cast<const int4*>(pieces + n % kTrPieces);
+    const int4 x = p[0], y = p[1], z = p[2];
+    w.s = x.x, w.g = x.y, w.tile = x.z, w.t = x.w;
+    w.c = y.x, w.q0 = y.y, w.j0 = y.z, w.n = y.w;
+    w.ka = z.x, w.kb = z.y;
+  };
+  // The next piece (the n-th) of the CTA; n = 0 in it: no more.  Whole warp; false: timed out.
+  auto get_piece = [&](uint32_t n, TreeWalk& w) {
+    if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar(kTrPiece + n % kTrPieces),
+                                                (n / kTrPieces) & 1u, kTrWaitNs)))
+      return false;
+    read_piece(n, w);
+    return true;
+  };
+
+  if (warp == kTrQWarp) {
+    // ---- the CTA's run and its pieces, the query tiles (TMA), and V looked through where rows
+    // of it must not reach every query ------------------------------------------------------
+    TreeWalk w{};  // the next piece to hand out
+    {
+      // lane 0 looks for the unit in which the run begins, lane 1 for the one in which it ends
       const long long C = cpre[a.S];
-      TreeWalk w{};
-      w.lo = C * blockIdx.x / gridDim.x;
-      w.hi = C * (blockIdx.x + 1) / gridDim.x;
-      w.s = a.S;
-      if (w.lo < C) {
-        int l = 0, h = a.S;  // the last sequence with cpre <= lo: it has units, and lo is in one
+      const long long lo = C * blockIdx.x / gridDim.x, hi = C * (blockIdx.x + 1) / gridDim.x;
+      const long long at = lane == 1 ? hi - 1 : lo;
+      int s = a.S, g = 0, u = 0, n = 0, t = 0, c = 0, q0 = 0, j0;
+      long long P = 0;
+      if (lane < 2 && hi > lo) {
+        int l = 0, h = a.S;  // the last sequence with cpre <= at: `at` lies in one of its units
         while (h - l > 1) {
           const int mid = (l + h) >> 1;
-          if (cpre[mid] <= w.lo) l = mid; else h = mid;
+          if (cpre[mid] <= at) l = mid; else h = mid;
         }
-        int j0;
-        tr_seq(a, l, w.t, w.c, w.q0, false);
-        const long long cost_g = (cpre[l + 1] - cpre[l]) / a.Hkv;
-        w.s = l;
-        w.g = static_cast<int>((w.lo - cpre[l]) / cost_g);
-        w.P = cpre[l] + w.g * cost_g;
-        for (;;) {
-          const int n = tr_tiles<KT>(a, w.t, w.c, w.tile, j0);
-          if (w.P + n + 1 > w.lo) break;
-          w.P += n + 1;
-          ++w.tile;
-        }
-      }
-      // the unit that this run begins and another ends, for the joining kernel
-      TreeCut cut{0, C, 0, 0, 0, 0};
-      if (w.hi > w.lo && w.hi < C) {
-        int l = 0, h = a.S;  // the unit that holds cost hi - 1 ...
-        while (h - l > 1) {
-          const int mid = (l + h) >> 1;
-          if (cpre[mid] <= w.hi - 1) l = mid; else h = mid;
-        }
-        int t, c, q0, j0, n = 0, u = 0;
-        tr_seq(a, l, t, c, q0, false);
-        const long long cost_g = (cpre[l + 1] - cpre[l]) / a.Hkv;
-        const int g = static_cast<int>((w.hi - 1 - cpre[l]) / cost_g);
-        long long P = cpre[l] + g * cost_g;
+        s = l;
+        tr_seq(a, s, t, c, q0, false);
+        const long long cost_g = (cpre[s + 1] - cpre[s]) / a.Hkv;
+        g = static_cast<int>((at - cpre[s]) / cost_g);
+        P = cpre[s] + g * cost_g;
         for (;; ++u) {
           n = tr_tiles<KT>(a, t, c, u, j0);
-          if (P + n + 1 > w.hi - 1) break;
+          if (P + n + 1 > at) break;
           P += n + 1;
         }
-        // ... if its first tile is this run's and its last is not
-        if (P >= w.lo && tr_first_tile(P, n, w.hi) < n) {
+      }
+      if (lane == 1) {
+        // the unit that this run begins and another ends, for the joining kernel
+        TreeCut cut{0, C, 0, 0, 0, 0};
+        if (hi > lo && hi < C && P >= lo && tr_first_tile(P, n, hi) < n) {
           cut.P = P;
           cut.n = n;
           cut.row0 = q0 + u * a.nodes;
           cut.rows = min(a.nodes, c - u * a.nodes) * a.G;
           cut.g = g;
         }
+        a.cuts[blockIdx.x] = cut;
       }
-      a.cuts[blockIdx.x] = cut;
-      *first = w;
+      w.s = __shfl_sync(0xffffffffu, s, 0);
+      w.g = __shfl_sync(0xffffffffu, g, 0);
+      w.tile = __shfl_sync(0xffffffffu, u, 0);
+      w.P = __shfl_sync(0xffffffffu, P, 0);
+      w.lo = lo;
+      w.hi = hi;
     }
-  }
-  ptx::tc_fence_before();
-  __syncthreads();  // (the prefix sums have been read: the rings may be filled)
-  ptx::tc_fence_after();
-  const uint32_t tmem = *slot;
-  TreeWalk w = *first;
-  bool more = tr_unit<KT>(a, w);
-
-  if (warp == kTrQWarp) {
-    // ---- query tiles (TMA), NQ pieces ahead; and V looked through where rows of it must not
-    // reach every query -------------------------------------------------------------------
-    uint32_t un = 0, it = 0;  // pieces whose queries are loaded; tiles
+    uint32_t out = 0;  // pieces handed out
+    bool more = tr_unit<KT>(a, w);
+    auto hand_out = [&]() {
+      if (lane == 0) {
+        int4* const p = reinterpret_cast<int4*>(pieces + out % kTrPieces);
+        p[0] = make_int4(w.s, w.g, w.tile, w.t);
+        p[1] = make_int4(w.c, w.q0, w.j0, more ? w.n : 0);
+        p[2] = make_int4(w.ka, w.kb, 0, 0);
+        ptx::mbar_arrive(bar(kTrPiece + out % kTrPieces));
+      }
+      __syncwarp();
+      ++out;
+      if (more) more = tr_next<KT>(a, w);
+    };
+    uint32_t loaded = 0, it = 0;  // pieces whose queries are loaded; tiles
     bool alive = true;
     const uint64_t policy = ptx::policy_evict_first();
-    TreeWalk ahead = w;  // the next piece whose queries are to be loaded
-    bool ahead_more = more;
-    auto load_q = [&]() {
-      const uint32_t qb = un % NQ;
-      const int here = min(a.nodes, ahead.c - ahead.tile * a.nodes);
+    auto load_q = [&](const TreeWalk& u) {
+      const int here = min(a.nodes, u.c - u.tile * a.nodes);
       const int boxes = (here + a.box - 1) / a.box;
       const uint32_t box_bytes = static_cast<uint32_t>(a.box * a.G) * 128u;
       bool ok = true;
       if (lane == 0) {
-        ok = ptx::mbar_wait(bar(kTrQEmpty + qb), ((un / NQ) & 1u) ^ 1u, kTrWaitNs);
-        if (ok) ptx::mbar_arrive_expect_tx(bar(kTrQFull + qb), boxes * box_bytes * Sh::kChunks);
+        ok = ptx::mbar_wait(bar(kTrQEmpty), (loaded & 1u) ^ 1u, kTrWaitNs);
+        if (ok) ptx::mbar_arrive_expect_tx(bar(kTrQFull), boxes * box_bytes * Sh::kChunks);
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
       __syncwarp();
       for (int i = lane; i < boxes * Sh::kChunks; i += 32) {
         const int bx = i / Sh::kChunks, cc = i - bx * Sh::kChunks;
-        ptx::tma_load_3d(base_s + Sh::kQOff + qb * Sh::kQTile + cc * kTrChunk + bx * box_bytes,
-                         &qmap, cc * 64, ahead.g * a.G,
-                         ahead.q0 + ahead.tile * a.nodes + bx * a.box, bar(kTrQFull + qb), policy);
+        ptx::tma_load_3d(base_s + Sh::kQOff + cc * kTrChunk + bx * box_bytes, &qmap, cc * 64,
+                         u.g * a.G, u.q0 + u.tile * a.nodes + bx * a.box, bar(kTrQFull), policy);
       }
-      ++un;
-      ahead_more = tr_next<KT>(a, ahead);
+      ++loaded;
       return true;
     };
     auto look_through = [&](uint32_t vt, const TreeWalk& u, int k, uint32_t n) {
@@ -566,7 +593,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           }
         }
         if (r1 <= r0 || !__any_sync(0xffffffffu, odd_pair<T>(pair_bits(sum)))) continue;
-        for (uint32_t i = lane; i < static_cast<uint32_t>((r1 + 7) >> 3) * (Sh::kGroup / 16); i += 32) {
+        for (uint32_t i = lane; i < static_cast<uint32_t>((r1 + 7) >> 3) * (Sh::kGroup / 16);
+             i += 32) {
           const int row = 8 * (i / (Sh::kGroup / 16)) + ((i >> 3) & 7);
           if (row < r0 || row >= r1) continue;
           const uint32_t at = vt + 16 * i;
@@ -585,36 +613,42 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
       }
       if (__any_sync(0xffffffffu, wrote)) {
-        if (lane == 0) odd_seen[n & 7u] = 1;
+        if (lane == 0) odd_seen[n % kTrPieces] = 1;
         __threadfence_block();
         ptx::fence_proxy_async_smem();
         __syncwarp();
       }
     };
-    for (uint32_t i = 0; i < NQ && alive && ahead_more; ++i) alive = load_q();
-    for (uint32_t n = 0; alive && more; more = tr_next<KT>(a, w), ++n) {
-      // the flag's last user, eight pieces before, has been read out: the ring holds fewer tiles
-      if (lane == 0) odd_seen[n & 7u] = 0;
-      __syncwarp();
-      for (int k = w.ka; k < w.kb; ++k, ++it) {
+    for (int i = 0; i < kTrAhead; ++i) hand_out();
+    TreeWalk u{}, next{};
+    alive = get_piece(0, u);
+    if (alive && u.n > 0) alive = load_q(u);
+    for (uint32_t n = 0; alive && u.n > 0; ++n) {
+      if (lane == 0) odd_seen[n % kTrPieces] = 0;  // (its last user has been read out)
+      hand_out();
+      alive = get_piece(n + 1, next);
+      for (int k = u.ka; alive && k < u.kb; ++k, ++it) {
+        // the next queries are loaded once the piece's last S is done, which waits for the
+        // products two tiles before: for no tile of V from here on
+        if (k == u.kb - 1 && next.n > 0 && !(alive = load_q(next))) break;
         // every tile is waited for, so that no phase of its barrier is missed
         const uint32_t st = it % NV;
         alive = __all_sync(0xffffffffu,
                            ptx::mbar_wait(bar(kTrVFull + st), (it / NV) & 1u, kTrWaitNs));
         if (!alive) break;
-        const bool special = tr_special<KT>(a, w, k);
-        if (special) look_through(base_s + Sh::kVOff + st * Sh::kTile, w, k, n);
+        const bool special = tr_special<KT>(a, u, k);
+        if (special) look_through(base_s + Sh::kVOff + st * Sh::kTile, u, k, n);
         if (lane == 0) {
           if (special) ptx::mbar_arrive(bar(kTrVReady + st));
           ptx::mbar_arrive(bar(kTrVEmpty + st));
         }
       }
-      if (alive && ahead_more) alive = load_q();
+      u = next;
     }
     if (lane == 0) {
       if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
-      for (uint32_t k = un > NQ ? un - NQ : 0u; k < un; ++k)  // copies in flight land first
-        ptx::mbar_wait(bar(kTrQFull + k % NQ), (k / NQ) & 1u, kTrWaitNs / 8);
+      if (loaded > 0)  // the copy in flight lands first
+        ptx::mbar_wait(bar(kTrQFull), (loaded - 1) & 1u, kTrWaitNs / 8);
     }
   } else if (warp == 0 || warp == kTrVWarp) {
     // ---- TMA producers of K (warp 0) and V (warp 10) ---------------------------------
@@ -627,8 +661,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const uint32_t ring = base_s + (is_k ? Sh::kKOff : Sh::kVOff);
     const uint32_t NS = is_k ? NK : NV;
     uint32_t it = 0;
+    TreeWalk w{};
     bool alive = true;
-    for (; alive && more; more = tr_next<KT>(a, w)) {
+    for (uint32_t n = 0; alive; ++n) {
+      if (!get_piece(n, w)) { alive = false; break; }
+      if (w.n == 0) break;
       int lo, hi;
       tr_keys(a, w.t, w.c, w.tile, lo, hi);
       for (int k = w.ka; k < w.kb; ++k, ++it) {
@@ -654,7 +691,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           ptx::tma_load_4d(ring + st * Sh::kTile + lane * (BS / 8) * Sh::kGroup, map, 0, 0, 0, y,
                            bar(full0 + st), policy);
       }
-      if (!alive) break;
     }
     if (lane == 0) {
       if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
@@ -662,49 +698,45 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         ptx::mbar_wait(bar(full0 + k % NS), (k / NS) & 1u, kTrWaitNs / 8);
     }
   } else if (warp == 1) {
-    // ---- MMA issuer: S of a tile ahead of P V of the one before, across units too --------
-    uint32_t it = 0, un = 0;
+    // ---- MMA issuer: S of a tile ahead of P V of the one before, across pieces too --------
+    uint32_t it = 0;
     bool alive = true;
     auto wait1 = [&](uint32_t b, uint32_t parity) {
       return __all_sync(0xffffffffu, ptx::mbar_wait(b, parity, kTrWaitNs)) != 0;
     };
     uint32_t ready = 0;  // phases of the V stages' kTrVReady
     // O (+)= P V for tile k of piece n (the x-th tile of the CTA)
-    auto pv = [&](uint32_t x, const TreeWalk& u, int k, uint32_t n) {
+    auto pv = [&](uint32_t x, bool begins, bool special, uint32_t n) {
       const int b = static_cast<int>(x & 1u);
       const uint32_t st = x % NV;
-      if (k == u.ka && !wait1(bar(kTrOEmpty), (n & 1u) ^ 1u)) return false;
+      if (begins && !wait1(bar(kTrOEmpty), (n & 1u) ^ 1u)) return false;
       if (!wait1(bar(kTrVFull + st), (x / NV) & 1u)) return false;
-      if (tr_special<KT>(a, u, k)) {
+      if (special) {
         if (!wait1(bar(kTrVReady + st), (ready >> st) & 1u)) return false;
         ready ^= 1u << st;
       }
-      const uint32_t vt = base_s + Sh::kVOff + st * Sh::kTile;
       if (!wait1(bar(kTrPFull + b), (x >> 1) & 1u)) return false;
       ptx::tc_fence_after();
+      const uint32_t vt = base_s + Sh::kVOff + st * Sh::kTile;
       const uint32_t pt = tmem + Sh::kPCol + b * (KT / 2);
 #pragma unroll
       for (int ks = 0; ks < KT / 16; ++ks)  // 16 keys = 8 packed columns of P
         ptx::umma_f16_ta_elect(tmem + Sh::kOCol, pt + ks * 8,
                                ptx::smem_desc_sw128(vt + ks * 2 * Sh::kGroup, 1024, Sh::kGroup),
-                               Sh::kIdPV, k > u.ka || ks > 0);
+                               Sh::kIdPV, !begins || ks > 0);
       ptx::umma_commit_elect(bar(kTrPvDone + b));
       ptx::umma_commit_elect(bar(kTrVEmpty + st));
       __syncwarp();
       return true;
     };
-    bool pending = false;  // a P V not issued yet: tile pk of pu, the px-th, in piece pn
+    bool pending = false;  // a P V not issued yet: the px-th tile, in piece pn
     uint32_t px = 0, pn = 0;
-    int pk = 0;
-    TreeWalk pu = w;
-    for (; alive && more; more = tr_next<KT>(a, w)) {
-      const uint32_t qb = un % NQ;
-      if (NQ == 1 && pending) {  // the queries come once the piece before has no use for theirs
-        if (!pv(px, pu, pk, pn)) { alive = false; break; }
-        pending = false;
-      }
-      if (!wait1(bar(kTrQFull + qb), (un / NQ) & 1u)) { alive = false; break; }
-      const uint32_t n = un++;
+    bool p_begins = false, p_special = false;
+    TreeWalk w{};
+    for (uint32_t n = 0; alive; ++n) {
+      if (!get_piece(n, w)) { alive = false; break; }
+      if (w.n == 0) break;
+      if (!wait1(bar(kTrQFull), n & 1u)) { alive = false; break; }
       ptx::tc_fence_after();
       for (int k = w.ka; k < w.kb; ++k, ++it) {
         const uint32_t st = it % NK;
@@ -715,7 +747,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t qa = base_s + Sh::kQOff + qb * Sh::kQTile;
+        const uint32_t qa = base_s + Sh::kQOff;
         const uint32_t kb = base_s + Sh::kKOff + st * Sh::kTile;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -727,18 +759,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         ptx::umma_commit_elect(bar(kTrSFull + b));
         ptx::umma_commit_elect(bar(kTrKEmpty + st));
-        if (k == w.kb - 1) ptx::umma_commit_elect(bar(kTrQEmpty + qb));
+        if (k == w.kb - 1) ptx::umma_commit_elect(bar(kTrQEmpty));
         __syncwarp();
-        if (pending && !pv(px, pu, pk, pn)) { alive = false; break; }
+        if (pending && !pv(px, p_begins, p_special, pn)) { alive = false; break; }
         pending = true;
         px = it;
-        pk = k;
         pn = n;
-        if (k == w.ka) pu = w;
+        p_begins = k == w.ka;
+        p_special = tr_special<KT>(a, w, k);
       }
-      if (!alive) break;
     }
-    if (alive && pending && !pv(px, pu, pk, pn)) alive = false;
+    if (alive && pending && !pv(px, p_begins, p_special, pn)) alive = false;
     if (lane == 0) {
       if (!alive) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
       ptx::umma_commit(bar(kTrDrain));  // lands once every MMA issued above is done
@@ -747,9 +778,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     __syncwarp();
   } else {
     // ---- row threads: scores, softmax, output ------------------------------------------
-    // The two warps of a lane quarter meet at every exchange (named barrier); a warp whose
-    // wait ran out skips ahead to the next exchange and flags itself there, and both leave
-    // together.  A quarter without rows only keeps the hand-offs going.
+    // The two warps of a lane quarter meet at every exchange (named barrier).  A warp whose wait
+    // ran out flags itself, arrives there once without waiting, and leaves; the other one
+    // finds the flag at its next exchange.  A quarter without rows only keeps the hand-offs going.
     const int q4 = warp & 3, h = (warp - 2) >> 2;
     const int r = 32 * q4 + lane;  // tile row = tensor-memory lane
     const int rn = r / a.G, rh = r - rn * a.G;
@@ -759,39 +790,37 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     float* const xch = reinterpret_cast<float*>(base_p + Sh::kXchOff);
     int* const dead_bits = reinterpret_cast<int*>(base_p + Sh::kBarOff + kTrDeadOff);
     const uint32_t pair_bar = 1 + q4;
-    bool dead = false;       // this warp gave up a wait
-    bool pair_dead = false;  // either warp of the pair did
+    bool gone = false;       // this warp leaves: a wait ran out, or the other one has left
+    bool pair_dead = false;  // ... the latter
     // the other half's x for this row; two buffers in turn: a value has been read once its
     // reader comes to the next exchange
     uint32_t turn = 0;
     auto exchange = [&](float x) {
       float* const at = xch + (turn ^= 2 * kTrRows);
-      if (dead && lane == 0) atomicOr(dead_bits + q4, 1 << h);
       at[h * kTrRows + r] = x;
       ptx::named_bar_sync(pair_bar, 64);
       pair_dead = *reinterpret_cast<volatile int*>(dead_bits + q4) != 0;
+      gone |= pair_dead;
       return at[(1 - h) * kTrRows + r];
     };
-    uint32_t it = 0, un = 0;
     auto wait_all = [&](uint32_t b, uint32_t parity) {
-      if (dead) return;
-      dead = !__all_sync(0xffffffffu, ptx::mbar_wait(b, parity, kTrWaitNs));
+      gone = !__all_sync(0xffffffffu, ptx::mbar_wait(b, parity, kTrWaitNs));
+      return !gone;
     };
     // A piece's output is written after the first tile of the next (its last P V is done by
     // then), so that the tensor cores are not left waiting on it.
     bool pend = false, pend_live = false, pend_valid = false;
-    TreeWalk pu = w;
     float pend_m = 0.f, pend_l = 0.f;
     uint32_t pend_x = 0, pend_n = 0;
     auto epilogue = [&]() {
       pend = false;
       float lt = pend_l;
       if (pend_live) lt += exchange(pend_l);
-      if (pair_dead) return;
-      wait_all(bar(kTrPvDone + (pend_x & 1u)), (pend_x >> 1) & 1u);
-      if (dead) return;
+      if (gone || !wait_all(bar(kTrPvDone + (pend_x & 1u)), (pend_x >> 1) & 1u)) return;
       if (pend_live) {
         ptx::tc_fence_after();
+        TreeWalk pu;
+        read_piece(pend_n, pu);
         const bool whole = pu.ka == 0 && pu.kb == pu.n;
         // a piece that begins its unit is the run's last one, another its first
         const int64_t cut_row =
@@ -803,7 +832,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         float* const part_row = a.part_o + cut_row * D + h * HD;
         if (!whole && pend_valid && h == 0) a.part_ml[cut_row] = make_float2(pend_m, lt);
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
-        const bool odd = odd_seen[pend_n & 7u] != 0;
+        const bool odd = odd_seen[pend_n % kTrPieces] != 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += 32) {
           uint32_t o[32];
@@ -838,15 +867,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             for (int i = 0; i < 16; ++i)
               y[i] = ptx::pack2<T>(__uint_as_float(o[2 * i]) * inv,
                                    __uint_as_float(o[2 * i + 1]) * inv);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<uint4*>(out_row + c0 + 2 * i) =
-                  make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            st_row<16>(out_row + c0, y);
           } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part_row + c0 + i) =
-                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            st_row<32>(part_row + c0, o);
           }
         }
         ptx::tc_fence_before();
@@ -854,13 +877,20 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(kTrOEmpty));
     };
-    for (; more && !pair_dead; more = tr_next<KT>(a, w)) {
+    uint32_t it = 0;
+    TreeWalk w{};
+    for (uint32_t n = 0; !gone; ++n) {
+      if (!get_piece(n, w)) { gone = true; break; }
+      if (w.n == 0) break;
       const int here = min(a.nodes, w.c - w.tile * a.nodes);
       const bool live = 32 * q4 < here * a.G;  // a row of this quarter
       const bool valid = rn < here;
       const int node = w.tile * a.nodes + (valid ? rn : 0);
       const int base = w.t - w.c;
       const int depth = live ? tr_depth(a, w.q0, node) : 0;
+      // keys of these positions are seen whatever the mask: no need to look at each
+      const int clear_to = a.mask != nullptr ? base : base + node + 1;
+      const int clear_from = a.window > 0 ? max(base + depth - a.window + 1, 0) : 0;
       float slope = 0.f;
       if constexpr (kBias) {
         if (live && a.slopes != nullptr)
@@ -872,92 +902,86 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int k = w.ka; k < w.kb; ++k, ++it) {
         const int b = static_cast<int>(it & 1u);
-        wait_all(bar(kTrSFull + b), (it >> 1) & 1u);
+        // (S of this tile was issued after P V of two tiles ago: its P buffer is free, too)
+        if (!wait_all(bar(kTrSFull + b), (it >> 1) & 1u)) break;
         if (live) {
           uint32_t v[HK];
           const int k0 = (w.j0 + k) * KT + h * HK;
-          float mx = -INFINITY;
-          if (!dead) {
-            ptx::tc_fence_after();
-            const uint32_t sa = tmem + lane_off + b * KT + h * HK;
+          ptx::tc_fence_after();
+          const uint32_t sa = tmem + lane_off + b * KT + h * HK;
 #pragma unroll
-            for (int i = 0; i < HK; i += 32)
-              ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
-            ptx::tmem_wait_ld();
-            if constexpr (kBias) {  // scores in log2 units
-              if (a.cap_log2 > 0.f) {
-                // tanh z = 1 - 2 / (1 + e^2z): off by some 1e-7 of the cap
+          for (int i = 0; i < HK; i += 32)
+            ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
+          ptx::tmem_wait_ld();
+          if constexpr (kBias) {  // scores in log2 units
+            if (a.cap_log2 > 0.f) {
+              // tanh z = 1 - 2 / (1 + e^2z): off by some 1e-7 of the cap
+#pragma unroll
+              for (int i = 0; i < HK; ++i)
+                v[i] = __float_as_uint(
+                    fmaf(-2.f * a.cap_log2,
+                         rcp_approx(1.f + ptx::ex2(__uint_as_float(v[i]) * a.cap_z)), a.cap_log2));
+            } else {
+#pragma unroll
+              for (int i = 0; i < HK; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * a.scale_log2);
+            }
+            if (slope != 0.f) {
+              if (a.depths == nullptr || k0 + HK <= base) {
+                const float d0 = static_cast<float>(k0 - base - depth);
 #pragma unroll
                 for (int i = 0; i < HK; ++i)
                   v[i] = __float_as_uint(
-                      fmaf(-2.f * a.cap_log2,
-                           rcp_approx(1.f + ptx::ex2(__uint_as_float(v[i]) * a.cap_z)), a.cap_log2));
+                      fmaf(slope, d0 + static_cast<float>(i), __uint_as_float(v[i])));
               } else {
 #pragma unroll
-                for (int i = 0; i < HK; ++i)
-                  v[i] = __float_as_uint(__uint_as_float(v[i]) * a.scale_log2);
-              }
-              if (slope != 0.f) {
-                if (a.depths == nullptr || k0 + HK <= base) {
-                  const float d0 = static_cast<float>(k0 - base - depth);
-#pragma unroll
-                  for (int i = 0; i < HK; ++i)
-                    v[i] = __float_as_uint(
-                        fmaf(slope, d0 + static_cast<float>(i), __uint_as_float(v[i])));
-                } else {
-#pragma unroll
-                  for (int i = 0; i < HK; ++i) {
-                    const int j = k0 + i - base;  // drafted token, or a cached one
-                    const int pos = j < 0 ? j : (j < w.c ? tr_depth(a, w.q0, j) : 0);
-                    v[i] = __float_as_uint(
-                        fmaf(slope, static_cast<float>(pos - depth), __uint_as_float(v[i])));
-                  }
+                for (int i = 0; i < HK; ++i) {
+                  const int j = k0 + i - base;  // drafted token, or a cached one
+                  const int pos = j < 0 ? j : (j < w.c ? tr_depth(a, w.q0, j) : 0);
+                  v[i] = __float_as_uint(
+                      fmaf(slope, static_cast<float>(pos - depth), __uint_as_float(v[i])));
                 }
               }
             }
-            // keys that the row does not see score -inf
+          }
+          // keys that the row does not see score -inf
+          if (__any_sync(0xffffffffu, valid && (k0 < clear_from || k0 + HK > clear_to))) {
             const uint64_t vis = valid ? tr_sees(a, w, node, depth, k0, HK) : 0ull;
             const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
-            if (!__all_sync(0xffffffffu, vis == low_bits(HK))) {
 #pragma unroll
-              for (int i = 0; i < HK; ++i)
-                if (!((i < 32 ? v0 >> (i & 31) : v1 >> (i & 31)) & 1u))
-                  v[i] = __float_as_uint(-INFINITY);
-            }
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < HK; i += 2)
-              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-            mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
+            for (int i = 0; i < HK; ++i)
+              if (!((i < 32 ? v0 >> (i & 31) : v1 >> (i & 31)) & 1u))
+                v[i] = __float_as_uint(-INFINITY);
           }
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < HK; i += 2)
+            mx4[(i >> 1) & 3] =
+                max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
           mx = fmaxf(mx, exchange(mx));
-          if (pair_dead) break;
+          if (gone) break;
           const float sc = kBias ? 1.f : a.scale_log2;
           const float mt = mx * sc;  // the row's maximum over this tile, log2 units
-          // this P buffer is free once the product of two tiles ago is done
-          wait_all(bar(kTrPvDone + b), ((it >> 1) & 1u) ^ 1u);
           // The reference m moves only when the maximum grows by more than 2^8 (at first from
           // -inf): O and l are scaled once the product before has landed.  The accesses are
           // warp-wide: the whole warp takes the branch, the other rows scale by 1.
           const bool move = mt > m + kTrRescale;
           if (k > w.ka && __any_sync(0xffffffffu, move)) {
             const float al = move ? ptx::ex2(m - mt) : 1.f;  // 2^-inf = 0
-            wait_all(bar(kTrPvDone + (b ^ 1)), ((it - 1) >> 1) & 1u);
-            if (!dead) {
-              ptx::tc_fence_after();
+            if (!wait_all(bar(kTrPvDone + (b ^ 1)), ((it - 1) >> 1) & 1u)) break;
+            ptx::tc_fence_after();
 #pragma unroll 1
-              for (int c0 = 0; c0 < HD; c0 += 32) {
-                uint32_t o[32];
-                ptx::tmem_ld32(oa + c0, o);
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+              uint32_t o[32];
+              ptx::tmem_ld32(oa + c0, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                ptx::tmem_st32(oa + c0, o);
-              }
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              ptx::tmem_st32(oa + c0, o);
             }
             l *= al;
           }
           if (move) m = mt;
-          if (dead) continue;  // on to the next exchange
           // a row that has seen nothing yet: every exponent is -inf whatever the reference
           const float ref = m == -INFINITY ? 0.f : m - Sh::kShift;
           float s0 = 0.f, s1 = 0.f;
@@ -975,7 +999,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           l += s0 + s1;
           ptx::tc_fence_before();
         }
-        if (dead) continue;
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(bar(kTrSEmpty + b));
@@ -983,23 +1006,29 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         if (k == w.ka && pend) {  // the previous piece's output
           epilogue();
-          if (pair_dead) break;
+          if (gone) break;
         }
       }
-      if (pair_dead) break;
-      if (pend) epilogue();  // only if a wait ran out: the flags go on to the next exchange
-      if (pair_dead) break;
+      if (gone) break;
       pend = true;
       pend_live = live;
       pend_valid = valid;
       pend_m = m == -INFINITY ? m : m - Sh::kShift;
       pend_l = l;
       pend_x = it - 1;
-      pend_n = un++;
-      pu = w;
+      pend_n = n;
     }
-    if (pend && !pair_dead) epilogue();
-    if ((dead || pair_dead) && lane == 0) tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+    if (pend && !gone) epilogue();
+    if (gone) {
+      if (lane == 0) {
+        tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
+        atomicOr(dead_bits + q4, 1 << h);
+        __threadfence_block();
+      }
+      __syncwarp();
+      if (!pair_dead)
+        asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
+    }
   }
 
   ptx::tc_fence_before();
