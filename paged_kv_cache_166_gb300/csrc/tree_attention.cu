@@ -48,6 +48,9 @@ constexpr int kTrRowWarps = 8;                 // softmax warps 2 .. 9: a lane q
 constexpr int kTrVWarp = 10, kTrQWarp = 11;    // producer of V; query tiles, and V looked through
 constexpr int kTrThreads = 12 * 32;
 constexpr int kTrChunk = 128 * 128;            // one [128 rows x 128 B] swizzled chunk of Q
+// Of a unit beside its key tiles, in tiles.  A 13B-shaped chunk with 1, 2, 3, 4: 197, 184, 174,
+// 176 us; trees of a 70B-shaped batch 170, 170, 174, 176.
+constexpr int kTrUnitCost = 2;
 constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximum that moves the reference
 
 // What a CTA leaves behind of the unit that its run begins and another one ends.
@@ -134,12 +137,19 @@ __device__ __forceinline__ int tr_tiles(const TreeArgs& a, int t, int c, int til
   return (hi - 1) / KT + 1 - j0;
 }
 
-// A unit of n key tiles costs n + 1: its first tile lies at cost P, tile k > 0 at P + k + 1.
-// First tile at or after cost x.
+// A unit of n key tiles costs n + kTrUnitCost: its first tile lies at cost P, tile k > 0 at
+// P + k + kTrUnitCost.  First tile at or after cost x.
 __device__ __forceinline__ int tr_first_tile(long long P, int n, long long x) {
   if (x <= P) return 0;
-  const long long k = x - P - 1;
+  const long long k = x - P - kTrUnitCost;
   return k < 1 ? (n < 1 ? n : 1) : (k < n ? static_cast<int>(k) : n);
+}
+
+// Where run x of `runs` begins, of C costs.
+__device__ __forceinline__ long long tr_border(long long C, int x, int runs) {
+  if (C < (1 << 23) && runs <= 256)  // the usual case, in 32 bits
+    return static_cast<uint32_t>(C) * static_cast<uint32_t>(x) / static_cast<uint32_t>(runs);
+  return C * x / runs;
 }
 
 template <int KT>
@@ -148,7 +158,7 @@ __device__ __forceinline__ long long tr_seq_cost(const TreeArgs& a, int s, bool 
   tr_seq(a, s, t, c, q0, report);
   long long cost = 0;
   const int nu = tr_units(a, c);
-  for (int u = 0; u < nu; ++u) cost += tr_tiles<KT>(a, t, c, u, j0) + 1;
+  for (int u = 0; u < nu; ++u) cost += tr_tiles<KT>(a, t, c, u, j0) + kTrUnitCost;
   return cost * a.Hkv;
 }
 
@@ -179,13 +189,13 @@ __device__ __forceinline__ bool tr_unit(const TreeArgs& a, TreeWalk& w) {
     w.ka = tr_first_tile(w.P, w.n, w.lo);
     w.kb = tr_first_tile(w.P, w.n, w.hi);
     if (w.kb > w.ka) return true;
-    w.P += w.n + 1;
+    w.P += w.n + kTrUnitCost;
     ++w.tile;
   }
 }
 template <int KT>
 __device__ __forceinline__ bool tr_next(const TreeArgs& a, TreeWalk& w) {
-  w.P += w.n + 1;
+  w.P += w.n + kTrUnitCost;
   ++w.tile;
   return tr_unit<KT>(a, w);
 }
@@ -398,7 +408,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   using Sh = TreeShape<T, D>;
   constexpr int KT = Sh::KT, HK = Sh::kHalfKeys, HD = Sh::kHalfD;
   constexpr uint32_t NK = Sh::kK, NV = Sh::kV;
-  // the joining kernel may be launched: it waits for the whole of this grid
+  // The joining kernel may be launched: it waits for the whole of this grid.  This grid itself
+  // may have been launched ahead of the end of a cache write or a joining kernel in front of it:
+  // lengths, tables and masks are read at once, q, the caches and the workspace once that is done.
   asm volatile("griddepcontrol.launch_dependents;");
   // swizzled tiles lie on 1,024-byte boundaries (there is no room to look for one)
   extern __shared__ __align__(1024) uint8_t base_p[];
@@ -489,7 +501,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     {
       // lane 0 looks for the unit in which the run begins, lane 1 for the one in which it ends
       const long long C = cpre[a.S];
-      const long long lo = C * blockIdx.x / gridDim.x, hi = C * (blockIdx.x + 1) / gridDim.x;
+      const long long lo = tr_border(C, blockIdx.x, gridDim.x);
+      const long long hi = tr_border(C, blockIdx.x + 1, gridDim.x);
       const long long at = lane == 1 ? hi - 1 : lo;
       int s = a.S, g = 0, u = 0, n = 0, t = 0, c = 0, q0 = 0, j0;
       long long P = 0;
@@ -501,13 +514,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         }
         s = l;
         tr_seq(a, s, t, c, q0, false);
-        const long long cost_g = (cpre[s + 1] - cpre[s]) / a.Hkv;
-        g = static_cast<int>((at - cpre[s]) / cost_g);
+        const long long cost = cpre[s + 1] - cpre[s], in = at - cpre[s];
+        const long long cost_g = cost < (1 << 30) ? static_cast<int>(cost) / a.Hkv : cost / a.Hkv;
+        g = static_cast<int>(cost < (1 << 30) ? static_cast<int>(in) / static_cast<int>(cost_g)
+                                              : in / cost_g);
         P = cpre[s] + g * cost_g;
         for (;; ++u) {
           n = tr_tiles<KT>(a, t, c, u, j0);
-          if (P + n + 1 > at) break;
-          P += n + 1;
+          if (P + n + kTrUnitCost > at) break;
+          P += n + kTrUnitCost;
         }
       }
       if (lane == 1) {
@@ -520,8 +535,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           cut.rows = min(a.nodes, c - u * a.nodes) * a.G;
           cut.g = g;
         }
+        // a joining kernel of a call before may still read its own
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         a.cuts[blockIdx.x] = cut;
       }
+      __syncwarp();
       w.s = __shfl_sync(0xffffffffu, s, 0);
       w.g = __shfl_sync(0xffffffffu, g, 0);
       w.tile = __shfl_sync(0xffffffffu, u, 0);
@@ -622,6 +640,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (int i = 0; i < kTrAhead; ++i) hand_out();
     TreeWalk u{}, next{};
     alive = get_piece(0, u);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (alive && u.n > 0) alive = load_q(u);
     for (uint32_t n = 0; alive && u.n > 0; ++n) {
       if (lane == 0) odd_seen[n % kTrPieces] = 0;  // (its last user has been read out)
@@ -663,6 +682,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint32_t it = 0;
     TreeWalk w{};
     bool alive = true;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the caches may have been written just now
     for (uint32_t n = 0; alive; ++n) {
       if (!get_piece(n, w)) { alive = false; break; }
       if (w.n == 0) break;
@@ -1039,61 +1059,78 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 
 // Joins the pieces of the units that runs' borders cut: CTA x looks after the unit that run x
 // begins, a warp a row.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in order.
-constexpr int kJoinWarps = 4, kJoinRows = 16;
+constexpr int kJoinWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeArgs a, int runs) {
   constexpr int E = D / 32;  // elements of a lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const TreeCut cut = a.cuts[blockIdx.x];
-  if (cut.n == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (cut.n == 0 || r >= cut.rows) return;
   // the runs that hold the unit's first and last tile; those between hold a tile or none
   const int x0 = blockIdx.x;
-  const long long end = cut.P + cut.n;
+  const long long end = cut.P + cut.n - 1 + kTrUnitCost;
   const int x1 = static_cast<int>(((end + 1) * runs - 1) / cut.C);
-  auto holds = [&](int x) {
-    const long long lo = cut.C * x / runs, hi = cut.C * (x + 1) / runs;
-    return tr_first_tile(cut.P, cut.n, hi) > tr_first_tile(cut.P, cut.n, lo);
-  };
-  for (int r = blockIdx.y * kJoinRows + warp; r < min(cut.rows, (blockIdx.y + 1) * kJoinRows);
-       r += kJoinWarps) {
-    auto row = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == x0)) * kTrRows + r; };
-    float M = -INFINITY;
-    for (int x = x0 + lane; x <= x1; x += 32)
-      if (holds(x)) M = fmaxf(M, a.part_ml[row(x)].x);
+  auto row = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == x0)) * kTrRows + r; };
+  float M = -INFINITY, total = 0.f, acc[E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float total = 0.f, acc[E];
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int b0 = x0; b0 <= x1; b0 += 32) {  // 32 pieces: a lane looks one up
+    const int x = b0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    bool here = false;
+    if (x <= x1) {
+      here = tr_first_tile(cut.P, cut.n, tr_border(cut.C, x + 1, runs)) >
+             tr_first_tile(cut.P, cut.n, tr_border(cut.C, x, runs));
+      if (here) ml = a.part_ml[row(x)];
+    }
+    float top = ml.x;
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    for (int b0 = x0; b0 <= x1; b0 += 32) {
-      const int x = b0 + lane;
-      float wt = 0.f, part = 0.f;
-      const bool here = x <= x1 && holds(x);
-      if (here) {
-        const float2 ml = a.part_ml[row(x)];
-        wt = M == -INFINITY ? 1.f : ptx::ex2(ml.x - M);
-        part = ml.y * wt;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top > M) {  // what is there is brought to the new reference
+      const float al = ptx::ex2(M - top);
+      total *= al;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= al;
+      M = top;
+    }
+    // a row that has seen nothing has sums of 0 (or of NaN), whatever the reference
+    const float wt = ml.x == -INFINITY ? 1.f : ptx::ex2(ml.x - M);
+    const float part = ml.y * wt;
+    const uint32_t on = __ballot_sync(0xffffffffu, here);
+    for (uint32_t left = on; left != 0;) {  // in order, four pieces' loads on their way
+      int at[4];
+      float src[4][E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        at[u] = left != 0 ? __ffs(left) - 1 : -1;
+        left &= left - 1;
+        if (at[u] >= 0) {
+          const float* const p = a.part_o + row(b0 + at[u]) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2*>(&src[u][e]) = *reinterpret_cast<const float2*>(p + e);
+        }
       }
-      const uint32_t on = __ballot_sync(0xffffffffu, here);
-      for (int i = 0; i < 32 && b0 + i <= x1; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, wt, i);
-        total += __shfl_sync(0xffffffffu, part, i);
-        if (!((on >> i) & 1u)) continue;
-        const float* const src = a.part_o + row(b0 + i) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], wi, acc[e]);
+      for (int u = 0; u < 4; ++u) {
+        if (at[u] < 0) continue;
+        const float wi = __shfl_sync(0xffffffffu, wt, at[u]);
+        total += __shfl_sync(0xffffffffu, part, at[u]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(src[u][e], wi, acc[e]);
       }
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const int rn = r / a.G, rh = r - rn * a.G;
-    T* const dst = static_cast<T*>(a.out) +
-                   (static_cast<int64_t>(cut.row0 + rn) * a.Hq + cut.g * a.G + rh) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack2<T>(acc[e] * inv, acc[e + 1] * inv);
   }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const int rn = r / a.G, rh = r - rn * a.G;
+  T* const dst = static_cast<T*>(a.out) +
+                 (static_cast<int64_t>(cut.row0 + rn) * a.Hq + cut.g * a.G + rh) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack2<T>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 template <typename T, int D, bool kBias>
@@ -1123,17 +1160,20 @@ int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, 
   if (rc != PKV_OK) return rc;
   rc = encode_map_4d(&vmap, a.v_cache, ty, kvdims, kvstrides, kvbox, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != PKV_OK) return rc;
-  tree_attention_kernel<T, D, kBias><<<sms, kTrThreads, Sh::kBytes, st>>>(qmap, kmap, vmap, a);
-  PKV_CUDA(cudaGetLastError());
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(sms, kTrRows / kJoinRows);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(kTrThreads);
+  cfg.dynamicSmemBytes = Sh::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, tree_attention_kernel<T, D, kBias>, qmap, kmap, vmap, a));
+  cfg.gridDim = dim3(sms, kTrRows / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
   PKV_CUDA(cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, a, sms));
   return PKV_OK;
 }
