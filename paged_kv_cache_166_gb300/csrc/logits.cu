@@ -8,11 +8,17 @@
 //   not allowed:  x = -infinity;
 // in fp32, each operation rounded, then rounded to the type.
 //
-// A CTA takes a piece of the vocabulary for one request: it counts the request's tokens that
-// fall there in shared memory (integers, so their order does not matter) and marks them in a
-// bit map, then goes through the request's rows.  In place, only tokens that are marked or
-// banned are touched: without a mask a row costs as much as the request has tokens, not the
-// vocabulary, and 16 bytes of banned tokens are written without being read.
+// What the mask bans, or everything if out is not logits, goes through a first kernel: a warp
+// takes 1,024 tokens of a row, writes 16 bytes of banned ones without reading them and, in
+// place, leaves allowed ones alone.  The second kernel, whose counting overlaps the first, puts
+// the adjusted logits over that: a CTA takes every NP-th segment of 256 tokens of the
+// vocabulary for one request (the low numbers, which most texts use most, are spread over all
+// CTAs), counts the request's tokens that fall there in shared memory (integers, so their order
+// does not matter) and goes through the rows with those that came.  Without a mask a row thus
+// costs, in place, as much as the request has tokens, not the vocabulary.
+//
+// Bound by memory latency for small calls (lengths, history, logits one after the other), else
+// by the bytes of the mask and of the logits that change (32 for each adjusted one alone).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,8 +33,10 @@
 namespace pkv {
 namespace {
 
-constexpr int kAdjThreads = 512;
-constexpr int kAdjChunk = 8192;                // tokens of the largest piece of the vocabulary
+constexpr int kAdjThreads = 256;
+constexpr int kAdjSegment = 256;              // tokens next to each other that one CTA has
+constexpr int kAdjSegments = 16;              // at most so many segments of a CTA
+constexpr int kAdjSpan = 1024;                // tokens of a row that a warp looks at together
 constexpr uint32_t kAdjPrompt = 0x80000000u;  // beside a token's count: it is in the prompt
 
 struct AdjustArgs {
@@ -47,7 +55,8 @@ struct AdjustArgs {
   const float* bias_values;
   const uint32_t* allowed;        // [T, W] or NULL
   int32_t S, T, V, L, P, NBias, W;
-  int32_t chunk;                  // tokens of a CTA's piece of the vocabulary, a multiple of 32
+  int32_t segments;               // of a CTA
+  int32_t log_ctas;               // log2 of the CTAs that share a request's vocabulary (NP)
 };
 
 template <typename T>
@@ -61,57 +70,164 @@ struct alignas(16) AdjPiece {
   T x[16 / sizeof(T)];
 };
 
-// Grid: pieces of the vocabulary, requests, shares of a request's rows.  Shared memory: counts
-// [chunk], bias entries [chunk] (with biases), marks [chunk / 32 + 1].
+// ---- what the mask bans, and what is copied ------------------------------------------------
+// A warp a span of a row; the mask's words are loaded by a lane each and handed round.
 template <typename T>
-__global__ void __launch_bounds__(kAdjThreads) adjust_logits_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(kAdjThreads) adjust_mask_kernel(const AdjustArgs a) {
+  // the second kernel may start to count; it waits for this grid before it touches a logit
+  asm volatile("griddepcontrol.launch_dependents;");
   constexpr int VEC = 16 / sizeof(T);
+  constexpr uint32_t all = (1u << VEC) - 1u;
+  constexpr int kSteps = kAdjSpan / VEC / 32;  // pieces of a lane (one more if they are shifted)
+  const int lane = threadIdx.x & 31;
+  const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
+  if (r >= a.T) return;
+  if (a.row_start != nullptr && (r < __ldg(a.row_start) || r >= __ldg(a.row_start + a.S))) return;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * (kAdjThreads / 32) + (threadIdx.x >> 5)) * kAdjSpan;
+  if (c0 >= a.V) return;
+  const int most = static_cast<int>(min(static_cast<int64_t>(kAdjSpan), a.V - c0));  // tokens of the span
+  const T* const in = static_cast<const T*>(a.logits) + r * a.in_stride + c0;
+  T* const out = static_cast<T*>(a.out) + r * a.out_stride + c0;
+  const bool in_place = a.logits == a.out && a.in_stride == a.out_stride;
+  uint32_t word = 0xffffffffu;
+  if (a.allowed != nullptr) {
+    const int64_t w = c0 / 32 + lane;
+    word = w < a.W ? __ldg(a.allowed + r * a.W + w) : 0u;
+  }
+  const uintptr_t off = reinterpret_cast<uintptr_t>(out) & 15;
+  const int before = static_cast<int>(off) / static_cast<int>(sizeof(T));
+  const bool wide = (reinterpret_cast<uintptr_t>(in) & 15) == off;
+  AdjPiece<T> ban;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) ban.x[e] = ptx::from_float<T>(-INFINITY);
+  constexpr int U = 4;
+  static_assert(kSteps % U == 0, "spans");
+#pragma unroll 1
+  for (int x0 = 0; x0 < kSteps + (before != 0 ? 1 : 0); x0 += U) {
+    uint32_t good[U];
+    bool whole[U], read[U];
+    AdjPiece<T> p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = ((x0 + u) * 32 + lane) * VEC - before;  // the piece's first token
+      const uint32_t lo = __shfl_sync(0xffffffffu, word, (t >> 5) & 31);
+      const uint32_t hi = __shfl_sync(0xffffffffu, word, ((t >> 5) + 1) & 31);
+      good[u] = __funnelshift_r(lo, hi, t & 31) & all;
+      whole[u] = wide && t >= 0 && t + VEC <= most;
+      read[u] = whole[u] && good[u] != 0 && !(in_place && good[u] == all);
+      if (read[u]) p[u] = *reinterpret_cast<const AdjPiece<T>*>(in + t);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = ((x0 + u) * 32 + lane) * VEC - before;
+      if (whole[u]) {
+        if (good[u] != 0 && !read[u]) continue;
+        AdjPiece<T> y = ban;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if ((good[u] >> e) & 1u) y.x[e] = p[u].x[e];
+        *reinterpret_cast<AdjPiece<T>*>(out + t) = y;
+      } else {  // the ends of the span, or rows that do not share the boundaries
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          if (t + e < 0 || t + e >= most) continue;
+          // (t < 0: the bits below the span's first come out of the last word; token t + e >= 0
+          // is bit e + t of the first)
+          const bool ok = (good[u] >> e) & 1u;
+          if (!ok) out[t + e] = ban.x[0];
+          else if (!in_place) out[t + e] = in[t + e];
+        }
+      }
+    }
+  }
+}
+
+// ---- the tokens that came, or have a bias ----------------------------------------------------
+// Shared memory words: counts [chunk], bias entries [chunk] (with biases), marks of the tokens in
+// any row's path [chunk / 32], the list of tokens that something touches, 16 bits each [chunk];
+// chunk = 256 * segments.
+__host__ __device__ constexpr int adjust_words(int segments, bool biases) {
+  const int chunk = segments * kAdjSegment;
+  return chunk * (biases ? 2 : 1) + chunk / 32 + chunk / 2;
+}
+
+// Grid: CTAs of a request's vocabulary (a power of two), requests, shares of a request's rows.
+template <typename T>
+__global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const AdjustArgs a) {
   extern __shared__ uint32_t adj_smem[];
-  const int CH = a.chunk, tid = threadIdx.x;
-  const int s = blockIdx.y;
-  const int v0 = blockIdx.x * CH, v1 = min(a.V, v0 + CH);
+  __shared__ int listed;
+  const int tid = threadIdx.x, s = blockIdx.y, first = blockIdx.x;
+  const int CH = a.segments * kAdjSegment;
   uint32_t* const count = adj_smem;
   uint32_t* const entry = count + CH;  // 1 + the bias entry of a token (0: none)
   uint32_t* const marks = entry + (a.bias_tokens != nullptr ? CH : 0);
-  const int words = static_cast<int>(marks - adj_smem) + CH / 32 + 1;
+  uint16_t* const list = reinterpret_cast<uint16_t*>(marks + CH / 32);
+  const int words = static_cast<int>(marks - adj_smem) + CH / 32;
   const int r_first = a.row_start != nullptr ? max(0, __ldg(a.row_start + s)) : s;
   const int r_end = a.row_start != nullptr ? min(a.T, __ldg(a.row_start + s + 1)) : s + 1;
+  const int held = min(max(__ldg(a.history_lens + s), 0), a.L);
+  const int prompt = a.prompt_lens != nullptr ? __ldg(a.prompt_lens + s) : 0;
   if (r_first + static_cast<int64_t>(blockIdx.z) >= r_end) return;
+  const int shares = gridDim.z, row0 = r_first + blockIdx.z;
+  const int rows = (r_end - row0 - 1) / shares + 1;  // row0, row0 + shares, ...
+  auto row = [&](int k) { return row0 + static_cast<int64_t>(k) * shares; };
+  // place of token v in the CTA's segments (-1: another CTA's), and the token at a place
+  auto place = [&](int v) {
+    const int seg = v >> 8;
+    if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(a.V) ||
+        (seg & ((1 << a.log_ctas) - 1)) != first)
+      return -1;
+    return (seg >> a.log_ctas) << 8 | (v & 255);
+  };
+  auto token = [&](int i) { return (((i >> 8) << a.log_ctas) + first) << 8 | (i & 255); };
+  static_assert(kAdjSegment == 256, "places");
   for (int i = tid; i < words; i += kAdjThreads) adj_smem[i] = 0u;
+  if (tid == 0) listed = 0;
   __syncthreads();
-  auto mark = [&](int i) { atomicOr(marks + (i >> 5), 1u << (i & 31)); };
   {
-    const int n = min(max(__ldg(a.history_lens + s), 0), a.L);
-    const int prompt = a.prompt_lens != nullptr ? __ldg(a.prompt_lens + s) : 0;
     const int32_t* const tokens = a.history + static_cast<int64_t>(s) * a.L;
     auto one = [&](int at, int tok) {
-      if (tok < v0 || tok >= v1) return;
-      if (at < prompt) atomicOr(count + (tok - v0), kAdjPrompt);
-      else atomicAdd(count + (tok - v0), 1u);
-      mark(tok - v0);
+      const int i = place(tok);
+      if (i < 0) return;
+      if (at >= prompt) atomicAdd(count + i, 1u);
+      else if ((count[i] & kAdjPrompt) == 0) atomicOr(count + i, kAdjPrompt);  // (often there already)
     };
-    // four tokens at once from the first 16-byte boundary on
+    // four tokens at once from the first 16-byte boundary on, four such loads on their way
     const int head =
-        min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(tokens) & 15)) & 15) / 4);
-    const int quads = (n - head) / 4;
-    if (tid < head) one(tid, __ldg(tokens + tid));
-    for (int i = tid; i < quads; i += kAdjThreads) {
-      const int4 q = __ldg(reinterpret_cast<const int4*>(tokens + head) + i);
-      const int at = head + 4 * i;
-      one(at, q.x);
-      one(at + 1, q.y);
-      one(at + 2, q.z);
-      one(at + 3, q.w);
+        min(held, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(tokens) & 15)) & 15) / 4);
+    const int quads = (held - head) / 4;
+    const int4* const body = reinterpret_cast<const int4*>(tokens + head);
+    for (int i0 = tid; i0 < quads; i0 += 4 * kAdjThreads) {
+      int4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kAdjThreads < quads) q[u] = __ldg(body + i0 + u * kAdjThreads);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = head + 4 * (i0 + u * kAdjThreads);
+        if (i0 + u * kAdjThreads >= quads) continue;
+        one(at, q[u].x);
+        one(at + 1, q[u].y);
+        one(at + 2, q[u].z);
+        one(at + 3, q[u].w);
+      }
     }
+    if (tid < head) one(tid, __ldg(tokens + tid));
     const int rest = head + 4 * quads + tid;
-    if (rest < n) one(rest, __ldg(tokens + rest));
+    if (rest < held) one(rest, __ldg(tokens + rest));
     if (a.bias_tokens != nullptr) {  // of entries for one token the last counts
       const int32_t* const ids = a.bias_tokens + static_cast<int64_t>(s) * a.NBias;
-      for (int i = tid; i < a.NBias; i += kAdjThreads) {
-        const int tok = __ldg(ids + i);
-        if (tok < v0 || tok >= v1) continue;
-        atomicMax(entry + (tok - v0), static_cast<uint32_t>(i) + 1u);
-        mark(tok - v0);
+      for (int e = tid; e < a.NBias; e += kAdjThreads) {
+        const int i = place(__ldg(ids + e));
+        if (i >= 0) atomicMax(entry + i, static_cast<uint32_t>(e) + 1u);
+      }
+    }
+    if (a.path != nullptr) {
+      for (int k = tid / 32; k < rows; k += kAdjThreads / 32) {  // a warp a row
+        for (int p = tid % 32; p < a.P; p += 32) {
+          const int i = place(__ldg(a.path + row(k) * a.P + p));
+          if (i >= 0) atomicOr(marks + (i >> 5), 1u << (i & 31));
+        }
       }
     }
   }
@@ -120,113 +236,105 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_logits_kernel(const Adjust
   const float pres = a.presence != nullptr ? __ldg(a.presence + s) : 0.f;
   const float* const values =
       a.bias_tokens != nullptr ? a.bias_values + static_cast<int64_t>(s) * a.NBias : nullptr;
-  // a marked token's logit (token v0 + i)
-  auto adjusted = [&](float x, int i) {
-    const uint32_t c = count[i];
-    const uint32_t n = c & ~kAdjPrompt;
-    if (c != 0) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-    if (n != 0) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, static_cast<float>(n))), pres);
-    if (values != nullptr) {
-      const uint32_t e = entry[i];
-      if (e != 0) x = __fadd_rn(x, __ldg(values + e - 1));
-    }
-    return x;
-  };
-  const bool in_place = a.logits == a.out && a.in_stride == a.out_stride;
-  for (int r = r_first + blockIdx.z; r < r_end; r += gridDim.z) {
-    const int32_t* const path =
-        a.path != nullptr ? a.path + static_cast<int64_t>(r) * a.P : nullptr;
-    __syncthreads();  // counts complete; the row before is done
-    if (path != nullptr) {
-      for (int i = tid; i < a.P; i += kAdjThreads) {
-        const int tok = __ldg(path + i);
-        if (tok < v0 || tok >= v1) continue;
-        atomicAdd(count + (tok - v0), 1u);
-        mark(tok - v0);
+  __syncthreads();
+  // the places that something touches, in any order (each is dealt with by itself): four
+  // neighbours a thread
+  for (int i0 = 0; i0 < CH; i0 += 4 * kAdjThreads) {
+    const int i = i0 + 4 * tid;
+    uint32_t on = 0;
+    if (i < CH) {
+      const uint4 c = *reinterpret_cast<const uint4*>(count + i);
+      on = (c.x != 0 ? 1u : 0u) | (c.y != 0 ? 2u : 0u) | (c.z != 0 ? 4u : 0u) | (c.w != 0 ? 8u : 0u);
+      on |= (marks[i >> 5] >> (i & 31)) & 15u;
+      if (values != nullptr) {
+        const uint4 e = *reinterpret_cast<const uint4*>(entry + i);
+        on |= (e.x != 0 ? 1u : 0u) | (e.y != 0 ? 2u : 0u) | (e.z != 0 ? 4u : 0u) | (e.w != 0 ? 8u : 0u);
       }
-      __syncthreads();
     }
-    const T* const src = static_cast<const T*>(a.logits) + r * a.in_stride;
-    T* const dst = static_cast<T*>(a.out) + r * a.out_stride;
-    const uint32_t* const ok =
-        a.allowed != nullptr ? a.allowed + static_cast<int64_t>(r) * a.W : nullptr;
-    // a mark may be of another row's path: only a token that something touches changes
-    auto touched = [&](int i) {
-      return count[i] != 0 || (values != nullptr && entry[i] != 0);
-    };
-    if (in_place && ok == nullptr) {
-      for (int w = tid; w < CH / 32; w += kAdjThreads) {
-        for (uint32_t m = marks[w]; m != 0; m &= m - 1) {
-          const int i = 32 * w + __ffs(m) - 1;
-          if (touched(i)) dst[v0 + i] = ptx::from_float<T>(adjusted(logit_of(src[v0 + i]), i));
-        }
-      }
-    } else {
-      // bits of tokens v .. v + 31 of a bit row of n words, the first being token 0's
-      auto bits = [](const uint32_t* row, int n, int v) {
-        const int w = v >> 5;
-        const uint32_t lo = w < n ? row[w] : 0u;
-        const uint32_t hi = (v & 31) != 0 && w + 1 < n ? row[w + 1] : 0u;
-        return __funnelshift_r(lo, hi, v & 31);
-      };
-      auto one = [&](int v) {  // a token by itself
-        const int i = v - v0;
-        if (ok != nullptr && !((__ldg(ok + (v >> 5)) >> (v & 31)) & 1u))
-          dst[v] = ptx::from_float<T>(-INFINITY);
-        else if (touched(i)) dst[v] = ptx::from_float<T>(adjusted(logit_of(src[v]), i));
-        else if (!in_place) dst[v] = src[v];
-      };
-      // 16 bytes at a time from the first boundary of the row on (if logits and out share it)
-      const uintptr_t off = reinterpret_cast<uintptr_t>(dst) & 15;
-      const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == off;
-      const int head = static_cast<int>((16 - off) & 15) / static_cast<int>(sizeof(T));
-      // whole pieces inside [v0, v1): n of them from token p0 on
-      int p0 = v0 <= head ? head : head + (v0 - head + VEC - 1) / VEC * VEC;
-      const int n = wide && v1 > p0 ? (v1 - p0) / VEC : 0;
-      if (n == 0) p0 = v1;
-      for (int v = v0 + tid; v < p0; v += kAdjThreads) one(v);
-      for (int v = p0 + n * VEC + tid; v < v1; v += kAdjThreads) one(v);
-      const uint32_t all = (1u << VEC) - 1u;
-      AdjPiece<T> ban;
+    const int own = __popc(on);
+    int upto = own;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) ban.x[e] = ptx::from_float<T>(-INFINITY);
-      for (int i = tid; i < n; i += kAdjThreads) {
-        const int v = p0 + i * VEC;
-        const uint32_t good = ok == nullptr ? all : bits(ok, a.W, v) & all;
-        const uint32_t mk = bits(marks, CH / 32 + 1, v - v0) & all;
-        if (good == 0) {
-          *reinterpret_cast<AdjPiece<T>*>(dst + v) = ban;
-          continue;
-        }
-        if (in_place && good == all && mk == 0) continue;
-        AdjPiece<T> p = *reinterpret_cast<const AdjPiece<T>*>(src + v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (!((good >> e) & 1u)) p.x[e] = ban.x[e];
-          else if (((mk >> e) & 1u) && touched(v - v0 + e))
-            p.x[e] = ptx::from_float<T>(adjusted(logit_of(p.x[e]), v - v0 + e));
-        }
-        *reinterpret_cast<AdjPiece<T>*>(dst + v) = p;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((tid & 31) >= o) upto += y;
     }
-    if (path != nullptr) {  // the row's own tokens are taken out again
-      __syncthreads();
-      for (int i = tid; i < a.P; i += kAdjThreads) {
-        const int tok = __ldg(path + i);
-        if (tok >= v0 && tok < v1) atomicSub(count + (tok - v0), 1u);
+    int at = 0;
+    if ((tid & 31) == 31 && upto != 0) at = atomicAdd(&listed, upto);
+    at = __shfl_sync(0xffffffffu, at, 31) + upto - own;
+    for (; on != 0; on &= on - 1) list[at++] = static_cast<uint16_t>(i + __ffs(on) - 1);
+  }
+  __syncthreads();
+  // the first kernel's logits, and whatever was queued before
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = listed;
+  int sh = 0;  // log2 of the threads that share a token's rows, if there are few tokens
+  while (sh < 5 && (n << (sh + 1)) <= kAdjThreads) ++sh;
+  const int step = 1 << sh;
+  const T* const in = static_cast<const T*>(a.logits);
+  T* const out = static_cast<T*>(a.out);
+  for (int e = tid >> sh; e < n; e += kAdjThreads >> sh) {
+    const int i = list[e], v = token(i);
+    const uint32_t held_count = count[i];
+    const uint32_t be = values != nullptr ? entry[i] : 0u;
+    const float bias = be != 0 ? __ldg(values + be - 1) : 0.f;
+    const bool in_path = (marks[i >> 5] >> (i & 31)) & 1u;
+    for (int k = tid & (step - 1); k < rows; k += 4 * step) {
+      T x[4];
+      bool on[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        on[u] = k + u * step < rows;
+        if (!on[u]) continue;
+        const int64_t r = row(k + u * step);
+        if (a.allowed != nullptr) on[u] = (__ldg(a.allowed + r * a.W + (v >> 5)) >> (v & 31)) & 1u;
+        x[u] = in[r * a.in_stride + v];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!on[u]) continue;
+        const int64_t r = row(k + u * step);
+        uint32_t c = held_count;
+        if (in_path) {
+          const int32_t* const path = a.path + r * a.P;
+          for (int p = 0; p < a.P; ++p) c += __ldg(path + p) == v ? 1u : 0u;
+        }
+        if (c == 0 && be == 0) continue;  // of another row's path
+        float y = logit_of(x[u]);
+        if (c != 0) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+        if ((c & ~kAdjPrompt) != 0)
+          y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, static_cast<float>(c & ~kAdjPrompt))), pres);
+        if (be != 0) y = __fadd_rn(y, bias);
+        out[r * a.out_stride + v] = ptx::from_float<T>(y);
       }
     }
   }
 }
 
 template <typename T>
-int launch_adjust(const AdjustArgs& a, int pieces, int shares, size_t smem, cudaStream_t st) {
+int launch_adjust(const AdjustArgs& a, int shares, cudaStream_t st) {
   static SmemOnce once;
-  const int rc = allow_dynamic_smem(once, reinterpret_cast<const void*>(adjust_logits_kernel<T>),
-                                    (2 * kAdjChunk + kAdjChunk / 32 + 1) * 4);
+  const int rc = allow_dynamic_smem(once, reinterpret_cast<const void*>(adjust_tokens_kernel<T>),
+                                    adjust_words(kAdjSegments, true) * 4);
   if (rc != PKV_OK) return rc;
-  adjust_logits_kernel<T><<<dim3(pieces, a.S, shares), kAdjThreads, smem, st>>>(a);
-  PKV_CUDA(cudaGetLastError());
+  const bool masks = a.allowed != nullptr || a.logits != a.out;
+  if (masks) {
+    const int spans = (a.V - 1) / kAdjSpan + 1, warps = kAdjThreads / 32;
+    const int deep = (a.T - 1) / 65535 + 1;
+    adjust_mask_kernel<T>
+        <<<dim3((spans - 1) / warps + 1, deep > 1 ? 65535 : a.T, deep), kAdjThreads, 0, st>>>(a);
+    PKV_CUDA(cudaGetLastError());
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1u << a.log_ctas, a.S, shares);
+  cfg.blockDim = dim3(kAdjThreads);
+  cfg.dynamicSmemBytes = adjust_words(a.segments, a.bias_tokens != nullptr) * sizeof(uint32_t);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = masks ? 1 : 0;
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, adjust_tokens_kernel<T>, a));
   return PKV_OK;
 }
 
@@ -299,23 +407,22 @@ extern "C" int pkv_adjust_logits(
   a.P = path_cols;
   a.NBias = bias_cols;
   a.W = allowed_words;
-  // pieces of the vocabulary small enough for every SM to have one, up to 8,192 tokens
-  a.chunk = kAdjChunk;
-  while (a.chunk > 1024 &&
-         static_cast<int64_t>((vocab + a.chunk - 1) / a.chunk) * num_requests < sms)
-    a.chunk /= 2;
-  const int pieces = (vocab + a.chunk - 1) / a.chunk;
+  // a power of two of CTAs with at most 16 segments each; more, down to 4 segments, until every
+  // SM has one
+  const int total = (vocab + kAdjSegment - 1) / kAdjSegment;
+  while ((int64_t(kAdjSegments) << a.log_ctas) < total) ++a.log_ctas;
+  while ((int64_t(4) << a.log_ctas) < total && (int64_t(num_requests) << a.log_ctas) < sms)
+    ++a.log_ctas;
+  a.segments = (total - 1) / (1 << a.log_ctas) + 1;
   // a request's rows are shared out until the SMs have two CTAs each
   const int per = (num_rows - 1) / num_requests + 1;
   int shares = 1;
   while (shares < per && shares < 64 &&
-         static_cast<int64_t>(pieces) * num_requests * shares < 2 * sms)
+         (int64_t(num_requests) << a.log_ctas) * shares < 2 * sms)
     shares *= 2;
-  const size_t smem =
-      (static_cast<size_t>(a.chunk) * (a.bias_tokens != nullptr ? 2 : 1) + a.chunk / 32 + 1) * 4;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = dtype == PKV_F32   ? launch_adjust<float>(a, pieces, shares, smem, st)
-       : dtype == PKV_F16 ? launch_adjust<__half>(a, pieces, shares, smem, st)
-                          : launch_adjust<__nv_bfloat16>(a, pieces, shares, smem, st);
+  rc = dtype == PKV_F32   ? launch_adjust<float>(a, shares, st)
+       : dtype == PKV_F16 ? launch_adjust<__half>(a, shares, st)
+                          : launch_adjust<__nv_bfloat16>(a, shares, st);
   return rc == PKV_OK ? ok() : rc;
 }
