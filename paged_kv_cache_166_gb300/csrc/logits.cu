@@ -13,16 +13,19 @@
 // place, leaves allowed ones alone.  The second kernel, whose counting overlaps the first, puts
 // the adjusted logits over that: a CTA takes every NP-th segment of 256 tokens of the
 // vocabulary for one request (the low numbers, which most texts use most, are spread over all
-// CTAs), counts the request's tokens that fall there in shared memory (integers, so their order
-// does not matter) and goes through the rows with those that came.  Without a mask a row thus
-// costs, in place, as much as the request has tokens, not the vocabulary.
+// CTAs).  The CTAs of a cluster share the request's tokens out and count each in the shared
+// memory of the CTA that has it (integers, so their order does not matter); then each goes
+// through the rows with those that came.  Without a mask a row thus costs, in place, as much as
+// the request has tokens, not the vocabulary.
 //
 // Bound by memory latency for small calls (lengths, history, logits one after the other), else
 // by the bytes of the mask and of the logits that change (32 for each adjusted one alone).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -33,10 +36,14 @@
 namespace pkv {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kAdjThreads = 256;
 constexpr int kAdjSegment = 256;              // tokens next to each other that one CTA has
-constexpr int kAdjSegments = 16;              // at most so many segments of a CTA
+constexpr int kAdjSegments = 32;              // at most so many segments of a CTA
+constexpr int kAdjCluster = 8;                // at most so many CTAs count together
 constexpr int kAdjSpan = 1024;                // tokens of a row that a warp looks at together
+constexpr int kAdjSpans = 4;                  // such spans of a warp, their masks loaded at once
 constexpr uint32_t kAdjPrompt = 0x80000000u;  // beside a token's count: it is in the prompt
 
 struct AdjustArgs {
@@ -73,7 +80,7 @@ struct alignas(16) AdjPiece {
 // ---- what the mask bans, and what is copied ------------------------------------------------
 // A warp a span of a row; the mask's words are loaded by a lane each and handed round.
 template <typename T>
-__global__ void __launch_bounds__(kAdjThreads) adjust_mask_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(kAdjThreads, 4) adjust_mask_kernel(const AdjustArgs a) {
   // the second kernel may start to count; it waits for this grid before it touches a logit
   asm volatile("griddepcontrol.launch_dependents;");
   constexpr int VEC = 16 / sizeof(T);
@@ -83,59 +90,68 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_mask_kernel(const AdjustAr
   const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
   if (r >= a.T) return;
   if (a.row_start != nullptr && (r < __ldg(a.row_start) || r >= __ldg(a.row_start + a.S))) return;
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * (kAdjThreads / 32) + (threadIdx.x >> 5)) * kAdjSpan;
-  if (c0 >= a.V) return;
-  const int most = static_cast<int>(min(static_cast<int64_t>(kAdjSpan), a.V - c0));  // tokens of the span
-  const T* const in = static_cast<const T*>(a.logits) + r * a.in_stride + c0;
-  T* const out = static_cast<T*>(a.out) + r * a.out_stride + c0;
+  const int64_t first =
+      (static_cast<int64_t>(blockIdx.x) * (kAdjThreads / 32) + (threadIdx.x >> 5)) * kAdjSpans * kAdjSpan;
   const bool in_place = a.logits == a.out && a.in_stride == a.out_stride;
-  uint32_t word = 0xffffffffu;
-  if (a.allowed != nullptr) {
-    const int64_t w = c0 / 32 + lane;
-    word = w < a.W ? __ldg(a.allowed + r * a.W + w) : 0u;
+  uint32_t word4[kAdjSpans];
+#pragma unroll
+  for (int q = 0; q < kAdjSpans; ++q) {
+    const int64_t w = first / 32 + q * 32 + lane;
+    word4[q] = a.allowed == nullptr ? 0xffffffffu : (w < a.W ? __ldg(a.allowed + r * a.W + w) : 0u);
   }
-  const uintptr_t off = reinterpret_cast<uintptr_t>(out) & 15;
+  const T* const in_row = static_cast<const T*>(a.logits) + r * a.in_stride;
+  T* const out_row = static_cast<T*>(a.out) + r * a.out_stride;
+  const uintptr_t off = reinterpret_cast<uintptr_t>(out_row) & 15;  // (spans are whole 16 bytes)
   const int before = static_cast<int>(off) / static_cast<int>(sizeof(T));
-  const bool wide = (reinterpret_cast<uintptr_t>(in) & 15) == off;
+  const bool wide = (reinterpret_cast<uintptr_t>(in_row) & 15) == off;
   AdjPiece<T> ban;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) ban.x[e] = ptx::from_float<T>(-INFINITY);
   constexpr int U = 4;
   static_assert(kSteps % U == 0, "spans");
 #pragma unroll 1
-  for (int x0 = 0; x0 < kSteps + (before != 0 ? 1 : 0); x0 += U) {
-    uint32_t good[U];
-    bool whole[U], read[U];
-    AdjPiece<T> p[U];
+  for (int q = 0; q < kAdjSpans; ++q) {
+    const int64_t c0 = first + q * kAdjSpan;
+    if (c0 >= a.V) break;
+    const int most = static_cast<int>(min(static_cast<int64_t>(kAdjSpan), a.V - c0));  // tokens of the span
+    const T* const in = in_row + c0;
+    T* const out = out_row + c0;
+    const uint32_t word = q == 0 ? word4[0] : (q == 1 ? word4[1] : (q == 2 ? word4[2] : word4[3]));
+#pragma unroll 1
+    for (int x0 = 0; x0 < kSteps + (before != 0 ? 1 : 0); x0 += U) {
+      uint32_t good[U];
+      bool whole[U], read[U];
+      AdjPiece<T> p[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = ((x0 + u) * 32 + lane) * VEC - before;  // the piece's first token
-      const uint32_t lo = __shfl_sync(0xffffffffu, word, (t >> 5) & 31);
-      const uint32_t hi = __shfl_sync(0xffffffffu, word, ((t >> 5) + 1) & 31);
-      good[u] = __funnelshift_r(lo, hi, t & 31) & all;
-      whole[u] = wide && t >= 0 && t + VEC <= most;
-      read[u] = whole[u] && good[u] != 0 && !(in_place && good[u] == all);
-      if (read[u]) p[u] = *reinterpret_cast<const AdjPiece<T>*>(in + t);
-    }
+      for (int u = 0; u < U; ++u) {
+        const int t = ((x0 + u) * 32 + lane) * VEC - before;  // the piece's first token
+        const uint32_t lo = __shfl_sync(0xffffffffu, word, (t >> 5) & 31);
+        const uint32_t hi = __shfl_sync(0xffffffffu, word, ((t >> 5) + 1) & 31);
+        good[u] = __funnelshift_r(lo, hi, t & 31) & all;
+        whole[u] = wide && t >= 0 && t + VEC <= most;
+        read[u] = whole[u] && good[u] != 0 && !(in_place && good[u] == all);
+        if (read[u]) p[u] = *reinterpret_cast<const AdjPiece<T>*>(in + t);
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = ((x0 + u) * 32 + lane) * VEC - before;
-      if (whole[u]) {
-        if (good[u] != 0 && !read[u]) continue;
-        AdjPiece<T> y = ban;
+      for (int u = 0; u < U; ++u) {
+        const int t = ((x0 + u) * 32 + lane) * VEC - before;
+        if (whole[u]) {
+          if (good[u] != 0 && !read[u]) continue;
+          AdjPiece<T> y = ban;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if ((good[u] >> e) & 1u) y.x[e] = p[u].x[e];
-        *reinterpret_cast<AdjPiece<T>*>(out + t) = y;
-      } else {  // the ends of the span, or rows that do not share the boundaries
+          for (int e = 0; e < VEC; ++e)
+            if ((good[u] >> e) & 1u) y.x[e] = p[u].x[e];
+          *reinterpret_cast<AdjPiece<T>*>(out + t) = y;
+        } else {  // the ends of the span, or rows that do not share the boundaries
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (t + e < 0 || t + e >= most) continue;
-          // (t < 0: the bits below the span's first come out of the last word; token t + e >= 0
-          // is bit e + t of the first)
-          const bool ok = (good[u] >> e) & 1u;
-          if (!ok) out[t + e] = ban.x[0];
-          else if (!in_place) out[t + e] = in[t + e];
+          for (int e = 0; e < VEC; ++e) {
+            if (t + e < 0 || t + e >= most) continue;
+            // (t < 0: the bits below the span's first come out of the last word; token t + e >= 0
+            // is bit e + t of the first)
+            const bool ok = (good[u] >> e) & 1u;
+            if (!ok) out[t + e] = ban.x[0];
+            else if (!in_place) out[t + e] = in[t + e];
+          }
         }
       }
     }
@@ -171,11 +187,17 @@ __global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const Adj
   const int shares = gridDim.z, row0 = r_first + blockIdx.z;
   const int rows = (r_end - row0 - 1) / shares + 1;  // row0, row0 + shares, ...
   auto row = [&](int k) { return row0 + static_cast<int64_t>(k) * shares; };
-  // place of token v in the CTA's segments (-1: another CTA's), and the token at a place
+  // CTAs of the cluster: numbers c0 .. c0 + cluster - 1 of the request's
+  const int cluster = min(kAdjCluster, static_cast<int>(gridDim.x)), c0 = first & ~(cluster - 1);
+  const int rank = first - c0;
+  // place of token v in its CTA's segments (-1: in none of this cluster's), and the token at a
+  // place of this CTA's
+  int owner = 0;  // that CTA's rank in the cluster
   auto place = [&](int v) {
     const int seg = v >> 8;
+    owner = (seg & ((1 << a.log_ctas) - 1)) - c0;
     if (static_cast<uint32_t>(v) >= static_cast<uint32_t>(a.V) ||
-        (seg & ((1 << a.log_ctas) - 1)) != first)
+        static_cast<uint32_t>(owner) >= static_cast<uint32_t>(cluster))
       return -1;
     return (seg >> a.log_ctas) << 8 | (v & 255);
   };
@@ -183,50 +205,54 @@ __global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const Adj
   static_assert(kAdjSegment == 256, "places");
   for (int i = tid; i < words; i += kAdjThreads) adj_smem[i] = 0u;
   if (tid == 0) listed = 0;
-  __syncthreads();
+  cg::cluster_group together = cg::this_cluster();
+  together.sync();  // every table of the cluster is cleared
   {
     const int32_t* const tokens = a.history + static_cast<int64_t>(s) * a.L;
     auto one = [&](int at, int tok) {
       const int i = place(tok);
       if (i < 0) return;
-      if (at >= prompt) atomicAdd(count + i, 1u);
-      else if ((count[i] & kAdjPrompt) == 0) atomicOr(count + i, kAdjPrompt);  // (often there already)
+      uint32_t* const c = together.map_shared_rank(count + i, owner);
+      if (at >= prompt) atomicAdd(c, 1u);
+      else atomicOr(c, kAdjPrompt);
     };
     // four tokens at once from the first 16-byte boundary on, four such loads on their way
     const int head =
         min(held, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(tokens) & 15)) & 15) / 4);
     const int quads = (held - head) / 4;
     const int4* const body = reinterpret_cast<const int4*>(tokens + head);
-    for (int i0 = tid; i0 < quads; i0 += 4 * kAdjThreads) {
+    const int threads = cluster * kAdjThreads, me = rank * kAdjThreads + tid;
+    for (int i0 = me; i0 < quads; i0 += 4 * threads) {
       int4 q[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (i0 + u * kAdjThreads < quads) q[u] = __ldg(body + i0 + u * kAdjThreads);
+        if (i0 + u * threads < quads) q[u] = __ldg(body + i0 + u * threads);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int at = head + 4 * (i0 + u * kAdjThreads);
-        if (i0 + u * kAdjThreads >= quads) continue;
+        const int at = head + 4 * (i0 + u * threads);
+        if (i0 + u * threads >= quads) continue;
         one(at, q[u].x);
         one(at + 1, q[u].y);
         one(at + 2, q[u].z);
         one(at + 3, q[u].w);
       }
     }
-    if (tid < head) one(tid, __ldg(tokens + tid));
-    const int rest = head + 4 * quads + tid;
+    if (me < head) one(me, __ldg(tokens + me));
+    const int rest = head + 4 * quads + me;
     if (rest < held) one(rest, __ldg(tokens + rest));
     if (a.bias_tokens != nullptr) {  // of entries for one token the last counts
       const int32_t* const ids = a.bias_tokens + static_cast<int64_t>(s) * a.NBias;
-      for (int e = tid; e < a.NBias; e += kAdjThreads) {
+      for (int e = me; e < a.NBias; e += threads) {
         const int i = place(__ldg(ids + e));
-        if (i >= 0) atomicMax(entry + i, static_cast<uint32_t>(e) + 1u);
+        if (i >= 0) atomicMax(together.map_shared_rank(entry + i, owner), static_cast<uint32_t>(e) + 1u);
       }
     }
     if (a.path != nullptr) {
-      for (int k = tid / 32; k < rows; k += kAdjThreads / 32) {  // a warp a row
-        for (int p = tid % 32; p < a.P; p += 32) {
+      for (int k = me / 32; k < rows; k += threads / 32) {  // a warp a row
+        for (int p = me % 32; p < a.P; p += 32) {
           const int i = place(__ldg(a.path + row(k) * a.P + p));
-          if (i >= 0) atomicOr(marks + (i >> 5), 1u << (i & 31));
+          if (i >= 0)
+            atomicOr(together.map_shared_rank(marks + (i >> 5), owner), 1u << (i & 31));
         }
       }
     }
@@ -236,7 +262,7 @@ __global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const Adj
   const float pres = a.presence != nullptr ? __ldg(a.presence + s) : 0.f;
   const float* const values =
       a.bias_tokens != nullptr ? a.bias_values + static_cast<int64_t>(s) * a.NBias : nullptr;
-  __syncthreads();
+  together.sync();  // everything is counted: no CTA looks into another one's tables from here on
   // the places that something touches, in any order (each is dealt with by itself): four
   // neighbours a thread
   for (int i0 = 0; i0 < CH; i0 += 4 * kAdjThreads) {
@@ -284,11 +310,12 @@ __global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const Adj
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         on[u] = k + u * step < rows;
-        if (!on[u]) continue;
-        const int64_t r = row(k + u * step);
-        if (a.allowed != nullptr) on[u] = (__ldg(a.allowed + r * a.W + (v >> 5)) >> (v & 31)) & 1u;
-        x[u] = in[r * a.in_stride + v];
+        if (on[u] && a.allowed != nullptr)
+          on[u] = (__ldg(a.allowed + row(k + u * step) * a.W + (v >> 5)) >> (v & 31)) & 1u;
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (on[u]) x[u] = in[row(k + u * step) * a.in_stride + v];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (!on[u]) continue;
@@ -318,7 +345,7 @@ int launch_adjust(const AdjustArgs& a, int shares, cudaStream_t st) {
   if (rc != PKV_OK) return rc;
   const bool masks = a.allowed != nullptr || a.logits != a.out;
   if (masks) {
-    const int spans = (a.V - 1) / kAdjSpan + 1, warps = kAdjThreads / 32;
+    const int spans = (a.V - 1) / (kAdjSpan * kAdjSpans) + 1, warps = kAdjThreads / 32;
     const int deep = (a.T - 1) / 65535 + 1;
     adjust_mask_kernel<T>
         <<<dim3((spans - 1) / warps + 1, deep > 1 ? 65535 : a.T, deep), kAdjThreads, 0, st>>>(a);
@@ -329,11 +356,14 @@ int launch_adjust(const AdjustArgs& a, int shares, cudaStream_t st) {
   cfg.blockDim = dim3(kAdjThreads);
   cfg.dynamicSmemBytes = adjust_words(a.segments, a.bias_tokens != nullptr) * sizeof(uint32_t);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = std::min(kAdjCluster, 1 << a.log_ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = masks ? 1 : 0;
+  cfg.numAttrs = masks ? 2 : 1;
   PKV_CUDA(cudaLaunchKernelEx(&cfg, adjust_tokens_kernel<T>, a));
   return PKV_OK;
 }
@@ -407,12 +437,17 @@ extern "C" int pkv_adjust_logits(
   a.P = path_cols;
   a.NBias = bias_cols;
   a.W = allowed_words;
-  // a power of two of CTAs with at most 16 segments each; more, down to 4 segments, until every
-  // SM has one
+  // A power of two of CTAs, as few as hold the vocabulary (256 rows of 65,537 under a mask: 104
+  // us with at most 16 segments a CTA, 82 with 32); of those of over 16 more until the SMs have
+  // eight (32 requests of 8 rows of 131,072: 42 us with 16 segments, 48 with 32), and of those of
+  // over 4 until they have three.
   const int total = (vocab + kAdjSegment - 1) / kAdjSegment;
+  auto more = [&](int segments, int each) {
+    return (int64_t(segments) << a.log_ctas) < total &&
+           (int64_t(num_requests) << a.log_ctas) < int64_t(each) * sms;
+  };
   while ((int64_t(kAdjSegments) << a.log_ctas) < total) ++a.log_ctas;
-  while ((int64_t(4) << a.log_ctas) < total && (int64_t(num_requests) << a.log_ctas) < sms)
-    ++a.log_ctas;
+  while (more(16, 8) || more(4, 3)) ++a.log_ctas;
   a.segments = (total - 1) / (1 << a.log_ctas) + 1;
   // a request's rows are shared out until the SMs have two CTAs each
   const int per = (num_rows - 1) / num_requests + 1;
