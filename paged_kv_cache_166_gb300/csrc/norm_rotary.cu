@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -32,6 +33,7 @@ namespace {
 
 constexpr int kMaxAxes = 4;
 constexpr int kNormThreads = 128;
+constexpr int kBulkTokens = 4;  // tokens an SM from which on whole tokens are fetched
 
 struct NormArgs : RotaryArgs {
   const void* qw;  // weights [D] or [heads, D], or NULL: ones
@@ -304,6 +306,308 @@ __global__ void __launch_bounds__(kNormThreads, 5)
   }
 }
 
+// ---- many tokens: rows of whole tokens by bulk copies ------------------------------------------
+// One warp fetches: the rows of a token's q, k and v and its rows of the table go to a stage of
+// shared memory by cp.async.bulk, several tokens ahead, so that neither positions nor tables nor
+// rows are waited for.  Eight warps norm, turn and write a stage's heads; the lanes of a head, and
+// so its bits, are those of the kernel above.
+constexpr int kBulkWarps = 8;
+constexpr int kBulkThreads = (kBulkWarps + 1) * 32;
+constexpr int kBulkStages = 8;                 // at most
+constexpr uint64_t kBulkWaitNs = 1000000000ull;  // 1 s per wait before giving up
+
+struct BulkShape {
+  uint32_t q, k, v, table, stage;  // bytes of a stage's parts and of a stage (with 16 for the slot)
+  int32_t stages;
+};
+
+template <typename T, bool kInter, int kCodes, int NU>
+__global__ void __launch_bounds__(kBulkThreads, 2)
+    norm_rotary_bulk_kernel(const __grid_constant__ NormArgs a, const BulkShape sh) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int VEC = 16 / sizeof(T);
+  constexpr int kAng = kInter ? VEC / 2 : VEC;
+  using P = Pack<T, VEC>;
+  extern __shared__ __align__(128) uint8_t bulk_smem[];
+  __shared__ uint64_t bar_mem[2 * kBulkStages];
+  const uint32_t bars = ptx::smem_addr(bar_mem);
+  auto full = [&](uint32_t st) { return bars + 8 * st; };
+  auto empty = [&](uint32_t st) { return bars + 8 * (kBulkStages + st); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBulkStages; ++i) {
+      ptx::mbar_init(full(i), 1);
+      ptx::mbar_init(empty(i), kBulkWarps);
+    }
+    ptx::fence_barrier_init();
+  }
+  __syncthreads();
+  const uint32_t stages = sh.stages;
+  const int64_t step = gridDim.x;
+  if (warp == kBulkWarps) {
+    uint32_t it = 0;
+    bool alive = true;
+    for (int64_t t0 = blockIdx.x; alive && t0 < a.T; t0 += 32 * step) {
+      // a lane looks up a token's slot and positions
+      const int64_t t = t0 + lane * step;
+      int32_t slot = -1, pos[kMaxAxes] = {0, 0, 0, 0};
+      if (t < a.T) {
+        slot = __ldg(a.slots + t);
+#pragma unroll
+        for (int x = 0; x < kMaxAxes; ++x) {
+          if (x >= a.axes) continue;
+          pos[x] = __ldg(a.positions + static_cast<int64_t>(x) * a.T + t);
+          if (pos[x] < 0 || pos[x] >= a.P) {
+            if (a.status != nullptr) atomicOr(a.status, PKV_DEV_BAD_POSITION);
+            pos[x] = pos[x] < 0 ? 0 : a.P - 1;
+          }
+        }
+      }
+      for (int l = 0; l < 32 && t0 + l * step < a.T; ++l, ++it) {
+        const int32_t sl = __shfl_sync(0xffffffffu, slot, l);
+        int32_t ps[kMaxAxes];
+#pragma unroll
+        for (int x = 0; x < kMaxAxes; ++x) ps[x] = __shfl_sync(0xffffffffu, pos[x], l);
+        const uint32_t st = it % stages;
+        if (lane == 0) {
+          alive = ptx::mbar_wait(empty(st), ((it / stages) & 1u) ^ 1u, kBulkWaitNs);
+          if (alive) {
+            uint8_t* const stage = bulk_smem + st * sh.stage;
+            const uint32_t at = ptx::smem_addr(stage);
+            *reinterpret_cast<int32_t*>(stage + sh.stage - 16) = sl;
+            const uint32_t row = static_cast<uint32_t>(a.rot) * 4;
+            ptx::mbar_arrive_expect_tx(full(st), sh.q + sh.k + sh.v + row * a.axes);
+            const int64_t tok = t0 + l * step;
+            ptx::bulk_load(at, static_cast<const T*>(a.q) + tok * a.q_stride, sh.q, full(st));
+            ptx::bulk_load(at + sh.q, static_cast<const T*>(a.k) + tok * a.k_stride, sh.k, full(st));
+            if constexpr (kCodes == 0)
+              ptx::bulk_load(at + sh.q + sh.k, static_cast<const T*>(a.v) + tok * a.v_stride, sh.v,
+                             full(st));
+#pragma unroll
+            for (int x = 0; x < kMaxAxes; ++x)
+              if (x < a.axes)
+                ptx::bulk_load(at + sh.q + sh.k + sh.v + x * row,
+                               a.table + static_cast<int64_t>(ps[x]) * a.rot, row, full(st));
+          }
+        }
+        alive = __shfl_sync(0xffffffffu, alive, 0);
+        if (!alive) break;
+      }
+    }
+    if (lane == 0) {
+      if (!alive && a.status != nullptr) atomicOr(a.status, PKV_DEV_WAIT_TIMEOUT);
+      for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)  // copies in flight land first
+        ptx::mbar_wait(full(i % stages), (i / stages) & 1u, kBulkWaitNs / 8);
+    }
+    return;
+  }
+  const int half = a.rot >> 1;
+  const int nturn = kInter ? a.rot / VEC : half / VEC;
+  const int units = nturn + (a.D - a.rot) / VEC;
+  int L = 1;  // lanes of a head
+  while (L < units && L < 32) L *= 2;
+  const uint32_t group = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
+  const int u0 = threadIdx.x & (L - 1), h0 = threadIdx.x / L, hstep = kBulkWarps * 32 / L;
+  auto turns = [&](int j) { return u0 + j * L < nturn; };
+  int at[NU];
+#pragma unroll
+  for (int j = 0; j < NU; ++j) {
+    const int u = u0 + j * L;
+    at[j] = u < nturn ? u * VEC : (u < units ? a.rot + (u - nturn) * VEC : a.D);
+  }
+  auto weight = [&](const void* w, int64_t d, float (&y)[VEC]) {
+    if (a.w_f32) {
+      const Pack<float, VEC> x = *reinterpret_cast<const Pack<float, VEC>*>(static_cast<const float*>(w) + d);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) y[i] = x.x[i];
+    } else {
+      const P x = *reinterpret_cast<const P*>(static_cast<const T*>(w) + d);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) y[i] = widen(x.x[i]);
+    }
+  };
+  uint32_t it = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += step, ++it) {
+    const uint32_t st = it % stages;
+    if (!__all_sync(0xffffffffu, ptx::mbar_wait(full(st), (it / stages) & 1u, kBulkWaitNs))) {
+      if (lane == 0 && a.status != nullptr) atomicOr(a.status, PKV_DEV_WAIT_TIMEOUT);
+      return;
+    }
+    const uint8_t* const stage = bulk_smem + st * sh.stage;
+    const int32_t slot = *reinterpret_cast<const int32_t*>(stage + sh.stage - 16);
+    const bool write = slot >= 0 && static_cast<int64_t>(slot) < static_cast<int64_t>(a.NB) * a.B;
+    const int32_t block = !write ? 0 : ((a.B & (a.B - 1)) == 0 ? slot >> (31 - __clz(a.B)) : slot / a.B);
+    const int64_t row0 =
+        (static_cast<int64_t>(block) * a.Hkv * a.B + (write ? slot - block * a.B : 0)) * a.D;
+    const int64_t head = static_cast<int64_t>(a.B) * a.D;
+    const float* const table = reinterpret_cast<const float*>(stage + sh.q + sh.k + sh.v);
+    float c[NU][kAng], s[NU][kAng];
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      if (!turns(j)) continue;
+      const int i0 = (u0 + j * L) * kAng;
+      if (a.axes == 1) {
+        const Pack<float, kAng> pc = *reinterpret_cast<const Pack<float, kAng>*>(table + i0);
+        const Pack<float, kAng> ps = *reinterpret_cast<const Pack<float, kAng>*>(table + half + i0);
+#pragma unroll
+        for (int i = 0; i < kAng; ++i) c[j][i] = pc.x[i], s[j][i] = ps.x[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kAng; ++i) {
+          const uint32_t x = (a.axis_bits[(i0 + i) >> 4] >> (2 * ((i0 + i) & 15))) & 3u;
+          c[j][i] = table[x * a.rot + i0 + i];
+          s[j][i] = table[x * a.rot + half + i0 + i];
+        }
+      }
+    }
+    const int heads = a.Hq + (write ? a.Hkv : 0);
+    for (int h = h0; h < heads; h += hstep) {  // q's heads, then k's: one behind the other
+      const bool is_q = h < a.Hq;
+      const int g = is_q ? h : h - a.Hq;
+      const T* const src = reinterpret_cast<const T*>(stage) + static_cast<int64_t>(h) * a.D;
+      const void* const w = is_q ? a.qw : a.kw;
+      const int64_t wd = a.per_head ? static_cast<int64_t>(g) * a.D : 0;
+      P x1[NU], x2[NU];
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        if (at[j] >= a.D) continue;
+        x1[j] = *reinterpret_cast<const P*>(src + at[j]);
+        if (!kInter && turns(j)) x2[j] = *reinterpret_cast<const P*>(src + at[j] + half);
+      }
+      float r = 1.f;
+      if (a.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+          if (at[j] >= a.D) continue;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x1[j].x[i]), widen(x1[j].x[i]), ss);
+          if (!kInter && turns(j)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x2[j].x[i]), widen(x2[j].x[i]), ss);
+          }
+        }
+        for (int o = L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+        r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(a.D)), a.eps));
+      }
+      T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + static_cast<int64_t>(g) * a.D;
+      Quotients by{};
+      if (kCodes != 0 && !is_q) by = quotients_by(__ldg(a.ks + g));
+      auto put = [&](int d, const float (&y)[VEC]) {
+        if (is_q) store_as<T, VEC>(qo + d, y);
+        else if constexpr (kCodes == 0) store_as<T, VEC>(static_cast<T*>(a.kc) + row0 + g * head + d, y);
+        else store_codes<kCodes, VEC>(static_cast<uint8_t*>(a.kc) + row0 + g * head + d, y, by);
+      };
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        if (at[j] >= a.D) continue;
+        float y1[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) y1[i] = widen(x1[j].x[i]);
+        if (a.norm) {
+          float w1[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) w1[i] = 1.f;
+          if (w != nullptr) weight(w, wd + at[j], w1);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) y1[i] = __fmul_rn(__fmul_rn(y1[i], r), w1[i]);
+        }
+        if (!turns(j)) {
+          if (!a.norm && (is_q || kCodes == 0)) {  // neither normed nor turned: its bits
+            T* const to = is_q ? qo : static_cast<T*>(a.kc) + row0 + g * head;
+            *reinterpret_cast<P*>(to + at[j]) = x1[j];
+          } else {
+            put(at[j], y1);
+          }
+          continue;
+        }
+        if constexpr (kInter) {
+          float z[VEC];
+#pragma unroll
+          for (int i = 0; i < kAng; ++i) {
+            const float p = y1[2 * i], q = y1[2 * i + 1];
+            z[2 * i] = __fsub_rn(__fmul_rn(p, c[j][i]), __fmul_rn(q, s[j][i]));
+            z[2 * i + 1] = __fadd_rn(__fmul_rn(q, c[j][i]), __fmul_rn(p, s[j][i]));
+          }
+          put(at[j], z);
+        } else {
+          float y2[VEC], z1[VEC], z2[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) y2[i] = widen(x2[j].x[i]);
+          if (a.norm) {
+            float w2[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w2[i] = 1.f;
+            if (w != nullptr) weight(w, wd + at[j] + half, w2);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y2[i] = __fmul_rn(__fmul_rn(y2[i], r), w2[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            z1[i] = __fsub_rn(__fmul_rn(y1[i], c[j][i]), __fmul_rn(y2[i], s[j][i]));
+            z2[i] = __fadd_rn(__fmul_rn(y2[i], c[j][i]), __fmul_rn(y1[i], s[j][i]));
+          }
+          put(at[j], z1);
+          put(at[j] + half, z2);
+        }
+      }
+    }
+    if constexpr (kCodes == 0) {  // V rows, copied
+      if (write) {
+        const uint4* const v = reinterpret_cast<const uint4*>(stage + sh.q + sh.k);
+        const int per = a.D * static_cast<int>(sizeof(T)) / 16;
+        for (int i = threadIdx.x; i < a.Hkv * per; i += kBulkWarps * 32) {
+          const int g = i / per;
+          reinterpret_cast<uint4*>(static_cast<T*>(a.vc) + row0 + g * head)[i - g * per] = v[i];
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty(st));
+  }
+}
+
+// V of 8-bit caches alone: the windows of rotary.cu's tokens, a.v_parts CTAs each.
+template <typename T, int kCodes>
+__global__ void __launch_bounds__(kNormThreads) v8_windows_kernel(const __grid_constant__ NormArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int window = blockIdx.x / a.v_parts, part = blockIdx.x - window * a.v_parts;
+  if (a.v_pairs) write_v8<T, true, kCodes>(a, window, part, a.v_parts);
+  else write_v8<T, false, kCodes>(a, window, part, a.v_parts);
+}
+
+// Stages of whole tokens, if three or more fit half of an SM's shared memory.
+template <typename T>
+bool bulk_shape(const NormArgs& a, bool values, BulkShape& sh) {
+  const int64_t q = static_cast<int64_t>(a.Hq) * a.D * sizeof(T);
+  const int64_t k = static_cast<int64_t>(a.Hkv) * a.D * sizeof(T);
+  const int64_t table = static_cast<int64_t>(a.axes) * a.rot * 4;
+  const int64_t stage = q + k + (values ? k : 0) + table + 16;
+  const int64_t room = 112 << 10;  // of the 227 KB, for two CTAs
+  if (stage * 3 > room || a.rot % 4 != 0) return false;
+  sh.q = static_cast<uint32_t>(q);
+  sh.k = static_cast<uint32_t>(k);
+  sh.v = static_cast<uint32_t>(values ? k : 0);
+  sh.table = static_cast<uint32_t>(table);
+  sh.stage = static_cast<uint32_t>(stage);
+  sh.stages = static_cast<int32_t>(std::min<int64_t>(kBulkStages, room / stage));
+  return true;
+}
+
+template <typename T, bool kInter, int kCodes>
+int launch_bulk(const NormArgs& a, const BulkShape& sh, int sms, cudaStream_t st) {
+  constexpr int NU = sizeof(T) == 4 ? 2 : 1;
+  static SmemOnce once;
+  const int rc = allow_dynamic_smem(
+      once, reinterpret_cast<const void*>(norm_rotary_bulk_kernel<T, kInter, kCodes, NU>), 112 << 10);
+  if (rc != PKV_OK) return rc;
+  const int64_t ctas = std::min<int64_t>(a.T, 2 * sms);
+  norm_rotary_bulk_kernel<T, kInter, kCodes, NU>
+      <<<static_cast<unsigned>(ctas), kBulkThreads, sh.stage * sh.stages, st>>>(a, sh);
+  PKV_CUDA(cudaGetLastError());
+  return PKV_OK;
+}
+
 int lanes_of(int units) {
   int l = 1;
   while (l < units && l < 32) l *= 2;
@@ -329,6 +633,21 @@ int launch_norm(NormArgs a, bool interleaved, cudaStream_t st) {
   int sms = 0, dev = 0;
   const int rc = device_sm_count(&sms, &dev);
   if (rc != PKV_OK) return rc;
+  BulkShape shape;
+  if (whole && strides && (aligned(a.qw, 16) && aligned(a.kw, 16)) && a.T >= kBulkTokens * sms &&
+      bulk_shape<T>(a, kCodes == 0, shape)) {
+    if constexpr (kCodes != 0) {  // V's windows: an item a thread if the window is one run
+      const int64_t windows = (static_cast<int64_t>(a.T) + 15) / 16;
+      const int64_t items = static_cast<int64_t>(a.Hkv) * a.D / 2;
+      a.v_parts = static_cast<int32_t>((items + kNormThreads - 1) / kNormThreads);
+      PKV_REQUIRE(windows * a.v_parts < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED, "too many tokens");
+      v8_windows_kernel<T, kCodes>
+          <<<static_cast<unsigned>(windows * a.v_parts), kNormThreads, 0, st>>>(a);
+      PKV_CUDA(cudaGetLastError());
+    }
+    return interleaved ? launch_bulk<T, true, kCodes>(a, shape, sms, st)
+                       : launch_bulk<T, false, kCodes>(a, shape, sms, st);
+  }
   // few tokens: their heads are spread over more CTAs until the SMs have a few each
   int split = 1;
   while (split * rows < a.Hq && static_cast<int64_t>(a.T) * split < 4 * sms) split *= 2;

@@ -204,6 +204,57 @@ def test_token_counts(T):
     Case(T, 8, 2, 128, 128, "bf16", fused=True, A=3).check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot,A", [(64, 64, 1), (128, 64, 2), (256, 256, 1), (96, 32, 4), (8, 8, 1)])
+@pytest.mark.parametrize("weight,per_head", [("same", False), ("f32", True), (None, False)])
+def test_many_tokens(dtype, inter, D, rot, A, weight, per_head):
+    """Enough tokens for whole ones to be fetched ahead."""
+    if D * DT[dtype].itemsize % 16:
+        pytest.skip("rows of whole 16 bytes")
+    Case(1300, 6, 2, D, rot, dtype, inter=inter, A=A, weight=weight, per_head=per_head).check()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("inter,A", [(False, 3), (True, 1)])
+def test_many_tokens_8_bit(kind, dtype, inter, A):
+    Case(1500, 4, 3, 128, 64, dtype, kind=kind, inter=inter, fused=True, A=A).check()
+
+
+def test_many_tokens_of_large_rows():
+    """Rows that leave no room for three tokens, and just some."""
+    Case(700, 128, 8, 256, 256, "bf16").check()
+    Case(700, 32, 8, 128, 128, "f32").check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("eps", [None, 1e-5])
+def test_a_tokens_bits_do_not_depend_on_how_many_come(dtype, inter, eps):
+    """The same tokens in one call and by few at a time, and out of tensors at odd places."""
+    c = Case(1000, 6, 2, 128, 64, dtype, inter=inter, eps=eps, A=2)
+    c.call()
+    q, kc, vc = c.q_out.clone(), c.kc.clone(), c.vc.clone()
+    whole = c.q, c.k, c.v, c.q_out, c.pos, c.slots
+    c.kc.fill_(7.0)
+    c.vc.fill_(7.0)
+    c.q_out.zero_()
+    for a in range(0, 1000, 300):
+        c.q, c.k, c.v, c.q_out = (x[a:a + 300] for x in whole[:4])
+        c.pos, c.slots = whole[4][:, a:a + 300], whole[5][a:a + 300]
+        c.call()
+    assert torch.equal(whole[3], q) and torch.equal(c.kc, kc) and torch.equal(c.vc, vc)
+    c.q, c.k, c.v, c.q_out, c.pos, c.slots = whole
+    odd = torch.zeros((1000, 6 * 128 + 2), dtype=c.dt, device="cuda")[:, 2:].unflatten(1, (6, 128))
+    odd.copy_(c.q)
+    c.q = odd
+    c.kc.fill_(7.0)
+    c.q_out.zero_()
+    c.call()
+    assert torch.equal(c.q_out, q) and torch.equal(c.kc, kc)
+
+
 @pytest.mark.parametrize("B", [1, 5, 8, 32])
 def test_block_sizes(B):
     Case(70, 4, 2, 64, 64, "f16", B=B).check()
