@@ -763,8 +763,9 @@ int pkv_evict_gather(void* k_cache, void* v_cache, const int32_t* block_tables,
  * one to four axes: for each head x of q and of k
  *   y_d = (x_d * r) * w_d,   r = 1 / sqrt(sum_e x_e^2 / head_dim + eps),
  * then its pairs are turned, pair i by the table's row at the token's position on axis
- * pair_axes[i]; v as it is.  fp32, each operation rounded once, one rounding to dtype (or
- * one quantisation from fp32) at the end.
+ * pair_axes[i]; v as it is.  fp32 (without a norm the operations and bits of
+ * pkv_rotary_write), one rounding to dtype or one quantisation from fp32 at the end.  A token's
+ * bits depend neither on its tensors' alignment nor on the other tokens of the call.
  * codes         0 (caches of dtype), PKV_FP8_E4M3 or PKV_INT8 (k_scale and v_scale only
  *               there; layouts and quantisation as pkv_kv_write_fp8 / _int8).
  * q_weight, k_weight  device, [head_dim], or with weight_per_head [num_heads, head_dim],

@@ -7,11 +7,14 @@
 // of the table at the token's position on the pair's axis.  q goes to q_out, k and v to their
 // slots, so q, k and v are read once and nothing between is written.
 //
-// Arithmetic: fp32, each product and sum rounded once (squares are added as they are formed;
-// the reciprocal square root is one rounding), then one rounding to the type, or one
-// quantisation straight from fp32.  A head's squares are summed in an order that depends on its
-// layout alone (D, rotary_dim, pairing, type), so a token's bits do not depend on strides or
-// alignment.
+// Arithmetic: fp32; squares are added as they are formed, the mean is a product with 1 / D, the
+// root an approximate one corrected by a Newton step, the two products of the norm are rounded
+// each, and of a turn (x1 c - x2 s) the second product is rounded, the first and the sum together.
+// (Without a norm each product and sum is rounded by itself: the bits of rotary.cu.)  Then one
+// rounding to the type, or one quantisation straight from fp32.  Two elements go through packed
+// instructions where a lane has them, which round as single ones do.  A head's squares are
+// summed in an order that depends on its layout alone (D, rotary_dim, pairing, type), so a token's
+// bits depend neither on strides or alignment nor on how many tokens come with it.
 //
 // A group of up to 32 lanes takes a head: a lane's pieces of 16 bytes (both halves' ones of a
 // turned pair), the sum of squares by shuffles; then the next head with the cos, sin and
@@ -33,12 +36,12 @@ namespace {
 
 constexpr int kMaxAxes = 4;
 constexpr int kNormThreads = 128;
-constexpr int kBulkTokens = 4;  // tokens an SM from which on whole tokens are fetched
+constexpr int kBulkTokens = 6;  // tokens an SM from which on whole tokens are fetched
 
 struct NormArgs : RotaryArgs {
   const void* qw;  // weights [D] or [heads, D], or NULL: ones
   const void* kw;
-  float eps;
+  float eps, inv_d;
   int32_t norm, axes, per_head, w_f32;
   int32_t wide, w_wide, v_pairs;  // addresses that allow 16 bytes (or a pair) at once
   uint32_t axis_bits[kMaxRotaryPairs / 16];  // two bits a pair
@@ -66,6 +69,105 @@ __device__ __forceinline__ void store_piece(T* p, const float (&y)[N], bool wide
   }
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Squares of a piece added to (even, odd) elements' sums.
+template <int VEC>
+__device__ __forceinline__ void add_squares(const float (&x)[VEC], float& even, float& odd) {
+  if constexpr (VEC == 1) {
+    even = __fmaf_rn(x[0], x[0], even);
+  } else {
+    uint64_t sum = ptx::pair(even, odd);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const uint64_t p = ptx::pair(x[i], x[i + 1]);
+      sum = ptx::fma2(p, p, sum);
+    }
+    ptx::unpair(sum, even, odd);
+  }
+}
+
+// 1 / sqrt(sum / D + eps).
+__device__ __forceinline__ float inverse_root(float sum, float inv_d, float eps) {
+  const float m = __fmaf_rn(sum, inv_d, eps);
+  const float y = rsqrtf(m);
+  if (!(m >= 0x1p-100f && m <= 0x1p100f)) return __frsqrt_rn(m);  // the step's squares need room
+  const float e = __fmaf_rn(__fmul_rn(m, y), -y, 1.f);
+  return __fmaf_rn(__fmul_rn(0.5f, y), e, y);
+}
+
+// x = (x * r) * w.
+template <int VEC>
+__device__ __forceinline__ void apply_norm(float (&x)[VEC], float r, const float (&w)[VEC]) {
+  if constexpr (VEC == 1) {
+    x[0] = __fmul_rn(__fmul_rn(x[0], r), w[0]);
+  } else {
+    const uint64_t rr = ptx::pair(r, r);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2)
+      ptx::unpair(mul2(mul2(ptx::pair(x[i], x[i + 1]), rr), ptx::pair(w[i], w[i + 1])), x[i], x[i + 1]);
+  }
+}
+
+// z1 = a c - b s, z2 = b c + a s for N pairs.  fused: the first product and the sum together.
+template <int N>
+__device__ __forceinline__ void turn_pairs(const float (&a)[N], const float (&b)[N],
+                                           const float (&c)[N], const float (&s)[N], bool fused,
+                                           float (&z1)[N], float (&z2)[N]) {
+  if (!fused) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      z1[i] = __fsub_rn(__fmul_rn(a[i], c[i]), __fmul_rn(b[i], s[i]));
+      z2[i] = __fadd_rn(__fmul_rn(b[i], c[i]), __fmul_rn(a[i], s[i]));
+    }
+  } else if constexpr (N == 1) {
+    z1[0] = __fmaf_rn(a[0], c[0], __fmul_rn(b[0], -s[0]));
+    z2[0] = __fmaf_rn(b[0], c[0], __fmul_rn(a[0], s[0]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t pa = ptx::pair(a[i], a[i + 1]), pb = ptx::pair(b[i], b[i + 1]);
+      const uint64_t pc = ptx::pair(c[i], c[i + 1]);
+      ptx::unpair(ptx::fma2(pa, pc, mul2(pb, ptx::pair(-s[i], -s[i + 1]))), z1[i], z1[i + 1]);
+      ptx::unpair(ptx::fma2(pb, pc, mul2(pa, ptx::pair(s[i], s[i + 1]))), z2[i], z2[i + 1]);
+    }
+  }
+}
+
+// A piece of a head normed (x1, x2 its halves' ones) and turned: f(0, z1) and, half layout,
+// f(half, z2).
+template <int VEC, bool kInter, typename F>
+__device__ __forceinline__ void turn_piece(const float (&x1)[VEC], const float (&x2)[VEC],
+                                           const float (&c)[kInter ? VEC / 2 : VEC],
+                                           const float (&s)[kInter ? VEC / 2 : VEC], bool fused,
+                                           int half, F f) {
+  if constexpr (kInter) {
+    constexpr int N = VEC / 2;
+    float a[N], b[N], z1[N], z2[N], z[VEC];
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = x1[2 * i], b[i] = x1[2 * i + 1];
+    turn_pairs<N>(a, b, c, s, fused, z1, z2);
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[2 * i] = z1[i], z[2 * i + 1] = z2[i];
+    f(0, z);
+  } else {
+    float z1[VEC], z2[VEC];
+    turn_pairs<VEC>(x1, x2, c, s, fused, z1, z2);
+    f(0, z1);
+    f(half, z2);
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void widen_piece(const Pack<T, VEC>& p, float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) x[i] = widen(p.x[i]);
+}
+
 // A lane's pieces of one head.
 template <typename T, int VEC, int NU>
 struct Pieces {
@@ -73,9 +175,13 @@ struct Pieces {
 };
 
 // blockIdx.x < T: a token, its heads split over gridDim.y CTAs and the CTA's groups of lanes;
-// 8-bit caches: then V's windows, a.v_parts CTAs each.
+// 8-bit caches: then V's windows, a.v_parts CTAs each.  Bound by the instructions of a head and by
+// how many warps hide its loads: 4,099 tokens of 32 + 8 heads of 128 into fp8, interleaved,
+// 37.8 us with eight CTAs an SM and two heads in flight, 42.3 with six, 43.1 with ten (spills);
+// the half layout holds a piece more and wants six (1,000 tokens of 64 + 8 heads 10.1 against
+// 11.4).  Loading a token's first rows ahead of its position was no gain (46).
 template <typename T, int VEC, bool kInter, int kCodes, int NU>
-__global__ void __launch_bounds__(kNormThreads, 5)
+__global__ void __launch_bounds__(kNormThreads, kInter ? 8 : 6)
     norm_rotary_kernel(const __grid_constant__ NormArgs a) {
   // as rotary_write_kernel: a launch queued behind reads and writes nothing of this one's
   // before this grid has completed
@@ -123,7 +229,11 @@ __global__ void __launch_bounds__(kNormThreads, 5)
   for (int j = 0; j < NU; ++j) {
     const int u = threadIdx.x + j * L;
     at[j] = u < nturn ? u * VEC : (u < units ? a.rot + (u - nturn) * VEC : a.D);
-    if (u >= nturn) continue;
+    if (u >= nturn) {
+#pragma unroll
+      for (int i = 0; i < kAng; ++i) c[j][i] = s[j][i] = 0.f;  // (not used)
+      continue;
+    }
     const int i0 = u * kAng;
     if (a.axes == 1) {
       const float* const row = a.table + static_cast<int64_t>(pos[0]) * a.rot + i0;
@@ -193,58 +303,49 @@ __global__ void __launch_bounds__(kNormThreads, 5)
   auto work = [&](const Own& x, auto put) {
     float r = 1.f;
     if (a.norm) {
-      float ss = 0.f;
+      float even = 0.f, odd = 0.f;
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
         if (at[j] >= a.D) continue;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x.one[j].x[i]), widen(x.one[j].x[i]), ss);
+        float y[VEC];
+        widen_piece(x.one[j], y);
+        add_squares<VEC>(y, even, odd);
         if (!kInter && turns(j)) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x.two[j].x[i]), widen(x.two[j].x[i]), ss);
+          widen_piece(x.two[j], y);
+          add_squares<VEC>(y, even, odd);
         }
       }
-      for (int o = L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-      r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(a.D)), a.eps));
+      float sum = __fadd_rn(even, odd);
+      for (int o = L >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
+      r = inverse_root(sum, a.inv_d, a.eps);
     }
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       if (at[j] >= a.D) continue;
-      float x1[VEC];
+      float x1[VEC], x2[VEC] = {};
+      widen_piece(x.one[j], x1);
+      if (a.norm) apply_norm<VEC>(x1, r, w1[j]);
+      if constexpr (kInter) {  // lanes that turn and lanes that don't side by side
+        turn_piece<VEC, true>(x1, x2, c[j], s[j], a.norm != 0, half,
+                              [&](int, const float (&z)[VEC]) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        x1[i] = widen(x.one[j].x[i]);
-        if (a.norm) x1[i] = __fmul_rn(__fmul_rn(x1[i], r), w1[j][i]);
+                                for (int i = 0; i < VEC; ++i) x1[i] = turns(j) ? z[i] : x1[i];
+                              });
+        put(j, at[j], x1);
+        continue;
       }
       if (!turns(j)) {
         put(j, at[j], x1);
         continue;
       }
-      float y1[VEC];
-      if constexpr (kInter) {
-#pragma unroll
-        for (int i = 0; i < kAng; ++i) {
-          const float p = x1[2 * i], q = x1[2 * i + 1];
-          y1[2 * i] = __fsub_rn(__fmul_rn(p, c[j][i]), __fmul_rn(q, s[j][i]));
-          y1[2 * i + 1] = __fadd_rn(__fmul_rn(q, c[j][i]), __fmul_rn(p, s[j][i]));
-        }
-        put(j, at[j], y1);
-      } else {
-        float x2[VEC], y2[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          x2[i] = widen(x.two[j].x[i]);
-          if (a.norm) x2[i] = __fmul_rn(__fmul_rn(x2[i], r), w2[j][i]);
-          y1[i] = __fsub_rn(__fmul_rn(x1[i], c[j][i]), __fmul_rn(x2[i], s[j][i]));
-          y2[i] = __fadd_rn(__fmul_rn(x2[i], c[j][i]), __fmul_rn(x1[i], s[j][i]));
-        }
-        put(j, at[j], y1);
-        put(j, at[j] + half, y2);
-      }
+      widen_piece(x.two[j], x2);
+      if (a.norm) apply_norm<VEC>(x2, r, w2[j]);
+      turn_piece<VEC, kInter>(x1, x2, c[j], s[j], a.norm != 0, half,
+                              [&](int d, const float (&z)[VEC]) { put(j, at[j] + d, z); });
     }
   };
   const int h0 = threadIdx.y + blockDim.y * blockIdx.y, step = blockDim.y * gridDim.y;
-  constexpr int U = NU > 1 ? 1 : (kInter ? 4 : 2);  // heads whose loads go out together
+  constexpr int U = NU == 1 && kInter ? 2 : 1;  // heads whose loads go out together
   auto each = [&](const T* src, int H, auto put) {
     for (int h = h0; h < H; h += U * step) {
       Own x[U];
@@ -309,23 +410,28 @@ __global__ void __launch_bounds__(kNormThreads, 5)
 // ---- many tokens: rows of whole tokens by bulk copies ------------------------------------------
 // One warp fetches: the rows of a token's q, k and v and its rows of the table go to a stage of
 // shared memory by cp.async.bulk, several tokens ahead, so that neither positions nor tables nor
-// rows are waited for.  Eight warps norm, turn and write a stage's heads; the lanes of a head, and
-// so its bits, are those of the kernel above.
-constexpr int kBulkWarps = 8;
+// rows are waited for.  Seven warps norm, turn and write a stage's heads (with the eighth a CTA of
+// 256 threads: two on an SM leave a thread 128 registers; eight and one spilled, and took 127 us
+// where this takes 112); the lanes of a head, and so its bits, are those of the kernel above.
+// Measured against it: 8,191 tokens of 40 + 40 heads of 128 on three axes 112 us (4.5 TB/s) to
+// 148, on one 107 to 134, without a norm 84 to 115; of 64 + 8 heads 1,000 tokens 15.9 to 17.6,
+// 640 tokens 12.3 to 10.1, hence six tokens an SM.  8-bit caches, 32-bit types (121 to 108) and a
+// weight for each head (56 to 46) stay with the kernel above.
+constexpr int kBulkWarps = 7;
 constexpr int kBulkThreads = (kBulkWarps + 1) * 32;
 constexpr int kBulkStages = 8;                 // at most
 constexpr uint64_t kBulkWaitNs = 1000000000ull;  // 1 s per wait before giving up
 
 struct BulkShape {
-  uint32_t q, k, v, table, stage;  // bytes of a stage's parts and of a stage (with 16 for the slot)
+  uint32_t q, k, stage;  // bytes of a token's q and k (and v), and of a stage (16 for the slot)
   int32_t stages;
 };
 
-template <typename T, bool kInter, int kCodes, int NU>
+template <typename T, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kBulkThreads, 2)
     norm_rotary_bulk_kernel(const __grid_constant__ NormArgs a, const BulkShape sh) {
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int VEC = 16 / sizeof(T);
+  constexpr int VEC = 8;  // of 16-bit types
   constexpr int kAng = kInter ? VEC / 2 : VEC;
   using P = Pack<T, VEC>;
   extern __shared__ __align__(128) uint8_t bulk_smem[];
@@ -376,17 +482,16 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
             const uint32_t at = ptx::smem_addr(stage);
             *reinterpret_cast<int32_t*>(stage + sh.stage - 16) = sl;
             const uint32_t row = static_cast<uint32_t>(a.rot) * 4;
-            ptx::mbar_arrive_expect_tx(full(st), sh.q + sh.k + sh.v + row * a.axes);
+            ptx::mbar_arrive_expect_tx(full(st), sh.q + 2 * sh.k + row * a.axes);
             const int64_t tok = t0 + l * step;
             ptx::bulk_load(at, static_cast<const T*>(a.q) + tok * a.q_stride, sh.q, full(st));
             ptx::bulk_load(at + sh.q, static_cast<const T*>(a.k) + tok * a.k_stride, sh.k, full(st));
-            if constexpr (kCodes == 0)
-              ptx::bulk_load(at + sh.q + sh.k, static_cast<const T*>(a.v) + tok * a.v_stride, sh.v,
-                             full(st));
+            ptx::bulk_load(at + sh.q + sh.k, static_cast<const T*>(a.v) + tok * a.v_stride, sh.k,
+                           full(st));
 #pragma unroll
             for (int x = 0; x < kMaxAxes; ++x)
               if (x < a.axes)
-                ptx::bulk_load(at + sh.q + sh.k + sh.v + x * row,
+                ptx::bulk_load(at + sh.q + 2 * sh.k + x * row,
                                a.table + static_cast<int64_t>(ps[x]) * a.rot, row, full(st));
           }
         }
@@ -403,27 +508,20 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
   }
   const int half = a.rot >> 1;
   const int nturn = kInter ? a.rot / VEC : half / VEC;
-  const int units = nturn + (a.D - a.rot) / VEC;
+  const int units = nturn + (a.D - a.rot) / VEC;  // at most 32
   int L = 1;  // lanes of a head
-  while (L < units && L < 32) L *= 2;
+  while (L < units) L *= 2;
   const uint32_t group = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
-  const int u0 = threadIdx.x & (L - 1), h0 = threadIdx.x / L, hstep = kBulkWarps * 32 / L;
-  auto turns = [&](int j) { return u0 + j * L < nturn; };
-  int at[NU];
-#pragma unroll
-  for (int j = 0; j < NU; ++j) {
-    const int u = u0 + j * L;
-    at[j] = u < nturn ? u * VEC : (u < units ? a.rot + (u - nturn) * VEC : a.D);
-  }
-  auto weight = [&](const void* w, int64_t d, float (&y)[VEC]) {
+  const int u = threadIdx.x & (L - 1), h0 = threadIdx.x / L, hstep = kBulkWarps * 32 / L;
+  const bool turns = u < nturn, mine = u < units;
+  const int at = turns ? u * VEC : a.rot + (u - nturn) * VEC;  // the lane's piece
+  auto weight = [&](const void* w, int d, float (&y)[VEC]) {
     if (a.w_f32) {
       const Pack<float, VEC> x = *reinterpret_cast<const Pack<float, VEC>*>(static_cast<const float*>(w) + d);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) y[i] = x.x[i];
     } else {
-      const P x = *reinterpret_cast<const P*>(static_cast<const T*>(w) + d);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) y[i] = widen(x.x[i]);
+      widen_piece(*reinterpret_cast<const P*>(static_cast<const T*>(w) + d), y);
     }
   };
   uint32_t it = 0;
@@ -440,126 +538,79 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
     const int64_t row0 =
         (static_cast<int64_t>(block) * a.Hkv * a.B + (write ? slot - block * a.B : 0)) * a.D;
     const int64_t head = static_cast<int64_t>(a.B) * a.D;
-    const float* const table = reinterpret_cast<const float*>(stage + sh.q + sh.k + sh.v);
-    float c[NU][kAng], s[NU][kAng];
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      if (!turns(j)) continue;
-      const int i0 = (u0 + j * L) * kAng;
+    const float* const table = reinterpret_cast<const float*>(stage + sh.q + 2 * sh.k);
+    float c[kAng], s[kAng];
+    if (turns) {
+      const int i0 = u * kAng;
       if (a.axes == 1) {
         const Pack<float, kAng> pc = *reinterpret_cast<const Pack<float, kAng>*>(table + i0);
         const Pack<float, kAng> ps = *reinterpret_cast<const Pack<float, kAng>*>(table + half + i0);
 #pragma unroll
-        for (int i = 0; i < kAng; ++i) c[j][i] = pc.x[i], s[j][i] = ps.x[i];
+        for (int i = 0; i < kAng; ++i) c[i] = pc.x[i], s[i] = ps.x[i];
       } else {
 #pragma unroll
         for (int i = 0; i < kAng; ++i) {
           const uint32_t x = (a.axis_bits[(i0 + i) >> 4] >> (2 * ((i0 + i) & 15))) & 3u;
-          c[j][i] = table[x * a.rot + i0 + i];
-          s[j][i] = table[x * a.rot + half + i0 + i];
+          c[i] = table[x * a.rot + i0 + i];
+          s[i] = table[x * a.rot + half + i0 + i];
         }
       }
     }
-    const int heads = a.Hq + (write ? a.Hkv : 0);
-    for (int h = h0; h < heads; h += hstep) {  // q's heads, then k's: one behind the other
-      const bool is_q = h < a.Hq;
-      const int g = is_q ? h : h - a.Hq;
-      const T* const src = reinterpret_cast<const T*>(stage) + static_cast<int64_t>(h) * a.D;
-      const void* const w = is_q ? a.qw : a.kw;
-      const int64_t wd = a.per_head ? static_cast<int64_t>(g) * a.D : 0;
-      P x1[NU], x2[NU];
+    auto some_heads = [&](const T* src, int H, T* dst, int64_t apart, const void* w) {
+      float w1[VEC], w2[VEC];  // (loaded once a token for all heads; they stay in L1)
 #pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        if (at[j] >= a.D) continue;
-        x1[j] = *reinterpret_cast<const P*>(src + at[j]);
-        if (!kInter && turns(j)) x2[j] = *reinterpret_cast<const P*>(src + at[j] + half);
+      for (int i = 0; i < VEC; ++i) w1[i] = w2[i] = 1.f;
+      if (kNorm && w != nullptr && mine) {
+        weight(w, at, w1);
+        if (!kInter && turns) weight(w, at + half, w2);
       }
-      float r = 1.f;
-      if (a.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          if (at[j] >= a.D) continue;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x1[j].x[i]), widen(x1[j].x[i]), ss);
-          if (!kInter && turns(j)) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) ss = fmaf(widen(x2[j].x[i]), widen(x2[j].x[i]), ss);
+      for (int h = h0; h < H; h += hstep) {
+        const T* const from = src + static_cast<int64_t>(h) * a.D;
+        T* const to = dst + h * apart;
+        P p1, p2;
+        float x1[VEC], x2[VEC] = {};
+        if (mine) {
+          p1 = *reinterpret_cast<const P*>(from + at);
+          widen_piece(p1, x1);
+          if (!kInter && turns) {
+            p2 = *reinterpret_cast<const P*>(from + at + half);
+            widen_piece(p2, x2);
           }
         }
-        for (int o = L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-        r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(a.D)), a.eps));
+        if constexpr (kNorm) {
+          float even = 0.f, odd = 0.f;
+          if (mine) {
+            add_squares<VEC>(x1, even, odd);
+            if (!kInter && turns) add_squares<VEC>(x2, even, odd);
+          }
+          float sum = __fadd_rn(even, odd);
+          for (int o = L >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
+          const float r = inverse_root(sum, a.inv_d, a.eps);
+          if (mine) {
+            apply_norm<VEC>(x1, r, w1);
+            if (!kInter && turns) apply_norm<VEC>(x2, r, w2);
+          }
+        }
+        if (!mine) continue;
+        if (turns)
+          turn_piece<VEC, kInter>(x1, x2, c, s, kNorm, half,
+                                  [&](int d, const float (&z)[VEC]) { store_as<T, VEC>(to + at + d, z); });
+        else if (kNorm)
+          store_as<T, VEC>(to + at, x1);
+        else  // neither normed nor turned: its bits
+          *reinterpret_cast<P*>(to + at) = p1;
       }
-      T* const qo = static_cast<T*>(a.q_out) + t * a.qo_stride + static_cast<int64_t>(g) * a.D;
-      Quotients by{};
-      if (kCodes != 0 && !is_q) by = quotients_by(__ldg(a.ks + g));
-      auto put = [&](int d, const float (&y)[VEC]) {
-        if (is_q) store_as<T, VEC>(qo + d, y);
-        else if constexpr (kCodes == 0) store_as<T, VEC>(static_cast<T*>(a.kc) + row0 + g * head + d, y);
-        else store_codes<kCodes, VEC>(static_cast<uint8_t*>(a.kc) + row0 + g * head + d, y, by);
-      };
-#pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        if (at[j] >= a.D) continue;
-        float y1[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y1[i] = widen(x1[j].x[i]);
-        if (a.norm) {
-          float w1[VEC];
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) w1[i] = 1.f;
-          if (w != nullptr) weight(w, wd + at[j], w1);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) y1[i] = __fmul_rn(__fmul_rn(y1[i], r), w1[i]);
-        }
-        if (!turns(j)) {
-          if (!a.norm && (is_q || kCodes == 0)) {  // neither normed nor turned: its bits
-            T* const to = is_q ? qo : static_cast<T*>(a.kc) + row0 + g * head;
-            *reinterpret_cast<P*>(to + at[j]) = x1[j];
-          } else {
-            put(at[j], y1);
-          }
-          continue;
-        }
-        if constexpr (kInter) {
-          float z[VEC];
-#pragma unroll
-          for (int i = 0; i < kAng; ++i) {
-            const float p = y1[2 * i], q = y1[2 * i + 1];
-            z[2 * i] = __fsub_rn(__fmul_rn(p, c[j][i]), __fmul_rn(q, s[j][i]));
-            z[2 * i + 1] = __fadd_rn(__fmul_rn(q, c[j][i]), __fmul_rn(p, s[j][i]));
-          }
-          put(at[j], z);
-        } else {
-          float y2[VEC], z1[VEC], z2[VEC];
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) y2[i] = widen(x2[j].x[i]);
-          if (a.norm) {
-            float w2[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) w2[i] = 1.f;
-            if (w != nullptr) weight(w, wd + at[j] + half, w2);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) y2[i] = __fmul_rn(__fmul_rn(y2[i], r), w2[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            z1[i] = __fsub_rn(__fmul_rn(y1[i], c[j][i]), __fmul_rn(y2[i], s[j][i]));
-            z2[i] = __fadd_rn(__fmul_rn(y2[i], c[j][i]), __fmul_rn(y1[i], s[j][i]));
-          }
-          put(at[j], z1);
-          put(at[j] + half, z2);
-        }
-      }
-    }
-    if constexpr (kCodes == 0) {  // V rows, copied
-      if (write) {
-        const uint4* const v = reinterpret_cast<const uint4*>(stage + sh.q + sh.k);
-        const int per = a.D * static_cast<int>(sizeof(T)) / 16;
-        for (int i = threadIdx.x; i < a.Hkv * per; i += kBulkWarps * 32) {
-          const int g = i / per;
-          reinterpret_cast<uint4*>(static_cast<T*>(a.vc) + row0 + g * head)[i - g * per] = v[i];
-        }
+    };
+    some_heads(reinterpret_cast<const T*>(stage), a.Hq, static_cast<T*>(a.q_out) + t * a.qo_stride,
+               a.D, a.qw);
+    if (write) {
+      some_heads(reinterpret_cast<const T*>(stage + sh.q), a.Hkv, static_cast<T*>(a.kc) + row0, head,
+                 a.kw);
+      const uint4* const v = reinterpret_cast<const uint4*>(stage + sh.q + sh.k);  // copied
+      const int per = a.D * static_cast<int>(sizeof(T)) / 16;
+      for (int i = threadIdx.x; i < a.Hkv * per; i += kBulkWarps * 32) {
+        const int g = i / per;
+        reinterpret_cast<uint4*>(static_cast<T*>(a.vc) + row0 + g * head)[i - g * per] = v[i];
       }
     }
     __syncwarp();
@@ -567,42 +618,27 @@ __global__ void __launch_bounds__(kBulkThreads, 2)
   }
 }
 
-// V of 8-bit caches alone: the windows of rotary.cu's tokens, a.v_parts CTAs each.
-template <typename T, int kCodes>
-__global__ void __launch_bounds__(kNormThreads) v8_windows_kernel(const __grid_constant__ NormArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int window = blockIdx.x / a.v_parts, part = blockIdx.x - window * a.v_parts;
-  if (a.v_pairs) write_v8<T, true, kCodes>(a, window, part, a.v_parts);
-  else write_v8<T, false, kCodes>(a, window, part, a.v_parts);
-}
-
 // Stages of whole tokens, if three or more fit half of an SM's shared memory.
-template <typename T>
-bool bulk_shape(const NormArgs& a, bool values, BulkShape& sh) {
-  const int64_t q = static_cast<int64_t>(a.Hq) * a.D * sizeof(T);
-  const int64_t k = static_cast<int64_t>(a.Hkv) * a.D * sizeof(T);
-  const int64_t table = static_cast<int64_t>(a.axes) * a.rot * 4;
-  const int64_t stage = q + k + (values ? k : 0) + table + 16;
+bool bulk_shape(const NormArgs& a, BulkShape& sh) {
+  const int64_t q = static_cast<int64_t>(a.Hq) * a.D * 2, k = static_cast<int64_t>(a.Hkv) * a.D * 2;
+  const int64_t stage = q + 2 * k + static_cast<int64_t>(a.axes) * a.rot * 4 + 16;
   const int64_t room = 112 << 10;  // of the 227 KB, for two CTAs
-  if (stage * 3 > room || a.rot % 4 != 0) return false;
+  if (stage * 3 > room) return false;
   sh.q = static_cast<uint32_t>(q);
   sh.k = static_cast<uint32_t>(k);
-  sh.v = static_cast<uint32_t>(values ? k : 0);
-  sh.table = static_cast<uint32_t>(table);
   sh.stage = static_cast<uint32_t>(stage);
   sh.stages = static_cast<int32_t>(std::min<int64_t>(kBulkStages, room / stage));
   return true;
 }
 
-template <typename T, bool kInter, int kCodes>
+template <typename T, bool kInter, bool kNorm>
 int launch_bulk(const NormArgs& a, const BulkShape& sh, int sms, cudaStream_t st) {
-  constexpr int NU = sizeof(T) == 4 ? 2 : 1;
   static SmemOnce once;
   const int rc = allow_dynamic_smem(
-      once, reinterpret_cast<const void*>(norm_rotary_bulk_kernel<T, kInter, kCodes, NU>), 112 << 10);
+      once, reinterpret_cast<const void*>(norm_rotary_bulk_kernel<T, kInter, kNorm>), 112 << 10);
   if (rc != PKV_OK) return rc;
   const int64_t ctas = std::min<int64_t>(a.T, 2 * sms);
-  norm_rotary_bulk_kernel<T, kInter, kCodes, NU>
+  norm_rotary_bulk_kernel<T, kInter, kNorm>
       <<<static_cast<unsigned>(ctas), kBulkThreads, sh.stage * sh.stages, st>>>(a, sh);
   PKV_CUDA(cudaGetLastError());
   return PKV_OK;
@@ -633,20 +669,16 @@ int launch_norm(NormArgs a, bool interleaved, cudaStream_t st) {
   int sms = 0, dev = 0;
   const int rc = device_sm_count(&sms, &dev);
   if (rc != PKV_OK) return rc;
-  BulkShape shape;
-  if (whole && strides && (aligned(a.qw, 16) && aligned(a.kw, 16)) && a.T >= kBulkTokens * sms &&
-      bulk_shape<T>(a, kCodes == 0, shape)) {
-    if constexpr (kCodes != 0) {  // V's windows: an item a thread if the window is one run
-      const int64_t windows = (static_cast<int64_t>(a.T) + 15) / 16;
-      const int64_t items = static_cast<int64_t>(a.Hkv) * a.D / 2;
-      a.v_parts = static_cast<int32_t>((items + kNormThreads - 1) / kNormThreads);
-      PKV_REQUIRE(windows * a.v_parts < (int64_t(1) << 31), PKV_ERR_UNSUPPORTED, "too many tokens");
-      v8_windows_kernel<T, kCodes>
-          <<<static_cast<unsigned>(windows * a.v_parts), kNormThreads, 0, st>>>(a);
-      PKV_CUDA(cudaGetLastError());
+  if constexpr (kCodes == 0 && sizeof(T) == 2) {
+    BulkShape shape;
+    if (whole && strides && a.w_wide && !a.per_head && a.T >= kBulkTokens * sms &&
+        bulk_shape(a, shape)) {
+      if (interleaved)
+        return a.norm ? launch_bulk<T, true, true>(a, shape, sms, st)
+                      : launch_bulk<T, true, false>(a, shape, sms, st);
+      return a.norm ? launch_bulk<T, false, true>(a, shape, sms, st)
+                    : launch_bulk<T, false, false>(a, shape, sms, st);
     }
-    return interleaved ? launch_bulk<T, true, kCodes>(a, shape, sms, st)
-                       : launch_bulk<T, false, kCodes>(a, shape, sms, st);
   }
   // few tokens: their heads are spread over more CTAs until the SMs have a few each
   int split = 1;
@@ -713,6 +745,7 @@ extern "C" int pkv_norm_rotary_write(
   a.qw = q_weight;
   a.kw = k_weight;
   a.eps = eps;
+  a.inv_d = 1.f / static_cast<float>(head_dim);
   a.norm = norm;
   a.axes = num_axes;
   a.per_head = weight_per_head != 0;

@@ -1,8 +1,9 @@
 """GPU parity of the norm, rotation and cache write in one pass.
 
 Bound of an element (u = 2^-24): the sum of D squares is off by at most (D + 1) u relative, the
-mean, eps, and the reciprocal root by u each, half of the sum's error reaching the root; the two
-products of the norm add u each: a normed value is off by ((D + 1) / 2 + 5) u relative.  Turning
+mean (1 / D and the product with it) and eps by u each, half of which reaches the root; the
+root's Newton step adds 2 u, the two products of the norm u each: a normed value is off by
+((D + 1) / 2 + 6) u relative.  Turning
 it: cos and sin are off by u (relative to 1), each product and the sum by u: 3 u (|y1| + |y2|)
 beside the values' own error.  One rounding to the type adds half a step.  A norm that is not
 asked for leaves the rotation's part.  8-bit codes lie between the codes of the bound's ends.
@@ -105,7 +106,7 @@ class Case:
         y = osp.norm_rotate(x, wn, self.eps, np.zeros_like(self.pos), self.axes, self.freq.numpy(),
                             self.inter)  # the norm alone
         z = osp.norm_rotate(x, wn, self.eps, self.pos, self.axes, self.freq.numpy(), self.inter)
-        rel = 0 if self.eps is None else ((self.D + 1) / 2 + 5) * U
+        rel = 0 if self.eps is None else ((self.D + 1) / 2 + 6) * U
         half, both = self.rot // 2, np.zeros_like(y)
         one, two = ((slice(0, self.rot, 2), slice(1, self.rot, 2)) if self.inter
                     else (slice(0, half), slice(half, self.rot)))
