@@ -69,12 +69,6 @@ __device__ __forceinline__ void store_piece(T* p, const float (&y)[N], bool wide
   }
 }
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Squares of a piece added to (even, odd) elements' sums.
 template <int VEC>
 __device__ __forceinline__ void add_squares(const float (&x)[VEC], float& even, float& odd) {
@@ -109,7 +103,8 @@ __device__ __forceinline__ void apply_norm(float (&x)[VEC], float r, const float
     const uint64_t rr = ptx::pair(r, r);
 #pragma unroll
     for (int i = 0; i < VEC; i += 2)
-      ptx::unpair(mul2(mul2(ptx::pair(x[i], x[i + 1]), rr), ptx::pair(w[i], w[i + 1])), x[i], x[i + 1]);
+      ptx::unpair(ptx::mul2(ptx::mul2(ptx::pair(x[i], x[i + 1]), rr), ptx::pair(w[i], w[i + 1])),
+                  x[i], x[i + 1]);
   }
 }
 
@@ -132,8 +127,8 @@ __device__ __forceinline__ void turn_pairs(const float (&a)[N], const float (&b)
     for (int i = 0; i < N; i += 2) {
       const uint64_t pa = ptx::pair(a[i], a[i + 1]), pb = ptx::pair(b[i], b[i + 1]);
       const uint64_t pc = ptx::pair(c[i], c[i + 1]);
-      ptx::unpair(ptx::fma2(pa, pc, mul2(pb, ptx::pair(-s[i], -s[i + 1]))), z1[i], z1[i + 1]);
-      ptx::unpair(ptx::fma2(pb, pc, mul2(pa, ptx::pair(s[i], s[i + 1]))), z2[i], z2[i + 1]);
+      ptx::unpair(ptx::fma2(pa, pc, ptx::mul2(pb, ptx::pair(-s[i], -s[i + 1]))), z1[i], z1[i + 1]);
+      ptx::unpair(ptx::fma2(pb, pc, ptx::mul2(pa, ptx::pair(s[i], s[i + 1]))), z2[i], z2[i + 1]);
     }
   }
 }

@@ -53,6 +53,12 @@ constexpr int kTrChunk = 128 * 128;            // one [128 rows x 128 B] swizzle
 constexpr int kTrUnitCost = 2;
 constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximum that moves the reference
 
+// How q . k becomes a score: times a scale that keeps its order (and by which a slope can be
+// divided); with slopes; capped, or by another scale, slopes or not.  (A form for all with slopes or a cap, its unused
+// parts jumped over: a 13B-shaped chunk with slopes 218 us, this one 196.)
+constexpr float kTrLeastScale = 0x1p-40f;
+enum TreeForm { kPlainScores, kSlopeScores, kAnyScores };
+
 // What a CTA leaves behind of the unit that its run begins and another one ends.
 struct TreeCut {
   long long P, C;   // cost before the unit; of all units
@@ -305,6 +311,49 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// min(a, b), NaN if one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// cap * tanh z of a score, 2^(x cap_z) = e^2z: tanh z = 1 - 2 / (1 + e^2z), off by some 5e-7 of
+// the cap.
+__device__ __forceinline__ uint32_t tanh_cap(uint32_t v, float cap_z, float cap) {
+  return __float_as_uint(
+      fmaf(-2.f * cap, rcp_approx(1.f + ptx::ex2(__uint_as_float(v) * cap_z)), cap));
+}
+// Of kCapN, a reciprocal for each four: of their product (one takes as long as two exponentials:
+// CAPPED).  Above 2^30 tanh is 1 in fp32, so that the product stays below 2^121.  False if one is
+// NaN: then its four all are.
+constexpr int kCapN = 16;
+__device__ __forceinline__ bool tanh_cap_n(uint32_t* v, float cap_z, float cap) {
+  float e[kCapN], r[kCapN / 4], ab[kCapN / 2];
+  bool fine = true;
+#pragma unroll
+  for (int k = 0; k < kCapN; ++k) e[k] = min_nan(__uint_as_float(v[k]) * cap_z, 30.f);
+#pragma unroll
+  for (int k = 0; k < kCapN; ++k) e[k] = ptx::ex2(e[k]);
+#pragma unroll
+  for (int k = 0; k < kCapN; ++k) e[k] += 1.f;
+#pragma unroll
+  for (int k = 0; k < kCapN / 2; ++k) ab[k] = e[2 * k] * e[2 * k + 1];
+#pragma unroll
+  for (int k = 0; k < kCapN / 4; ++k) r[k] = ab[2 * k] * ab[2 * k + 1];
+#pragma unroll
+  for (int k = 0; k < kCapN / 4; ++k) r[k] = rcp_approx(r[k]);
+#pragma unroll
+  for (int k = 0; k < kCapN / 4; ++k) {
+    fine &= r[k] == r[k];
+    const float x = ab[2 * k];
+    ab[2 * k] = r[k] * ab[2 * k + 1] * (-2.f * cap);
+    ab[2 * k + 1] = r[k] * x * (-2.f * cap);
+  }
+#pragma unroll
+  for (int k = 0; k < kCapN; ++k) v[k] = __float_as_uint(fmaf(ab[k / 2], e[k ^ 1], cap));
+  return fine;
+}
 
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
@@ -400,11 +449,12 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {  // 0 in place of 
   return x;
 }
 
-template <typename T, int D, bool kBias>
+template <typename T, int D, TreeForm kForm>
 __global__ void __launch_bounds__(kTrThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
+  constexpr bool kSlopes = kForm != kPlainScores;
   using Sh = TreeShape<T, D>;
   constexpr int KT = Sh::KT, HK = Sh::kHalfKeys, HD = Sh::kHalfD;
   constexpr uint32_t NK = Sh::kK, NV = Sh::kV;
@@ -911,10 +961,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       // keys of these positions are seen whatever the mask: no need to look at each
       const int clear_to = a.mask != nullptr ? base : base + node + 1;
       const int clear_from = a.window > 0 ? max(base + depth - a.window + 1, 0) : 0;
-      float slope = 0.f;
-      if constexpr (kBias) {
-        if (live && a.slopes != nullptr)
+      float slope = 0.f, slope_by = 0.f;  // in log2 units, in those of the scores as they come
+      float by = a.scale_log2;
+      if constexpr (kForm == kAnyScores) {
+        if (a.cap_log2 > 0.f || by < kTrLeastScale) by = 1.f;
+      }
+      if constexpr (kSlopes) {
+        if (live && a.slopes != nullptr) {
           slope = __ldg(a.slopes + w.g * a.G + rh) * 1.4426950408889634f;
+          slope_by = min_nan(-min_nan(-slope / by, 0x1p90f), 0x1p90f);
+          slope = slope_by * by;  // (beyond that, the nearest key that is seen takes all)
+        }
       }
       if (live && a.depths != nullptr && h == 0 && valid && w.ka == 0 &&
           __ldg(a.depths + w.q0 + node) != depth)
@@ -929,39 +986,57 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           const int k0 = (w.j0 + k) * KT + h * HK;
           ptx::tc_fence_after();
           const uint32_t sa = tmem + lane_off + b * KT + h * HK;
+          auto load_s = [&]() {
 #pragma unroll
-          for (int i = 0; i < HK; i += 32)
-            ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
-          ptx::tmem_wait_ld();
-          if constexpr (kBias) {  // scores in log2 units
+            for (int i = 0; i < HK; i += 32)
+              ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
+            ptx::tmem_wait_ld();
+          };
+          load_s();
+          float off = 0.f;  // a score in log2 units: v * by + off
+          if constexpr (kForm == kAnyScores) {
             if (a.cap_log2 > 0.f) {
-              // tanh z = 1 - 2 / (1 + e^2z): off by some 1e-7 of the cap
+              bool fine = true;  // (of rows behind the last, whatever they hold)
 #pragma unroll
-              for (int i = 0; i < HK; ++i)
-                v[i] = __float_as_uint(
-                    fmaf(-2.f * a.cap_log2,
-                         rcp_approx(1.f + ptx::ex2(__uint_as_float(v[i]) * a.cap_z)), a.cap_log2));
-            } else {
+              for (int i = 0; i < HK; i += kCapN) fine &= tanh_cap_n(&v[i], a.cap_z, a.cap_log2);
+              if (!__all_sync(0xffffffffu, fine || !valid)) {  // each by itself
+                load_s();
+#pragma unroll
+                for (int i = 0; i < HK; ++i) v[i] = tanh_cap(v[i], a.cap_z, a.cap_log2);
+              }
+            }
+            if (a.cap_log2 <= 0.f && a.scale_log2 < kTrLeastScale) {
 #pragma unroll
               for (int i = 0; i < HK; ++i)
                 v[i] = __float_as_uint(__uint_as_float(v[i]) * a.scale_log2);
             }
-            if (slope != 0.f) {
-              if (a.depths == nullptr || k0 + HK <= base) {
-                const float d0 = static_cast<float>(k0 - base - depth);
+          }
+          if constexpr (kSlopes) {
+            if (kForm == kSlopeScores || a.slopes != nullptr) {
+              int own = depth;
+              if (a.depths != nullptr && k0 + HK > base) {
+                // drafted tokens: how far each one's position is from its place in the chunk
+                own = node;
+                int there[HK / 32];  // of a lane's keys
 #pragma unroll
-                for (int i = 0; i < HK; ++i)
-                  v[i] = __float_as_uint(
-                      fmaf(slope, d0 + static_cast<float>(i), __uint_as_float(v[i])));
-              } else {
+                for (int e = 0; e < HK / 32; ++e) {
+                  const int j = k0 + 32 * e + lane - base;
+                  there[e] = j < 0 || j >= w.c ? 0 : tr_depth(a, w.q0, j) - j;
+                }
 #pragma unroll
                 for (int i = 0; i < HK; ++i) {
-                  const int j = k0 + i - base;  // drafted token, or a cached one
-                  const int pos = j < 0 ? j : (j < w.c ? tr_depth(a, w.q0, j) : 0);
+                  const int x = __shfl_sync(0xffffffffu, there[i >> 5], i & 31) - (depth - node);
                   v[i] = __float_as_uint(
-                      fmaf(slope, static_cast<float>(pos - depth), __uint_as_float(v[i])));
+                      fmaf(slope_by, static_cast<float>(x), __uint_as_float(v[i])));
                 }
               }
+              // neighbouring keys lie a position apart: multiples of the slope beside the scores,
+              // the first key's distance beside the reference
+              off = slope * static_cast<float>(k0 - base - own);
+#pragma unroll
+              for (int i = 0; i < HK; ++i)
+                v[i] = __float_as_uint(
+                    fmaf(slope_by, static_cast<float>(i), __uint_as_float(v[i])));
             }
           }
           // keys that the row does not see score -inf
@@ -978,11 +1053,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           for (int i = 0; i < HK; i += 2)
             mx4[(i >> 1) & 3] =
                 max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-          float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
-          mx = fmaxf(mx, exchange(mx));
+          // the row's maximum over this tile, log2 units
+          float mt = fmaf(max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]), by, off);
+          mt = fmaxf(mt, exchange(mt));
           if (gone) break;
-          const float sc = kBias ? 1.f : a.scale_log2;
-          const float mt = mx * sc;  // the row's maximum over this tile, log2 units
           // The reference m moves only when the maximum grows by more than 2^8 (at first from
           // -inf): O and l are scaled once the product before has landed.  The accesses are
           // warp-wide: the whole warp takes the branch, the other rows scale by 1.
@@ -1004,12 +1078,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           if (move) m = mt;
           // a row that has seen nothing yet: every exponent is -inf whatever the reference
           const float ref = m == -INFINITY ? 0.f : m - Sh::kShift;
+          const float less = off - ref;
           float s0 = 0.f, s1 = 0.f;
           uint32_t pk[HK / 2];
 #pragma unroll
           for (int i = 0; i < HK / 2; ++i) {  // keys 2i, 2i + 1 of the half
-            const float x0 = ptx::ex2(fmaf(__uint_as_float(v[2 * i]), sc, -ref));
-            const float x1 = ptx::ex2(fmaf(__uint_as_float(v[2 * i + 1]), sc, -ref));
+            const float x0 = ptx::ex2(fmaf(__uint_as_float(v[2 * i]), by, less));
+            const float x1 = ptx::ex2(fmaf(__uint_as_float(v[2 * i + 1]), by, less));
             pk[i] = ptx::pack2<T>(x0, x1);
             s0 += x0;
             s1 += x1;
@@ -1133,12 +1208,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeAr
     *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack2<T>(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <typename T, int D, bool kBias>
+template <typename T, int D, TreeForm kForm>
 int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, cudaStream_t st) {
   using Sh = TreeShape<T, D>;
   static SmemOnce once;
   int rc = allow_dynamic_smem(
-      once, reinterpret_cast<const void*>(tree_attention_kernel<T, D, kBias>), Sh::kBytes);
+      once, reinterpret_cast<const void*>(tree_attention_kernel<T, D, kForm>), Sh::kBytes);
   if (rc != PKV_OK) return rc;
   static_assert((kTrMaxSeqs + 1 + 12) * 8 <= Sh::kK * Sh::kTile, "the prefix sums' room");
   CUtensorMap qmap, kmap, vmap;
@@ -1170,7 +1245,7 @@ int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  PKV_CUDA(cudaLaunchKernelEx(&cfg, tree_attention_kernel<T, D, kBias>, qmap, kmap, vmap, a));
+  PKV_CUDA(cudaLaunchKernelEx(&cfg, tree_attention_kernel<T, D, kForm>, qmap, kmap, vmap, a));
   cfg.gridDim = dim3(sms, kTrRows / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
@@ -1180,10 +1255,11 @@ int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, 
 
 template <typename T>
 int launch_tree_d(const TreeArgs& a, const void* k_cache, int32_t dtype, int32_t head_dim,
-                  bool bias, int sms, cudaStream_t st) {
-#define PKV_TREE(D)                                                  \
-  (bias ? launch_tree<T, D, true>(a, k_cache, dtype, sms, st)        \
-        : launch_tree<T, D, false>(a, k_cache, dtype, sms, st))
+                  TreeForm form, int sms, cudaStream_t st) {
+#define PKV_TREE(D)                                                                          \
+  (form == kPlainScores   ? launch_tree<T, D, kPlainScores>(a, k_cache, dtype, sms, st)      \
+   : form == kSlopeScores ? launch_tree<T, D, kSlopeScores>(a, k_cache, dtype, sms, st)      \
+                          : launch_tree<T, D, kAnyScores>(a, k_cache, dtype, sms, st))
   return head_dim == 64 ? PKV_TREE(64) : (head_dim == 128 ? PKV_TREE(128) : PKV_TREE(256));
 #undef PKV_TREE
 }
@@ -1297,12 +1373,13 @@ int pkv_tree_attention(const void* q, const void* k_cache, const void* v_cache,
   a.scale_log2 = static_cast<float>(scale * log2e);
   a.cap_log2 = static_cast<float>(cap * log2e);
   a.cap_z = cap > 0.f ? static_cast<float>(2.0 * log2e * scale / cap) : 0.f;
-  // without cap and slopes the maximum is taken of q . k, which a positive scale keeps in order
-  const bool bias = cap > 0.f || slopes != nullptr || !(a.scale_log2 > 0.f);
+  const TreeForm form = cap > 0.f || !(a.scale_log2 >= kTrLeastScale) ? kAnyScores
+                        : slopes != nullptr                           ? kSlopeScores
+                                                                      : kPlainScores;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = dtype == PKV_BF16
-           ? launch_tree_d<__nv_bfloat16>(a, k_cache, dtype, head_dim, bias, sms, st)
-           : launch_tree_d<__half>(a, k_cache, dtype, head_dim, bias, sms, st);
+           ? launch_tree_d<__nv_bfloat16>(a, k_cache, dtype, head_dim, form, sms, st)
+           : launch_tree_d<__half>(a, k_cache, dtype, head_dim, form, sms, st);
   return rc == PKV_OK ? ok() : rc;
 }
 

@@ -265,6 +265,47 @@ def test_what_is_not_seen_does_not_reach_a_row(kind, bad, D):
     assert not np.isfinite(got[sees][..., ::3]).any()
 
 
+@pytest.mark.parametrize("kw", [dict(cap=20.0), dict(cap=20.0, slopes=[1.0, 0.5, 0.1, 2.0]),
+                                dict(slopes=[1.0, 0.5, 0.1, -2.0])])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D", [64, 256])
+def test_what_is_not_seen_does_not_reach_its_neighbours(kw, bad, D):
+    """Keys that are not finite between keys that are, under a cap and slopes: rows that do not
+    see them are as without; a NaN that is seen stays one (an infinite score is capped)."""
+    c = Case([300, 61], [12, 40], D=D, dtype="f16", kind="tree", seed=3)
+    c.kw = dict(kw)
+    want, spread, size = c.oracle()
+    c.kc[c.tables[0, (300 - 12 + 5) // c.B], :, (300 - 12 + 5) % c.B] = bad
+    last = c.tables[0, (c.lens[0] - 1) // c.B]  # slots past the context
+    c.kc[last, :, c.lens[0] % c.B:] = bad
+    sees = np.zeros(c.T, dtype=bool)
+    sees[:12] = c.seen[0][:, 5]
+    assert sees.any() and not sees[:12].all()
+    c.call()
+    got = np64(c.out[:c.T])
+    fine = np.abs(got - want) <= c.bound(want, spread, size)
+    assert fine[~sees].all()
+    if bad != bad:
+        assert np.isnan(got[sees]).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-30, 2.0 ** -42])
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_slopes_beside_any_scale(scale, kind):
+    c = Case([300, 40], [9, 40], D=128, dtype="f16", kind=kind, seed=5)
+    c.scale = scale
+    c.kw = dict(slopes=[1.0, 0.0, 0.03125, -0.25])
+    c.check()
+
+
+def test_depths_far_from_a_token_s_place():
+    """Depths that leave gaps, under slopes: distances are taken of them, not of places."""
+    c = Case([700, 40], [150, 40], D=128, dtype="bf16", kind="tree", seed=6)
+    c.depths = c.depths * 1000003 % 40009 + 100
+    c.kw = dict(slopes=[1e-4, 3e-5, 1e-3, 2e-4])
+    c.check()
+
+
 def test_value_alone_not_finite():
     """Finite keys, an infinite value: exactly its columns are infinite, in exactly its rows."""
     c = Case([300], [12], D=128, dtype="f16", seed=4)
