@@ -859,8 +859,9 @@ int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int32_t n
  *               after its parent, are); another one is not moved and sets PKV_DEV_BAD_POSITION.
  * path_lens     device int32 [num_seqs], in [0, min(c, path_cols)]: others are clamped and
  *               reported likewise.
- * k_caches, v_caches  HOST arrays as in pkv_copy_blocks_layers; the blocks of the drafted
- *               positions belong to one sequence alone (pkv_seq_append has seen to that).
+ * k_caches, v_caches  HOST arrays as in pkv_copy_blocks_layers, no cache twice; the blocks of
+ *               the drafted positions belong to one sequence alone (pkv_seq_append has seen to
+ *               that).
  * block_tables, context_lens, query_start: as pkv_tree_attention; a sequence whose lengths
  *               do not fit is left alone (PKV_DEV_BAD_CONTEXT_LEN).
  * status        device int32 word or NULL; bits are ORed in (PKV_DEV_BAD_BLOCK_ID too).

@@ -185,6 +185,10 @@ extern "C" int pkv_tree_commit(void* const* k_caches, void* const* v_caches, int
     PKV_REQUIRE(k_caches[l] && v_caches[l], PKV_ERR_INVALID_ARG, "NULL cache of layer %d", l);
     PKV_REQUIRE(aligned(k_caches[l], 16) && aligned(v_caches[l], 16), PKV_ERR_INVALID_ARG,
                 "caches of layer %d must be 16-byte aligned", l);
+    for (int m = 0; m < l; ++m)  // two CTAs would move its rows at the same time
+      PKV_REQUIRE(k_caches[l] != k_caches[m] && v_caches[l] != v_caches[m] &&
+                      k_caches[l] != v_caches[m] && v_caches[l] != k_caches[m],
+                  PKV_ERR_INVALID_ARG, "layers %d and %d share a cache", m, l);
     caches.k[l] = k_caches[l];
     caches.v[l] = v_caches[l];
   }

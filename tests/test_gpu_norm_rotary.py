@@ -229,6 +229,44 @@ def test_many_tokens_of_large_rows():
     Case(700, 32, 8, 128, 128, "f32").check()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("inter,D,rot,A", [(False, 128, 128, 1), (False, 128, 48, 3),
+                                           (True, 64, 64, 1), (True, 256, 128, 2),
+                                           (False, 256, 256, 4), (True, 96, 40, 1),
+                                           (False, 64, 16, 1)])
+@pytest.mark.parametrize("weight,eps", [(None, 1e-6), ("f32", 1e-5), ("own", 0.0), (None, None)])
+def test_a_prompt(dtype, inter, D, rot, A, weight, eps):
+    """More tokens than CTAs, several of them through each."""
+    Case(2501, 7, 3, D, rot, dtype, inter=inter, A=A, weight=weight, eps=eps, fused=True,
+         seed=D + rot).check()
+
+
+def test_a_prompt_of_rows_that_leave_just_room():
+    """Tokens of 37,392 bytes fit three times, of 39,440 do not."""
+    Case(1000, 80, 32, 128, 128, "bf16").check()
+    Case(1000, 88, 32, 128, 128, "bf16").check()
+
+
+def test_a_prompt_in_place_and_out_of_range():
+    from paged_kv_cache_166_gb300 import _native as N
+    c = Case(2000, 4, 2, 128, 128, "f16", A=2, fused=True)
+    c.call()
+    want, kc = c.q_out.clone(), c.kc.clone()
+    c.kc.fill_(7.0)
+    c.q_out = c.q
+    q = c.q.clone()
+    assert torch.equal(c.call(), want) and torch.equal(c.kc, kc)
+    c.q.copy_(q)
+    c.pos[0, 1900], c.pos[1, 3] = -1, 1 << 30
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = c.call(status=status).clone()
+    assert int(status) == N.PKV_DEV_BAD_POSITION
+    c.q.copy_(q)
+    c.pos[0, 1900], c.pos[1, 3] = 0, 2999
+    status.zero_()
+    assert torch.equal(c.call(status=status), got) and int(status) == 0
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("eps", [None, 1e-5])

@@ -182,6 +182,9 @@ def test_refusals():
         c.call(status=torch.zeros(1, device="cuda"))
     with pytest.raises(m.PkvError):
         c.call(kc=c.kc * 65, vc=c.vc * 65)
+    for kc, vc in ((c.kc[:1] * 2, c.vc), (c.kc, c.vc[:1] * 2), (c.kc, [c.vc[1], c.kc[0]])):
+        with pytest.raises(m.PkvError, match="share a cache"):
+            c.call(kc=kc, vc=vc)
     c.n = c.n[:1]
     with pytest.raises(ValueError):
         c.call()
