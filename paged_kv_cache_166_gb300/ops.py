@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from array import array
 from typing import Optional
 
 import torch
@@ -460,12 +461,14 @@ def wait_timeout_selftest(limit_us: int = 20000, device=None) -> tuple:
     return int(status.item()), int(r[0]), bool(r[1] == 1)
 
 
-def _copy_code(cache: torch.Tensor) -> int:
-    if cache.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", None)):
+def _copy_code(dt: torch.dtype) -> int:
+    if dt in (torch.uint8, getattr(torch, "float8_e4m3fn", None)):
         return N.PKV_FP8_E4M3
-    if cache.dtype == torch.int8:
+    if dt == torch.int8:
         return N.PKV_INT8
-    return dtype_code(cache)
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    return _DTYPES[dt]
 
 
 def paged_copy_blocks_layers(k_caches, v_caches, src_dst_pairs: torch.Tensor) -> None:
@@ -487,7 +490,7 @@ def paged_copy_blocks_layers(k_caches, v_caches, src_dst_pairs: torch.Tensor) ->
     kp = (ctypes.c_void_p * L)(*[c.data_ptr() for c in k_caches])
     vp = (ctypes.c_void_p * L)(*[c.data_ptr() for c in v_caches])
     N.check(N.lib().pkv_copy_blocks_layers(kp, vp, L, src_dst_pairs.data_ptr(), n, ref.shape[0],
-                                           ref[0].numel(), _copy_code(ref), _stream(dev)))
+                                           ref[0].numel(), _copy_code(ref.dtype), _stream(dev)))
 
 
 def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -835,7 +838,7 @@ def paged_evict_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table
     and 32-bit, fp8 or int8).  The new blocks belong to one sequence alone
     (``BlockAllocator.evict``)."""
     kc, vc = k_cache, v_cache
-    code = _copy_code(kc)
+    code = _copy_code(kc.dtype)
     dev = _check_cuda(kc, vc, block_tables, kept, new_lens, new_tables)
     if kc.dim() != 4 or vc.dim() != 4 or kc.dtype != vc.dtype:
         raise ValueError("caches must be 4-dimensional and share a dtype")
@@ -1135,25 +1138,24 @@ def paged_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 
 
 def _layer_pointers(caches, name):
-    """(first cache, pointers of the layers' caches) of a list of caches, or of one tensor that
-    holds the layers one after another."""
+    """(a layer's shape, dtype, device, the layers' addresses) of a list of caches, or of one
+    tensor that holds the layers one after another."""
     if isinstance(caches, torch.Tensor):
         if caches.dim() != 5 or not caches.is_contiguous() or caches.shape[0] < 1:
             raise ValueError(f"{name} in one tensor must be a contiguous [layers, NB, Hkv, ., .]")
-        L, p = caches.shape[0], caches.data_ptr()
-        step = caches.stride(0) * caches.element_size()
-        return caches[0], (ctypes.c_void_p * L)(*[p + i * step for i in range(L)])
+        L, *shape = caches.shape
+        p, step = caches.data_ptr(), caches.stride(0) * caches.element_size()
+        return tuple(shape), caches.dtype, caches.device, array("Q", [p + i * step for i in range(L)])
     caches = list(caches)
     if not caches:
         raise ValueError("at least one layer")
-    ref = caches[0]
-    shape, dt, dev = ref.shape, ref.dtype, ref.device
+    shape, dt, dev = caches[0].shape, caches[0].dtype, caches[0].device
     for c in caches:
         if c.shape != shape or c.dtype != dt:
             raise ValueError("every layer's caches must have one shape and dtype")
         if c.device != dev or not c.is_contiguous():
             raise ValueError("tensors must be contiguous and on one device")
-    return ref, (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    return tuple(shape), dt, dev, array("Q", [c.data_ptr() for c in caches])
 
 
 def paged_tree_commit(k_caches, v_caches, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -1164,14 +1166,16 @@ def paged_tree_commit(k_caches, v_caches, block_tables: torch.Tensor, context_le
     minus the drafted tokens, in every layer's caches (lists of caches, or tensors with the
     layers in front; 16- and 32-bit, fp8 or int8).  path [S, columns] int32: numbers within the
     sequence's drafted tokens, ascending.  ``BlockAllocator.truncate`` then gives the rest back."""
-    kc, kp = _layer_pointers(k_caches, "k_caches")
-    vc, vp = _layer_pointers(v_caches, "v_caches")
-    dev = _check_cuda(kc, vc, block_tables, context_lens, query_start, path, path_lens)
-    code = _copy_code(kc)
-    if kc.dim() != 4 or kc.dtype != vc.dtype or len(kp) != len(vp):
+    kshape, dt, kdev, kp = _layer_pointers(k_caches, "k_caches")
+    vshape, vdt, vdev, vp = _layer_pointers(v_caches, "v_caches")
+    dev = _check_cuda(block_tables, context_lens, query_start, path, path_lens)
+    if kdev != dev or vdev != dev:
+        raise ValueError("tensors must be on one device")
+    code = _copy_code(dt)
+    if len(kshape) != 4 or vdt != dt or len(kp) != len(vp):
         raise ValueError("one K and one V cache per layer, 4-dimensional, of one dtype")
-    NB, Hkv, B, D = kc.shape
-    if vc.shape != ((NB, Hkv, D, B) if code in _CODES.values() else kc.shape):
+    NB, Hkv, B, D = kshape
+    if vshape != ((NB, Hkv, D, B) if code in _CODES.values() else kshape):
         raise ValueError("v_cache must be [NB, Hkv, B, D] ([NB, Hkv, D, 16] if 8-bit)")
     for t, name in ((block_tables, "block_tables"), (context_lens, "context_lens"),
                     (query_start, "query_start"), (path, "path"), (path_lens, "path_lens")):
@@ -1185,9 +1189,10 @@ def paged_tree_commit(k_caches, v_caches, block_tables: torch.Tensor, context_le
     st = _status_ptr(status, dev)
     with _current(dev):
         N.check(N.lib().pkv_tree_commit(
-            kp, vp, len(kp), block_tables.data_ptr(), block_tables.shape[1],
-            context_lens.data_ptr(), query_start.data_ptr(), path.data_ptr(), path.shape[1],
-            path_lens.data_ptr(), S, NB, Hkv, B, D, st, code, _stream(dev)))
+            kp.buffer_info()[0], vp.buffer_info()[0], len(kp), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(),
+            path.data_ptr(), path.shape[1], path_lens.data_ptr(), S, NB, Hkv, B, D, st, code,
+            _stream(dev)))
 
 
 def adjust_logits(logits: torch.Tensor, history: torch.Tensor, history_lens: torch.Tensor,
