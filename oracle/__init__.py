@@ -40,6 +40,9 @@ written from the pages that describe PagedAttention:
 * ``beam``             — beam search's selection over beams and vocabulary
   ("PagedAttention: How vLLM Borrowed Virtual Memory...", section "Copy-on-Write
   for Beam Search and Parallel Sampling", whose forked tables it reorders).
+* ``speculative``      — a speculative step: norms in front of rotary positions on
+  several axes, attention of trees of drafted tokens, penalties and masks on
+  logits, the accepted path's rows moved together.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against values the
 pages print, library routines on special cases, closed forms and invariants.

@@ -217,10 +217,11 @@ def test_norm_rotary_refusals():
 
 
 def test_commit_refusals():
-    one = (ctypes.c_void_p * 2)(P, P)
+    one, two = (ctypes.c_void_p * 2)(P, P + 64), (ctypes.c_void_p * 2)(P + 128, P + 192)
+    same, other = (ctypes.c_void_p * 2)(P, P), (ctypes.c_void_p * 2)(P + 128, P)
     off = (ctypes.c_void_p * 2)(P, P + 8)
     gone = (ctypes.c_void_p * 2)(P, None)
-    base = dict(kc=one, vc=one, L=2, bt=P, maxb=4, ctx=P, qs=P, path=P, cols=3, lens=P, S=2, NB=8,
+    base = dict(kc=one, vc=two, L=2, bt=P, maxb=4, ctx=P, qs=P, path=P, cols=3, lens=P, S=2, NB=8,
                 Hkv=2, B=16, D=128, status=P, dt=N.PKV_BF16, stream=None)
     refused(N.lib().pkv_tree_commit, base, [
         (dict(dt=9), D_), (dict(L=0), U), (dict(L=129), U), (dict(S=-1), A), (dict(cols=-1), A),
@@ -228,6 +229,7 @@ def test_commit_refusals():
         (dict(dt=N.PKV_INT8, B=8), U), (dict(D=4), A), (dict(D=8192), A), (dict(Hkv=70000), U),
         (dict(maxb=1 << 28), U), (dict(NB=1 << 28), U), (dict(kc=None), A), (dict(vc=None), A),
         (dict(kc=off), A), (dict(vc=off), A), (dict(kc=gone), A), (dict(bt=None), A),
+        (dict(kc=same), A), (dict(vc=same), A), (dict(vc=other), A), (dict(vc=same, S=0), A),
         (dict(ctx=None), A), (dict(qs=None), A), (dict(path=None), A), (dict(lens=None), A),
         (dict(path=P + 2), A), (dict(status=P + 1), A)])
     for kw in (dict(S=0), dict(cols=0)):
