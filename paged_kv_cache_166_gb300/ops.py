@@ -34,15 +34,14 @@ def _stream(device: torch.device) -> int:
 
 
 def _check_cuda(*ts) -> torch.device:
-    dev = ts[0].device
+    at = ts[0].get_device()  # (-1: not a GPU's; numbers compare faster than devices)
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if t.device != dev:
-            raise ValueError("tensors must be on one device")
+        if t.get_device() != at or at < 0:
+            raise ValueError("tensors must be on one device" if t.is_cuda and ts[0].is_cuda else
+                             "tensors must be CUDA tensors")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-    return dev
+    return ts[0].device
 
 
 def _check_index(t: torch.Tensor, name: str) -> None:
@@ -537,7 +536,7 @@ def _fits(name: str, *values: int) -> None:
 
 def _current(dev: torch.device):
     """A context in which ``dev`` is the current device (the library launches there)."""
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _status_ptr(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
@@ -923,7 +922,8 @@ def _norm_rotary_write(kind, q, k, v, q_weight, k_weight, eps, positions, table,
     else:
         kc, vc, scales = k_cache, v_cache, (None, None)
         dev = _check_cuda(positions, table, slot_mapping, kc, vc)
-    if not (q.device == k.device == v.device == q_out.device == dev):
+    at = kc.get_device()
+    if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == at):
         raise ValueError("q, k, v and q_out must be on the caches' device")
     if not (q.dim() == k.dim() == v.dim() == q_out.dim() == 3) or kc.dim() != 4 or vc.dim() != 4:
         raise ValueError("expected q, q_out [T, Hq, D], k, v [T, Hkv, D] and 4-dimensional caches")
@@ -966,7 +966,7 @@ def _norm_rotary_write(kind, q, k, v, q_weight, k_weight, eps, positions, table,
     for w, H, name in ((q_weight, Hq, "q_weight"), (k_weight, Hkv, "k_weight")):
         if w is None:
             continue
-        if w.device != dev or not w.is_contiguous() or w.shape not in ((D,), (H, D)):
+        if w.get_device() != at or not w.is_contiguous() or w.shape not in ((D,), (H, D)):
             raise ValueError(f"{name} must be a contiguous [{D}] or [{H}, {D}] tensor on the "
                              "caches' device")
         kinds.add((dtype_code(w), w.dim() == 2))
@@ -1216,7 +1216,8 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor, history_lens: tor
     [T, words] int32, a bit a token: the others become -infinity."""
     y = logits if out is None else out
     dev = _check_cuda(history, history_lens)
-    if logits.device != dev or y.device != dev:
+    at = history.get_device()
+    if logits.get_device() != at or y.get_device() != at:
         raise ValueError("logits and out must be on the device of history")
     if logits.dim() != 2 or y.shape != logits.shape or y.dtype != logits.dtype:
         raise ValueError("expected logits [T, V], and out of the same shape and dtype")
@@ -1232,7 +1233,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor, history_lens: tor
             return None
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {str(dtype)[6:]}")
-        if t.shape != shape or t.device != dev or not t.is_contiguous():
+        if t.get_device() != at or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {list(shape)} on the logits' device")
         return t.data_ptr()
 
