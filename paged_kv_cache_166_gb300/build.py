@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libpkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "decode_attention.cu", "decode_weights.cu", "prefill_attention.cu",
            "prefill_tcgen05.cu", "kv_ops.cu", "rotary.cu", "evict.cu", "beam.cu", "tree_attention.cu",
-           "tree_commit.cu", "norm_rotary.cu", "logits.cu", "allocator.cpp"]
+           "tree_commit.cu", "norm_rotary.cu", "norm_rotary_8bit.cu", "logits.cu", "allocator.cpp"]
 
 
 def nvcc() -> str:

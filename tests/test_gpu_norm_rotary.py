@@ -210,7 +210,7 @@ def test_token_counts(T):
 @pytest.mark.parametrize("D,rot,A", [(64, 64, 1), (128, 64, 2), (256, 256, 1), (96, 32, 4), (8, 8, 1)])
 @pytest.mark.parametrize("weight,per_head", [("same", False), ("f32", True), (None, False)])
 def test_many_tokens(dtype, inter, D, rot, A, weight, per_head):
-    """Enough tokens for whole ones to be fetched ahead."""
+    """Several tokens through each SM."""
     if D * DT[dtype].itemsize % 16:
         pytest.skip("rows of whole 16 bytes")
     Case(1300, 6, 2, D, rot, dtype, inter=inter, A=A, weight=weight, per_head=per_head).check()
@@ -224,7 +224,6 @@ def test_many_tokens_8_bit(kind, dtype, inter, A):
 
 
 def test_many_tokens_of_large_rows():
-    """Rows that leave no room for three tokens, and just some."""
     Case(700, 128, 8, 256, 256, "bf16").check()
     Case(700, 32, 8, 128, 128, "f32").check()
 
@@ -241,8 +240,7 @@ def test_a_prompt(dtype, inter, D, rot, A, weight, eps):
          seed=D + rot).check()
 
 
-def test_a_prompt_of_rows_that_leave_just_room():
-    """Tokens of 37,392 bytes fit three times, of 39,440 do not."""
+def test_a_prompt_of_many_heads():
     Case(1000, 80, 32, 128, 128, "bf16").check()
     Case(1000, 88, 32, 128, 128, "bf16").check()
 
