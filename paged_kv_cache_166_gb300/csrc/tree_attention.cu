@@ -24,7 +24,7 @@
 // 4 * 128 * 128 operations: memory, if the softmax of a tile (16,384 exponentials) stays below
 // the 1.5 us that its 64 KB take.  Measured: trees on a 70B-shaped batch (64 / 8 heads of 128, bf16,
 // 128 contexts, 976 MB) 166 us, 5.9 TB/s; on contexts of 32,768 to 131,072 270 us, 6.5 TB/s; chunks
-// of 513 with slopes on 8 sequences of 40 / 40 heads, f16, 197 us, bound by the row warps' chain of
+// of 513 with slopes on 8 sequences of 40 / 40 heads, f16, 194 us, bound by the row warps' chain of
 // phases, not by memory or products; the smallest calls 10 us, two launches and their chains.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -58,7 +58,7 @@ constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximu
 
 // How q . k becomes a score: times a scale that keeps its order (and by which a slope can be
 // divided); with slopes; capped, or by another scale, slopes or not.  (A form for all with slopes or a cap, its unused
-// parts jumped over: a 13B-shaped chunk with slopes 218 us, this one 196.)
+// parts jumped over: a 13B-shaped chunk with slopes 218 us, this one 194.)
 constexpr float kTrLeastScale = 0x1p-40f;
 enum TreeForm { kPlainScores, kSlopeScores, kAnyScores };
 
@@ -321,41 +321,19 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return d;
 }
 
-// cap * tanh z of a score, 2^(x cap_z) = e^2z: tanh z = 1 - 2 / (1 + e^2z), off by some 5e-7 of
-// the cap.
-__device__ __forceinline__ uint32_t tanh_cap(uint32_t v, float cap_z, float cap) {
-  return __float_as_uint(
-      fmaf(-2.f * cap, rcp_approx(1.f + ptx::ex2(__uint_as_float(v) * cap_z)), cap));
-}
-// Of kCapN, a reciprocal for each four: of their product (one takes as long as two exponentials: a
-// 70B-shaped batch, capped, 226 us with one for each, 206 so).  Above 2^30 tanh is 1 in fp32, so
-// that the product stays below 2^121.  False if one is NaN: then its four all are.
-constexpr int kCapN = 16;
-__device__ __forceinline__ bool tanh_cap_n(uint32_t* v, float cap_z, float cap) {
-  float e[kCapN], r[kCapN / 4], ab[kCapN / 2];
-  bool fine = true;
-#pragma unroll
-  for (int k = 0; k < kCapN; ++k) e[k] = min_nan(__uint_as_float(v[k]) * cap_z, 30.f);
-#pragma unroll
-  for (int k = 0; k < kCapN; ++k) e[k] = ptx::ex2(e[k]);
-#pragma unroll
-  for (int k = 0; k < kCapN; ++k) e[k] += 1.f;
-#pragma unroll
-  for (int k = 0; k < kCapN / 2; ++k) ab[k] = e[2 * k] * e[2 * k + 1];
-#pragma unroll
-  for (int k = 0; k < kCapN / 4; ++k) r[k] = ab[2 * k] * ab[2 * k + 1];
-#pragma unroll
-  for (int k = 0; k < kCapN / 4; ++k) r[k] = rcp_approx(r[k]);
-#pragma unroll
-  for (int k = 0; k < kCapN / 4; ++k) {
-    fine &= r[k] == r[k];
-    const float x = ab[2 * k];
-    ab[2 * k] = r[k] * ab[2 * k + 1] * (-2.f * cap);
-    ab[2 * k + 1] = r[k] * x * (-2.f * cap);
-  }
-#pragma unroll
-  for (int k = 0; k < kCapN; ++k) v[k] = __float_as_uint(fmaf(ab[k / 2], e[k ^ 1], cap));
-  return fine;
+// cap * tanh z of two scores x, 2^(x cap_z) = e^2z: tanh z = 1 - 2 / (1 + e^2z), off by some 3e-7
+// of the cap.  (One reciprocal for four scores, of their product, was 5% faster for a 70B-shaped
+// batch of small trees, 206 against 216 us, and 18% slower where tiles are full, 303 against 257:
+// a NaN then needs its neighbours done again, each by itself.)
+__device__ __forceinline__ void tanh_cap2(uint32_t& v0, uint32_t& v1, float cap_z, float cap) {
+  float x, y;
+  ptx::unpair(ptx::mul2(ptx::pair(__uint_as_float(v0), __uint_as_float(v1)),
+                        ptx::pair(cap_z, cap_z)), x, y);
+  ptx::unpair(ptx::add2(ptx::pair(ptx::ex2(x), ptx::ex2(y)), ptx::pair(1.f, 1.f)), x, y);
+  ptx::unpair(ptx::fma2(ptx::pair(rcp_approx(x), rcp_approx(y)),
+                        ptx::pair(-2.f * cap, -2.f * cap), ptx::pair(cap, cap)), x, y);
+  v0 = __float_as_uint(x);
+  v1 = __float_as_uint(y);
 }
 
 __device__ __forceinline__ uint64_t low_bits(int n) {
@@ -989,24 +967,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           const int k0 = (w.j0 + k) * KT + h * HK;
           ptx::tc_fence_after();
           const uint32_t sa = tmem + lane_off + b * KT + h * HK;
-          auto load_s = [&]() {
 #pragma unroll
-            for (int i = 0; i < HK; i += 32)
-              ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
-            ptx::tmem_wait_ld();
-          };
-          load_s();
+          for (int i = 0; i < HK; i += 32)
+            ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
+          ptx::tmem_wait_ld();
           float off = 0.f;  // a score in log2 units: v * by + off
           if constexpr (kForm == kAnyScores) {
             if (a.cap_log2 > 0.f) {
-              bool fine = true;  // (of rows behind the last, whatever they hold)
 #pragma unroll
-              for (int i = 0; i < HK; i += kCapN) fine &= tanh_cap_n(&v[i], a.cap_z, a.cap_log2);
-              if (!__all_sync(0xffffffffu, fine || !valid)) {  // each by itself
-                load_s();
-#pragma unroll
-                for (int i = 0; i < HK; ++i) v[i] = tanh_cap(v[i], a.cap_z, a.cap_log2);
-              }
+              for (int i = 0; i < HK; i += 2) tanh_cap2(v[i], v[i + 1], a.cap_z, a.cap_log2);
             }
             if (a.cap_log2 <= 0.f && a.scale_log2 < kTrLeastScale) {
 #pragma unroll
