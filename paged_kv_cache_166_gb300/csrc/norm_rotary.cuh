@@ -18,7 +18,7 @@
 //
 // A group of up to 32 lanes takes a head: a lane's pieces of 16 bytes (both halves' ones of a
 // turned pair), the sum of squares by shuffles; then the next head with the cos, sin and
-// weights that the lane has loaded once.  Bound by memory.
+// weights that the lane has loaded once.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
