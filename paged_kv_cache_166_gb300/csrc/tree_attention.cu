@@ -381,15 +381,21 @@ __device__ __forceinline__ uint64_t tr_sees(const TreeArgs& a, const TreeWalk& w
   return n >= 64 ? vis : vis & low_bits(n);
 }
 
+// Whether a drafted key's place does not tell which rows see it.
+__device__ __forceinline__ bool tr_by_row(const TreeArgs& a) {
+  return a.mask != nullptr || (a.depths != nullptr && a.window > 0);
+}
+
 // Keys whose values must not reach every row of a unit, as up to two ranges: those that some row
 // sees and another does not, and the rest of the first and last cache blocks that are read.
-// There, values of V that are not finite would (0 * infinity).
+// There, values of V that are not finite would (0 * infinity).  Depths let a window hide a drafted
+// token from any row, in whatever order they stand.
 __device__ __forceinline__ void tr_mixed(const TreeArgs& a, const TreeWalk& w, int (&from)[2],
                                          int (&to)[2]) {
   const int base = w.t - w.c, i0 = w.tile * a.nodes, last = min(w.c, i0 + a.nodes) - 1;
   int lo, hi;
   tr_keys(a, w.t, w.c, w.tile, lo, hi);
-  from[1] = a.mask != nullptr ? base : base + i0 + 1;
+  from[1] = tr_by_row(a) ? base : base + i0 + 1;
   to[1] = (hi + a.bs - 1) & -a.bs;
   from[0] = lo & -a.bs;
   to[0] = lo;
@@ -939,8 +945,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       const int node = w.tile * a.nodes + (valid ? rn : 0);
       const int base = w.t - w.c;
       const int depth = live ? tr_depth(a, w.q0, node) : 0;
-      // keys of these positions are seen whatever the mask: no need to look at each
-      const int clear_to = a.mask != nullptr ? base : base + node + 1;
+      // keys at these places are seen whatever the mask: no need to look at each
+      const int clear_to = tr_by_row(a) ? base : base + node + 1;
       const int clear_from = a.window > 0 ? max(base + depth - a.window + 1, 0) : 0;
       float slope = 0.f, slope_by = 0.f;  // in log2 units, in those of the scores as they come
       float by = a.scale_log2;
