@@ -819,7 +819,8 @@ int pkv_norm_rotary_write(int32_t codes, const void* q, int64_t q_stride, const 
  *               calls that may overlap need their own.
  * Supported: F16 and BF16, head_dim 64, 128 or 256, up to 16 query heads per KV head,
  * block_size 8, 16 or 32, num_seqs <= 2048, max_blocks_per_seq * block_size < 2^30.
- * Scores, softmax and sums are fp32, probabilities rounded to dtype for the product with V.
+ * Scores, softmax and sums are fp32, probabilities rounded to dtype for the product with V.  A
+ * cap (any finite one) adds at most 5e-7 cap to a score's error up to 128, above that 1e-6 |x|.
  * Two launches; the same bits on every run, and on any blocks that hold the same data.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_DTYPE, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  */

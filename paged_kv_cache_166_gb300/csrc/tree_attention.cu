@@ -31,6 +31,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -57,10 +59,12 @@ constexpr int kTrUnitCost = 2;
 constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximum that moves the reference
 
 // How q . k becomes a score: times a scale that keeps its order (and by which a slope can be
-// divided); with slopes; capped, or by another scale, slopes or not.  (A form for all with slopes or a cap, its unused
-// parts jumped over: a 13B-shaped chunk with slopes 218 us, this one 194.)
+// divided); with slopes; capped, or by another scale, slopes or not; under a cap above kTrSmallCap.
+// (A form for all with slopes or a cap, its unused parts jumped over: a 13B-shaped chunk with
+// slopes 218 us, this one 194.  One for all caps: that chunk capped at 30, without slopes, 266 us, this one 259.)
 constexpr float kTrLeastScale = 0x1p-40f;
-enum TreeForm { kPlainScores, kSlopeScores, kAnyScores };
+constexpr float kTrSmallCap = 128.f;
+enum TreeForm { kPlainScores, kSlopeScores, kAnyScores, kLargeCapScores };
 
 // What a CTA leaves behind of the unit that its run begins and another one ends.
 struct TreeCut {
@@ -88,6 +92,7 @@ struct TreeArgs {
   int32_t nodes, box;     // drafted tokens of a unit and of one TMA box of q
   float scale_log2;       // without cap: x in log2 units is S * scale_log2
   float cap_log2, cap_z;  // with cap: cap_log2 * tanh, 2^(S * cap_z) = e^(2 x / cap)
+  float cap_inv;          // above kTrSmallCap: 1 / cap_log2
 };
 
 __device__ __forceinline__ void tr_flag(const TreeArgs& a, int bits) {
@@ -322,7 +327,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 }
 
 // cap * tanh z of two scores x, 2^(x cap_z) = e^2z: tanh z = 1 - 2 / (1 + e^2z), off by some 3e-7
-// of the cap.  (One reciprocal for four scores, of their product, was 5% faster for a 70B-shaped
+// of the cap, however small the score: up to kTrSmallCap that is 4e-5, below an eighth of f16's half
+// step, of the probability that follows.  (One reciprocal for four scores, of their product, was 5% faster for a 70B-shaped
 // batch of small trees, 206 against 216 us, and 18% slower where tiles are full, 303 against 257:
 // a NaN then needs its neighbours done again, each by itself.)
 __device__ __forceinline__ void tanh_cap2(uint32_t& v0, uint32_t& v1, float cap_z, float cap) {
@@ -334,6 +340,32 @@ __device__ __forceinline__ void tanh_cap2(uint32_t& v0, uint32_t& v1, float cap_
                         ptx::pair(-2.f * cap, -2.f * cap), ptx::pair(cap, cap)), x, y);
   v0 = __float_as_uint(x);
   v1 = __float_as_uint(y);
+}
+
+// The same for any cap, off by some 1e-6 of the capped score itself: for |z| <= 1/2, where the form
+// above cancels, x (tanh z / z) with the Taylor series of tanh z / z up to z^14 (the next term is
+// below 2^-26).  Both forms are computed: a 70B-shaped batch of small trees 308 us, 215 under a small
+// cap.  by: the scores' scale in log2 units; inv: 1 / cap.
+__device__ __forceinline__ void tanh_any_cap2(uint32_t& v0, uint32_t& v1, float by, float inv,
+                                              float cap) {
+  const uint64_t x = ptx::mul2(ptx::pair(__uint_as_float(v0), __uint_as_float(v1)),
+                               ptx::pair(by, by));
+  const uint64_t z = ptx::mul2(x, ptx::pair(inv, inv)), u = ptx::mul2(z, z);
+  constexpr float kC[7] = {21844.f / 6081075.f, -1382.f / 155925.f, 62.f / 2835.f, -17.f / 315.f,
+                           2.f / 15.f,          -1.f / 3.f,         1.f};
+  uint64_t p = ptx::pair(-929569.f / 638512875.f, -929569.f / 638512875.f);
+#pragma unroll
+  for (int i = 0; i < 7; ++i) p = ptx::fma2(p, u, ptx::pair(kC[i], kC[i]));
+  float z0, z1, y0, y1, w0, w1;
+  ptx::unpair(z, z0, z1);
+  ptx::unpair(ptx::mul2(x, p), y0, y1);
+  constexpr float kTwoLog2e = 2.8853900817779268f;
+  ptx::unpair(ptx::add2(ptx::pair(ptx::ex2(z0 * kTwoLog2e), ptx::ex2(z1 * kTwoLog2e)),
+                        ptx::pair(1.f, 1.f)), w0, w1);
+  ptx::unpair(ptx::mul2(ptx::fma2(ptx::pair(rcp_approx(w0), rcp_approx(w1)), ptx::pair(-2.f, -2.f),
+                                  ptx::pair(1.f, 1.f)), ptx::pair(cap, cap)), w0, w1);
+  v0 = __float_as_uint(fabsf(z0) <= 0.5f ? y0 : w0);
+  v1 = __float_as_uint(fabsf(z1) <= 0.5f ? y1 : w1);
 }
 
 __device__ __forceinline__ uint64_t low_bits(int n) {
@@ -953,6 +985,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
       if constexpr (kForm == kAnyScores) {
         if (a.cap_log2 > 0.f || by < kTrLeastScale) by = 1.f;
       }
+      if constexpr (kForm == kLargeCapScores) by = 1.f;
       if constexpr (kSlopes) {
         if (live && a.slopes != nullptr) {
           slope = __ldg(a.slopes + w.g * a.G + rh) * 1.4426950408889634f;
@@ -978,6 +1011,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             ptx::tmem_ld32_nowait(sa + i, *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
           ptx::tmem_wait_ld();
           float off = 0.f;  // a score in log2 units: v * by + off
+          if constexpr (kForm == kLargeCapScores) {
+#pragma unroll
+            for (int i = 0; i < HK; i += 2)
+              tanh_any_cap2(v[i], v[i + 1], a.scale_log2, a.cap_inv, a.cap_log2);
+          }
           if constexpr (kForm == kAnyScores) {
             if (a.cap_log2 > 0.f) {
 #pragma unroll
@@ -1237,7 +1275,8 @@ int launch_tree_d(const TreeArgs& a, const void* k_cache, int32_t dtype, int32_t
 #define PKV_TREE(D)                                                                          \
   (form == kPlainScores   ? launch_tree<T, D, kPlainScores>(a, k_cache, dtype, sms, st)      \
    : form == kSlopeScores ? launch_tree<T, D, kSlopeScores>(a, k_cache, dtype, sms, st)      \
-                          : launch_tree<T, D, kAnyScores>(a, k_cache, dtype, sms, st))
+   : form == kAnyScores   ? launch_tree<T, D, kAnyScores>(a, k_cache, dtype, sms, st)        \
+                          : launch_tree<T, D, kLargeCapScores>(a, k_cache, dtype, sms, st))
   return head_dim == 64 ? PKV_TREE(64) : (head_dim == 128 ? PKV_TREE(128) : PKV_TREE(256));
 #undef PKV_TREE
 }
@@ -1349,11 +1388,16 @@ int pkv_tree_attention(const void* q, const void* k_cache, const void* v_cache,
   a.nodes = kTrRows / G / a.box * a.box;
   const double log2e = 1.4426950408889634;
   a.scale_log2 = static_cast<float>(scale * log2e);
-  a.cap_log2 = static_cast<float>(cap * log2e);
-  a.cap_z = cap > 0.f ? static_cast<float>(2.0 * log2e * scale / cap) : 0.f;
-  const TreeForm form = cap > 0.f || !(a.scale_log2 >= kTrLeastScale) ? kAnyScores
-                        : slopes != nullptr                           ? kSlopeScores
-                                                                      : kPlainScores;
+  // (caps next to the largest float: log2 units end there; scores that large are a tie or take all)
+  const double most = FLT_MAX;
+  a.cap_log2 = static_cast<float>(std::min(cap * log2e, most));
+  // (kept finite: a score of 0 stays one under the smallest caps)
+  a.cap_z = cap > 0.f ? static_cast<float>(std::clamp(2.0 * log2e * scale / cap, -most, most)) : 0.f;
+  a.cap_inv = cap > kTrSmallCap ? static_cast<float>(1.0 / a.cap_log2) : 0.f;
+  const TreeForm form = cap > kTrSmallCap                               ? kLargeCapScores
+                        : cap > 0.f || !(a.scale_log2 >= kTrLeastScale) ? kAnyScores
+                        : slopes != nullptr                             ? kSlopeScores
+                                                                        : kPlainScores;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = dtype == PKV_BF16
            ? launch_tree_d<__nv_bfloat16>(a, k_cache, dtype, head_dim, form, sms, st)
