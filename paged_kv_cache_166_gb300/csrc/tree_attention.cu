@@ -61,7 +61,8 @@ constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximu
 // How q . k becomes a score: times a scale that keeps its order (and by which a slope can be
 // divided); with slopes; capped, or by another scale, slopes or not; under a cap above kTrSmallCap.
 // (A form for all with slopes or a cap, its unused parts jumped over: a 13B-shaped chunk with
-// slopes 218 us, this one 194.  One for all caps: that chunk capped at 30, without slopes, 266 us, this one 259.)
+// slopes 218 us, this one 194.  One for all caps: that chunk capped at 30, without slopes, 266 us,
+// this one 259.)
 constexpr float kTrLeastScale = 0x1p-40f;
 constexpr float kTrSmallCap = 128.f;
 enum TreeForm { kPlainScores, kSlopeScores, kAnyScores, kLargeCapScores };
@@ -1224,6 +1225,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeAr
     *reinterpret_cast<uint32_t*>(dst + e) = ptx::pack2<T>(acc[e] * inv, acc[e + 1] * inv);
 }
 
+// The two launches of a call hand pieces over through the workspace: they are queued one behind the
+// other, whatever other host threads queue on the stream with the same workspace.
+std::mutex tree_queue;
+
 template <typename T, int D, TreeForm kForm>
 int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, cudaStream_t st) {
   using Sh = TreeShape<T, D>;
@@ -1261,6 +1266,7 @@ int launch_tree(const TreeArgs& a, const void* k_cache, int32_t dtype, int sms, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const std::lock_guard<std::mutex> both(tree_queue);
   PKV_CUDA(cudaLaunchKernelEx(&cfg, tree_attention_kernel<T, D, kForm>, qmap, kmap, vmap, a));
   cfg.gridDim = dim3(sms, kTrRows / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
