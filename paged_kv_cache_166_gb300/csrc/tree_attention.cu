@@ -479,14 +479,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
   constexpr int KT = Sh::KT, HK = Sh::kHalfKeys, HD = Sh::kHalfD;
   constexpr uint32_t NK = Sh::kK, NV = Sh::kV;
   // The joining kernel may be launched: it waits for the whole of this grid.  This grid itself
-  // may have been launched ahead of the end of a cache write or a joining kernel in front of it:
-  // lengths, tables and masks are read at once, q, the caches and the workspace once that is done.
+  // may have been launched ahead of the end of what is in front of it: nothing is read or
+  // written in memory before the wait below.
   asm volatile("griddepcontrol.launch_dependents;");
   // swizzled tiles lie on 1,024-byte boundaries (there is no room to look for one)
   extern __shared__ __align__(1024) uint8_t base_p[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base_s = ptx::smem_addr(base_p);
   if ((base_s & 1023u) != 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) {
       tr_flag(a, PKV_DEV_WAIT_TIMEOUT);
       a.cuts[blockIdx.x] = TreeCut{0, 0, 0, 0, 0, 0};
@@ -517,6 +518,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     ptx::tmem_alloc(ptx::smem_addr(slot), Sh::kTmemCols);
     ptx::tmem_relinquish();
   }
+  // Every thread waits: lengths, masks and depths may have been written by the kernel in front as well
+  // as the caches, a joining kernel there may still read its cuts, and whatever comes behind this
+  // call relies on all in front of it being done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- costs of all sequences summed up (in the K ring, free until the first load) --------
   long long* const cpre = reinterpret_cast<long long*>(base_p + Sh::kKOff);
@@ -605,8 +610,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
           cut.rows = min(a.nodes, c - u * a.nodes) * a.G;
           cut.g = g;
         }
-        // a joining kernel of a call before may still read its own
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         a.cuts[blockIdx.x] = cut;
       }
       __syncwarp();
@@ -710,7 +713,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     for (int i = 0; i < kTrAhead; ++i) hand_out();
     TreeWalk u{}, next{};
     alive = get_piece(0, u);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (alive && u.n > 0) alive = load_q(u);
     for (uint32_t n = 0; alive && u.n > 0; ++n) {
       if (lane == 0) odd_seen[n % kTrPieces] = 0;  // (its last user has been read out)
@@ -752,7 +754,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint32_t it = 0;
     TreeWalk w{};
     bool alive = true;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the caches may have been written just now
     for (uint32_t n = 0; alive; ++n) {
       if (!get_piece(n, w)) { alive = false; break; }
       if (w.n == 0) break;
