@@ -844,7 +844,7 @@ int pkv_tree_workspace_size(int32_t head_dim, size_t* bytes);
  * context's end).
  * parents       host int32 [num_tokens]: at query_start[s] + i the number within the
  *               sequence of drafted token i's parent, less than i, or -1.
- * query_start   host int32 [num_seqs + 1], non-decreasing.
+ * query_start   host int32 [num_seqs + 1], non-decreasing from 0 or more; the last one is num_tokens.
  * tree_mask     host int32 [num_tokens, mask_words]; depths host int32 [num_tokens].
  * Errors: PKV_ERR_INVALID_ARG (nothing written).
  */

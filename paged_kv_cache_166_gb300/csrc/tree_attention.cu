@@ -1419,9 +1419,13 @@ int pkv_tree_masks(const int32_t* parents, const int32_t* query_start, int32_t n
               PKV_ERR_INVALID_ARG, "NULL pointer");
   PKV_REQUIRE(num_seqs == 0 || query_start[0] >= 0, PKV_ERR_INVALID_ARG,
               "query_start must not be negative");
-  for (int32_t s = 0; s < num_seqs; ++s) {  // all checked before anything is written
+  // all checked before anything is written, every border before a parent is read: the last one is
+  // the number of parents
+  for (int32_t s = 0; s < num_seqs; ++s)
+    PKV_REQUIRE(query_start[s + 1] >= query_start[s], PKV_ERR_INVALID_ARG,
+                "query_start must not decrease");
+  for (int32_t s = 0; s < num_seqs; ++s) {
     const int32_t q0 = query_start[s], q1 = query_start[s + 1];
-    PKV_REQUIRE(q1 >= q0, PKV_ERR_INVALID_ARG, "query_start must not decrease");
     PKV_REQUIRE(q1 - q0 <= static_cast<int64_t>(mask_words) * 32, PKV_ERR_INVALID_ARG,
                 "sequence %d has %d drafted tokens, a mask row holds %lld", s, q1 - q0,
                 static_cast<long long>(mask_words) * 32);

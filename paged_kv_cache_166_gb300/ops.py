@@ -1048,7 +1048,7 @@ def tree_masks(parents: torch.Tensor, query_start: torch.Tensor, words: int = 0)
         raise ValueError(f"query_start must go from 0 to {T}")
     if words <= 0:
         most = int((query_start[1:] - query_start[:-1]).max()) if S else 0
-        words = max(1, -(-most // 32))
+        words = max(1, -(-min(most, T) // 32))  # (more than T: borders that the call refuses)
     _fits("words", words)
     mask = torch.zeros((T, words), dtype=torch.int32)
     depths = torch.zeros(T, dtype=torch.int32)
