@@ -186,7 +186,11 @@ __global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const Adj
   const int r_end = a.row_start != nullptr ? min(a.T, __ldg(a.row_start + s + 1)) : s + 1;
   const int held = min(max(__ldg(a.history_lens + s), 0), a.L);
   const int prompt = a.prompt_lens != nullptr ? __ldg(a.prompt_lens + s) : 0;
-  if (r_first + static_cast<int64_t>(blockIdx.z) >= r_end) return;
+  if (r_first + static_cast<int64_t>(blockIdx.z) >= r_end) {
+    // (what is queued behind this grid relies on the first kernel being done, too)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int shares = gridDim.z, row0 = r_first + blockIdx.z;
   const int rows = (r_end - row0 - 1) / shares + 1;  // row0, row0 + shares, ...
   auto row = [&](int k) { return row0 + static_cast<int64_t>(k) * shares; };
