@@ -173,7 +173,7 @@ __host__ __device__ constexpr int adjust_words(int segments, bool biases) {
 // Grid: CTAs of a request's vocabulary (a power of two), requests, shares of a request's rows.
 template <typename T>
 __global__ void __launch_bounds__(kAdjThreads, 5) adjust_tokens_kernel(const AdjustArgs a) {
-  extern __shared__ uint32_t adj_smem[];
+  extern __shared__ __align__(16) uint32_t adj_smem[];  // (read four words at a time)
   __shared__ int listed;
   const int tid = threadIdx.x, s = blockIdx.y, first = blockIdx.x;
   const int CH = a.segments * kAdjSegment;
