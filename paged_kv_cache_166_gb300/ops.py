@@ -34,11 +34,12 @@ def _stream(device: torch.device) -> int:
 
 
 def _check_cuda(*ts) -> torch.device:
-    at = ts[0].get_device()  # (-1: not a GPU's; numbers compare faster than devices)
+    at = ts[0].get_device()  # (of GPUs: numbers compare faster than devices)
     for t in ts:
-        if t.get_device() != at or at < 0:
-            raise ValueError("tensors must be on one device" if t.is_cuda and ts[0].is_cuda else
-                             "tensors must be CUDA tensors")
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if t.get_device() != at:
+            raise ValueError("tensors must be on one device")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
     return ts[0].device
@@ -923,7 +924,8 @@ def _norm_rotary_write(kind, q, k, v, q_weight, k_weight, eps, positions, table,
         kc, vc, scales = k_cache, v_cache, (None, None)
         dev = _check_cuda(positions, table, slot_mapping, kc, vc)
     at = kc.get_device()
-    if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == at):
+    if not (q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == at
+            and q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda):
         raise ValueError("q, k, v and q_out must be on the caches' device")
     if not (q.dim() == k.dim() == v.dim() == q_out.dim() == 3) or kc.dim() != 4 or vc.dim() != 4:
         raise ValueError("expected q, q_out [T, Hq, D], k, v [T, Hkv, D] and 4-dimensional caches")
@@ -966,7 +968,8 @@ def _norm_rotary_write(kind, q, k, v, q_weight, k_weight, eps, positions, table,
     for w, H, name in ((q_weight, Hq, "q_weight"), (k_weight, Hkv, "k_weight")):
         if w is None:
             continue
-        if w.get_device() != at or not w.is_contiguous() or w.shape not in ((D,), (H, D)):
+        if not w.is_cuda or w.get_device() != at or not w.is_contiguous() \
+                or w.shape not in ((D,), (H, D)):
             raise ValueError(f"{name} must be a contiguous [{D}] or [{H}, {D}] tensor on the "
                              "caches' device")
         kinds.add((dtype_code(w), w.dim() == 2))
@@ -1217,7 +1220,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor, history_lens: tor
     y = logits if out is None else out
     dev = _check_cuda(history, history_lens)
     at = history.get_device()
-    if logits.get_device() != at or y.get_device() != at:
+    if not (logits.is_cuda and y.is_cuda) or logits.get_device() != at or y.get_device() != at:
         raise ValueError("logits and out must be on the device of history")
     if logits.dim() != 2 or y.shape != logits.shape or y.dtype != logits.dtype:
         raise ValueError("expected logits [T, V], and out of the same shape and dtype")
@@ -1233,7 +1236,7 @@ def adjust_logits(logits: torch.Tensor, history: torch.Tensor, history_lens: tor
             return None
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {str(dtype)[6:]}")
-        if t.get_device() != at or t.shape != shape or not t.is_contiguous():
+        if not t.is_cuda or t.get_device() != at or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {list(shape)} on the logits' device")
         return t.data_ptr()
 
