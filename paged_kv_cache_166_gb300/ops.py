@@ -537,7 +537,7 @@ def _fits(name: str, *values: int) -> None:
 
 def _current(dev: torch.device):
     """A context in which ``dev`` is the current device (the library launches there)."""
-    return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _status_ptr(status: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
