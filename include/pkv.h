@@ -818,7 +818,8 @@ int pkv_norm_rotary_write(int32_t codes, const void* q, int64_t q_stride, const 
  * workspace     >= pkv_tree_workspace_size(head_dim) bytes, 256-byte aligned, any contents;
  *               calls that may overlap need their own (host threads that call on one stream
  *               may share one: a call's two launches are queued one behind the other).
- * Supported: F16 and BF16, head_dim 64, 128 or 256, up to 16 query heads per KV head,
+ * Supported: F16 and BF16 (8-bit caches: none of the attentions of several tokens a sequence
+ * takes them), head_dim 64, 128 or 256, up to 16 query heads per KV head,
  * block_size 8, 16 or 32, num_seqs <= 2048, max_blocks_per_seq * block_size < 2^30.
  * Scores, softmax and sums are fp32, probabilities rounded to dtype for the product with V.  A
  * cap (any finite one) adds at most 5e-7 cap to a score's error up to 128, above that 1e-6 |x|.

@@ -181,11 +181,13 @@ struct Pieces {
 };
 
 // blockIdx.x < T: a token, its heads split over gridDim.y CTAs and the CTA's groups of lanes;
-// 8-bit caches: then V's windows, a.v_parts CTAs each.  Bound by the instructions of a head and by
-// how many warps hide its loads.  CTAs an SM: 8,191 tokens of 40 + 40 heads of 128, f16, half
+// 8-bit caches: then V's windows, a.v_parts CTAs each.  Bound by how many loads are on their
+// way: with seven CTAs an SM a prompt keeps DRAM at 50% and the SM at 38% of their peaks, its warps
+// waiting for loads (into fp8 the SM at 57%).  CTAs an SM: 8,191 tokens of 40 + 40 heads of 128, f16, half
 // layout, 114 us with six, 105 with seven (4.8 TB/s), 101 with eight; 1,000 of 64 + 8 heads 12.9,
 // 10.2, 12.1; 640 of them 7.8, 8.6, 9.8: seven.  Interleaved, 4,099 tokens of 32 + 8 heads into fp8
-// 32.7 with eight, 31.8 with nine, 34.4 with ten.  Two heads' loads in flight pay where a head is
+// 32.7 with eight, 31.8 with nine, 34.4 with ten.  (Most forms with a norm spill for it, 16-bit caches
+// 8 to 44 bytes; the other types' numbers were not measured one by one.)  Two heads' loads in flight pay where a head is
 // one piece a lane (37.8 us there with two, 44.6 with four).
 template <typename T, int VEC, bool kInter, int kCodes, int NU, NormForm kForm>
 __global__ void __launch_bounds__(kNormThreads, kInter ? 9 : 7)

@@ -25,7 +25,10 @@
 // the 1.5 us that its 64 KB take.  Measured: trees on a 70B-shaped batch (64 / 8 heads of 128, bf16,
 // 128 contexts, 976 MB) 166 us, 5.9 TB/s; on contexts of 32,768 to 131,072 270 us, 6.5 TB/s; chunks
 // of 513 with slopes on 8 sequences of 40 / 40 heads, f16, 194 us, bound by the row warps' chain of
-// phases, not by memory or products; the smallest calls 10 us, two launches and their chains.
+// phases, not by memory or products; the smallest calls 10 us, two launches and their chains (the
+// joining kernel is launched whether a unit is cut or not).  Behind a cache write a call takes some
+// 1 us more than if lengths and masks were read before that write is done (with a step's norm and
+// rotary write 42.0 us against 40.8 for 16 sequences, 16.8 against 16.1 for the smallest call).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,8 +56,9 @@ constexpr int kTrRowWarps = 8;                 // softmax warps 2 .. 9: a lane q
 constexpr int kTrVWarp = 10, kTrQWarp = 11;    // producer of V; query tiles, and V looked through
 constexpr int kTrThreads = 12 * 32;
 constexpr int kTrChunk = 128 * 128;            // one [128 rows x 128 B] swizzled chunk of Q
-// Of a unit beside its key tiles, in tiles.  A 13B-shaped chunk with 1, 2, 3, 4: 197, 184, 174,
-// 176 us; trees of a 70B-shaped batch 170, 170, 174, 176.
+// Of a unit beside its key tiles, in tiles.  With 1, 2, 3, 4: trees of a 70B-shaped batch 166, 166,
+// 173, 171 us, with slopes 176, 168, 172, 176; a 13B-shaped chunk with slopes 205, 195, 194, 195, without
+// 190, 179, 169, 170; long contexts and heads of 256 the same.
 constexpr int kTrUnitCost = 2;
 constexpr float kTrRescale = 8.f;              // log2 of the growth of a maximum that moves the reference
 
@@ -1390,7 +1394,8 @@ int pkv_tree_attention(const void* q, const void* k_cache, const void* v_cache,
   a.bs = block_size;
   a.W = mask_words;
   a.window = window > (1 << 30) + kTrMaxDepth ? 0 : window;  // no two positions are as far apart
-  // whole 8-row swizzle atoms: a box of q is 8 / gcd(G, 8) drafted tokens, a unit whole boxes
+  // whole 8-row swizzle atoms: a box of q is 8 / gcd(G, 8) drafted tokens, a unit whole boxes (a G
+  // that is no power of two leaves rows idle: 72 of 128 used for 9, 88 for 11, 104 for 13, else 112 or 120)
   a.box = G % 8 == 0 ? 1 : (G % 4 == 0 ? 2 : (G % 2 == 0 ? 4 : 8));
   a.nodes = kTrRows / G / a.box * a.box;
   const double log2e = 1.4426950408889634;

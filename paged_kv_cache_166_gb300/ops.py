@@ -1082,7 +1082,7 @@ def paged_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     (``tree_masks``; None: a chunk, each its predecessors and itself).  ``cap``: scores x become
     cap * tanh(x / cap); ``slopes`` [Hq] (float32): a bias of slope * (key's position - query's);
     ``window``: only the last positions are seen; a drafted token's position is the context's end
-    plus its ``depths`` [T] (None: its number).  Writes and returns out."""
+    plus its ``depths`` [T] (None: its number).  f16 and bf16 caches.  Writes and returns out."""
     dev = _check_cuda(q, k_cache, v_cache, block_tables, context_lens, query_start, out)
     if q.dim() != 3 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or out.shape != q.shape:
         raise ValueError("expected q, out [T, Hq, D] and caches [NB, Hkv, B, D]")
